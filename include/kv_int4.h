@@ -10,7 +10,9 @@
  *   kv_int8_write            the INT8 per-(token, head) comparator's cache write;
  *   kv_int8_paged_attention  decode attention over the INT8 comparator's cache;
  *   kv_int2_write            the INT2 per-(token, head) Lloyd-Max cache write;
- *   kv_int2_paged_attention  decode attention over the INT2 cache.
+ *   kv_int2_paged_attention  decode attention over the INT2 cache;
+ *   kv_int{4,8,2}_rope_write the writes with the rotary position embedding of queries and keys;
+ *   kv_int{4,8,2}_read       cached rows back as the keys and values they stand for.
  *
  * The caller owns every buffer.  The library never allocates device or host memory: the
  * attention's split-KV partials live in a caller-provided workspace whose size
@@ -62,12 +64,14 @@ typedef enum { KV_INT4_F16 = 0, KV_INT4_BF16 = 1, KV_INT4_F32 = 2 } kv_int4_dtyp
 
 /* Indices into the device status array (kv_int4_read_device_status). */
 enum {
-    KV_INT4_STAT_SLOT_OUT_OF_RANGE = 0,  /* write: slot >= num_blocks * block_size (row skipped)      */
+    KV_INT4_STAT_SLOT_OUT_OF_RANGE = 0,  /* write: slot >= num_blocks * block_size (row skipped); read:
+                                            the same (row zero)                                         */
     KV_INT4_STAT_BLOCK_OUT_OF_RANGE = 1, /* attention: block id outside [0, num_blocks) (block skipped) */
     KV_INT4_STAT_BAD_SEQUENCE = 2,       /* attention: query chunk longer than its sequence, or a
                                             sequence longer than its block table                        */
     KV_INT4_STAT_WAIT_TIMEOUT = 3,       /* a pipeline wait gave up; the CTA's output is not valid      */
     KV_INT4_STAT_BAD_SIGN = 4,           /* a rotation sign that is not exactly +1.0f or -1.0f           */
+    KV_INT4_STAT_POSITION_OUT_OF_RANGE = 5,  /* rotary write: position outside the table (token skipped)  */
     KV_INT4_STAT_COUNT = 8
 };
 
@@ -157,6 +161,93 @@ kv_int4_status kv_int2_write(const void* k, const void* v, kv_int4_dtype dtype, 
                              int32_t num_kv_heads, int32_t head_size, const int64_t* slot_mapping,
                              const float* rht_signs, uint8_t* cache, int64_t num_blocks,
                              int32_t block_size, kv_int4_stream_t stream);
+
+/*
+ * kv_int4_rope_write -- kv_int4_write with the rotary position embedding applied on the way: the step
+ * that takes a batch's projected queries, keys and values to rotated queries and cached keys and values,
+ * in one launch.
+ *
+ * Token t at position p = positions[t] takes the row cs = cos_sin[p] (rot_dim / 2 cosines, then
+ * rot_dim / 2 sines).  In every query and key head vector x, upcast exactly to fp32, the first rot_dim
+ * dimensions are rotated in pairs (a, b), i = 0 .. rot_dim / 2 - 1:
+ *   (x_i, x_{i + rot_dim/2}) when interleaved is 0, (x_{2i}, x_{2i+1}) otherwise:
+ *   a' = fp32(fp32(a cs_i) - fp32(b cs_{rot_dim/2 + i})),  b' = fp32(fp32(b cs_i) + fp32(a cs_{rot_dim/2 + i}));
+ * the other dimensions stay.  Rotated queries are rounded once to dtype and stored in q_out.  Rotated
+ * keys (still fp32, not rounded to dtype) and the values are encoded and stored exactly as
+ * kv_int4_write does, so the bytes are bit-exact with this definition.
+ *
+ * q              [num_tokens, num_q_heads, head_size], dtype F16 or BF16, q_token_stride elements from
+ *                one token to the next (its heads contiguous), as the slices of a fused projection are;
+ *                k, v and q_out likewise with their strides.  Strides are multiples of 8, at least the
+ *                heads' elements (of no meaning for a single token); base pointers 16-B aligned.
+ * num_q_heads    0..1024; 0: only keys and values (q and q_out may be NULL).
+ * positions      [num_tokens] int64.  A token whose position is outside [0, max_position) is skipped
+ *                whole (its cache row and its q_out row are left as they were) and counted
+ *                (KV_INT4_STAT_POSITION_OUT_OF_RANGE), unless its slot and its position are both
+ *                negative: a padding token, not counted.
+ * cos_sin        [max_position, rot_dim] fp32, 16-B aligned.  rot_dim: a multiple of 16, 16..head_size.
+ * slot_mapping   as kv_int4_write; a token with a negative slot still has its query rotated.  Slots
+ *                that are not negative must be distinct within the call.
+ * q_out          may be q itself with the same stride (rotation in place); otherwise it must not
+ *                overlap q, k or v.
+ * Other arguments, limits and errors as kv_int4_write.
+ */
+kv_int4_status kv_int4_rope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                                  int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                                  int64_t num_tokens, int32_t num_kv_heads, int32_t head_size,
+                                  const int64_t* positions, const float* cos_sin, int64_t max_position,
+                                  int32_t rot_dim, int32_t interleaved, const int64_t* slot_mapping,
+                                  const float* rht_signs, void* q_out, int64_t q_out_token_stride, uint8_t* cache,
+                                  int64_t num_blocks, int32_t block_size, kv_int4_stream_t stream);
+
+/* kv_int8_rope_write -- the same into the INT8 comparator's cache (rows as kv_int8_write; no signs). */
+kv_int4_status kv_int8_rope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                                  int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                                  int64_t num_tokens, int32_t num_kv_heads, int32_t head_size,
+                                  const int64_t* positions, const float* cos_sin, int64_t max_position,
+                                  int32_t rot_dim, int32_t interleaved, const int64_t* slot_mapping, void* q_out,
+                                  int64_t q_out_token_stride, uint8_t* cache, int64_t num_blocks, int32_t block_size,
+                                  kv_int4_stream_t stream);
+
+/* kv_int2_rope_write -- the same into the INT2 Lloyd-Max cache (rows as kv_int2_write). */
+kv_int4_status kv_int2_rope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                                  int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                                  int64_t num_tokens, int32_t num_kv_heads, int32_t head_size,
+                                  const int64_t* positions, const float* cos_sin, int64_t max_position,
+                                  int32_t rot_dim, int32_t interleaved, const int64_t* slot_mapping,
+                                  const float* rht_signs, void* q_out, int64_t q_out_token_stride, uint8_t* cache,
+                                  int64_t num_blocks, int32_t block_size, kv_int4_stream_t stream);
+
+/*
+ * kv_int4_read -- the keys and values that cached rows stand for: the inverse of kv_int4_write, for
+ * handing a cached prefix to dense attention, moving a sequence to another cache or mode, or checking
+ * what was stored.
+ *
+ * For every token t with slot = slot_mapping[t], every kv head and both planes, with the row's codes,
+ * scale s' and zero-point zp:  x = c D H_d ((code - zp) s')  (D = diag(rht_signs), c = fp32(1/sqrt(head_size)));
+ * the integer sums are exact, and x = fp32(fp32(s' c) n) is rounded once more to out_dtype.
+ *
+ * slot_mapping   [num_tokens] int64, repeats allowed.  A negative slot gives a row of zeros; a slot
+ *                >= num_blocks * block_size does too and is counted (KV_INT4_STAT_SLOT_OUT_OF_RANGE).
+ * rht_signs      as passed to the write.
+ * k_out, v_out   [num_tokens, num_kv_heads, head_size] contiguous, out_dtype F16, BF16 or F32, 16-B
+ *                aligned.
+ * cache, limits and errors as kv_int4_write.  num_tokens == 0 launches nothing and returns KV_INT4_OK.
+ */
+kv_int4_status kv_int4_read(const uint8_t* cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                            int32_t head_size, const int64_t* slot_mapping, int64_t num_tokens, const float* rht_signs,
+                            void* k_out, void* v_out, kv_int4_dtype out_dtype, kv_int4_stream_t stream);
+
+/* kv_int8_read -- the same for the INT8 comparator's rows: x = fp32(code s), rounded to out_dtype. */
+kv_int4_status kv_int8_read(const uint8_t* cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                            int32_t head_size, const int64_t* slot_mapping, int64_t num_tokens, void* k_out,
+                            void* v_out, kv_int4_dtype out_dtype, kv_int4_stream_t stream);
+
+/* kv_int2_read -- the same for the INT2 Lloyd-Max rows: x = sigma c D H_d centroid(code), the sums in
+ * fp32 butterflies at strides 1, 2, ..., head_size/2. */
+kv_int4_status kv_int2_read(const uint8_t* cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                            int32_t head_size, const int64_t* slot_mapping, int64_t num_tokens, const float* rht_signs,
+                            void* k_out, void* v_out, kv_int4_dtype out_dtype, kv_int4_stream_t stream);
 
 /*
  * Bytes of workspace kv_int4_paged_attention needs for these sizes (same arguments as the

@@ -17,7 +17,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_lib", "libkv_int4.so")
 
 KV_INT4_F16, KV_INT4_BF16, KV_INT4_F32 = 0, 1, 2
-STAT_NAMES = ["slot_out_of_range", "block_out_of_range", "bad_sequence", "wait_timeout", "bad_sign"]
+STAT_NAMES = ["slot_out_of_range", "block_out_of_range", "bad_sequence", "wait_timeout", "bad_sign",
+              "position_out_of_range"]
 _STAT_COUNT = 8
 _DTYPES = {torch.float16: KV_INT4_F16, torch.bfloat16: KV_INT4_BF16, torch.float32: KV_INT4_F32}
 
@@ -58,6 +59,20 @@ def _load():
     lib.kv_int2_row_bytes.restype = i32
     lib.kv_int2_write.argtypes = lib.kv_int4_write.argtypes
     lib.kv_int2_write.restype = ctypes.c_int
+    lib.kv_int4_rope_write.argtypes = [vp, i64, i32, vp, i64, vp, i64, ctypes.c_int, i64, i32, i32, vp, vp, i64, i32, i32,
+                                       vp, vp, vp, i64, vp, i64, i32, vp]
+    lib.kv_int4_rope_write.restype = ctypes.c_int
+    lib.kv_int8_rope_write.argtypes = [vp, i64, i32, vp, i64, vp, i64, ctypes.c_int, i64, i32, i32, vp, vp, i64, i32, i32,
+                                       vp, vp, i64, vp, i64, i32, vp]
+    lib.kv_int8_rope_write.restype = ctypes.c_int
+    lib.kv_int2_rope_write.argtypes = lib.kv_int4_rope_write.argtypes
+    lib.kv_int2_rope_write.restype = ctypes.c_int
+    lib.kv_int4_read.argtypes = [vp, i64, i32, i32, i32, vp, i64, vp, vp, vp, ctypes.c_int, vp]
+    lib.kv_int4_read.restype = ctypes.c_int
+    lib.kv_int8_read.argtypes = [vp, i64, i32, i32, i32, vp, i64, vp, vp, ctypes.c_int, vp]
+    lib.kv_int8_read.restype = ctypes.c_int
+    lib.kv_int2_read.argtypes = lib.kv_int4_read.argtypes
+    lib.kv_int2_read.restype = ctypes.c_int
     lib.kv_int4_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
     lib.kv_int4_attention_workspace_bytes.restype = szt
     lib.kv_int4_attention_segment_len.argtypes = [i32, i32, i32]
@@ -209,6 +224,151 @@ def kv_int2_write(key: torch.Tensor, value: torch.Tensor, slot_mapping: torch.Te
     """Rotate ``key``/``value`` [T, H, d] as kv_int4_write does, quantise them to INT2 Lloyd-Max codes
     and pack them into ``kv_cache`` at ``slot_mapping``."""
     _rotated_write("kv_int2_write", kv_int2_row_bytes, key, value, slot_mapping, rht_signs, kv_cache, stream)
+
+
+def _token_rows(t: torch.Tensor, name: str, dtypes) -> torch.Tensor:
+    """A CUDA tensor [tokens, heads, head_size] whose tokens' rows are contiguous, any stride between them."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} must be [num_tokens, num_heads, head_size] with each token's heads contiguous")
+    return t
+
+
+def _rope_write(fn, row_bytes, query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache, query_out,
+                interleaved, stream):
+    _token_rows(key, "key", (torch.float16, torch.bfloat16))
+    _token_rows(value, "value", (key.dtype,))
+    _cuda(positions, "positions", (torch.int64,))
+    _cuda(cos_sin, "cos_sin", (torch.float32,))
+    _cuda(slot_mapping, "slot_mapping", (torch.int64,))
+    _cuda(kv_cache, "kv_cache", (torch.uint8,))
+    if value.shape != key.shape:
+        raise ValueError("key and value must both be [num_tokens, num_kv_heads, head_size]")
+    T, H, d = key.shape
+    if rht_signs is not None:
+        _cuda(rht_signs, "rht_signs", (torch.float32,))
+        if rht_signs.shape != (d,):
+            raise ValueError("rht_signs must be [head_size]")
+    if slot_mapping.shape != (T,) or positions.shape != (T,):
+        raise ValueError("positions and slot_mapping must be [num_tokens]")
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_position, rot_dim]")
+    if kv_cache.dim() != 5 or kv_cache.shape[1] != 2 or kv_cache.shape[3] != H or kv_cache.shape[4] != row_bytes(d):
+        raise ValueError(f"kv_cache must be (NB, 2, bs, {H}, {row_bytes(d)})")
+    Hq = 0
+    if query is not None:
+        _token_rows(query, "query", (key.dtype,))
+        if query.shape[0] != T or query.shape[2] != d:
+            raise ValueError("query must be [num_tokens, num_q_heads, head_size]")
+        Hq = query.shape[1]
+        if query_out is None:
+            query_out = torch.empty((T, Hq, d), dtype=query.dtype, device=query.device)
+        _token_rows(query_out, "query_out", (key.dtype,))
+        if query_out.shape != query.shape:
+            raise ValueError("query_out must have the query's shape")
+    elif query_out is not None:
+        raise ValueError("query_out needs a query")
+    with torch.cuda.device(_one_device(query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache,
+                                       query_out)):
+        signs = () if rht_signs is None else (rht_signs.data_ptr(),)
+        st = getattr(load(), fn)(query.data_ptr() if Hq else None, query.stride(0) if Hq else 0, Hq, key.data_ptr(),
+                                 key.stride(0), value.data_ptr(), value.stride(0), _DTYPES[key.dtype], T, H, d,
+                                 positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
+                                 int(bool(interleaved)), slot_mapping.data_ptr(), *signs,
+                                 query_out.data_ptr() if Hq else None, query_out.stride(0) if Hq else 0,
+                                 kv_cache.data_ptr(), kv_cache.shape[0], kv_cache.shape[2], _stream(stream))
+    _check(fn, st)
+    return query_out
+
+
+def kv_int4_rope_write(query, key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                       slot_mapping: torch.Tensor, rht_signs: torch.Tensor, kv_cache: torch.Tensor, query_out=None,
+                       interleaved: bool = False, stream=None):
+    """kv_int4_write with the rotary position embedding applied on the way: ``query`` [T, Hq, d] (or None)
+    and ``key`` [T, H, d] are rotated by the rows ``cos_sin[positions]`` (fp32 [max_position, rot_dim]:
+    rot_dim / 2 cosines, then as many sines; halves paired, or neighbours when ``interleaved``), the keys
+    and values go into ``kv_cache`` at ``slot_mapping``, and the rotated queries are returned
+    (``query_out``, which may be ``query`` itself).  Query, key, value and query_out may have any stride
+    between tokens, as the slices of a fused projection do.  A token whose position is outside the table
+    is skipped: its ``query_out`` row is left as it was."""
+    if rht_signs is None:
+        raise ValueError("rht_signs must be a CUDA tensor")
+    return _rope_write("kv_int4_rope_write", kv_int4_row_bytes, query, key, value, positions, cos_sin, slot_mapping,
+                       rht_signs, kv_cache, query_out, interleaved, stream)
+
+
+def kv_int8_rope_write(query, key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                       slot_mapping: torch.Tensor, kv_cache: torch.Tensor, query_out=None, interleaved: bool = False,
+                       stream=None):
+    """kv_int4_rope_write into the INT8 comparator's cache (no signs)."""
+    return _rope_write("kv_int8_rope_write", kv_int8_row_bytes, query, key, value, positions, cos_sin, slot_mapping,
+                       None, kv_cache, query_out, interleaved, stream)
+
+
+def kv_int2_rope_write(query, key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                       slot_mapping: torch.Tensor, rht_signs: torch.Tensor, kv_cache: torch.Tensor, query_out=None,
+                       interleaved: bool = False, stream=None):
+    """kv_int4_rope_write into the INT2 Lloyd-Max cache."""
+    if rht_signs is None:
+        raise ValueError("rht_signs must be a CUDA tensor")
+    return _rope_write("kv_int2_rope_write", kv_int2_row_bytes, query, key, value, positions, cos_sin, slot_mapping,
+                       rht_signs, kv_cache, query_out, interleaved, stream)
+
+
+def _read(fn, row_bytes, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, stream):
+    _cuda(kv_cache, "kv_cache", (torch.uint8,))
+    _cuda(slot_mapping, "slot_mapping", (torch.int64,))
+    if slot_mapping.dim() != 1:
+        raise ValueError("slot_mapping must be [num_tokens]")
+    sizes = {row_bytes(d): d for d in (64, 128)}
+    if kv_cache.dim() != 5 or kv_cache.shape[1] != 2 or kv_cache.shape[4] not in sizes:
+        raise ValueError(f"kv_cache must be (NB, 2, bs, H, row bytes) with rows of {sorted(sizes)} bytes")
+    T, H, d = slot_mapping.shape[0], kv_cache.shape[3], sizes[kv_cache.shape[4]]
+    if rht_signs is not None:
+        _cuda(rht_signs, "rht_signs", (torch.float32,))
+        if rht_signs.shape != (d,):
+            raise ValueError("rht_signs must be [head_size]")
+    if key_out is None:
+        key_out = torch.empty((T, H, d), dtype=dtype, device=kv_cache.device)
+    if value_out is None:
+        value_out = torch.empty((T, H, d), dtype=key_out.dtype, device=kv_cache.device)
+    _cuda(key_out, "key_out", tuple(_DTYPES))
+    _cuda(value_out, "value_out", (key_out.dtype,))
+    if key_out.shape != (T, H, d) or value_out.shape != (T, H, d):
+        raise ValueError(f"key_out and value_out must be [num_tokens, {H}, {d}]")
+    with torch.cuda.device(_one_device(kv_cache, slot_mapping, rht_signs, key_out, value_out)):
+        signs = () if rht_signs is None else (rht_signs.data_ptr(),)
+        st = getattr(load(), fn)(kv_cache.data_ptr(), kv_cache.shape[0], kv_cache.shape[2], H, d,
+                                 slot_mapping.data_ptr(), T, *signs, key_out.data_ptr(), value_out.data_ptr(),
+                                 _DTYPES[key_out.dtype], _stream(stream))
+    _check(fn, st)
+    return key_out, value_out
+
+
+def kv_int4_read(kv_cache: torch.Tensor, slot_mapping: torch.Tensor, rht_signs: torch.Tensor, dtype=torch.bfloat16,
+                 key_out=None, value_out=None, stream=None):
+    """The keys and values [T, H, d] (``dtype``: fp16, bf16 or fp32, or that of ``key_out``) that the cached
+    rows at ``slot_mapping`` stand for; negative slots give rows of zeros."""
+    if rht_signs is None:
+        raise ValueError("rht_signs must be a CUDA tensor")
+    return _read("kv_int4_read", kv_int4_row_bytes, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, stream)
+
+
+def kv_int8_read(kv_cache: torch.Tensor, slot_mapping: torch.Tensor, dtype=torch.bfloat16, key_out=None, value_out=None,
+                 stream=None):
+    """kv_int4_read for the INT8 comparator's cache (no signs)."""
+    return _read("kv_int8_read", kv_int8_row_bytes, kv_cache, slot_mapping, None, dtype, key_out, value_out, stream)
+
+
+def kv_int2_read(kv_cache: torch.Tensor, slot_mapping: torch.Tensor, rht_signs: torch.Tensor, dtype=torch.bfloat16,
+                 key_out=None, value_out=None, stream=None):
+    """kv_int4_read for the INT2 Lloyd-Max cache."""
+    if rht_signs is None:
+        raise ValueError("rht_signs must be a CUDA tensor")
+    return _read("kv_int2_read", kv_int2_row_bytes, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, stream)
 
 
 def kv_int4_attention_segment_len(num_seqs: int, max_seq_len: int, segment_len: int = 0) -> int:

@@ -178,6 +178,158 @@ kv_int4_status kv_int2_write(const void* k, const void* v, kv_int4_dtype dtype, 
                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
+}  // extern "C"
+
+namespace {
+
+// The checks and the launch that the rotary writes of the three modes share (bits 4, 8 or 2).
+kv_int4_status rope_write_impl(int bits, const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                               int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                               int64_t num_tokens, int32_t num_kv_heads, int32_t head_size, const int64_t* positions,
+                               const float* cos_sin, int64_t max_position, int32_t rot_dim, int32_t interleaved,
+                               const int64_t* slot_mapping, const float* rht_signs, void* q_out,
+                               int64_t q_out_token_stride, uint8_t* cache, int64_t num_blocks, int32_t block_size,
+                               kv_int4_stream_t stream) {
+    if (num_tokens < 0 || num_blocks < 0 || num_kv_heads <= 0 || num_q_heads < 0 || max_position < 0 || rot_dim < 0)
+        return KV_INT4_EINVAL;
+    if (head_size != 64 && head_size != 128) return KV_INT4_EUNSUPPORTED;
+    if (block_size != kBlockSize || num_kv_heads > 64 || num_q_heads > 1024 || !valid_dtype_16(dtype))
+        return KV_INT4_EUNSUPPORTED;
+    if (rot_dim == 0 || rot_dim > head_size || rot_dim % 16 != 0) return KV_INT4_EUNSUPPORTED;
+    if (num_tokens == 0) return KV_INT4_OK;
+    // 32-bit vector and item indices
+    if (num_tokens >= ((int64_t)1 << 31) / (2 * num_kv_heads) || (num_q_heads > 0 && num_tokens >= ((int64_t)1 << 31) / num_q_heads))
+        return KV_INT4_EUNSUPPORTED;
+    if (!k || !v || !positions || !cos_sin || !slot_mapping || (bits != 8 && !rht_signs) || !cache ||
+        (num_q_heads > 0 && (!q || !q_out)))
+        return KV_INT4_EINVAL;
+    const int64_t kv_row = (int64_t)num_kv_heads * head_size, q_row = (int64_t)num_q_heads * head_size;
+    // rows of different tokens must not overlap (a single token needs no stride)
+    if (num_tokens > 1 && (k_token_stride < kv_row || v_token_stride < kv_row ||
+                           (num_q_heads > 0 && (q_token_stride < q_row || q_out_token_stride < q_row))))
+        return KV_INT4_EINVAL;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned16(cos_sin)) return KV_INT4_EALIGN;
+    if (num_tokens > 1 && (k_token_stride % 8 != 0 || v_token_stride % 8 != 0)) return KV_INT4_EALIGN;
+    if (num_q_heads > 0 && (!aligned16(q) || !aligned16(q_out) ||
+                            (num_tokens > 1 && (q_token_stride % 8 != 0 || q_out_token_stride % 8 != 0))))
+        return KV_INT4_EALIGN;
+    RopeWriteParams p;
+    p.w.k = k;
+    p.w.v = v;
+    p.w.slots = slot_mapping;
+    p.w.signs = bits != 8 ? rht_signs : nullptr;
+    p.w.cache = cache;
+    p.w.status = status_ptr();
+    p.w.num_tokens = num_tokens;
+    p.w.num_slots = num_blocks * block_size;
+    p.w.H = num_kv_heads;
+    p.w.c = bits != 8 ? (float)(1.0 / std::sqrt((double)head_size)) : 1.0f;
+    p.q = q;
+    p.q_out = q_out;
+    p.positions = positions;
+    p.cos_sin = cos_sin;
+    p.max_position = max_position;
+    p.q_stride = q_token_stride;
+    p.k_stride = k_token_stride;
+    p.v_stride = v_token_stride;
+    p.qo_stride = q_out_token_stride;
+    p.Hq = num_q_heads;
+    p.rot = rot_dim;
+    const DType dt = dtype == KV_INT4_BF16 ? DType::BF16 : DType::F16;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool inter = interleaved != 0;
+    return from_cuda(bits == 8   ? launch_rope_write_int8(p, head_size, dt, inter, s)
+                     : bits == 2 ? launch_rope_write_int2(p, head_size, dt, inter, s)
+                                 : launch_rope_write(p, head_size, dt, inter, s));
+}
+
+kv_int4_status read_impl(int bits, const uint8_t* cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                         int32_t head_size, const int64_t* slot_mapping, int64_t num_tokens, const float* rht_signs,
+                         void* k_out, void* v_out, kv_int4_dtype out_dtype, kv_int4_stream_t stream) {
+    if (num_tokens < 0 || num_blocks < 0 || num_kv_heads <= 0) return KV_INT4_EINVAL;
+    if (head_size != 64 && head_size != 128) return KV_INT4_EUNSUPPORTED;
+    if (block_size != kBlockSize || num_kv_heads > 64 || !(valid_dtype_16(out_dtype) || out_dtype == KV_INT4_F32))
+        return KV_INT4_EUNSUPPORTED;
+    if (num_tokens == 0) return KV_INT4_OK;
+    if (num_tokens >= ((int64_t)1 << 31) / (2 * num_kv_heads)) return KV_INT4_EUNSUPPORTED;   // 32-bit vector index
+    if (!cache || !slot_mapping || (bits != 8 && !rht_signs) || !k_out || !v_out) return KV_INT4_EINVAL;
+    if (!aligned16(cache) || !aligned16(k_out) || !aligned16(v_out)) return KV_INT4_EALIGN;
+    ReadParams p;
+    p.cache = cache;
+    p.slots = slot_mapping;
+    p.signs = bits != 8 ? rht_signs : nullptr;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.status = status_ptr();
+    p.num_tokens = num_tokens;
+    p.num_slots = num_blocks * block_size;
+    p.H = num_kv_heads;
+    p.c = bits != 8 ? (float)(1.0 / std::sqrt((double)head_size)) : 1.0f;
+    const DType dt = out_dtype == KV_INT4_BF16 ? DType::BF16 : (out_dtype == KV_INT4_F16 ? DType::F16 : DType::F32);
+    return from_cuda(launch_read(p, bits, head_size, dt, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+kv_int4_status kv_int4_rope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                                  int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                                  int64_t num_tokens, int32_t num_kv_heads, int32_t head_size,
+                                  const int64_t* positions, const float* cos_sin, int64_t max_position,
+                                  int32_t rot_dim, int32_t interleaved, const int64_t* slot_mapping,
+                                  const float* rht_signs, void* q_out, int64_t q_out_token_stride, uint8_t* cache,
+                                  int64_t num_blocks, int32_t block_size, kv_int4_stream_t stream) {
+    return rope_write_impl(4, q, q_token_stride, num_q_heads, k, k_token_stride, v, v_token_stride, dtype, num_tokens,
+                           num_kv_heads, head_size, positions, cos_sin, max_position, rot_dim, interleaved, slot_mapping,
+                           rht_signs, q_out, q_out_token_stride, cache, num_blocks, block_size, stream);
+}
+
+kv_int4_status kv_int8_rope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                                  int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                                  int64_t num_tokens, int32_t num_kv_heads, int32_t head_size,
+                                  const int64_t* positions, const float* cos_sin, int64_t max_position,
+                                  int32_t rot_dim, int32_t interleaved, const int64_t* slot_mapping, void* q_out,
+                                  int64_t q_out_token_stride, uint8_t* cache, int64_t num_blocks, int32_t block_size,
+                                  kv_int4_stream_t stream) {
+    return rope_write_impl(8, q, q_token_stride, num_q_heads, k, k_token_stride, v, v_token_stride, dtype, num_tokens,
+                           num_kv_heads, head_size, positions, cos_sin, max_position, rot_dim, interleaved, slot_mapping,
+                           nullptr, q_out, q_out_token_stride, cache, num_blocks, block_size, stream);
+}
+
+kv_int4_status kv_int2_rope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                                  int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                                  int64_t num_tokens, int32_t num_kv_heads, int32_t head_size,
+                                  const int64_t* positions, const float* cos_sin, int64_t max_position,
+                                  int32_t rot_dim, int32_t interleaved, const int64_t* slot_mapping,
+                                  const float* rht_signs, void* q_out, int64_t q_out_token_stride, uint8_t* cache,
+                                  int64_t num_blocks, int32_t block_size, kv_int4_stream_t stream) {
+    return rope_write_impl(2, q, q_token_stride, num_q_heads, k, k_token_stride, v, v_token_stride, dtype, num_tokens,
+                           num_kv_heads, head_size, positions, cos_sin, max_position, rot_dim, interleaved, slot_mapping,
+                           rht_signs, q_out, q_out_token_stride, cache, num_blocks, block_size, stream);
+}
+
+kv_int4_status kv_int4_read(const uint8_t* cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                            int32_t head_size, const int64_t* slot_mapping, int64_t num_tokens, const float* rht_signs,
+                            void* k_out, void* v_out, kv_int4_dtype out_dtype, kv_int4_stream_t stream) {
+    return read_impl(4, cache, num_blocks, block_size, num_kv_heads, head_size, slot_mapping, num_tokens, rht_signs,
+                     k_out, v_out, out_dtype, stream);
+}
+
+kv_int4_status kv_int8_read(const uint8_t* cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                            int32_t head_size, const int64_t* slot_mapping, int64_t num_tokens, void* k_out,
+                            void* v_out, kv_int4_dtype out_dtype, kv_int4_stream_t stream) {
+    return read_impl(8, cache, num_blocks, block_size, num_kv_heads, head_size, slot_mapping, num_tokens, nullptr,
+                     k_out, v_out, out_dtype, stream);
+}
+
+kv_int4_status kv_int2_read(const uint8_t* cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
+                            int32_t head_size, const int64_t* slot_mapping, int64_t num_tokens, const float* rht_signs,
+                            void* k_out, void* v_out, kv_int4_dtype out_dtype, kv_int4_stream_t stream) {
+    return read_impl(2, cache, num_blocks, block_size, num_kv_heads, head_size, slot_mapping, num_tokens, rht_signs,
+                     k_out, v_out, out_dtype, stream);
+}
+
 int32_t kv_int4_attention_segment_len(int32_t num_seqs, int32_t max_seq_len, int32_t segment_len) {
     if (num_seqs < 0 || max_seq_len < 0 || segment_len < 0) return 0;
     if (segment_len > 0) return (segment_len % kBlockSize == 0) ? segment_len : 0;

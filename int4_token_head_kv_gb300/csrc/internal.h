@@ -30,6 +30,32 @@ struct WriteParams {
     float c;            // fp32(1 / sqrt(head_size))
 };
 
+// The write with the position rotation: queries and keys are rotated, then keys and values written.
+struct RopeWriteParams {
+    WriteParams w;
+    const void* q;
+    void* q_out;
+    const int64_t* positions;
+    const float* cos_sin;   // [max_position][rot]: rot / 2 cosines, then rot / 2 sines
+    int64_t max_position;
+    int64_t q_stride, k_stride, v_stride, qo_stride;   // elements from one token to the next
+    int Hq;                 // 0: no queries
+    int rot;                // rotated dimensions, a multiple of 16
+};
+
+struct ReadParams {
+    const uint8_t* cache;
+    const int64_t* slots;
+    const float* signs;
+    void* k_out;
+    void* v_out;
+    uint32_t* status;
+    int64_t num_tokens;
+    int64_t num_slots;
+    int H;
+    float c;
+};
+
 struct AttnParams {
     const void* q;
     const uint8_t* cache;
@@ -85,6 +111,12 @@ cudaError_t launch_write(const WriteParams& p, int head_size, DType dt, cudaStre
 cudaError_t launch_write_int8(const WriteParams& p, int head_size, DType dt, cudaStream_t stream);
 // INT2 Lloyd-Max rows (D/4 code bytes + the fp32 RMS scale) after the INT4 mode's rotation.
 cudaError_t launch_write_int2(const WriteParams& p, int head_size, DType dt, cudaStream_t stream);
+// The same with the position rotation on the way.
+cudaError_t launch_rope_write(const RopeWriteParams& p, int head_size, DType dt, bool interleaved, cudaStream_t stream);
+cudaError_t launch_rope_write_int8(const RopeWriteParams& p, int head_size, DType dt, bool interleaved, cudaStream_t stream);
+cudaError_t launch_rope_write_int2(const RopeWriteParams& p, int head_size, DType dt, bool interleaved, cudaStream_t stream);
+// Cached rows back as the values they stand for (bits 4, 8 or 2).
+cudaError_t launch_read(const ReadParams& p, int bits, int head_size, DType out_dt, cudaStream_t stream);
 // Decode path: query rotation, the split-KV segment walker, and the combine that finishes every
 // decode sequence.  num_ctas is the walker's grid (decode_grid_size).
 // bits: 4 for the INT4 cache, 8 for the INT8 comparator's cache (no rotation, no zero-points), 2 for
