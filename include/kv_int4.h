@@ -12,7 +12,8 @@
  *   kv_int2_write            the INT2 per-(token, head) Lloyd-Max cache write;
  *   kv_int2_paged_attention  decode attention over the INT2 cache;
  *   kv_int{4,8,2}_rope_write the writes with the rotary position embedding of queries and keys;
- *   kv_int{4,8,2}_read       cached rows back as the keys and values they stand for.
+ *   kv_int{4,8,2}_read       cached rows back as the keys and values they stand for;
+ *   kv_int4_shared_prefix_attention  decode attention of a batch that shares a cached prefix.
  *
  * The caller owns every buffer.  The library never allocates device or host memory: the
  * attention's split-KV partials live in a caller-provided workspace whose size
@@ -357,6 +358,50 @@ kv_int4_status kv_int4_paged_attention_ex(const void* q, kv_int4_dtype q_dtype, 
                                           kv_int4_dtype out_dtype, void* workspace,
                                           size_t workspace_bytes, kv_int4_stream_t stream,
                                           const kv_int4_attn_options* options);
+
+/*
+ * kv_int4_shared_prefix_attention -- kv_int4_paged_attention for a decode batch whose sequences start
+ * with the same cached tokens (samples of one prompt, questions on one document): the same result, with
+ * the shared tokens read and dequantised once for up to 128 / (num_q_heads / num_kv_heads) sequences
+ * instead of once for each.
+ *
+ * The first prefix_len / 16 (rounded down) blocks of every sequence are prefix_blocks, and the first
+ * entries of its block_tables row name the same blocks (entry i of a row is the sequence's tokens 16 i ..
+ * 16 i + 15, as in the plain call); the library reads either.  A row whose sequence ends inside the prefix
+ * needs no more entries than its tokens: it sees its first seq_lens[b] tokens of the prefix; seq_lens 0 (a
+ * padding row) yields zeros.
+ *
+ * Computation: one kernel takes every query row of the batch against the prefix's keys, split among the
+ * SMs, as the prefill does (tcgen05), the decode path takes the tokens behind the prefix, and the
+ * combine merges both in a fixed order.  With one sequence, or a prefix below 128 tokens, it is the
+ * plain call.  The prefix's split depends on the batch's size, so a sequence's output may differ in the
+ * last bits between batches; the same call gives the same bits.
+ *
+ * prefix_blocks  [prefix_len / 16] int32, may be NULL when prefix_len < 16.
+ * prefix_len     0 .. 16 max_blocks_per_seq + 15.
+ * max_query_len  1 (a larger value returns KV_INT4_EUNSUPPORTED and launches nothing).
+ * workspace      >= kv_int4_shared_prefix_workspace_bytes(...) bytes.
+ * Other arguments, alignment, supported sizes, clamping and error behaviour as kv_int4_paged_attention.
+ */
+kv_int4_status kv_int4_shared_prefix_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens,
+                                               int32_t num_q_heads, const uint8_t* cache, int64_t num_blocks,
+                                               int32_t num_kv_heads, int32_t head_size, int32_t block_size,
+                                               const int32_t* prefix_blocks, int32_t prefix_len,
+                                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                               const int32_t* seq_lens, const int32_t* query_start_loc,
+                                               int32_t num_seqs, int32_t max_query_len, int32_t max_seq_len,
+                                               float softmax_scale, const float* rht_signs, int32_t segment_len,
+                                               void* out, kv_int4_dtype out_dtype, void* workspace,
+                                               size_t workspace_bytes, kv_int4_stream_t stream);
+
+/*
+ * Bytes of workspace kv_int4_shared_prefix_attention needs for these sizes: the decode path's for the
+ * tokens behind the prefix, then per split of the prefix and query row an fp32 output and a (max, sum)
+ * pair.  0 when the arguments are invalid or num_seqs or num_q_tokens is 0.
+ */
+size_t kv_int4_shared_prefix_workspace_bytes(int64_t num_q_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                             int32_t head_size, int32_t num_seqs, int32_t prefix_len,
+                                             int32_t max_seq_len, int32_t segment_len);
 
 /*
  * kv_int8_paged_attention -- decode attention over the INT8 comparator's cache (as written by

@@ -93,6 +93,11 @@ def _load():
     lib.kv_int8_paged_attention.restype = ctypes.c_int
     lib.kv_int2_paged_attention.argtypes = lib.kv_int4_paged_attention.argtypes
     lib.kv_int2_paged_attention.restype = ctypes.c_int
+    lib.kv_int4_shared_prefix_attention.argtypes = [vp, ctypes.c_int, i64, i32, vp, i64, i32, i32, i32, vp, i32, vp, i32,
+                                                    vp, vp, i32, i32, i32, f32, vp, i32, vp, ctypes.c_int, vp, szt, vp]
+    lib.kv_int4_shared_prefix_attention.restype = ctypes.c_int
+    lib.kv_int4_shared_prefix_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, i32, i32]
+    lib.kv_int4_shared_prefix_workspace_bytes.restype = szt
     lib.kv_int4_read_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
     lib.kv_int4_read_device_status.restype = ctypes.c_int
     lib.kv_int4_clear_device_status.argtypes = [vp]
@@ -565,6 +570,58 @@ def kv_int2_paged_attention(query: torch.Tensor, kv_cache: torch.Tensor, block_t
                                           max_seq_len, float(softmax_scale), rht_signs.data_ptr(), segment_len,
                                           out.data_ptr(), _DTYPES[out.dtype], ws_ptr, ws_bytes, _stream(stream))
     _check("kv_int2_paged_attention", st)
+    return out
+
+
+def kv_int4_shared_prefix_workspace_bytes(num_q_tokens: int, num_q_heads: int, num_kv_heads: int, head_size: int,
+                                          num_seqs: int, prefix_len: int, max_seq_len: int, segment_len: int = 0) -> int:
+    return int(load().kv_int4_shared_prefix_workspace_bytes(num_q_tokens, num_q_heads, num_kv_heads, head_size, num_seqs,
+                                                          prefix_len, max_seq_len, segment_len))
+
+
+def kv_int4_shared_prefix_attention(query: torch.Tensor, kv_cache: torch.Tensor, prefix_blocks: torch.Tensor,
+                                    prefix_len: int, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                                    query_start_loc: torch.Tensor, softmax_scale: float, rht_signs: torch.Tensor,
+                                    max_seq_len: int, out=None, out_dtype=None, segment_len: int = 0, workspace=None,
+                                    stream=None) -> torch.Tensor:
+    """kv_int4_paged_attention of a decode batch (one query token per sequence) whose first ``prefix_len``
+    cached tokens are the same: their whole blocks are ``prefix_blocks`` (int32 [prefix_len // 16]), read once
+    for the batch; the other arguments as there, ``block_tables`` and ``seq_lens`` counting the prefix."""
+    _cuda(query, "query", (torch.float16, torch.bfloat16))
+    _cuda(kv_cache, "kv_cache", (torch.uint8,))
+    _cuda(prefix_blocks, "prefix_blocks", (torch.int32,))
+    _cuda(block_tables, "block_tables", (torch.int32,))
+    _cuda(seq_lens, "seq_lens", (torch.int32,))
+    _cuda(query_start_loc, "query_start_loc", (torch.int32,))
+    _cuda(rht_signs, "rht_signs", (torch.float32,))
+    Nq, Hq, d = query.shape
+    NB, two, bs, H, rb = kv_cache.shape
+    S = seq_lens.shape[0]
+    if two != 2 or rb != kv_int4_row_bytes(d) or rht_signs.shape != (d,):
+        raise ValueError("kv_cache / rht_signs do not match the query's head size")
+    if query_start_loc.shape != (S + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and query_start_loc [num_seqs + 1]")
+    if prefix_blocks.dim() != 1 or prefix_blocks.shape[0] < prefix_len // bs:
+        raise ValueError("prefix_blocks must hold the prefix's prefix_len // block_size block ids")
+    if out is None:
+        out = torch.empty((Nq, Hq, d), dtype=out_dtype or query.dtype, device=query.device)
+    _cuda(out, "out", tuple(_DTYPES))
+    if out.shape != query.shape:
+        raise ValueError("out must have the query's shape")
+    need = kv_int4_shared_prefix_workspace_bytes(Nq, Hq, H, d, S, prefix_len, max_seq_len, segment_len)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+    ws_ptr = workspace.data_ptr() if workspace is not None else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    with torch.cuda.device(_one_device(query, kv_cache, prefix_blocks, block_tables, seq_lens, query_start_loc,
+                                       rht_signs, out, workspace)):
+        st = load().kv_int4_shared_prefix_attention(query.data_ptr(), _DTYPES[query.dtype], Nq, Hq, kv_cache.data_ptr(),
+                                                  NB, H, d, bs, prefix_blocks.data_ptr(), prefix_len,
+                                                  block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
+                                                  query_start_loc.data_ptr(), S, 1, max_seq_len, float(softmax_scale),
+                                                  rht_signs.data_ptr(), segment_len, out.data_ptr(), _DTYPES[out.dtype],
+                                                  ws_ptr, ws_bytes, _stream(stream))
+    _check("kv_int4_shared_prefix_attention", st)
     return out
 
 

@@ -349,6 +349,13 @@ int32_t kv_int4_attention_segment_len(int32_t num_seqs, int32_t max_seq_len, int
 
 namespace {
 
+// Workspace of the shared-prefix partials, behind the decode path's (both 256-byte aligned).
+struct PrefixLayout {
+    int32_t len;       // shared tokens that the prefix kernel takes: whole blocks; 0: the decode path takes all
+    int splits;
+    size_t o, ml, total;   // offsets and bytes behind the decode workspace
+};
+
 // Workspace of the decode path, in 256-byte-aligned regions:
 //   meta  [num_seqs + 1] int32             first unit of each sequence
 //   ptile [num_seqs + 1] int32             first prefill query tile of each sequence
@@ -380,6 +387,24 @@ bool ws_layout(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size, int
     return true;
 }
 
+// The shared-prefix rule.  Sharing pays from two sequences on (one sequence's prefix is read once
+// either way) and from a prefix of kMinShared tokens on, below which the extra launch costs more than
+// the repeated reads.
+PrefixLayout prefix_layout(int64_t num_q_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                           int32_t num_seqs, int32_t prefix_len) {
+    constexpr int32_t kMinShared = 128;
+    PrefixLayout x = {};
+    const int32_t len = prefix_len / kBlockSize * kBlockSize;
+    if (num_seqs < 2 || len < kMinShared) return x;
+    const int64_t bq = kPrefillRows / (num_q_heads / num_kv_heads);
+    x.len = len;
+    x.splits = prefix_splits((num_q_tokens + bq - 1) / bq, num_kv_heads, len);
+    const size_t rows = (size_t)x.splits * (size_t)num_q_tokens * (size_t)num_q_heads;
+    x.ml = align256(rows * (size_t)head_size * 4);
+    x.total = x.ml + rows * 8;
+    return x;
+}
+
 kv_int4_status paged_attention_impl(int bits, const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens,
                                        int32_t num_q_heads, const uint8_t* cache, int64_t num_blocks,
                                        int32_t num_kv_heads, int32_t head_size, int32_t block_size,
@@ -388,7 +413,8 @@ kv_int4_status paged_attention_impl(int bits, const void* q, kv_int4_dtype q_dty
                                        int32_t max_query_len, int32_t max_seq_len, float softmax_scale,
                                        const float* rht_signs, int32_t segment_len, void* out,
                                        kv_int4_dtype out_dtype, void* workspace, size_t workspace_bytes,
-                                       kv_int4_stream_t stream, const kv_int4_attn_options* options) {
+                                       kv_int4_stream_t stream, const kv_int4_attn_options* options,
+                                       const int32_t* prefix_blocks = nullptr, int32_t prefix_len = 0) {
     if (num_q_tokens < 0 || num_seqs < 0 || num_blocks < 0 || max_query_len < 0 || max_seq_len < 0 ||
         max_blocks_per_seq < 0 || segment_len < 0)
         return KV_INT4_EINVAL;
@@ -411,14 +437,18 @@ kv_int4_status paged_attention_impl(int bits, const void* q, kv_int4_dtype q_dty
     if (max_query_len < 1 || max_blocks_per_seq < 1) return KV_INT4_EINVAL;
     if (!aligned16(q) || !aligned16(out) || !aligned16(cache)) return KV_INT4_EALIGN;
 
-    const int32_t seg = kv_int4_attention_segment_len(num_seqs, max_seq_len, segment_len);
+    PrefixLayout px = {};
+    if (prefix_len > 0) px = prefix_layout(num_q_tokens, num_q_heads, num_kv_heads, head_size, num_seqs, prefix_len);
+    const int32_t walk_len = std::max(0, max_seq_len - px.len);   // tokens of a sequence that the decode path walks
+    const int32_t seg = kv_int4_attention_segment_len(num_seqs, walk_len, segment_len);
     if (seg <= 0) return KV_INT4_EINVAL;
     const int64_t len_cap = std::min<int64_t>(max_seq_len, (int64_t)max_blocks_per_seq * kBlockSize);
     const int64_t max_blocks_total = (int64_t)num_seqs * ((len_cap + kBlockSize - 1) / kBlockSize);
     if (max_blocks_total >= ((int64_t)1 << 31)) return KV_INT4_EUNSUPPORTED;   // 32-bit block positions
     WsLayout w;
-    if (!ws_layout(num_q_heads, num_kv_heads, head_size, num_seqs, max_seq_len, seg, &w)) return KV_INT4_EINVAL;
-    if (workspace == nullptr || workspace_bytes < w.total) return KV_INT4_EWORKSPACE;
+    if (!ws_layout(num_q_heads, num_kv_heads, head_size, num_seqs, walk_len, seg, &w)) return KV_INT4_EINVAL;
+    const size_t px_at = align256(w.total);
+    if (workspace == nullptr || workspace_bytes < (px.len ? px_at + px.total : w.total)) return KV_INT4_EWORKSPACE;
     if (!aligned16(workspace)) return KV_INT4_EALIGN;
 
     AttnParams p;
@@ -439,6 +469,7 @@ kv_int4_status paged_attention_impl(int bits, const void* q, kv_int4_dtype q_dty
     {   // warps per (sequence, kv head) in the combine: about one per four records, 1..16
         int cw = 1;
         while (cw < 16 && (int64_t)cw * 4 < w.records) cw <<= 1;
+        if (px.len) cw = std::max(cw, G);   // a warp per head for the prefix's partials
         p.combine_warps = cw;
     }
     p.seg_rcp = div_rcp((uint32_t)seg);
@@ -474,6 +505,11 @@ kv_int4_status paged_attention_impl(int bits, const void* q, kv_int4_dtype q_dty
     p.alibi = nullptr;
     p.qq_bias = nullptr;
     p.qq_stride = 0;
+    p.px_blocks = prefix_blocks;
+    p.px_o = reinterpret_cast<float*>(ws + px_at + px.o);
+    p.px_ml = reinterpret_cast<float*>(ws + px_at + px.ml);
+    p.px_len = px.len;
+    p.px_splits = px.splits;
     if (options) {
         if (options->window_left >= 0) {
             p.opts |= kOptWindow;
@@ -495,7 +531,7 @@ kv_int4_status paged_attention_impl(int bits, const void* q, kv_int4_dtype q_dty
         }
     }
 
-    const int64_t max_units = (int64_t)num_seqs * (((int64_t)max_seq_len + seg - 1) / seg);
+    const int64_t max_units = (int64_t)num_seqs * (((int64_t)walk_len + seg - 1) / seg);
     // balance weight bound: the blocks, plus at most one padded unit per sequence
     const int ctas = decode_grid_size(max_blocks_total + (int64_t)num_seqs * (seg / kBlockSize), max_units);
     const DType qd = q_dtype == KV_INT4_BF16 ? DType::BF16 : DType::F16;
@@ -547,6 +583,41 @@ kv_int4_status kv_int4_paged_attention_ex(const void* q, kv_int4_dtype q_dtype, 
                                 block_size, block_tables, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs,
                                 max_query_len, max_seq_len, softmax_scale, rht_signs, segment_len, out, out_dtype,
                                 workspace, workspace_bytes, stream, options);
+}
+
+size_t kv_int4_shared_prefix_workspace_bytes(int64_t num_q_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                             int32_t head_size, int32_t num_seqs, int32_t prefix_len,
+                                             int32_t max_seq_len, int32_t segment_len) {
+    if (num_seqs <= 0 || max_seq_len < 0 || num_q_tokens <= 0 || prefix_len < 0 || num_kv_heads <= 0 || num_q_heads <= 0 ||
+        num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > kPrefillRows)
+        return 0;
+    const PrefixLayout px = prefix_layout(num_q_tokens, num_q_heads, num_kv_heads, head_size, num_seqs, prefix_len);
+    const int32_t walk_len = std::max(0, max_seq_len - px.len);
+    const int32_t seg = kv_int4_attention_segment_len(num_seqs, walk_len, segment_len);
+    WsLayout w;
+    if (!ws_layout(num_q_heads, num_kv_heads, head_size, num_seqs, walk_len, seg, &w)) return 0;
+    return px.len ? align256(w.total) + px.total : w.total;
+}
+
+kv_int4_status kv_int4_shared_prefix_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens,
+                                               int32_t num_q_heads, const uint8_t* cache, int64_t num_blocks,
+                                               int32_t num_kv_heads, int32_t head_size, int32_t block_size,
+                                               const int32_t* prefix_blocks, int32_t prefix_len,
+                                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                               const int32_t* seq_lens, const int32_t* query_start_loc,
+                                               int32_t num_seqs, int32_t max_query_len, int32_t max_seq_len,
+                                               float softmax_scale, const float* rht_signs, int32_t segment_len,
+                                               void* out, kv_int4_dtype out_dtype, void* workspace,
+                                               size_t workspace_bytes, kv_int4_stream_t stream) {
+    if (prefix_len < 0 || max_query_len < 0) return KV_INT4_EINVAL;
+    if (max_query_len > 1) return KV_INT4_EUNSUPPORTED;   // decode batches
+    if (num_q_tokens > 0 && num_seqs > 0 && prefix_len >= kBlockSize && !prefix_blocks) return KV_INT4_EINVAL;
+    // the prefix's blocks are the first of every sequence's table
+    if (prefix_len / kBlockSize > max_blocks_per_seq) return KV_INT4_EINVAL;
+    return paged_attention_impl(4, q, q_dtype, num_q_tokens, num_q_heads, cache, num_blocks, num_kv_heads, head_size,
+                                block_size, block_tables, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs,
+                                max_query_len, max_seq_len, softmax_scale, rht_signs, segment_len, out, out_dtype,
+                                workspace, workspace_bytes, stream, nullptr, prefix_blocks, prefix_len);
 }
 
 kv_int4_status kv_int8_paged_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens,

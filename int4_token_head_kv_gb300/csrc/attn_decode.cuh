@@ -53,6 +53,8 @@
 // attn_decode_int8.cu, attn_decode_int2.cu) so that the three compile in parallel.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_common.cuh"
 
 namespace kvi4 {
@@ -321,8 +323,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
     // griddep_wait() below reads only the host-provided metadata (query_start_loc, seq_lens, block
     // tables, signs) and writes only shared memory.  The combine may be scheduled right away: it
     // waits for this grid before reading anything, and its CTAs become resident as walker CTAs
-    // retire.
-    griddep_launch_dependents();
+    // retire.  The shared-prefix kernel reads the queries and the cache without waiting for this grid, so
+    // in front of it the trigger comes after the wait below.
+    if (p.px_splits == 0) griddep_launch_dependents();
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
             if (count) count_status(p.status, 2);
             L = p.len_cap;
         }
-        return make_int2(max(L, 0), q0);
+        return make_int2(max(L - p.px_len, 0), q0);   // tokens behind the shared prefix (px_len 0: all)
     };
     // Stage (L, q0) of every sequence in shared memory (the ring is idle until the first copy).
     // Thread t's i-th sequence t * per + i sits at entry i * 256 + t, so the passes below read
@@ -487,7 +490,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
             else hi = mid - 1;
         }
         const int4 u = units[lo];
-        return __ldg(p.block_tables + (int64_t)u.x * p.max_blocks_per_seq + u.y + (i - (ustart[lo] - Bs)));
+        return __ldg(p.block_tables + (int64_t)u.x * p.max_blocks_per_seq + p.px_len / kBlockSize + u.y + (i - (ustart[lo] - Bs)));
     };
     for (int i = threadIdx.x; i < min(nb_cta, kTableWin); i += kDecodeThreads) tbl[i] = block_id(i);
     __syncthreads();
@@ -528,6 +531,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
         if (blk >= 0 && (int64_t)blk < p.num_blocks) bulk_prefetch_l2(p.cache + (int64_t)blk * stage_bytes, stage_bytes);
     }
     griddep_wait();   // the query records, and through them the cache, come from earlier kernels
+    if (p.px_splits != 0) griddep_launch_dependents();
     if (blockIdx.x == 0 && p.max_query_len > 1 && p.pf_tiles_cap > 0) {
         // The prefill's tile index: sequence b's first query tile among the batch's prefill tiles
         // (tiles of 128 / G tokens over its first min(q_len, max_query_len) queries; none for q_len
@@ -765,7 +769,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
                         x[b][1] = x[b][3] = -INFINITY;
                     }
                     if constexpr (OPTS) {   // window / softcap / ALiBi
-                        const int jb = u.y * kBlockSize + tb;   // position of this block's first token
+                        const int jb = p.px_len + u.y * kBlockSize + tb;   // position of this block's first token
                         x[b][0] = apply_opts(x[b][0], jb + tk0, posd, sl0, p, posd);
                         x[b][2] = apply_opts(x[b][2], jb + tk1, posd, sl0, p, posd);
                         if constexpr (WIDE) {
@@ -999,7 +1003,9 @@ __host__ __device__ inline size_t combine_smem_bytes(int W, int G) {
 // the accumulator slots lane + 32 j of the fragment-ordered partials (whole 512-byte rows, so
 // every load is coalesced, several records in flight), and the chunk states are then folded in
 // chunk order through shared memory, normalised, and the G outputs un-rotated by the group's warps.
-template <int D, bool WIDE, int BITS, typename OT>
+// PREFIX: the item's heads then take in the shared prefix's partials (one per split, in split order),
+// each head by one warp.
+template <int D, bool WIDE, int BITS, typename OT, bool PREFIX>
 __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __grid_constant__ AttnParams p) {
     constexpr int NLS = WIDE ? 32 : 16;
     constexpr int NT = Geo<D>::MT * NLS;   // float4 slots of one record
@@ -1013,7 +1019,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
     extern __shared__ __align__(16) float4 cbuf[];
     float4* sacc = cbuf;                                   // [16 warps][NT]
     float4* sml = cbuf + kCombineWarps * NT;               // [16 warps][4]
-    float* sout = reinterpret_cast<float*>(sml + kCombineWarps * 4);   // [groups][G][SO]
+    float* sout = reinterpret_cast<float*>(sml + kCombineWarps * 4);   // [groups][G][SO]; PREFIX: row ends hold (max, sum)
     // Up to the wait on the walker this kernel reads only host inputs, so it overlaps the walker's
     // last CTAs on the SMs they have left.
     if constexpr (BITS != 8)
@@ -1023,7 +1029,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
     auto segments_of = [&](int b) -> int {
         const int qb = __ldg(p.qsl + b);
         if (__ldg(p.qsl + b + 1) - qb != 1 || qb < 0 || (int64_t)qb >= p.num_q_tokens) return 0;
-        const int L = min(max(__ldg(p.seq_lens + b), 0), p.len_cap);
+        const int L = max(min(__ldg(p.seq_lens + b), p.len_cap) - p.px_len, 0);
         return (int)fast_div((uint32_t)(L + p.seg_len - 1), (uint32_t)p.seg_len, p.seg_rcp);
     };
     const bool local_first = p.num_seqs <= kThreads;   // else the walker's index in ws_meta
@@ -1056,7 +1062,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
         active = __ldg(p.qsl + seq + 1) - q0 == 1 && q0 >= 0 && (int64_t)q0 < p.num_q_tokens;
     }
     if (active) {
-        const int L = min(max(__ldg(p.seq_lens + seq), 0), p.len_cap);
+        const int L = max(min(__ldg(p.seq_lens + seq), p.len_cap) - p.px_len, 0);
         nseg = (int)fast_div((uint32_t)(L + p.seg_len - 1), (uint32_t)p.seg_len, p.seg_rcp);
     }
     const int64_t obase = ((int64_t)q0 * Hq + (int64_t)h * G) * D;
@@ -1146,16 +1152,62 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
                 const float inv = L0 > 0.0f ? 1.0f / L0 : 0.0f;
                 gout[c0 * SO + dlo] = a.x * inv;
                 gout[c0 * SO + dhi] = a.z * inv;
+                if (PREFIX && dlo == 0) {
+                    gout[c0 * SO + D] = M0;
+                    gout[c0 * SO + D + 1] = L0;
+                }
             }
             if (c1 < G) {
                 const float inv = L1 > 0.0f ? 1.0f / L1 : 0.0f;
                 gout[c1 * SO + dlo] = a.y * inv;
                 gout[c1 * SO + dhi] = a.w * inv;
+                if (PREFIX && dlo == 0) {
+                    gout[c1 * SO + D] = M1;
+                    gout[c1 * SO + D + 1] = L1;
+                }
             }
         }
     }
     __syncthreads();
     if (!active) return;
+    if constexpr (PREFIX) {
+        const int64_t rows = p.num_q_tokens * Hq, row0 = (int64_t)q0 * Hq + (int64_t)h * G;
+        for (int col = sub; col < G; col += W) {
+            const float ms = R > 0 ? gout[col * SO + D] : kNegBig, ls = R > 0 ? gout[col * SO + D + 1] : 0.0f;
+            // the splits' (max, sum): lane s holds split s (and s + 32), then all of them by shuffles
+            const float2* ml = reinterpret_cast<const float2*>(p.px_ml) + row0 + col;
+            float2 v[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                v[i] = lane + 32 * i < p.px_splits ? ml[(int64_t)(lane + 32 * i) * rows] : make_float2(kNegBig, 0.0f);
+            const float M = fmaxf(ms, warp_max(fmaxf(v[0].x, v[1].x)));
+            const float e0 = fast_exp2(v[0].x - M), e1 = fast_exp2(v[1].x - M), es = fast_exp2(ms - M);
+            float L = 0.0f;
+            for (int s = 0; s < p.px_splits; ++s) {
+                const float l = __shfl_sync(0xffffffffu, s < 32 ? v[0].y : v[1].y, s & 31);
+                L += l * __shfl_sync(0xffffffffu, s < 32 ? e0 : e1, s & 31);
+            }
+            L += ls * es;
+            float x[D / 32];
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) x[k] = 0.0f;
+            // dimension d sits at this column of a partial (the prefix kernel's tile order)
+            const int c8 = lane & 7, pc = (lane & ~7) + (c8 < 4 ? 2 * c8 : 2 * c8 - 7);
+            const float* po_s = p.px_o + (row0 + col) * D + pc;
+#pragma unroll 8
+            for (int s = 0; s < p.px_splits; ++s) {
+                const float w = __shfl_sync(0xffffffffu, s < 32 ? e0 : e1, s & 31);
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) x[k] = fmaf(po_s[(int64_t)s * rows * D + 32 * k], w, x[k]);
+            }
+            if (R > 0) {
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) x[k] = fmaf(gout[col * SO + lane + 32 * k], ls * es, x[k]);
+            }
+            unrotate_store<D, OT>(x, L > 0.0f ? 1.0f / L : 0.0f, sgn, p.c, p.out, obase + (int64_t)col * D);
+        }
+        return;
+    }
     if (R == 0) {   // empty context: zero output
         for (int i = sub * 32 + lane; i < G * D; i += W * 32) store_elem<OT>(p.out, obase + i, 0.0f);
         return;
@@ -1209,11 +1261,20 @@ cudaError_t launch_decode_t(const AttnParams& p, int num_ctas, cudaStream_t stre
     err = cudaLaunchKernelEx(&wcfg, walker, p);
     if (err != cudaSuccess) return err;
 
+    if constexpr (BITS == 4) {
+        if (p.px_splits > 0) {
+            err = launch_prefix(p, D, std::is_same<QT, __nv_bfloat16>::value ? DType::BF16 : DType::F16, stream);
+            if (err != cudaSuccess) return err;
+        }
+    }
+
     const int W = p.combine_warps;
     const int64_t items = (int64_t)p.num_seqs * p.H;
     const int64_t per_cta = kCombineWarps / W;
     const size_t csmem = combine_smem_bytes<D, WIDE>(W, p.G);
-    err = opt_in_smem<combine_kernel<D, WIDE, BITS, OT>>(csmem);
+    const bool prefix = BITS == 4 && p.px_splits > 0;
+    err = prefix ? opt_in_smem<combine_kernel<D, WIDE, BITS, OT, BITS == 4>>(csmem)
+                 : opt_in_smem<combine_kernel<D, WIDE, BITS, OT, false>>(csmem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((items + per_cta - 1) / per_cta));
@@ -1222,7 +1283,7 @@ cudaError_t launch_decode_t(const AttnParams& p, int num_ctas, cudaStream_t stre
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, combine_kernel<D, WIDE, BITS, OT>, p);
+    return cudaLaunchKernelEx(&cfg, prefix ? combine_kernel<D, WIDE, BITS, OT, BITS == 4> : combine_kernel<D, WIDE, BITS, OT, false>, p);
 }
 
 template <int D, bool WIDE, int BITS, typename QT>

@@ -1,0 +1,650 @@
+// Attention of a decode batch over the cached prefix that its sequences share: every query row of the
+// batch against the same keys, so the prefix is read and dequantised once per 128 query rows instead of
+// once per sequence, and the products fill the tensor cores' tiles although each sequence has one query.
+//
+// The mathematics is the chunked prefill's (attn_prefill.cuh: rotated queries as fp16 high + low halves,
+// S = Q' (K - zp)^T, logit = S s'_K k0 2^-e, weights 2^(logit - m + 127 - E) s'_V, O += P_w (V - zp), all
+// accumulated in fp32), with two differences: a row is one (query token, q head) of any sequence and sees
+// the prefix keys below its own limit (its sequence's length, when that ends inside the prefix; a padding
+// row sees none), and a CTA writes its key range's partial (reference maximum m in log2 units, sum l,
+// unnormalised O, still rotated), which the combine merges with the suffix's.
+//
+// Grid: (row tiles of 128 / G tokens) x kv heads x splits of the prefix's 128-key tiles, one CTA per SM.
+// The splits fill the SMs when the batch alone does not (prefix_splits).
+//
+// Warp roles (640 threads): warps 0-7 own the rows (rotation, softmax, epilogue), warps 8-11 dequantise
+// the K rows and warps 12-15 the V rows of a tile (one row per thread), warp 16 issues the MMAs, warps
+// 17-18 stage packed rows four tiles ahead, warp 19 is idle (it completes the last warpgroup, which the
+// register split needs).  The prefill dequantises with four warps, K then V, and is bound by that chain
+// (3 200 of its 3 500 cycles per tile); two plane groups halve it, and the registers they need come from
+// a setmaxnreg split: 136 for the rows, 72 for the dequantisation, 64 for the rest, together what 640
+// threads are launched with at 96.
+#pragma once
+
+#include "attn_prefill.cuh"
+
+namespace kvi4 {
+namespace {
+
+constexpr int kPxDequantWarp = kPfSoftmaxWarps;          // K group, then the V group
+constexpr int kPxMmaWarp = kPxDequantWarp + 8;
+constexpr int kPxLoadWarp = kPxMmaWarp + 1;              // one per plane (K, V)
+constexpr int kPxThreads = (kPxMmaWarp + 4) * 32;
+constexpr int kPxLaunchRegs = 96, kPxRowRegs = 136, kPxDequantRegs = 72, kPxOtherRegs = 64;
+static_assert(kPxRowRegs * 256 + kPxDequantRegs * 256 + kPxOtherRegs * 128 == kPxLaunchRegs * kPxThreads, "register split");
+
+// Shared memory: the prefill's tiles and staging, then this kernel's own records and barriers.
+template <int D>
+struct PxLayout {
+    using Pf = PfLayout<D>;
+    static constexpr uint32_t kTile = Pf::kTile;
+    static constexpr uint32_t kRaw = Pf::kRaw;
+    static constexpr uint32_t kChunks = Pf::kChunks, kWindow = Pf::kWindow;
+    static constexpr uint32_t kPlane = kPfKeys * kWindow * 4;                    // one plane of a staged tile
+    static constexpr uint32_t kSk = kRaw + kPfRawStages * 2 * kPlane;            // [kring][128] f32 s'_K * k0 (0: no key)
+    static constexpr uint32_t kDeadF = kSk + kPfKRing * kPfKeys * 4;             // [kring][4] u32: a K warp saw a key with no row
+    static constexpr uint32_t kSv = kDeadF + kPfKRing * 4 * 4;                   // [pairs][128] f32 s'_V
+    static constexpr uint32_t kEblk = kSv + kPfPairs * kPfKeys * 4;              // [pairs][4] per-warp max V exponent
+    static constexpr uint32_t kSignBits = kEblk + kPfPairs * 4 * 4;              // [D / 32] u32
+    static constexpr uint32_t kBars = (kSignBits + D / 8 + 7u) & ~7u;
+    // k_full[kring], k_free[pairs], v_full[pairs], v_free[pairs], pv_done[2], s_full[2], p_full[2], q_ready,
+    // flush, q_tma, rot_in, rot_done, raw_full[plane][stages], raw_free[plane][stages]
+    static constexpr int kNumBars = kPfKRing + 3 * kPfPairs + 6 + 5 + 4 * kPfRawStages;
+    static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
+    static constexpr uint32_t kFlags = kTmemSlot + 4;
+    static constexpr uint32_t kBytes = kFlags + 4 + 1024;                        // + alignment slack
+};
+
+template <int REGS>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
+
+template <int D, typename QT>
+__global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap) {
+    using Gm = Geo<D>;
+    using Ly = PxLayout<D>;
+    using Tm = PfTmem<D>;
+    constexpr int KSTEPS = D / 16;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    griddep_launch_dependents();   // the combine waits for this grid before it reads anything
+
+    const int G = p.G, Hq = p.Hq, H = p.H;
+    const int BQ = kPfRows / G;
+    const int h = (int)(blockIdx.x % (unsigned)H), qt0 = (int)(blockIdx.x / (unsigned)H) * BQ;
+    const int split = blockIdx.y;
+    const int tiles_all = (p.px_len + kPfKeys - 1) / kPfKeys;
+    const int kt0 = (int)((int64_t)tiles_all * split / p.px_splits), kt1 = (int)((int64_t)tiles_all * (split + 1) / p.px_splits);
+    const int nkt = kt1 - kt0;   // at least one: the host takes no more splits than tiles
+
+    float* sk = reinterpret_cast<float*>(smem + Ly::kSk);
+    float* sv = reinterpret_cast<float*>(smem + Ly::kSv);
+    uint32_t* eblkw = reinterpret_cast<uint32_t*>(smem + Ly::kEblk);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::kBars);
+    uint64_t* k_full = bars;                    // [kring] K tile and scales of tile j (128 arrivals)
+    uint64_t* k_free = k_full + kPfKRing;       // [pairs] K tile j % 2 read by S of tile j (commit)
+    uint64_t* v_full = k_free + kPfPairs;       // [pairs] V tile and scales of tile j (128 arrivals)
+    uint64_t* v_free = v_full + kPfPairs;       // [pairs] V tile j % 2 read by P.V of tile j (commit)
+    uint64_t* pv_done = v_free + kPfPairs;      // [2] P.V of tile j done (commit): S buffer j % 2 and O free
+    uint64_t* s_full = pv_done + 2;             // [2] S of the tile in tensor memory (commit)
+    uint64_t* p_full = s_full + 2;              // [2] P of the tile in tensor memory (256 arrivals)
+    uint64_t* q_ready = p_full + 2;             // queries in tensor memory, staging free (256 arrivals)
+    uint64_t* flush = q_ready + 1;              // the MMA thread's last commit (teardown)
+    uint64_t* q_tma = flush + 1;                // the CTA's query rows in shared memory (bytes)
+    uint64_t* rot_in = q_tma + 1;               // the rotation matrix in shared memory (256 arrivals)
+    uint64_t* rot_done = rot_in + 1;            // the rotated queries in tensor memory (commit)
+    uint64_t* raw_full = rot_done + 1;          // [plane][stages] packed rows of a key tile landed (32 lanes)
+    uint64_t* raw_free = raw_full + 2 * kPfRawStages;   // [plane][stages] that plane converted (128 arrivals)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::kTmemSlot);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kFlags);
+    uint32_t* deadf = reinterpret_cast<uint32_t*>(smem + Ly::kDeadF);
+
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < kPfKRing; ++b) mbar_init(&k_full[b], 128);
+        for (int b = 0; b < kPfPairs; ++b) {
+            mbar_init(&k_free[b], 1);
+            mbar_init(&v_full[b], 128);
+            mbar_init(&v_free[b], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&pv_done[b], 1);
+            mbar_init(&s_full[b], 1);
+            mbar_init(&p_full[b], kPfSoftmaxThreads);
+        }
+        mbar_init(q_ready, kPfSoftmaxThreads);
+        mbar_init(flush, 1);
+        mbar_init(q_tma, 1);
+        mbar_init(rot_in, kPfSoftmaxThreads);
+        mbar_init(rot_done, 1);
+        for (int i = 0; i < 2 * kPfRawStages; ++i) {
+            mbar_init(&raw_full[i], 32);
+            mbar_init(&raw_free[i], 128);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    uint32_t* signbits = reinterpret_cast<uint32_t*>(smem + Ly::kSignBits);
+    if (threadIdx.x < D) {   // whole warps (D is a multiple of 32)
+        const uint32_t m = __ballot_sync(0xffffffffu, p.signs[threadIdx.x] < 0.0f);
+        if (lane == 0) signbits[warp] = m;
+    }
+    if (warp == kPxMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "n"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    uint8_t* tiles = smem;   // [K0][V0][K1][V1]
+    auto ktile = [&](int b) { return tiles + (uint32_t)b * 2u * Ly::kTile; };
+    auto vtile = [&](int b) { return tiles + (uint32_t)b * 2u * Ly::kTile + Ly::kTile; };
+    // a wait that runs out counts once and winds the CTA down
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (*abort_flag) return false;
+        if (mbar_wait(bar, parity)) return true;
+        if (atomicExch(const_cast<int*>(abort_flag), 1) == 0) count_status(p.status, 3);
+        return false;
+    };
+
+    if (warp < kPfSoftmaxWarps) {
+        more_registers<kPxRowRegs>();
+        // ================================================================ rows: softmax + partials
+        // Rows and tensor-memory layout as in the prefill: warp w owns the 16 rows 32 (w % 4) +
+        // 16 (w / 4) ..; thread (g, t) holds rows ra = rbase + g and rb = ra + 8 and, of every group of
+        // 8 columns, columns 2t and 2t + 1.
+        const int rbase = 32 * (warp & 3) + 16 * (warp >> 2);
+        const int t4 = lane & 3;
+        const int ra = rbase + (lane >> 2), rb = ra + 8;
+        const uint32_t trow = tmem + ((uint32_t)rbase << 16);
+        // ---- the rotation matrix B[p][k] = sign_k (-1)^popcount(n(p) & k) in pair 1's V tile
+        {
+            constexpr int kRowChunks = D / 8, kThreadsPerRow = kPfSoftmaxThreads / D, kChunksPerThread = kRowChunks / kThreadsPerRow;
+            uint8_t* qb = vtile(1);
+            const uint32_t one = std::is_same<QT, __nv_bfloat16>::value ? 0x3F80u : 0x3C00u;
+            const int prow = threadIdx.x / kThreadsPerRow;
+            const int n = dim_of_column(slot_of_column(prow));
+            uint32_t par8 = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) par8 |= ((uint32_t)__popc(n & j) & 1u) << j;
+#pragma unroll
+            for (int it = 0; it < kChunksPerThread; ++it) {
+                const int k8 = (threadIdx.x % kThreadsPerRow) * kChunksPerThread + it;
+                const uint32_t sb = (signbits[k8 / 4] >> (8 * (k8 % 4))) & 0xFFu;
+                const uint32_t neg = par8 ^ sb ^ ((__popc(n & (8 * k8)) & 1) ? 0xFFu : 0u);
+                uint32_t w[4];
+                pm1_words(neg, one, w);
+                *reinterpret_cast<uint4*>(qb + (uint32_t)(k8 / 8) * (uint32_t)(D * 128) + swz128((uint32_t)prow, (uint32_t)(k8 % 8))) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // generic writes -> tensor core reads
+            mbar_arrive(rot_in);
+        }
+        // ---- each row's limit: keys [0, vis) of the prefix, from its token's sequence
+        auto visible = [&](int tok) -> int {
+            if ((int64_t)tok >= p.num_q_tokens) return 0;
+            // the sequence holding the token: sequence tok itself when every one before it has one query
+            int b = min(tok, p.num_seqs - 1);
+            if (__ldg(p.qsl + b) != tok) {
+                int lo = 0, hi = p.num_seqs;   // the last b with qsl[b] <= tok
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (__ldg(p.qsl + mid) <= tok) lo = mid;
+                    else hi = mid;
+                }
+                b = lo;
+            }
+            // sequences without a query may share the start: the last one with this start holds it
+            while (b + 1 < p.num_seqs && __ldg(p.qsl + b + 1) == tok) ++b;
+            if (__ldg(p.qsl + b) != tok || __ldg(p.qsl + b + 1) != tok + 1) return 0;
+            return max(0, min(min(__ldg(p.seq_lens + b), p.len_cap), p.px_len));
+        };
+        const int vis_a = visible(qt0 + ra / G), vis_b = visible(qt0 + rb / G);
+        // ---- power-of-two prescale, fp16 high + low halves into tensor memory
+        float rs_a = 1.0f, rs_b = 1.0f;   // 2^-e of each row
+        bool ok = wait(rot_done, 0);
+        if (__all_sync(0xffffffffu, ok)) {
+            tc_fence_after();
+            float v[D / 2];   // v[4i], v[4i + 1]: row a, columns 8i + 2t, + 1; v[4i + 2], v[4i + 3]: row b
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 64) tmem_ld_q8(trow + Tm::kS0 + c0, reinterpret_cast<uint32_t*>(v) + c0 / 2);
+            tmem_ld_wait();
+            float mxa = 0.0f, mxb = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                mxa = fmaxf(mxa, fmaxf(fabsf(v[4 * i]), fabsf(v[4 * i + 1])));
+                mxb = fmaxf(mxb, fmaxf(fabsf(v[4 * i + 2]), fabsf(v[4 * i + 3])));
+            }
+            mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
+            mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
+            mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
+            mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
+            const int ea = prescale_exponent(mxa), eb = prescale_exponent(mxb);   // rows of zeros: 2^0
+            const float sca = exp2i(ea), scb = exp2i(eb);
+            rs_a = exp2i(-ea);
+            rs_b = exp2i(-eb);
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+                uint32_t hw[4], lw[4];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int i = 2 * q + e;
+#pragma unroll
+                    for (int rr = 0; rr < 2; ++rr) {
+                        const float sc = rr ? scb : sca;
+                        split_f16x2(v[4 * i + 2 * rr] * sc, v[4 * i + 2 * rr + 1] * sc, hw[2 * rr + e], lw[2 * rr + e]);
+                    }
+                }
+                tmem_st_q1(trow + Tm::kQh + 8 * q, hw);
+                tmem_st_q1(trow + Tm::kQl + 8 * q, lw);
+            }
+            tmem_st_wait();
+        } else {
+            ok = false;
+        }
+        tc_fence_before();
+        mbar_arrive(q_ready);
+        // ---- the key tiles
+        float m_a = kNegBig, m_b = kNegBig;     // reference maxima (log2 units)
+        float l_a = 0.0f, l_b = 0.0f;           // this thread's part of the sums of 2^(127-E) p
+        uint32_t E = 0;                         // reference biased exponent of the V scales (0: none yet)
+        for (int j = 0; j < nkt && ok; ++j) {
+            const int b = j & 1;
+            const uint32_t ph = (uint32_t)(j >> 1) & 1u;
+            const int kb = j % kPfPairs, kr = j % kPfKRing;
+            ok = wait(&s_full[b], ph) && wait(&k_full[kr], (uint32_t)(j / kPfKRing) & 1u) &&
+                 wait(&v_full[kb], (uint32_t)(j / kPfPairs) & 1u);
+            if (__any_sync(0xffffffffu, !ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t scol = trow + (b ? Tm::kS1 : Tm::kS0);
+            uint32_t s[64];   // s[4i], s[4i + 1]: row a, columns 8i + 2t, + 1; s[4i + 2], s[4i + 3]: row b
+            tmem_ld_q8(scol, s);
+            tmem_ld_q8(scol + 64, s + 32);
+            tmem_ld_wait();
+            // x = S * s'_K * k0 (0 scale: no key), masked; the row maxima
+            const int key0 = (kt0 + j) * kPfKeys;
+            const float* skb = sk + kr * kPfKeys + 2 * t4;
+            const bool clean = (deadf[kr * 4] | deadf[kr * 4 + 1] | deadf[kr * 4 + 2] | deadf[kr * 4 + 3]) == 0u &&
+                               key0 + kPfKeys <= min(vis_a, vis_b);
+            float bma = -INFINITY, bmb = -INFINITY;
+            if (__all_sync(0xffffffffu, clean)) {   // every key live and visible to both rows
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 k2 = *reinterpret_cast<const float2*>(skb + 8 * i);
+                    const float2 xa = mul_f32x2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), k2);
+                    const float2 xb = mul_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k2);
+                    s[4 * i] = __float_as_uint(xa.x);
+                    s[4 * i + 1] = __float_as_uint(xa.y);
+                    s[4 * i + 2] = __float_as_uint(xb.x);
+                    s[4 * i + 3] = __float_as_uint(xb.y);
+                    bma = max3(bma, xa.x, xa.y);
+                    bmb = max3(bmb, xb.x, xb.y);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 k2 = *reinterpret_cast<const float2*>(skb + 8 * i);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float kk = e ? k2.y : k2.x;
+                        const int key = key0 + 8 * i + 2 * t4 + e;
+                        const float xa = kk > 0.0f && key < vis_a ? __uint_as_float(s[4 * i + e]) * kk : -INFINITY;
+                        const float xb = kk > 0.0f && key < vis_b ? __uint_as_float(s[4 * i + 2 + e]) * kk : -INFINITY;
+                        s[4 * i + e] = __float_as_uint(xa);
+                        s[4 * i + 2 + e] = __float_as_uint(xb);
+                        bma = fmaxf(bma, xa);
+                        bmb = fmaxf(bmb, xb);
+                    }
+                }
+            }
+            bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 1));
+            bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 1));
+            bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 2));
+            bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 2));
+            // in log2 units (rs > 0: a power of two scales exactly); the four threads of a row take
+            // the same decisions
+            bma *= rs_a;
+            bmb *= rs_b;
+            const bool up_a = bma > m_a + kPfLazyMax, up_b = bmb > m_b + kPfLazyMax;
+            const float fm_a = up_a ? fast_exp2(m_a - bma) : 1.0f, fm_b = up_b ? fast_exp2(m_b - bmb) : 1.0f;
+            if (up_a) m_a = bma;
+            if (up_b) m_b = bmb;
+            const uint32_t* eb4 = eblkw + kb * 4;
+            const uint32_t eb = max(max(eb4[0], eb4[1]), max(eb4[2], eb4[3]));
+            const uint32_t Eeff = E ? E : 127u;
+            float fe = 1.0f;
+            if (E == 0u ? eb > 0u : eb > E + kPfLazyExp) {
+                // rebase from 2^(127 - Eeff) to 2^(127 - eb); 0 when the jump underflows
+                fe = eb > Eeff + 126u ? 0.0f : __uint_as_float((127u + Eeff - eb) << 23);
+                E = eb;
+            }
+            const float f_a = fm_a * fe, f_b = fm_b * fe;
+            l_a *= f_a;
+            l_b *= f_b;
+            if (j > 0 && __any_sync(0xffffffffu, f_a != 1.0f || f_b != 1.0f)) {
+                // O must hold P.V of the previous tile before it is rescaled
+                ok = wait(&pv_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u);
+                if (__any_sync(0xffffffffu, !ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float2 fa2 = make_float2(f_a, f_a), fb2 = make_float2(f_b, f_b);
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 8) {
+                    uint32_t o[4];
+                    tmem_ld_q1(trow + Tm::kO + c0, o);
+                    tmem_ld_wait();
+                    const float2 oa = mul_f32x2(make_float2(__uint_as_float(o[0]), __uint_as_float(o[1])), fa2);
+                    const float2 ob = mul_f32x2(make_float2(__uint_as_float(o[2]), __uint_as_float(o[3])), fb2);
+                    o[0] = __float_as_uint(oa.x);
+                    o[1] = __float_as_uint(oa.y);
+                    o[2] = __float_as_uint(ob.x);
+                    o[3] = __float_as_uint(ob.y);
+                    tmem_st_q1(trow + Tm::kO + c0, o);
+                }
+                tmem_st_wait();
+            }
+            // p' = 2^(x rs - m + 127 - E), w = p' s'_V as fp16 pairs over the first 64 S columns
+            const float eoff = (float)(127 - (int)(E ? E : 127u));
+            const float2 rsa2 = make_float2(rs_a, rs_a), rsb2 = make_float2(rs_b, rs_b);
+            const float2 moa2 = make_float2(eoff - m_a, eoff - m_a), mob2 = make_float2(eoff - m_b, eoff - m_b);
+            const float* svb = sv + kb * kPfKeys + 2 * t4;
+            float2 lsa = make_float2(0.0f, 0.0f), lsb = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                uint32_t pw[4];
+#pragma unroll
+                for (int i = 2 * q; i < 2 * q + 2; ++i) {
+                    const float2 v2 = *reinterpret_cast<const float2*>(svb + 8 * i);
+                    const float2 ea = fma_f32x2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), rsa2, moa2);
+                    const float2 eb2 = fma_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), rsb2, mob2);
+                    const float2 pa = make_float2(fast_exp2(ea.x), fast_exp2(ea.y));
+                    const float2 pb = make_float2(fast_exp2(eb2.x), fast_exp2(eb2.y));
+                    lsa = add_f32x2(lsa, pa);
+                    lsb = add_f32x2(lsb, pb);
+                    const float2 wa = mul_f32x2(pa, v2), wb = mul_f32x2(pb, v2);
+                    const int e = i & 1;
+                    pw[e] = pack_f16x2(wa.x, wa.y);
+                    pw[2 + e] = pack_f16x2(wb.x, wb.y);
+                }
+                tmem_st_q1(scol + 8 * q, pw);
+            }
+            l_a += lsa.x + lsa.y;
+            l_b += lsb.x + lsb.y;
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&p_full[b]);
+        }
+        // ---- the partial: (m, l 2^(E - 127), O 2^(E - 127)), O's columns in the tile's dimension order
+        if (ok && nkt > 0) ok = wait(&pv_done[(nkt - 1) & 1], (uint32_t)((nkt - 1) >> 1) & 1u);
+        tc_fence_after();
+        l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
+        l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
+        l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
+        l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
+        const bool good = __all_sync(0xffffffffu, ok) && nkt > 0;
+        const float es = good && E ? __uint_as_float(E << 23) : 0.0f;   // 2^(E - 127)
+        const int64_t rows = p.num_q_tokens * Hq;
+        const int tok_a = qt0 + ra / G, tok_b = qt0 + rb / G;
+        const bool in_a = (int64_t)tok_a < p.num_q_tokens, in_b = (int64_t)tok_b < p.num_q_tokens;
+        const int64_t rec_a = (int64_t)split * rows + (int64_t)tok_a * Hq + h * G + ra % G;
+        const int64_t rec_b = (int64_t)split * rows + (int64_t)tok_b * Hq + h * G + rb % G;
+        if (t4 == 0) {
+            if (in_a) reinterpret_cast<float2*>(p.px_ml)[rec_a] = make_float2(good ? m_a : kNegBig, l_a * es);
+            if (in_b) reinterpret_cast<float2*>(p.px_ml)[rec_b] = make_float2(good ? m_b : kNegBig, l_b * es);
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t o[16];
+            if (good) {
+                tmem_ld_q4(trow + Tm::kO + c0, o);
+                tmem_ld_wait();
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + 8 * i + 2 * t4;
+                const float2 oa = good ? make_float2(__uint_as_float(o[4 * i]) * es, __uint_as_float(o[4 * i + 1]) * es) : make_float2(0.0f, 0.0f);
+                const float2 ob = good ? make_float2(__uint_as_float(o[4 * i + 2]) * es, __uint_as_float(o[4 * i + 3]) * es) : make_float2(0.0f, 0.0f);
+                if (in_a) *reinterpret_cast<float2*>(p.px_o + rec_a * D + c) = oa;
+                if (in_b) *reinterpret_cast<float2*>(p.px_o + rec_b * D + c) = ob;
+            }
+        }
+    } else if (warp < kPxMmaWarp) {
+        fewer_registers<kPxDequantRegs>();
+        // ================================================================ dequantisation of key tiles
+        const int pl = (warp - kPxDequantWarp) >> 2;      // 0: K rows, 1: V rows
+        const int k = (threadIdx.x - kPfSoftmaxThreads) & 127;   // this thread's key of every tile
+        constexpr int NW = D / 8 + 1;                     // words of a row: codes, then the scale word
+        const float k0 = p.c * p.softmax_scale * kLog2e;  // raw score -> log2 logit, before 2^-e
+        // word offset of this key's rows in their windows (the prefill's rule)
+        const int row_off = ((k % kBlockSize) * H + h) & 3;
+        // a V tile keeps its rows in the order the weights are laid out in
+        const uint32_t trow = pl ? (uint32_t)slot_of_column(k) : (uint32_t)k;
+        for (int j = 0; j < nkt; ++j) {
+            const int kb = j % kPfPairs, st = j % kPfRawStages;
+            bool ok = wait(&raw_full[pl * kPfRawStages + st], (uint32_t)(j / kPfRawStages) & 1u);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const uint4* win4 = reinterpret_cast<const uint4*>(smem + Ly::kRaw + (uint32_t)(st * 2 + pl) * Ly::kPlane) + k * Ly::kChunks;
+            uint32_t kw[NW];
+            {
+                uint32_t wv[Ly::kWindow];
+#pragma unroll
+                for (int c = 0; c < (int)Ly::kChunks; ++c) {
+                    const uint4 v = win4[c];
+                    wv[4 * c] = v.x;
+                    wv[4 * c + 1] = v.y;
+                    wv[4 * c + 2] = v.z;
+                    wv[4 * c + 3] = v.w;
+                }
+#pragma unroll
+                for (int w = 0; w < NW + 1; ++w) wv[w] = (row_off & 2) ? wv[w + 2] : wv[w];
+#pragma unroll
+                for (int w = 0; w < NW; ++w) kw[w] = (row_off & 1) ? wv[w + 1] : wv[w];
+            }
+            mbar_arrive(&raw_free[pl * kPfRawStages + st]);
+            ok = j != 1 || wait(q_ready, 0);        // the query rows and the rotation matrix sat on pair 1
+            if (ok && j >= kPfPairs) ok = wait(pl ? &v_free[kb] : &k_free[kb], (uint32_t)(j / kPfPairs - 1) & 1u);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            uint8_t* t = pl ? vtile(kb) : ktile(kb);
+            const uint32_t zp = kw[Gm::KW] & 15u;
+            const uint32_t zl = zp_lo_half(zp) * 0x10001u, zh = zp_hi_half(zp) * 0x10001u;
+#pragma unroll
+            for (int w = 0; w < Gm::KW; ++w) {
+                // code - zp of dimensions 8w + (0, 4), (1, 5), (2, 6), (3, 7): the tile order
+                uint32_t o[4];
+                unpack_word(kw[w], zl, zh, o);
+                *reinterpret_cast<uint4*>(t + (uint32_t)(w / 8) * (kPfKeys * 128u) + swz128(trow, (uint32_t)(w % 8))) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            if (pl == 0) {
+                sk[(j % kPfKRing) * kPfKeys + k] = __uint_as_float(kw[Gm::KW] & 0xFFFFFFF0u) * k0;
+                const uint32_t nodead = __ballot_sync(0xffffffffu, kw[Gm::KW] == 0u);
+                if (lane == 0) deadf[(j % kPfKRing) * 4 + (warp & 3)] = nodead;
+            } else {
+                sv[kb * kPfKeys + k] = __uint_as_float(kw[Gm::KW] & 0xFFFFFFF0u);
+                const uint32_t wmax = __reduce_max_sync(0xffffffffu, kw[Gm::KW]);   // positive floats order like their bits
+                if (lane == 0) eblkw[kb * 4 + (warp & 3)] = (wmax >> 23) & 0xFFu;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // generic writes -> tensor core reads
+            mbar_arrive(pl ? &v_full[kb] : &k_full[j % kPfKRing]);
+        }
+    } else {
+        fewer_registers<kPxOtherRegs>();
+        if (warp == kPxLoadWarp || warp == kPxLoadWarp + 1) {
+            // ============================================================ loads of packed rows
+            // As the prefill's loaders: 16-byte copies of each row's aligned window, keys past the prefix
+            // or in a block outside the cache zero-filled (scale word 0: no key).
+            constexpr int C = Ly::kChunks;
+            constexpr int kCopies = kPfKeys * C / 32;
+            static_assert(kPfKeys * C % 32 == 0, "whole copies per lane");
+            const int pl = warp - kPxLoadWarp;
+            const int32_t* table = p.px_blocks;
+            const int64_t tok_stride = (int64_t)H * Gm::RB, blk_stride = 2 * kBlockSize * tok_stride;
+            const uint8_t* base = p.cache + (int64_t)pl * kBlockSize * tok_stride;
+            uint32_t cp[kCopies];
+#pragma unroll
+            for (int t = 0; t < kCopies; ++t) {
+                const int i = lane + 32 * t, key = i / C, c = i - key * C;
+                const uint32_t row = (uint32_t)h * (uint32_t)Gm::RB + (uint32_t)(key % kBlockSize) * (uint32_t)tok_stride;
+                cp[t] = ((uint32_t)key << 24) | ((row & ~15u) + 16u * (uint32_t)c);
+            }
+            const int nblocks = p.px_len / kBlockSize;
+            auto lookup = [&](int j) -> int {   // lane b < 8: the block of keys 16 b .. of tile kt0 + j (-1: none)
+                const int i = (kt0 + j) * (kPfKeys / kBlockSize) + lane;
+                return lane < kPfKeys / kBlockSize && i < nblocks ? __ldg(table + i) : -1;
+            };
+            int blk_next = nkt > 0 ? lookup(0) : -1;
+            bool ok = true;
+            for (int j = 0; j < nkt && ok; ++j) {
+                const int st = j % kPfRawStages;
+                if (j >= kPfRawStages) ok = wait(&raw_free[pl * kPfRawStages + st], (uint32_t)(j / kPfRawStages - 1) & 1u);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                int blkv = blk_next;
+                if (j + 1 < nkt) blk_next = lookup(j + 1);
+                if (blkv != -1 && (blkv < 0 || (int64_t)blkv >= p.num_blocks)) {
+                    if (pl == 0 && h == 0 && qt0 == 0) count_status(p.status, 1);
+                    blkv = -1;
+                }
+                const uint32_t dst = smem_u32(smem + Ly::kRaw + (uint32_t)(st * 2 + pl) * Ly::kPlane);
+#pragma unroll
+                for (int t = 0; t < kCopies; ++t) {
+                    const int key = (int)(cp[t] >> 24);
+                    const int blk = __shfl_sync(0xffffffffu, blkv, key / kBlockSize);
+                    const bool live = blk >= 0;
+                    const uint8_t* src = base + (int64_t)(live ? blk : 0) * blk_stride + (cp[t] & 0xFFFFFFu);
+                    cp_async16_zfill(dst + 16u * (uint32_t)(lane + 32 * t), src, live);
+                }
+                cp_async_arrive_noinc(&raw_full[pl * kPfRawStages + st]);
+            }
+            cp_async_wait_all();   // no copy outlives the CTA
+        } else if (warp == kPxMmaWarp && lane == 0) {
+            // ============================================================ the MMA issuer (as the prefill's)
+            constexpr uint32_t idS = idesc_f16(kPfKeys, 0), idPV = idesc_f16(D, 1);
+            {
+                mbar_arrive_expect_tx(q_tma, Ly::kTile);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d(ktile(1) + c * (kPfRows * 128), &qmap, 64 * c, h * G, qt0, q_tma);
+                if (wait(q_tma, 0) && wait(rot_in, 0)) {
+                    tc_fence_after();
+                    constexpr uint32_t idR = std::is_same<QT, __nv_bfloat16>::value ? idesc_bf16(D, 0) : idesc_f16(D, 0);
+                    const uint32_t qa = smem_u32(ktile(1)), qb = smem_u32(vtile(1));
+#pragma unroll
+                    for (int kk = 0; kk < KSTEPS; ++kk) {
+                        const uint64_t ad = smem_desc_sw128(qa + (uint32_t)(kk / 4) * (kPfRows * 128u) + (uint32_t)(kk % 4) * 32u, 16u, 1024u);
+                        const uint64_t bd = smem_desc_sw128(qb + (uint32_t)(kk / 4) * (uint32_t)(D * 128) + (uint32_t)(kk % 4) * 32u, 16u, 1024u);
+                        mma_ss(tmem + Tm::kS0, ad, bd, idR, kk > 0);
+                    }
+                    mma_commit(rot_done);
+                }
+            }
+            auto issue_s = [&](int j) {
+                const uint32_t sd = tmem + ((j & 1) ? Tm::kS1 : Tm::kS0);
+                const uint32_t kbase = smem_u32(ktile(j % kPfPairs));
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int kk = 0; kk < KSTEPS; ++kk) {
+                        const uint64_t bd = smem_desc_sw128(
+                            kbase + (uint32_t)(kk / 4) * (kPfKeys * 128u) + (uint32_t)(kk % 4) * 32u, 16u, 1024u);
+                        mma_ts(sd, tmem + (half ? Tm::kQl : Tm::kQh) + 8u * kk, bd, idS, half > 0 || kk > 0);
+                    }
+                }
+                mma_commit(&s_full[j & 1]);
+                mma_commit(&k_free[j % kPfPairs]);
+            };
+            auto issue_pv = [&](int t) {
+                const uint32_t pcol = tmem + ((t & 1) ? Tm::kS1 : Tm::kS0);
+                const uint32_t vb = smem_u32(vtile(t % kPfPairs));
+#pragma unroll
+                for (int kk = 0; kk < kPfKeys / 16; ++kk) {
+                    const uint32_t a = pcol + 8u * kk;   // P of keys 16 kk .. 16 kk + 15 (in contraction order)
+                    const uint64_t bd = smem_desc_sw128(vb + (uint32_t)kk * 16u * 128u, kPfKeys * 128u, 1024u);
+                    mma_ts(tmem + Tm::kO, a, bd, idPV, t > 0 || kk > 0);
+                }
+                mma_commit(&pv_done[t & 1]);
+                mma_commit(&v_free[t % kPfPairs]);
+            };
+            bool ok = nkt == 0 || wait(q_ready, 0);
+            int js = 0, jp = 0;
+            uint64_t t0 = global_timer_ns();
+            while (ok && jp < nkt) {
+                bool did = false;
+                if (js < nkt && js < jp + 2 && mbar_test_wait(&k_full[js % kPfKRing], (uint32_t)(js / kPfKRing) & 1u) &&
+                    (js < 2 || mbar_test_wait(&pv_done[js & 1], (uint32_t)((js - 2) >> 1) & 1u))) {
+                    tc_fence_after();
+                    issue_s(js++);
+                    did = true;
+                }
+                if (jp < js && mbar_test_wait(&p_full[jp & 1], (uint32_t)(jp >> 1) & 1u)) {
+                    tc_fence_after();
+                    issue_pv(jp++);
+                    did = true;
+                }
+                if (did) {
+                    t0 = global_timer_ns();
+                } else {
+                    if (*abort_flag) {
+                        ok = false;
+                    } else if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+                        if (atomicExch(const_cast<int*>(abort_flag), 1) == 0) count_status(p.status, 3);
+                        ok = false;
+                    }
+                }
+            }
+            // every MMA issued has completed before the CTA tears tensor memory down
+            mma_commit(flush);
+            (void)mbar_wait(flush, 0);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kPxMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
+    // Complete only after the walker has: whoever waits for this kernel then also sees its partials.
+    griddep_wait();
+}
+
+template <int D, typename QT>
+cudaError_t launch_prefix_t(const AttnParams& p, cudaStream_t stream) {
+    const size_t smem = PxLayout<D>::kBytes;
+    cudaError_t err = opt_in_smem<prefix_kernel<D, QT>>(smem);
+    if (err != cudaSuccess) return err;
+    // the register split waits for registers the launch did not give out if this does not hold
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_acquire) == 0) {
+        cudaFuncAttributes fa;
+        err = cudaFuncGetAttributes(&fa, prefix_kernel<D, QT>);
+        if (err != cudaSuccess) return err;
+        regs.store(fa.numRegs, std::memory_order_release);
+    }
+    if (regs.load(std::memory_order_acquire) != kPxLaunchRegs) return cudaErrorInvalidKernelImage;
+    CUtensorMap qmap;
+    err = query_map<D, QT>(p, &qmap);
+    if (err != cudaSuccess) return err;
+    const int64_t bq = kPfRows / p.G, tiles = (p.num_q_tokens + bq - 1) / bq;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * p.H), (unsigned)p.px_splits);
+    cfg.blockDim = dim3(kPxThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefix_kernel<D, QT>, p, qmap);
+}
+
+}  // namespace
+}  // namespace kvi4

@@ -102,6 +102,13 @@ struct AttnParams {
     const float* alibi;       // [Hq] slopes (natural-log units)
     const float* qq_bias;     // [rows >= max_query_len][qq_stride] (natural-log units)
     int qq_stride;            // elements per row, >= max_query_len
+    // shared prefix (decode batches; px_splits 0: none): the decode path walks only the tokens from
+    // px_len on, the prefix kernel the px_len before them, and the combine merges both
+    const int32_t* px_blocks; // [px_len / 16] block ids of the prefix
+    float* px_o;              // [px_splits][num_q_tokens * Hq][head_size] unnormalised partial outputs
+    float* px_ml;             // [px_splits][num_q_tokens * Hq][2] partial (max in log2 units, sum)
+    int px_len;               // tokens, a multiple of 16
+    int px_splits;
 };
 constexpr int kOptWindow = 1, kOptSoftcap = 2, kOptAlibi = 4, kOptQQ = 8;
 
@@ -147,6 +154,13 @@ cudaError_t launch_prefill(const AttnParams& p, int head_size, int max_query_len
 // The prefill kernel instantiated with the logit options (p.opts != 0); launch_prefill calls it.
 cudaError_t launch_prefill_opts(const AttnParams& p, int head_size, int max_query_len, DType q_dt, DType out_dt,
                                 cudaStream_t stream);
+
+// Shared prefix: every query row of a decode batch against the prefix's keys, one partial per split
+// (launch_decode launches it between its walker and its combine).
+cudaError_t launch_prefix(const AttnParams& p, int head_size, DType q_dt, cudaStream_t stream);
+// Splits of the prefix's keys for a batch of row_tiles 128-row tiles per kv head.
+int prefix_splits(int64_t row_tiles, int num_kv_heads, int prefix_len);
+constexpr int kMaxPrefixSplits = 64;
 
 int num_sms();
 

@@ -234,8 +234,9 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
     constexpr int OW = INT8 ? NW + 1 : NW / 2 + 1;   // words one thread stores (the last: the scale word)
     using Sm = WriteSmem<D, TV>;
     extern __shared__ __align__(128) uint8_t smem[];
-    griddep_wait();   // the previous kernel may produce any of the inputs
-    griddep_launch_dependents();
+    // The previous kernel may produce any of the inputs.  Unlike the plain write, this kernel lets no
+    // dependent start early: the attention that follows reads its queries before it waits.
+    griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int vl = lane / TPV, part = lane % TPV;   // this thread's vector of the tile and its part
     uint8_t* wbuf = smem + warp * Sm::kPerWarp;

@@ -1,0 +1,242 @@
+"""GPU parity of the shared-prefix attention: against the oracle (which knows nothing of sharing) on small
+batches, and against the plain decode call on larger ones."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import workloads
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from gpu_helpers import clear_status
+    clear_status()
+
+
+def _kv():
+    import int4_token_head_kv_gb300 as kv
+    return kv
+
+
+class Batch:
+    """A decode batch on a shared prefix: a written cache, tables and lengths (on the host and the GPU)."""
+
+    def __init__(self, prefix, lens, Hq, H, d, dtype=torch.bfloat16, seed=0, query_lens=None, outliers=True, extra_q=0):
+        r = np.random.default_rng(seed)
+        S, shared = len(lens), prefix // 16
+        mine = max(0, -(-max(lens) // 16) - shared)
+        nb = shared + S * mine + 2
+        ids = r.permutation(nb).astype(np.int32)
+        self.prefix, self.prefix_blocks = prefix, ids[:shared].copy()
+        self.tables = np.concatenate([np.tile(ids[:shared], (S, 1)), ids[shared:shared + S * mine].reshape(S, mine)], 1)
+        if self.tables.shape[1] == 0:
+            self.tables = np.zeros((S, 1), np.int32)
+        self.lens = np.asarray(lens, np.int32)
+        self.qlens = np.ones(S, np.int32) if query_lens is None else np.asarray(query_lens, np.int32)
+        self.qsl = np.concatenate([[0], np.cumsum(self.qlens)]).astype(np.int32)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        k = torch.randn(nb * 16, H, d, generator=g, device="cuda")
+        if outliers:
+            k[:, :, :4] *= 10.0
+        v = torch.randn(nb * 16, H, d, generator=g, device="cuda")
+        self.signs = workloads.splitmix64_signs(d)
+        self.gsigns = torch.from_numpy(self.signs).cuda()
+        kv = _kv()
+        self.cache = torch.zeros(kv.kv_int4_cache_shape(nb, 16, H, d), dtype=torch.uint8, device="cuda")
+        kv.kv_int4_write(k.to(dtype), v.to(dtype), torch.arange(nb * 16, device="cuda"), self.gsigns, self.cache)
+        self.q = torch.randn(int(self.qsl[-1]) + extra_q, Hq, d, generator=g, device="cuda").to(dtype)
+        self.scale = d ** -0.5
+        self.max_len = int(max(lens))
+
+    def _args(self):
+        return (torch.from_numpy(self.tables).cuda(), torch.from_numpy(self.lens).cuda(), torch.from_numpy(self.qsl).cuda())
+
+    def shared(self, out_dtype=torch.float32, **kw):
+        t, l, q = self._args()
+        return _kv().kv_int4_shared_prefix_attention(self.q, self.cache, torch.from_numpy(self.prefix_blocks).cuda(),
+                                                     self.prefix, t, l, q, self.scale, self.gsigns,
+                                                     **{"max_seq_len": self.max_len, "out_dtype": out_dtype, **kw})
+
+    def plain(self, out_dtype=torch.float32, **kw):
+        t, l, q = self._args()
+        return _kv().kv_int4_paged_attention(self.q, self.cache, t, l, q, self.scale, self.gsigns, max_query_len=1,
+                                             max_seq_len=self.max_len, out_dtype=out_dtype, **kw)
+
+    def oracle(self):
+        return oracle.paged_attention(self.q, self.cache.cpu().numpy(), self.tables, self.lens, self.qsl, self.scale,
+                                      self.signs)
+
+
+def _check(b, **kw):
+    from gpu_helpers import assert_attention_close, status
+    got = b.shared(**kw)
+    assert_attention_close(got, b.oracle(), "shared prefix")
+    assert not any(status().values())
+    return got
+
+
+@pytest.mark.parametrize("Hq, H", [(1, 1), (4, 1), (8, 8), (8, 4), (8, 2), (16, 2), (64, 8)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_head_layouts(Hq, H, d):
+    _check(Batch(256, [256 + n for n in (1, 40, 17)], Hq, H, d, seed=Hq + d))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_types(dtype, out_dtype):
+    _check(Batch(400, [401, 450, 520], 8, 2, 128, dtype=dtype, seed=2), out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("prefix", [16, 112, 128, 129, 144, 205, 256, 391, 640, 1025])
+def test_prefix_lengths(prefix):
+    _check(Batch(prefix, [prefix + 1, prefix + 30, prefix + 100, prefix + 16], 8, 2, 64, seed=prefix))
+
+
+@pytest.mark.parametrize("S", [1, 2, 31, 32, 33, 70])
+def test_batch_sizes(S):
+    r = np.random.default_rng(S)
+    _check(Batch(160, list(160 + r.integers(1, 40, S)), 4, 1, 64, seed=S))
+
+
+def test_lengths_inside_and_at_the_prefix():
+    # padding rows, rows that end inside the prefix, at its end, and behind it
+    got = _check(Batch(300, [0, 1, 128, 129, 200, 288, 300, 301, 330, 0], 8, 2, 128, seed=3))
+    assert not got[0].any() and not got[9].any()
+
+
+def test_every_sequence_ends_inside_the_prefix():
+    _check(Batch(512, [512, 512, 100, 1], 8, 4, 128, seed=4))
+
+
+def test_sequences_without_a_query_and_rows_behind_the_last():
+    b = Batch(256, [260, 300, 270, 256, 290], 8, 2, 64, seed=5, query_lens=[0, 1, 0, 1, 1], extra_q=3)
+    out = torch.full(b.q.shape, 5.0, device="cuda")
+    got = b.shared(out=out)
+    ref = b.oracle()
+    from gpu_helpers import assert_attention_close
+    assert_attention_close(got[:3], ref[:3])
+    assert bool((out[3:] == 5.0).all())
+
+
+def test_bad_prefix_block_is_counted_and_skipped():
+    from gpu_helpers import assert_attention_close, status
+    b = Batch(256, [257, 280, 260], 8, 2, 64, seed=6)
+    keep = b.prefix_blocks.copy()
+    b.prefix_blocks[3], b.prefix_blocks[9] = -7, 10 ** 6
+    got = b.shared()
+    assert status()["block_out_of_range"] > 0
+    # the tokens of those blocks are no keys: the oracle on the sequences without them
+    b.prefix_blocks = keep
+    drop = np.ones(256 // 16, bool)
+    drop[[3, 9]] = False
+    cols = np.concatenate([drop, np.ones(b.tables.shape[1] - 16, bool)])
+    ref = oracle.paged_attention(b.q, b.cache.cpu().numpy(), b.tables[:, cols], b.lens - 32, b.qsl, b.scale, b.signs)
+    assert_attention_close(got, ref)
+
+
+def test_heavy_tails_and_large_scales():
+    b = Batch(384, [390, 500, 385], 16, 2, 128, seed=7)
+    kv = _kv()
+    n = b.cache.shape[0] * 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    t3 = torch.randn(n, 2, 128, generator=g, device="cuda") / torch.rand(n, 2, 128, generator=g, device="cuda").clamp(min=0.02)
+    mag = 10.0 ** (torch.rand(n, 1, 1, generator=g, device="cuda") * 4 - 2)
+    kv.kv_int4_write((t3 * 0.5).bfloat16(), (t3.flip(0) * mag).bfloat16(), torch.arange(n, device="cuda"), b.gsigns, b.cache)
+    ref = b.oracle()
+    got = b.shared().double().cpu().numpy()
+    # the weights are rounded to fp16 (2^-11 each) and the error of a row is at most that share of its
+    # largest value magnitude; the values span four decades, so the bound is relative to the row's largest
+    big = np.abs(ref).max(axis=2, keepdims=True)
+    assert np.all(np.abs(got - ref) <= 1e-2 * np.abs(ref) + 1e-2 * big + 2e-3)
+
+
+@pytest.mark.parametrize("S, prefix, Hq, H, d", [(64, 8192, 32, 8, 128), (100, 3000, 64, 8, 128), (40, 20000, 8, 1, 64)])
+def test_larger_batches_match_the_plain_call(S, prefix, Hq, H, d):
+    from gpu_helpers import ATOL, RTOL, status
+    r = np.random.default_rng(S)
+    b = Batch(prefix, list(prefix + r.integers(1, 600, S)), Hq, H, d, seed=S, outliers=False)
+    a, c = b.shared().double(), b.plain().double()
+    assert bool(((a - c).abs() <= 2 * (ATOL + RTOL * c.abs())).all())
+    # far closer in the mean: both carry fp16 weights (a relative 2^-11 at most, independent per key)
+    assert float((a - c).norm() / c.norm()) < 1e-3
+    assert not any(status().values())
+
+
+def test_same_bits_again_and_captured():
+    b = Batch(1000, [1001 + 9 * i for i in range(20)], 32, 8, 128, seed=8)
+    first = b.shared(out_dtype=torch.bfloat16)
+    t, l, q = b._args()
+    pb = torch.from_numpy(b.prefix_blocks).cuda()
+    need = _kv().kv_int4_shared_prefix_workspace_bytes(20, 32, 8, 128, 20, 1000, b.max_len)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(b.q)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        _kv().kv_int4_shared_prefix_attention(b.q, b.cache, pb, 1000, t, l, q, b.scale, b.gsigns, max_seq_len=b.max_len,
+                                              out=out, workspace=ws)
+    for _ in range(3):
+        out.zero_()
+        ws.fill_(0xFF)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+
+
+def test_python_checks():
+    kv = _kv()
+    b = Batch(256, [260, 270], 8, 2, 64, seed=9)
+    with pytest.raises(ValueError):
+        b.shared(workspace=torch.empty(1 << 20, dtype=torch.uint8))
+    keep, b.prefix_blocks = b.prefix_blocks, b.prefix_blocks[:15]
+    with pytest.raises(ValueError):
+        b.shared()
+    b.prefix_blocks = keep
+    with pytest.raises(kv.KVInt4Error) as e:
+        b.shared(workspace=torch.empty(1024, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 4
+
+
+def test_a_serving_step_as_it_runs():
+    """Rotary append of the batch's new tokens, attention over the shared prefix with the rotated queries,
+    and the new rows read back: one step after another on one stream, no synchronisation between."""
+    from gpu_helpers import assert_attention_close
+    from oracle import rope
+    kv = _kv()
+    S, P, Hq, H, d, steps = 24, 512, 32, 8, 128, 5
+    b = Batch(P, [P + 1 + 3 * i + steps for i in range(S)], Hq, H, d, seed=10)
+    r = np.random.default_rng(0)
+    tab = rope.table(1024, d)
+    start = b.lens - steps
+    gtab, gt = torch.from_numpy(tab).cuda(), torch.from_numpy(b.tables).cuda()
+    pb, qsl = torch.from_numpy(b.prefix_blocks).cuda(), torch.from_numpy(b.qsl).cuda()
+    xs, lens, slots, poss = [], [], [], []
+    for i in range(steps):
+        xs.append(torch.from_numpy(r.standard_normal((S, Hq + 2 * H, d)).astype(np.float32)).bfloat16())
+        pos = (start + i).astype(np.int64)
+        poss.append(pos)
+        slots.append(b.tables[np.arange(S), pos // 16].astype(np.int64) * 16 + pos % 16)
+        lens.append((start + i + 1).astype(np.int32))
+    gx = [x.cuda() for x in xs]
+    gl, gs, gp = ([torch.from_numpy(a).cuda() for a in z] for z in (lens, slots, poss))
+    torch.cuda.synchronize()
+    outs, rows = [], []
+    for i in range(steps):
+        q = kv.kv_int4_rope_write(gx[i][:, :Hq], gx[i][:, Hq:Hq + H], gx[i][:, Hq + H:], gp[i], gtab, gs[i], b.gsigns, b.cache)
+        outs.append(kv.kv_int4_shared_prefix_attention(q, b.cache, pb, P, gt, gl[i], qsl, b.scale, b.gsigns,
+                                                       max_seq_len=b.max_len, out_dtype=torch.float32))
+        rows.append(kv.kv_int4_read(b.cache, gs[i], b.gsigns, dtype=torch.float32))
+    torch.cuda.synchronize()
+    cache = b.cache.cpu().numpy()   # later steps only added rows behind the earlier ones' lengths
+    for i in (0, steps - 1):
+        qr = torch.from_numpy(rope.rotate(xs[i][:, :Hq], poss[i], tab)).bfloat16()
+        ref = oracle.paged_attention(qr, cache, b.tables, lens[i], b.qsl, b.scale, b.signs)
+        assert_attention_close(outs[i], ref, f"step {i}")
+        want = oracle.decode_rows(cache[slots[i] // 16, 0, slots[i] % 16].reshape(S * H, -1), b.signs).reshape(S, H, d)
+        assert np.allclose(rows[i][0].cpu().numpy(), want, rtol=1e-6, atol=1e-9)
