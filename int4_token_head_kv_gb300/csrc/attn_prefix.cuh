@@ -45,15 +45,30 @@ struct PxLayout {
     static constexpr uint32_t kDeadF = kSk + kPfKRing * kPfKeys * 4;             // [kring][4] u32: a K warp saw a key with no row
     static constexpr uint32_t kSv = kDeadF + kPfKRing * 4 * 4;                   // [pairs][128] f32 s'_V
     static constexpr uint32_t kEblk = kSv + kPfPairs * kPfKeys * 4;              // [pairs][4] per-warp max V exponent
-    static constexpr uint32_t kSignBits = kEblk + kPfPairs * 4 * 4;              // [D / 32] u32
+    static constexpr uint32_t kQmax = kEblk + kPfPairs * 4 * 4;                  // u32: bits of the rows' largest |v|
+    static constexpr uint32_t kSignBits = kQmax + 16;                            // [D / 32] u32
     static constexpr uint32_t kBars = (kSignBits + D / 8 + 7u) & ~7u;
     // k_full[kring], k_free[pairs], v_full[pairs], v_free[pairs], pv_done[2], s_full[2], p_full[2], q_ready,
-    // flush, q_tma, rot_in, rot_done, raw_full[plane][stages], raw_free[plane][stages]
-    static constexpr int kNumBars = kPfKRing + 3 * kPfPairs + 6 + 5 + 4 * kPfRawStages;
+    // flush, q_tma, rot_in, rot_done, q_max, raw_full[plane][stages], raw_free[plane][stages]
+    static constexpr int kNumBars = kPfKRing + 3 * kPfPairs + 6 + 6 + 4 * kPfRawStages;
     static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr uint32_t kFlags = kTmemSlot + 4;
     static constexpr uint32_t kBytes = kFlags + 4 + 1024;                        // + alignment slack
 };
+
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// inverse of slot_of_column
+__host__ __device__ constexpr int column_of_slot(int s) {
+    return (s & ~15) + 2 * ((s >> 2) & 3) + 8 * ((s >> 1) & 1) + (s & 1);
+}
+static_assert(column_of_slot(slot_of_column(2)) == 2 && column_of_slot(slot_of_column(9)) == 9 &&
+              column_of_slot(slot_of_column(30)) == 30, "inverse");
 
 template <int REGS>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
@@ -95,11 +110,13 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     uint64_t* q_tma = flush + 1;                // the CTA's query rows in shared memory (bytes)
     uint64_t* rot_in = q_tma + 1;               // the rotation matrix in shared memory (256 arrivals)
     uint64_t* rot_done = rot_in + 1;            // the rotated queries in tensor memory (commit)
-    uint64_t* raw_full = rot_done + 1;          // [plane][stages] packed rows of a key tile landed (32 lanes)
+    uint64_t* q_max = rot_done + 1;             // the rows' largest magnitude is known (256 arrivals)
+    uint64_t* raw_full = q_max + 1;          // [plane][stages] packed rows of a key tile landed (32 lanes)
     uint64_t* raw_free = raw_full + 2 * kPfRawStages;   // [plane][stages] that plane converted (128 arrivals)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kFlags);
     uint32_t* deadf = reinterpret_cast<uint32_t*>(smem + Ly::kDeadF);
+    uint32_t* qmax = reinterpret_cast<uint32_t*>(smem + Ly::kQmax);
 
     if (threadIdx.x == 0) {
         for (int b = 0; b < kPfKRing; ++b) mbar_init(&k_full[b], 128);
@@ -118,6 +135,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         mbar_init(q_tma, 1);
         mbar_init(rot_in, kPfSoftmaxThreads);
         mbar_init(rot_done, 1);
+        mbar_init(q_max, kPfSoftmaxThreads);
+        *qmax = 0u;
         for (int i = 0; i < 2 * kPfRawStages; ++i) {
             mbar_init(&raw_full[i], 32);
             mbar_init(&raw_free[i], 128);
@@ -125,6 +144,37 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         *abort_flag = 0;
         fence_mbar_init();
     }
+    // Metadata of this thread's two rows, loaded early and at once: (query start, end, length) as they are
+    // when every sequence before a token has one query.
+    struct RowMeta {
+        int q0, q1, len;
+    };
+    auto row_meta = [&](int tok) -> RowMeta {
+        const int b = min(tok, p.num_seqs - 1);
+        return RowMeta{__ldg(p.qsl + b), __ldg(p.qsl + b + 1), __ldg(p.seq_lens + b)};
+    };
+    RowMeta meta_a = {}, meta_b = {};
+    if (warp < kPfSoftmaxWarps) {
+        const int r = 32 * (warp & 3) + 16 * (warp >> 2) + (lane >> 2);
+        meta_a = row_meta(qt0 + r / G);
+        meta_b = row_meta(qt0 + (r + 8) / G);
+    }
+    // keys [0, n) of the prefix that a query token sees
+    auto visible = [&](int tok, const RowMeta& mt) -> int {
+        if ((int64_t)tok >= p.num_q_tokens) return 0;
+        int len = mt.len;
+        if (tok >= p.num_seqs || mt.q0 != tok || mt.q1 != tok + 1) {   // some sequences have no query: search
+            int lo = 0, hi = p.num_seqs;   // the last b with qsl[b] <= tok
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (__ldg(p.qsl + mid) <= tok) lo = mid;
+                else hi = mid;
+            }
+            if (__ldg(p.qsl + lo) != tok || __ldg(p.qsl + lo + 1) != tok + 1) return 0;
+            len = __ldg(p.seq_lens + lo);
+        }
+        return max(0, min(min(len, p.len_cap), p.px_len));
+    };
     uint32_t* signbits = reinterpret_cast<uint32_t*>(smem + Ly::kSignBits);
     if (threadIdx.x < D) {   // whole warps (D is a multiple of 32)
         const uint32_t m = __ballot_sync(0xffffffffu, p.signs[threadIdx.x] < 0.0f);
@@ -185,27 +235,17 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             mbar_arrive(rot_in);
         }
         // ---- each row's limit: keys [0, vis) of the prefix, from its token's sequence
-        auto visible = [&](int tok) -> int {
-            if ((int64_t)tok >= p.num_q_tokens) return 0;
-            // the sequence holding the token: sequence tok itself when every one before it has one query
-            int b = min(tok, p.num_seqs - 1);
-            if (__ldg(p.qsl + b) != tok) {
-                int lo = 0, hi = p.num_seqs;   // the last b with qsl[b] <= tok
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (__ldg(p.qsl + mid) <= tok) lo = mid;
-                    else hi = mid;
-                }
-                b = lo;
-            }
-            // sequences without a query may share the start: the last one with this start holds it
-            while (b + 1 < p.num_seqs && __ldg(p.qsl + b + 1) == tok) ++b;
-            if (__ldg(p.qsl + b) != tok || __ldg(p.qsl + b + 1) != tok + 1) return 0;
-            return max(0, min(min(__ldg(p.seq_lens + b), p.len_cap), p.px_len));
-        };
-        const int vis_a = visible(qt0 + ra / G), vis_b = visible(qt0 + rb / G);
-        // ---- power-of-two prescale, fp16 high + low halves into tensor memory
-        float rs_a = 1.0f, rs_b = 1.0f;   // 2^-e of each row
+        // A row that sees none (a padding row, or one past the batch) goes along as if it saw all, so that it
+        // does not put its warp on the masked path, and its partial is empty at the end; a warp of such rows
+        // leaves its weights unwritten.
+        int vis_a = visible(qt0 + ra / G, meta_a), vis_b = visible(qt0 + rb / G, meta_b);
+        const bool none_a = vis_a == 0, none_b = vis_b == 0;
+        if (none_a) vis_a = p.px_len;
+        if (none_b) vis_b = p.px_len;
+        const bool idle = __all_sync(0xffffffffu, none_a && none_b);
+        // ---- one power-of-two prescale 2^e for the CTA's rows, bringing the largest |v| into [2^14, 2^15), and
+        // fp16 high + low halves into tensor memory.  (A row 2^16 smaller than the largest still keeps 22
+        // bits; with one exponent, 2^-e goes into the keys' scales instead of a factor per row.)
         bool ok = wait(rot_done, 0);
         if (__all_sync(0xffffffffu, ok)) {
             tc_fence_after();
@@ -213,20 +253,15 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 64) tmem_ld_q8(trow + Tm::kS0 + c0, reinterpret_cast<uint32_t*>(v) + c0 / 2);
             tmem_ld_wait();
-            float mxa = 0.0f, mxb = 0.0f;
+            float mx = 0.0f;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                mxa = fmaxf(mxa, fmaxf(fabsf(v[4 * i]), fabsf(v[4 * i + 1])));
-                mxb = fmaxf(mxb, fmaxf(fabsf(v[4 * i + 2]), fabsf(v[4 * i + 3])));
-            }
-            mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
-            mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
-            mxa = fmaxf(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
-            mxb = fmaxf(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
-            const int ea = prescale_exponent(mxa), eb = prescale_exponent(mxb);   // rows of zeros: 2^0
-            const float sca = exp2i(ea), scb = exp2i(eb);
-            rs_a = exp2i(-ea);
-            rs_b = exp2i(-eb);
+            for (int i = 0; i < D / 4; ++i) mx = max3(mx, fabsf(v[2 * i]), fabsf(v[2 * i + 1]));
+            const uint32_t wmx = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));   // non-negative floats order like their bits
+            if (lane == 0) atomicMax(qmax, wmx);
+            __syncwarp();
+            mbar_arrive(q_max);
+            ok = __all_sync(0xffffffffu, wait(q_max, 0));
+            const float sc = exp2i(prescale_exponent(__uint_as_float(*reinterpret_cast<volatile uint32_t*>(qmax))));
 #pragma unroll
             for (int q = 0; q < D / 16; ++q) {
                 uint32_t hw[4], lw[4];
@@ -234,10 +269,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                 for (int e = 0; e < 2; ++e) {
                     const int i = 2 * q + e;
 #pragma unroll
-                    for (int rr = 0; rr < 2; ++rr) {
-                        const float sc = rr ? scb : sca;
+                    for (int rr = 0; rr < 2; ++rr)
                         split_f16x2(v[4 * i + 2 * rr] * sc, v[4 * i + 2 * rr + 1] * sc, hw[2 * rr + e], lw[2 * rr + e]);
-                    }
                 }
                 tmem_st_q1(trow + Tm::kQh + 8 * q, hw);
                 tmem_st_q1(trow + Tm::kQl + 8 * q, lw);
@@ -249,10 +282,20 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         tc_fence_before();
         mbar_arrive(q_ready);
         // ---- the key tiles
-        float m_a = kNegBig, m_b = kNegBig;     // reference maxima (log2 units)
+        // Reference maxima m (log2 units) as the exponents' offsets off = 127 - E - m; m = 0 and E = 127 until a
+        // row has a key (any).
+        float off_a = 0.0f, off_b = 0.0f;
+        bool any_a = false, any_b = false;
         float l_a = 0.0f, l_b = 0.0f;           // this thread's part of the sums of 2^(127-E) p
         uint32_t E = 0;                         // reference biased exponent of the V scales (0: none yet)
-        for (int j = 0; j < nkt && ok; ++j) {
+        if (idle) {   // a loop of its own: the test in the loop below cost 3% of the whole call
+            for (int j = 0; j < nkt && ok; ++j) {
+                ok = wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) mbar_arrive(&p_full[j & 1]);
+            }
+        }
+        for (int j = idle ? nkt : 0; j < nkt && ok; ++j) {
             const int b = j & 1;
             const uint32_t ph = (uint32_t)(j >> 1) & 1u;
             const int kb = j % kPfPairs, kr = j % kPfKRing;
@@ -268,39 +311,43 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             tmem_ld_q8(scol, s);
             tmem_ld_q8(scol + 64, s + 32);
             tmem_ld_wait();
-            // x = S * s'_K * k0 (0 scale: no key), masked; the row maxima
+            // Exponents e = S s'_K k0 2^-e - m + 127 - E (one FMA; scale 0: no key) against the references as they
+            // are, and their row maxima; a reference that moves is added to them afterwards, which is rare.
             const int key0 = (kt0 + j) * kPfKeys;
-            const float* skb = sk + kr * kPfKeys + 2 * t4;
+            const float4* skb = reinterpret_cast<const float4*>(sk + kr * kPfKeys) + t4;   // columns 16q + (2t, 2t + 1, 8 + 2t, 9 + 2t)
             const bool clean = (deadf[kr * 4] | deadf[kr * 4 + 1] | deadf[kr * 4 + 2] | deadf[kr * 4 + 3]) == 0u &&
                                key0 + kPfKeys <= min(vis_a, vis_b);
             float bma = -INFINITY, bmb = -INFINITY;
             if (__all_sync(0xffffffffu, clean)) {   // every key live and visible to both rows
+                const float2 moa2 = make_float2(off_a, off_a), mob2 = make_float2(off_b, off_b);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 k2 = *reinterpret_cast<const float2*>(skb + 8 * i);
-                    const float2 xa = mul_f32x2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), k2);
-                    const float2 xb = mul_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k2);
-                    s[4 * i] = __float_as_uint(xa.x);
-                    s[4 * i + 1] = __float_as_uint(xa.y);
-                    s[4 * i + 2] = __float_as_uint(xb.x);
-                    s[4 * i + 3] = __float_as_uint(xb.y);
-                    bma = max3(bma, xa.x, xa.y);
-                    bmb = max3(bmb, xb.x, xb.y);
+                    const float4 k4 = skb[4 * (i / 2)];
+                    const float2 k2 = (i & 1) ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
+                    const float2 ea = fma_f32x2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), k2, moa2);
+                    const float2 eb = fma_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k2, mob2);
+                    s[4 * i] = __float_as_uint(ea.x);
+                    s[4 * i + 1] = __float_as_uint(ea.y);
+                    s[4 * i + 2] = __float_as_uint(eb.x);
+                    s[4 * i + 3] = __float_as_uint(eb.y);
+                    bma = max3(bma, ea.x, ea.y);
+                    bmb = max3(bmb, eb.x, eb.y);
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 k2 = *reinterpret_cast<const float2*>(skb + 8 * i);
+                    const float4 k4 = skb[4 * (i / 2)];
+                    const float2 k2 = (i & 1) ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float kk = e ? k2.y : k2.x;
                         const int key = key0 + 8 * i + 2 * t4 + e;
-                        const float xa = kk > 0.0f && key < vis_a ? __uint_as_float(s[4 * i + e]) * kk : -INFINITY;
-                        const float xb = kk > 0.0f && key < vis_b ? __uint_as_float(s[4 * i + 2 + e]) * kk : -INFINITY;
-                        s[4 * i + e] = __float_as_uint(xa);
-                        s[4 * i + 2 + e] = __float_as_uint(xb);
-                        bma = fmaxf(bma, xa);
-                        bmb = fmaxf(bmb, xb);
+                        const float ea = kk > 0.0f && key < vis_a ? fmaf(__uint_as_float(s[4 * i + e]), kk, off_a) : -INFINITY;
+                        const float eb = kk > 0.0f && key < vis_b ? fmaf(__uint_as_float(s[4 * i + 2 + e]), kk, off_b) : -INFINITY;
+                        s[4 * i + e] = __float_as_uint(ea);
+                        s[4 * i + 2 + e] = __float_as_uint(eb);
+                        bma = fmaxf(bma, ea);
+                        bmb = fmaxf(bmb, eb);
                     }
                 }
             }
@@ -308,66 +355,79 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 1));
             bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 2));
             bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 2));
-            // in log2 units (rs > 0: a power of two scales exactly); the four threads of a row take
-            // the same decisions
-            bma *= rs_a;
-            bmb *= rs_b;
-            const bool up_a = bma > m_a + kPfLazyMax, up_b = bmb > m_b + kPfLazyMax;
-            const float fm_a = up_a ? fast_exp2(m_a - bma) : 1.0f, fm_b = up_b ? fast_exp2(m_b - bmb) : 1.0f;
-            if (up_a) m_a = bma;
-            if (up_b) m_b = bmb;
+            // the four threads of a row take the same decisions; a row without a reference takes the first one
             const uint32_t* eb4 = eblkw + kb * 4;
             const uint32_t eb = max(max(eb4[0], eb4[1]), max(eb4[2], eb4[3]));
-            const uint32_t Eeff = E ? E : 127u;
-            float fe = 1.0f;
-            if (E == 0u ? eb > 0u : eb > E + kPfLazyExp) {
-                // rebase from 2^(127 - Eeff) to 2^(127 - eb); 0 when the jump underflows
-                fe = eb > Eeff + 126u ? 0.0f : __uint_as_float((127u + Eeff - eb) << 23);
-                E = eb;
-            }
-            const float f_a = fm_a * fe, f_b = fm_b * fe;
-            l_a *= f_a;
-            l_b *= f_b;
-            if (j > 0 && __any_sync(0xffffffffu, f_a != 1.0f || f_b != 1.0f)) {
-                // O must hold P.V of the previous tile before it is rescaled
-                ok = wait(&pv_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u);
-                if (__any_sync(0xffffffffu, !ok)) {
-                    ok = false;
-                    break;
+            const float eoff0 = (float)(127 - (int)(E ? E : 127u));
+            const bool newE = E == 0u ? eb > 0u : eb > E + kPfLazyExp;
+            const bool up_a = any_a ? bma > eoff0 + kPfLazyMax : bma > -INFINITY;
+            const bool up_b = any_b ? bmb > eoff0 + kPfLazyMax : bmb > -INFINITY;
+            if (__any_sync(0xffffffffu, up_a || up_b || newE)) {
+                const float da = up_a ? eoff0 - bma : 0.0f, db = up_b ? eoff0 - bmb : 0.0f;   // old reference - new one
+                const float fm_a = up_a ? (any_a ? fast_exp2(da) : 0.0f) : 1.0f, fm_b = up_b ? (any_b ? fast_exp2(db) : 0.0f) : 1.0f;
+                any_a = any_a || up_a;
+                any_b = any_b || up_b;
+                const uint32_t Eeff = E ? E : 127u;
+                float fe = 1.0f, de = 0.0f;
+                if (newE) {
+                    // rebase from 2^(127 - Eeff) to 2^(127 - eb); 0 when the jump underflows
+                    fe = eb > Eeff + 126u ? 0.0f : __uint_as_float((127u + Eeff - eb) << 23);
+                    de = (float)((int)Eeff - (int)eb);
+                    E = eb;
                 }
-                tc_fence_after();
-                const float2 fa2 = make_float2(f_a, f_a), fb2 = make_float2(f_b, f_b);
+                const float f_a = fm_a * fe, f_b = fm_b * fe;
+                l_a *= f_a;
+                l_b *= f_b;
+                off_a += da + de;
+                off_b += db + de;
+                const float2 da2 = make_float2(da + de, da + de), db2 = make_float2(db + de, db + de);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 ea = add_f32x2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), da2);
+                    const float2 eb2 = add_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), db2);
+                    s[4 * i] = __float_as_uint(ea.x);
+                    s[4 * i + 1] = __float_as_uint(ea.y);
+                    s[4 * i + 2] = __float_as_uint(eb2.x);
+                    s[4 * i + 3] = __float_as_uint(eb2.y);
+                }
+                if (j > 0 && __any_sync(0xffffffffu, f_a != 1.0f || f_b != 1.0f)) {
+                    // O must hold P.V of the previous tile before it is rescaled
+                    ok = wait(&pv_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u);
+                    if (__any_sync(0xffffffffu, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const float2 fa2 = make_float2(f_a, f_a), fb2 = make_float2(f_b, f_b);
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 8) {
-                    uint32_t o[4];
-                    tmem_ld_q1(trow + Tm::kO + c0, o);
-                    tmem_ld_wait();
-                    const float2 oa = mul_f32x2(make_float2(__uint_as_float(o[0]), __uint_as_float(o[1])), fa2);
-                    const float2 ob = mul_f32x2(make_float2(__uint_as_float(o[2]), __uint_as_float(o[3])), fb2);
-                    o[0] = __float_as_uint(oa.x);
-                    o[1] = __float_as_uint(oa.y);
-                    o[2] = __float_as_uint(ob.x);
-                    o[3] = __float_as_uint(ob.y);
-                    tmem_st_q1(trow + Tm::kO + c0, o);
+                    for (int c0 = 0; c0 < D; c0 += 8) {
+                        uint32_t o[4];
+                        tmem_ld_q1(trow + Tm::kO + c0, o);
+                        tmem_ld_wait();
+                        const float2 oa = mul_f32x2(make_float2(__uint_as_float(o[0]), __uint_as_float(o[1])), fa2);
+                        const float2 ob = mul_f32x2(make_float2(__uint_as_float(o[2]), __uint_as_float(o[3])), fb2);
+                        o[0] = __float_as_uint(oa.x);
+                        o[1] = __float_as_uint(oa.y);
+                        o[2] = __float_as_uint(ob.x);
+                        o[3] = __float_as_uint(ob.y);
+                        tmem_st_q1(trow + Tm::kO + c0, o);
+                    }
+                    tmem_st_wait();
                 }
-                tmem_st_wait();
             }
-            // p' = 2^(x rs - m + 127 - E), w = p' s'_V as fp16 pairs over the first 64 S columns
-            const float eoff = (float)(127 - (int)(E ? E : 127u));
-            const float2 rsa2 = make_float2(rs_a, rs_a), rsb2 = make_float2(rs_b, rs_b);
-            const float2 moa2 = make_float2(eoff - m_a, eoff - m_a), mob2 = make_float2(eoff - m_b, eoff - m_b);
-            const float* svb = sv + kb * kPfKeys + 2 * t4;
+            // p' = 2^e, w = p' s'_V as fp16 pairs over the first 64 S columns: the pair of columns 8i + 2t, + 1
+            // goes to column 8 (i / 2) + 2t + i % 2 (the V tile holds its rows in the matching order)
+            const float4* svb = reinterpret_cast<const float4*>(sv + kb * kPfKeys) + t4;
             float2 lsa = make_float2(0.0f, 0.0f), lsb = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 uint32_t pw[4];
+                const float4 v4 = svb[4 * q];
 #pragma unroll
                 for (int i = 2 * q; i < 2 * q + 2; ++i) {
-                    const float2 v2 = *reinterpret_cast<const float2*>(svb + 8 * i);
-                    const float2 ea = fma_f32x2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), rsa2, moa2);
-                    const float2 eb2 = fma_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), rsb2, mob2);
-                    const float2 pa = make_float2(fast_exp2(ea.x), fast_exp2(ea.y));
-                    const float2 pb = make_float2(fast_exp2(eb2.x), fast_exp2(eb2.y));
+                    const float2 v2 = (i & 1) ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y);
+                    const float2 pa = make_float2(fast_exp2(__uint_as_float(s[4 * i])), fast_exp2(__uint_as_float(s[4 * i + 1])));
+                    const float2 pb = make_float2(fast_exp2(__uint_as_float(s[4 * i + 2])), fast_exp2(__uint_as_float(s[4 * i + 3])));
                     lsa = add_f32x2(lsa, pa);
                     lsb = add_f32x2(lsb, pb);
                     const float2 wa = mul_f32x2(pa, v2), wb = mul_f32x2(pb, v2);
@@ -391,16 +451,21 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
         l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
         const bool good = __all_sync(0xffffffffu, ok) && nkt > 0;
+        if (none_a) any_a = false;
+        if (none_b) any_b = false;
         const float es = good && E ? __uint_as_float(E << 23) : 0.0f;   // 2^(E - 127)
+        const float eoff = (float)(127 - (int)(E ? E : 127u));
+        const float m_a = any_a ? eoff - off_a : kNegBig, m_b = any_b ? eoff - off_b : kNegBig;
         const int64_t rows = p.num_q_tokens * Hq;
-        const int tok_a = qt0 + ra / G, tok_b = qt0 + rb / G;
-        const bool in_a = (int64_t)tok_a < p.num_q_tokens, in_b = (int64_t)tok_b < p.num_q_tokens;
-        const int64_t rec_a = (int64_t)split * rows + (int64_t)tok_a * Hq + h * G + ra % G;
-        const int64_t rec_b = (int64_t)split * rows + (int64_t)tok_b * Hq + h * G + rb % G;
+        auto record = [&](int r) -> int64_t { return (int64_t)split * rows + (int64_t)(qt0 + r / G) * Hq + h * G + r % G; };
+        auto in_batch = [&](int r) -> bool { return (int64_t)(qt0 + r / G) < p.num_q_tokens; };
         if (t4 == 0) {
-            if (in_a) reinterpret_cast<float2*>(p.px_ml)[rec_a] = make_float2(good ? m_a : kNegBig, l_a * es);
-            if (in_b) reinterpret_cast<float2*>(p.px_ml)[rec_b] = make_float2(good ? m_b : kNegBig, l_b * es);
+            if (in_batch(ra)) reinterpret_cast<float2*>(p.px_ml)[record(ra)] = any_a && good ? make_float2(m_a, l_a * es) : make_float2(kNegBig, 0.0f);
+            if (in_batch(rb)) reinterpret_cast<float2*>(p.px_ml)[record(rb)] = any_b && good ? make_float2(m_b, l_b * es) : make_float2(kNegBig, 0.0f);
         }
+        const bool full_a = good && any_a, full_b = good && any_b, in_a = in_batch(ra), in_b = in_batch(rb);
+        float* oa_row = p.px_o + (in_a ? record(ra) : 0) * D + 2 * t4;
+        float* ob_row = p.px_o + (in_b ? record(rb) : 0) * D + 2 * t4;
 #pragma unroll
         for (int c0 = 0; c0 < D; c0 += 32) {
             uint32_t o[16];
@@ -410,24 +475,26 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int c = c0 + 8 * i + 2 * t4;
-                const float2 oa = good ? make_float2(__uint_as_float(o[4 * i]) * es, __uint_as_float(o[4 * i + 1]) * es) : make_float2(0.0f, 0.0f);
-                const float2 ob = good ? make_float2(__uint_as_float(o[4 * i + 2]) * es, __uint_as_float(o[4 * i + 3]) * es) : make_float2(0.0f, 0.0f);
-                if (in_a) *reinterpret_cast<float2*>(p.px_o + rec_a * D + c) = oa;
-                if (in_b) *reinterpret_cast<float2*>(p.px_o + rec_b * D + c) = ob;
+                const float2 oa = full_a ? make_float2(__uint_as_float(o[4 * i]) * es, __uint_as_float(o[4 * i + 1]) * es) : make_float2(0.0f, 0.0f);
+                const float2 ob = full_b ? make_float2(__uint_as_float(o[4 * i + 2]) * es, __uint_as_float(o[4 * i + 3]) * es) : make_float2(0.0f, 0.0f);
+                if (in_a) *reinterpret_cast<float2*>(oa_row + c0 + 8 * i) = oa;
+                if (in_b) *reinterpret_cast<float2*>(ob_row + c0 + 8 * i) = ob;
             }
         }
     } else if (warp < kPxMmaWarp) {
         fewer_registers<kPxDequantRegs>();
         // ================================================================ dequantisation of key tiles
         const int pl = (warp - kPxDequantWarp) >> 2;      // 0: K rows, 1: V rows
-        const int k = (threadIdx.x - kPfSoftmaxThreads) & 127;   // this thread's key of every tile
+        // This thread's key of every tile.  A V tile keeps its rows in the order the weights are laid out
+        // in, and a V thread takes the key of row i (its index in the group), so that eight neighbouring
+        // threads store eight neighbouring swizzled rows (by key they hit four of them twice).
+        const int i128 = (threadIdx.x - kPfSoftmaxThreads) & 127;
+        const int k = pl ? column_of_slot(i128) : i128;
         constexpr int NW = D / 8 + 1;                     // words of a row: codes, then the scale word
-        const float k0 = p.c * p.softmax_scale * kLog2e;  // raw score -> log2 logit, before 2^-e
+        float k0 = p.c * p.softmax_scale * kLog2e;        // raw score -> log2 logit, with 2^-e once it is known
         // word offset of this key's rows in their windows (the prefill's rule)
         const int row_off = ((k % kBlockSize) * H + h) & 3;
-        // a V tile keeps its rows in the order the weights are laid out in
-        const uint32_t trow = pl ? (uint32_t)slot_of_column(k) : (uint32_t)k;
+        const uint32_t trow = (uint32_t)i128;
         for (int j = 0; j < nkt; ++j) {
             const int kb = j % kPfPairs, st = j % kPfRawStages;
             bool ok = wait(&raw_full[pl * kPfRawStages + st], (uint32_t)(j / kPfRawStages) & 1u);
@@ -465,11 +532,16 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                     make_uint4(o[0], o[1], o[2], o[3]);
             }
             if (pl == 0) {
-                sk[(j % kPfKRing) * kPfKeys + k] = __uint_as_float(kw[Gm::KW] & 0xFFFFFFF0u) * k0;
+                if (j == 0) {   // the rows' prescale
+                    ok = wait(q_max, 0);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    k0 *= exp2i(-prescale_exponent(__uint_as_float(*reinterpret_cast<volatile uint32_t*>(qmax))));
+                }
+                sk[(j % kPfKRing) * kPfKeys + slot_of_column(k)] = __uint_as_float(kw[Gm::KW] & 0xFFFFFFF0u) * k0;
                 const uint32_t nodead = __ballot_sync(0xffffffffu, kw[Gm::KW] == 0u);
                 if (lane == 0) deadf[(j % kPfKRing) * 4 + (warp & 3)] = nodead;
             } else {
-                sv[kb * kPfKeys + k] = __uint_as_float(kw[Gm::KW] & 0xFFFFFFF0u);
+                sv[kb * kPfKeys + (int)trow] = __uint_as_float(kw[Gm::KW] & 0xFFFFFFF0u);
                 const uint32_t wmax = __reduce_max_sync(0xffffffffu, kw[Gm::KW]);   // positive floats order like their bits
                 if (lane == 0) eblkw[kb * 4 + (warp & 3)] = (wmax >> 23) & 0xFFu;
             }
@@ -482,126 +554,134 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             // ============================================================ loads of packed rows
             // As the prefill's loaders: 16-byte copies of each row's aligned window, keys past the prefix
             // or in a block outside the cache zero-filled (scale word 0: no key).
-            constexpr int C = Ly::kChunks;
-            constexpr int kCopies = kPfKeys * C / 32;
-            static_assert(kPfKeys * C % 32 == 0, "whole copies per lane");
+            // A pass moves kKeys whole windows (C lanes each; 30 of 32 lanes), so that a lane keeps its chunk
+            // and the offsets are a few integer operations: a precomputed table of them spilled in this
+            // warp's 64 registers and made a tile's copies 2 500 cycles.
+            constexpr int C = Ly::kChunks, kKeys = 32 / C, kPasses = (kPfKeys + kKeys - 1) / kKeys;
             const int pl = warp - kPxLoadWarp;
             const int32_t* table = p.px_blocks;
-            const int64_t tok_stride = (int64_t)H * Gm::RB, blk_stride = 2 * kBlockSize * tok_stride;
+            const int tok_stride = H * Gm::RB;
+            const int64_t blk_stride = 2 * kBlockSize * (int64_t)tok_stride;
             const uint8_t* base = p.cache + (int64_t)pl * kBlockSize * tok_stride;
-            uint32_t cp[kCopies];
-#pragma unroll
-            for (int t = 0; t < kCopies; ++t) {
-                const int i = lane + 32 * t, key = i / C, c = i - key * C;
-                const uint32_t row = (uint32_t)h * (uint32_t)Gm::RB + (uint32_t)(key % kBlockSize) * (uint32_t)tok_stride;
-                cp[t] = ((uint32_t)key << 24) | ((row & ~15u) + 16u * (uint32_t)c);
-            }
+            const int ck = lane / C, cc = lane - ck * C;   // this lane's key of a pass and its chunk
+            const bool mine = ck < kKeys;
+            // Block ids of four tiles at a time, lane l's those of tile (group) + l / 8, block l % 8 of it
+            // (-1: none), loaded a group ahead: one tile ahead, the load's latency bounded every tile (the
+            // K rows' wait was 2 100 of 3 600 cycles).
             const int nblocks = p.px_len / kBlockSize;
-            auto lookup = [&](int j) -> int {   // lane b < 8: the block of keys 16 b .. of tile kt0 + j (-1: none)
+            auto lookup = [&](int j) -> int {
                 const int i = (kt0 + j) * (kPfKeys / kBlockSize) + lane;
-                return lane < kPfKeys / kBlockSize && i < nblocks ? __ldg(table + i) : -1;
+                int blk = j + lane / 8 < nkt && i < nblocks ? __ldg(table + i) : -1;
+                return blk;
             };
-            int blk_next = nkt > 0 ? lookup(0) : -1;
+            int blk_next = lookup(0), blkv = -1;
             bool ok = true;
             for (int j = 0; j < nkt && ok; ++j) {
                 const int st = j % kPfRawStages;
+                if ((j & 3) == 0) {
+                    blkv = blk_next;
+                    blk_next = lookup(j + 4);
+                    if (blkv != -1 && (blkv < 0 || (int64_t)blkv >= p.num_blocks)) {
+                        if (pl == 0 && h == 0 && qt0 == 0) count_status(p.status, 1);
+                        blkv = -1;
+                    }
+                }
                 if (j >= kPfRawStages) ok = wait(&raw_free[pl * kPfRawStages + st], (uint32_t)(j / kPfRawStages - 1) & 1u);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                int blkv = blk_next;
-                if (j + 1 < nkt) blk_next = lookup(j + 1);
-                if (blkv != -1 && (blkv < 0 || (int64_t)blkv >= p.num_blocks)) {
-                    if (pl == 0 && h == 0 && qt0 == 0) count_status(p.status, 1);
-                    blkv = -1;
-                }
                 const uint32_t dst = smem_u32(smem + Ly::kRaw + (uint32_t)(st * 2 + pl) * Ly::kPlane);
 #pragma unroll
-                for (int t = 0; t < kCopies; ++t) {
-                    const int key = (int)(cp[t] >> 24);
-                    const int blk = __shfl_sync(0xffffffffu, blkv, key / kBlockSize);
+                for (int t = 0; t < kPasses; ++t) {
+                    const int key = t * kKeys + ck;
+                    const int blk = __shfl_sync(0xffffffffu, blkv, (j & 3) * 8 + ((key / kBlockSize) & 7));
                     const bool live = blk >= 0;
-                    const uint8_t* src = base + (int64_t)(live ? blk : 0) * blk_stride + (cp[t] & 0xFFFFFFu);
-                    cp_async16_zfill(dst + 16u * (uint32_t)(lane + 32 * t), src, live);
+                    const uint32_t row = (uint32_t)(h * Gm::RB + (key % kBlockSize) * tok_stride);
+                    const uint8_t* src = base + (int64_t)(live ? blk : 0) * blk_stride + ((row & ~15u) + 16u * (uint32_t)cc);
+                    if (mine && key < kPfKeys) cp_async16_zfill(dst + 16u * (uint32_t)(key * C + cc), src, live);
                 }
                 cp_async_arrive_noinc(&raw_full[pl * kPfRawStages + st]);
             }
             cp_async_wait_all();   // no copy outlives the CTA
-        } else if (warp == kPxMmaWarp && lane == 0) {
-            // ============================================================ the MMA issuer (as the prefill's)
+        } else if (warp == kPxMmaWarp) {
+            // ============================================================ the MMA issuer
+            // S of tile t (its K tile dequantised, its S buffer read by P.V of tile t - 2), then P.V of tile t - 1
+            // (its weights in tensor memory).  The whole warp runs the loop with uniform values and one elected
+            // lane issues: descriptors are a base per tile pair plus a constant, in uniform registers (formed
+            // by one lane alone, they cost 100 cycles per MMA against the 66 it takes).
             constexpr uint32_t idS = idesc_f16(kPfKeys, 0), idPV = idesc_f16(D, 1);
+            const bool leader = elect_one();
+            const uint64_t kd0 = smem_desc_sw128(smem_u32(ktile(0)), 16u, 1024u), kd1 = smem_desc_sw128(smem_u32(ktile(1)), 16u, 1024u);
+            const uint64_t vd0 = smem_desc_sw128(smem_u32(vtile(0)), kPfKeys * 128u, 1024u);
+            const uint64_t vd1 = smem_desc_sw128(smem_u32(vtile(1)), kPfKeys * 128u, 1024u);
             {
-                mbar_arrive_expect_tx(q_tma, Ly::kTile);
+                if (leader) {
+                    mbar_arrive_expect_tx(q_tma, Ly::kTile);
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                    tma_load_3d(ktile(1) + c * (kPfRows * 128), &qmap, 64 * c, h * G, qt0, q_tma);
-                if (wait(q_tma, 0) && wait(rot_in, 0)) {
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_3d(ktile(1) + c * (kPfRows * 128), &qmap, 64 * c, h * G, qt0, q_tma);
+                }
+                __syncwarp();
+                if (__all_sync(0xffffffffu, wait(q_tma, 0) && wait(rot_in, 0))) {
                     tc_fence_after();
                     constexpr uint32_t idR = std::is_same<QT, __nv_bfloat16>::value ? idesc_bf16(D, 0) : idesc_f16(D, 0);
-                    const uint32_t qa = smem_u32(ktile(1)), qb = smem_u32(vtile(1));
+                    const uint64_t rd = smem_desc_sw128(smem_u32(vtile(1)), 16u, 1024u);
+                    if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < KSTEPS; ++kk) {
-                        const uint64_t ad = smem_desc_sw128(qa + (uint32_t)(kk / 4) * (kPfRows * 128u) + (uint32_t)(kk % 4) * 32u, 16u, 1024u);
-                        const uint64_t bd = smem_desc_sw128(qb + (uint32_t)(kk / 4) * (uint32_t)(D * 128) + (uint32_t)(kk % 4) * 32u, 16u, 1024u);
-                        mma_ss(tmem + Tm::kS0, ad, bd, idR, kk > 0);
+                        for (int kk = 0; kk < KSTEPS; ++kk)
+                            mma_ss(tmem + Tm::kS0, kd1 + (((kk / 4) * (kPfRows * 128) + (kk % 4) * 32) >> 4),
+                                   rd + (((kk / 4) * (D * 128) + (kk % 4) * 32) >> 4), idR, kk > 0);
+                        mma_commit(rot_done);
                     }
-                    mma_commit(rot_done);
+                    __syncwarp();
                 }
             }
             auto issue_s = [&](int j) {
                 const uint32_t sd = tmem + ((j & 1) ? Tm::kS1 : Tm::kS0);
-                const uint32_t kbase = smem_u32(ktile(j % kPfPairs));
+                const uint64_t kd = (j & 1) ? kd1 : kd0;
+                if (leader) {
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                    for (int half = 0; half < 2; ++half) {
 #pragma unroll
-                    for (int kk = 0; kk < KSTEPS; ++kk) {
-                        const uint64_t bd = smem_desc_sw128(
-                            kbase + (uint32_t)(kk / 4) * (kPfKeys * 128u) + (uint32_t)(kk % 4) * 32u, 16u, 1024u);
-                        mma_ts(sd, tmem + (half ? Tm::kQl : Tm::kQh) + 8u * kk, bd, idS, half > 0 || kk > 0);
+                        for (int kk = 0; kk < KSTEPS; ++kk)
+                            mma_ts(sd, tmem + (half ? Tm::kQl : Tm::kQh) + 8u * kk,
+                                   kd + (((kk / 4) * (kPfKeys * 128) + (kk % 4) * 32) >> 4), idS, half > 0 || kk > 0);
                     }
+                    mma_commit(&s_full[j & 1]);
+                    mma_commit(&k_free[j % kPfPairs]);
                 }
-                mma_commit(&s_full[j & 1]);
-                mma_commit(&k_free[j % kPfPairs]);
+                __syncwarp();
             };
             auto issue_pv = [&](int t) {
                 const uint32_t pcol = tmem + ((t & 1) ? Tm::kS1 : Tm::kS0);
-                const uint32_t vb = smem_u32(vtile(t % kPfPairs));
+                const uint64_t vd = (t & 1) ? vd1 : vd0;
+                if (leader) {
 #pragma unroll
-                for (int kk = 0; kk < kPfKeys / 16; ++kk) {
-                    const uint32_t a = pcol + 8u * kk;   // P of keys 16 kk .. 16 kk + 15 (in contraction order)
-                    const uint64_t bd = smem_desc_sw128(vb + (uint32_t)kk * 16u * 128u, kPfKeys * 128u, 1024u);
-                    mma_ts(tmem + Tm::kO, a, bd, idPV, t > 0 || kk > 0);
+                    for (int kk = 0; kk < kPfKeys / 16; ++kk)   // P of keys 16 kk .. 16 kk + 15 (in contraction order)
+                        mma_ts(tmem + Tm::kO, pcol + 8u * kk, vd + ((kk * 16 * 128) >> 4), idPV, t > 0 || kk > 0);
+                    mma_commit(&pv_done[t & 1]);
+                    mma_commit(&v_free[t % kPfPairs]);
                 }
-                mma_commit(&pv_done[t & 1]);
-                mma_commit(&v_free[t % kPfPairs]);
+                __syncwarp();
             };
-            bool ok = nkt == 0 || wait(q_ready, 0);
-            int js = 0, jp = 0;
-            uint64_t t0 = global_timer_ns();
-            while (ok && jp < nkt) {
-                bool did = false;
-                if (js < nkt && js < jp + 2 && mbar_test_wait(&k_full[js % kPfKRing], (uint32_t)(js / kPfKRing) & 1u) &&
-                    (js < 2 || mbar_test_wait(&pv_done[js & 1], (uint32_t)((js - 2) >> 1) & 1u))) {
+            static_assert(kPfPairs == 2, "one descriptor per pair");
+            bool ok = __all_sync(0xffffffffu, nkt == 0 || wait(q_ready, 0));
+            for (int t = 0; t <= nkt && ok; ++t) {
+                if (t < nkt) {
+                    ok = wait(&k_full[t % kPfKRing], (uint32_t)(t / kPfKRing) & 1u) &&
+                         (t < 2 || wait(&pv_done[t & 1], (uint32_t)((t - 2) >> 1) & 1u));
+                    if (!__all_sync(0xffffffffu, ok)) break;
                     tc_fence_after();
-                    issue_s(js++);
-                    did = true;
+                    issue_s(t);
                 }
-                if (jp < js && mbar_test_wait(&p_full[jp & 1], (uint32_t)(jp >> 1) & 1u)) {
+                if (t > 0) {
+                    ok = wait(&p_full[(t - 1) & 1], (uint32_t)((t - 1) >> 1) & 1u);
+                    if (!__all_sync(0xffffffffu, ok)) break;
                     tc_fence_after();
-                    issue_pv(jp++);
-                    did = true;
-                }
-                if (did) {
-                    t0 = global_timer_ns();
-                } else {
-                    if (*abort_flag) {
-                        ok = false;
-                    } else if (global_timer_ns() - t0 > kWaitTimeoutNs) {
-                        if (atomicExch(const_cast<int*>(abort_flag), 1) == 0) count_status(p.status, 3);
-                        ok = false;
-                    }
+                    issue_pv(t - 1);
                 }
             }
             // every MMA issued has completed before the CTA tears tensor memory down
-            mma_commit(flush);
+            if (leader) mma_commit(flush);
+            __syncwarp();
             (void)mbar_wait(flush, 0);
         }
     }

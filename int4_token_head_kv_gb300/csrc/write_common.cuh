@@ -357,14 +357,6 @@ struct WriteSmem {
     static constexpr int kBytes = kBars + kWriteWarps * 2 * 8 + (int)sizeof(WriteSigns<D>);
 };
 
-
-__device__ __forceinline__ void bulk_store_s2g(void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)),
-                 "r"(bytes)
-                 : "memory");
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
 // Vector index -> (row of K/V, plane) with 32-bit arithmetic; shifts when H is a power of two.
 struct VecIndex {
     uint32_t H, hmask;

@@ -68,14 +68,14 @@ def test_shared_prefix(lib):
     f.restype = ctypes.c_int
     f.argtypes = [vp, ctypes.c_int, i64, i32, vp, i64, i32, i32, i32, vp, i32, vp, i32, vp, vp, i32, i32, i32, f32, vp,
                   i32, vp, ctypes.c_int, vp, szt, vp]
-    base = dict(q=FAKE, qd=1, nq=4, hq=32, cache=FAKE, nb=64, h=8, d=128, bs=16, pb=FAKE, pl=256, bt=FAKE, mb=20, sl=FAKE,
-                qsl=FAKE, ns=4, mql=1, msl=320, scale=0.088, signs=FAKE, seg=0, out=FAKE, od=2, ws=None, wsb=0, st=None)
+    base = dict(q=FAKE, qd=1, nq=4, hq=32, cache=FAKE, nb=64, h=8, d=128, bs=16, pb=FAKE, pl=4096, bt=FAKE, mb=260, sl=FAKE,
+                qsl=FAKE, ns=4, mql=1, msl=4160, scale=0.088, signs=FAKE, seg=0, out=FAKE, od=2, ws=None, wsb=0, st=None)
 
     def call(**kw):
         return f(*dict(base, **kw).values())
 
     assert call(mql=2) == 2 and call(h=3, hq=24) == 2 and call(d=80) == 2 and call(seg=24) == 2 and call(od=5) == 2
-    assert call(pl=-1) == 1 and call(pb=None) == 1 and call(pl=16 * 21) == 1 and call(q=None) == 1 and call(signs=None) == 1
+    assert call(pl=-1) == 1 and call(pb=None) == 1 and call(pl=16 * 261) == 1 and call(q=None) == 1 and call(signs=None) == 1
     assert call(out=FAKE + 4) == 3
     assert call() == 4                                        # no workspace
     assert call(ws=FAKE, wsb=1000) == 4
@@ -86,12 +86,14 @@ def test_shared_prefix(lib):
     plain = lib.kv_int4_attention_workspace_bytes
     plain.restype = szt
     plain.argtypes = [i32] * 6
-    need = w(4, 32, 8, 128, 4, 256, 320, 0)
-    suffix = plain(32, 8, 128, 4, 320 - 256, 0)
+    need = w(4, 32, 8, 128, 4, 4096, 4160, 0)
+    suffix = plain(32, 8, 128, 4, 4160 - 4096, 0)
     # behind the suffix's workspace: per split and query row 128 fp32 outputs and a (max, sum) pair
     rows = need - (suffix + 255) // 256 * 256
     assert rows % (4 * 32 * (128 * 4 + 8)) == 0 and rows > 0
     assert call(ws=FAKE, wsb=need - 1) == 4
     assert w(4, 32, 8, 128, 4, 0, 320, 0) == plain(32, 8, 128, 4, 320, 0)    # nothing shared: the plain call's
-    assert w(1, 32, 8, 128, 1, 256, 320, 0) == plain(32, 8, 128, 1, 320, 0)  # one sequence
+    assert w(1, 32, 8, 128, 1, 4096, 4160, 0) == plain(32, 8, 128, 1, 4160, 0)  # one sequence
+    assert w(4, 32, 8, 128, 4, 4080, 4160, 0) == plain(32, 8, 128, 4, 4160, 0)  # below 16 384 tokens in all
+    assert w(2, 8, 2, 128, 2, 4096, 4160, 0) > plain(8, 2, 128, 2, 64, 0)       # 8 192 with few kv heads
     assert w(0, 32, 8, 128, 4, 256, 320, 0) == 0 and w(4, 30, 8, 128, 4, 256, 320, 0) == 0 and w(4, 32, 8, 128, 0, 256, 320, 0) == 0

@@ -1,5 +1,6 @@
-"""GPU parity of the shared-prefix attention: against the oracle (which knows nothing of sharing) on small
-batches, and against the plain decode call on larger ones."""
+"""GPU parity of the shared-prefix attention: against the oracle (which knows nothing of sharing), and on
+larger batches against the plain decode call.  Batches of num_seqs x prefix >= 16 384 tokens take the
+prefix kernel, smaller ones the plain walk; each case says which it means."""
 import numpy as np
 import pytest
 import torch
@@ -67,80 +68,123 @@ class Batch:
         return _kv().kv_int4_paged_attention(self.q, self.cache, t, l, q, self.scale, self.gsigns, max_query_len=1,
                                              max_seq_len=self.max_len, out_dtype=out_dtype, **kw)
 
-    def oracle(self):
+    def is_shared(self):
+        """Whether the call takes the prefix kernel: its workspace holds more than the plain walk's."""
+        S, Hq, d = len(self.lens), self.q.shape[1], self.q.shape[2]
+        H = self.cache.shape[3]
+        kv = _kv()
+        return kv.kv_int4_shared_prefix_workspace_bytes(self.q.shape[0], Hq, H, d, S, self.prefix, self.max_len) != \
+            kv.kv_int4_attention_workspace_bytes(Hq, H, d, S, self.max_len)
+
+    def oracle(self, seqs=None):
         return oracle.paged_attention(self.q, self.cache.cpu().numpy(), self.tables, self.lens, self.qsl, self.scale,
-                                      self.signs)
+                                      self.signs, seqs=seqs)
 
 
-def _check(b, **kw):
+def _check(b, shared=True, seqs=None, **kw):
     from gpu_helpers import assert_attention_close, status
+    assert b.is_shared() == shared
     got = b.shared(**kw)
-    assert_attention_close(got, b.oracle(), "shared prefix")
+    assert_attention_close(got, b.oracle(seqs), "shared prefix")
     assert not any(status().values())
     return got
+
+
+def _lens(prefix, S, most, seed):
+    return list(prefix + np.random.default_rng(seed).integers(1, most + 1, S))
 
 
 @pytest.mark.parametrize("Hq, H", [(1, 1), (4, 1), (8, 8), (8, 4), (8, 2), (16, 2), (64, 8)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_head_layouts(Hq, H, d):
-    _check(Batch(256, [256 + n for n in (1, 40, 17)], Hq, H, d, seed=Hq + d))
+    _check(Batch(1024, _lens(1024, 16, 40, Hq), Hq, H, d, seed=Hq + d), seqs=range(0, 16, 3))
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float16, torch.float32])
 def test_types(dtype, out_dtype):
-    _check(Batch(400, [401, 450, 520], 8, 2, 128, dtype=dtype, seed=2), out_dtype=out_dtype)
+    _check(Batch(1000, _lens(1000, 17, 60, 1), 8, 2, 128, dtype=dtype, seed=2), out_dtype=out_dtype, seqs=range(0, 17, 4))
 
 
-@pytest.mark.parametrize("prefix", [16, 112, 128, 129, 144, 205, 256, 391, 640, 1025])
-def test_prefix_lengths(prefix):
-    _check(Batch(prefix, [prefix + 1, prefix + 30, prefix + 100, prefix + 16], 8, 2, 64, seed=prefix))
+@pytest.mark.parametrize("prefix, S", [(128, 130), (129, 128), (144, 120), (205, 90), (256, 64), (391, 45), (640, 27),
+                                       (1025, 16), (5000, 4), (4096, 2), (8200, 3)])
+def test_prefix_lengths(prefix, S):
+    _check(Batch(prefix, _lens(prefix, S, 50, S), 8, 2, 64, seed=prefix), seqs=range(0, S, max(1, S // 6)))
 
 
-@pytest.mark.parametrize("S", [1, 2, 31, 32, 33, 70])
-def test_batch_sizes(S):
-    r = np.random.default_rng(S)
-    _check(Batch(160, list(160 + r.integers(1, 40, S)), 4, 1, 64, seed=S))
+@pytest.mark.parametrize("prefix, S", [(0, 3), (15, 2), (16, 5), (256, 3), (1025, 15), (20000, 1), (4096, 1)])
+def test_small_ones_take_the_plain_walk(prefix, S):
+    b = Batch(prefix, _lens(prefix, S, 50, S), 8, 2, 64, seed=prefix)
+    got = _check(b, shared=False)
+    assert torch.equal(got, b.plain())
+
+
+@pytest.mark.parametrize("Hq, H", [(1, 1), (2, 1), (4, 1), (8, 1)])
+def test_batch_sizes_around_a_row_tile(Hq, H):
+    tile = 128 // (Hq // H)
+    for S in (tile - 1, tile, tile + 1, 2 * tile + 3):
+        P = -(-16384 // S) + 20
+        _check(Batch(P, _lens(P, S, 30, S), Hq, H, 64, seed=S), seqs=sorted({0, 1, tile - 2, min(tile, S - 1), S - 1}))
 
 
 def test_lengths_inside_and_at_the_prefix():
     # padding rows, rows that end inside the prefix, at its end, and behind it
-    got = _check(Batch(300, [0, 1, 128, 129, 200, 288, 300, 301, 330, 0], 8, 2, 128, seed=3))
-    assert not got[0].any() and not got[9].any()
+    lens = [0, 1, 128, 129, 1000, 2031, 2032, 2040, 2041, 2100, 0, 16]
+    got = _check(Batch(2040, lens, 8, 2, 128, seed=3))
+    assert not got[0].any() and not got[10].any()
 
 
 def test_every_sequence_ends_inside_the_prefix():
-    _check(Batch(512, [512, 512, 100, 1], 8, 4, 128, seed=4))
+    _check(Batch(4500, [4496, 4496, 100, 1, 0], 8, 4, 128, seed=4))
+
+
+def test_a_batch_of_padding_rows():
+    b = Batch(8192, [0, 8192, 0], 8, 2, 64, seed=14)
+    b.lens[1] = 0
+    assert b.is_shared() and not b.shared().any()
 
 
 def test_sequences_without_a_query_and_rows_behind_the_last():
-    b = Batch(256, [260, 300, 270, 256, 290], 8, 2, 64, seed=5, query_lens=[0, 1, 0, 1, 1], extra_q=3)
+    from gpu_helpers import assert_attention_close
+    r = np.random.default_rng(5)
+    S, P = 70, 256
+    qlens = (r.random(S) < 0.7).astype(np.int32)
+    qlens[[0, 1, 2, S - 1]] = [0, 0, 1, 1]
+    b = Batch(P, _lens(P, S, 40, 5), 8, 2, 64, seed=5, query_lens=qlens, extra_q=3)
+    n = int(qlens.sum())
+    assert b.is_shared()
     out = torch.full(b.q.shape, 5.0, device="cuda")
     got = b.shared(out=out)
-    ref = b.oracle()
-    from gpu_helpers import assert_attention_close
-    assert_attention_close(got[:3], ref[:3])
-    assert bool((out[3:] == 5.0).all())
+    assert_attention_close(got[:n], b.oracle()[:n])
+    assert bool((out[n:] == 5.0).all())
 
 
 def test_bad_prefix_block_is_counted_and_skipped():
     from gpu_helpers import assert_attention_close, status
-    b = Batch(256, [257, 280, 260], 8, 2, 64, seed=6)
-    keep = b.prefix_blocks.copy()
+    b = Batch(2048, [2049, 2080, 2060, 2055, 2048, 2100, 2070, 2050], 8, 2, 64, seed=6)
+    assert b.is_shared()
     b.prefix_blocks[3], b.prefix_blocks[9] = -7, 10 ** 6
     got = b.shared()
     assert status()["block_out_of_range"] > 0
     # the tokens of those blocks are no keys: the oracle on the sequences without them
-    b.prefix_blocks = keep
-    drop = np.ones(256 // 16, bool)
+    drop = np.ones(2048 // 16, bool)
     drop[[3, 9]] = False
-    cols = np.concatenate([drop, np.ones(b.tables.shape[1] - 16, bool)])
+    cols = np.concatenate([drop, np.ones(b.tables.shape[1] - 128, bool)])
     ref = oracle.paged_attention(b.q, b.cache.cpu().numpy(), b.tables[:, cols], b.lens - 32, b.qsl, b.scale, b.signs)
     assert_attention_close(got, ref)
 
 
+def test_queries_of_very_different_magnitudes():
+    """One prescale serves a CTA's 128 rows: rows 2^12 apart, and rows of zeros."""
+    b = Batch(2048, _lens(2048, 12, 20, 3), 8, 2, 128, seed=15, outliers=False)
+    b.q *= (2.0 ** torch.tensor([0, -12, 0, -6, 0, 2, -12, -3, 0, 0, 1, -9], device="cuda")).to(b.q.dtype)[:, None, None]
+    b.q[8] = 0
+    _check(b)
+
+
 def test_heavy_tails_and_large_scales():
-    b = Batch(384, [390, 500, 385], 16, 2, 128, seed=7)
+    b = Batch(2000, _lens(2000, 9, 90, 7), 16, 2, 128, seed=7)
+    assert b.is_shared()
     kv = _kv()
     n = b.cache.shape[0] * 16
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -155,7 +199,8 @@ def test_heavy_tails_and_large_scales():
     assert np.all(np.abs(got - ref) <= 1e-2 * np.abs(ref) + 1e-2 * big + 2e-3)
 
 
-@pytest.mark.parametrize("S, prefix, Hq, H, d", [(64, 8192, 32, 8, 128), (100, 3000, 64, 8, 128), (40, 20000, 8, 1, 64)])
+@pytest.mark.parametrize("S, prefix, Hq, H, d", [(64, 8192, 32, 8, 128), (100, 3000, 64, 8, 128), (40, 20000, 8, 1, 64),
+                                                 (300, 700, 16, 4, 64)])
 def test_larger_batches_match_the_plain_call(S, prefix, Hq, H, d):
     from gpu_helpers import ATOL, RTOL, status
     r = np.random.default_rng(S)
@@ -172,6 +217,7 @@ def test_same_bits_again_and_captured():
     first = b.shared(out_dtype=torch.bfloat16)
     t, l, q = b._args()
     pb = torch.from_numpy(b.prefix_blocks).cuda()
+    assert b.is_shared()
     need = _kv().kv_int4_shared_prefix_workspace_bytes(20, 32, 8, 128, 20, 1000, b.max_len)
     ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     out = torch.empty_like(b.q)
@@ -191,10 +237,10 @@ def test_same_bits_again_and_captured():
 
 def test_python_checks():
     kv = _kv()
-    b = Batch(256, [260, 270], 8, 2, 64, seed=9)
+    b = Batch(16384, [16390, 16384], 8, 2, 64, seed=9)
     with pytest.raises(ValueError):
         b.shared(workspace=torch.empty(1 << 20, dtype=torch.uint8))
-    keep, b.prefix_blocks = b.prefix_blocks, b.prefix_blocks[:15]
+    keep, b.prefix_blocks = b.prefix_blocks, b.prefix_blocks[:1023]
     with pytest.raises(ValueError):
         b.shared()
     b.prefix_blocks = keep
@@ -209,8 +255,9 @@ def test_a_serving_step_as_it_runs():
     from gpu_helpers import assert_attention_close
     from oracle import rope
     kv = _kv()
-    S, P, Hq, H, d, steps = 24, 512, 32, 8, 128, 5
+    S, P, Hq, H, d, steps = 24, 720, 32, 8, 128, 5
     b = Batch(P, [P + 1 + 3 * i + steps for i in range(S)], Hq, H, d, seed=10)
+    assert b.is_shared()
     r = np.random.default_rng(0)
     tab = rope.table(1024, d)
     start = b.lens - steps
@@ -236,7 +283,7 @@ def test_a_serving_step_as_it_runs():
     cache = b.cache.cpu().numpy()   # later steps only added rows behind the earlier ones' lengths
     for i in (0, steps - 1):
         qr = torch.from_numpy(rope.rotate(xs[i][:, :Hq], poss[i], tab)).bfloat16()
-        ref = oracle.paged_attention(qr, cache, b.tables, lens[i], b.qsl, b.scale, b.signs)
+        ref = oracle.paged_attention(qr, cache, b.tables, lens[i], b.qsl, b.scale, b.signs, seqs=range(0, S, 5))
         assert_attention_close(outs[i], ref, f"step {i}")
         want = oracle.decode_rows(cache[slots[i] // 16, 0, slots[i] % 16].reshape(S * H, -1), b.signs).reshape(S, H, d)
         assert np.allclose(rows[i][0].cpu().numpy(), want, rtol=1e-6, atol=1e-9)
