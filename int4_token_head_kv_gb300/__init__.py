@@ -231,61 +231,105 @@ def kv_int2_write(key: torch.Tensor, value: torch.Tensor, slot_mapping: torch.Te
     _rotated_write("kv_int2_write", kv_int2_row_bytes, key, value, slot_mapping, rht_signs, kv_cache, stream)
 
 
-def _token_rows(t: torch.Tensor, name: str, dtypes) -> torch.Tensor:
-    """A CUDA tensor [tokens, heads, head_size] whose tokens' rows are contiguous, any stride between them."""
+# The serving calls below run once per layer and step, where a Python call of 25 us would be most of a small
+# step: they ask for the stream by its raw handle, enter a device only when it is not the current one, and
+# size rows without a call into the library (the framework's own calls above cost what they did).
+try:
+    _raw_stream = torch._C._cuda_getCurrentRawStream   # what torch.cuda.current_stream(device).cuda_stream holds
+except AttributeError:
+    def _raw_stream(device: int) -> int:
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+def _call(fn: str, tensors, stream, *args) -> None:
+    """Call the library's ``fn`` with ``args`` and the stream on the device that all ``tensors`` (None entries
+    skipped) are on."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            i = t.get_device()
+            if i != dev:
+                if dev >= 0:
+                    _one_device(*tensors)   # raises
+                dev = i
+    if stream is None:
+        stream = _raw_stream(dev)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    f = getattr(_lib or load(), fn)
+    if dev == torch.cuda.current_device():
+        st = f(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, stream)
+    if st != 0:
+        _check(fn, st)
+
+
+def _token_rows(t: torch.Tensor, name: str, dtypes):
+    """Shape and token stride of a CUDA tensor [tokens, heads, head_size] whose tokens' rows are contiguous,
+    with any stride between them."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in dtypes:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
         raise ValueError(f"{name} must be [num_tokens, num_heads, head_size] with each token's heads contiguous")
-    return t
+    return shape, stride[0]
 
 
-def _rope_write(fn, row_bytes, query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache, query_out,
+_HALF_TYPES = (torch.float16, torch.bfloat16)
+_I64, _F32, _U8, _I32 = (torch.int64,), (torch.float32,), (torch.uint8,), (torch.int32,)
+
+
+def _rope_write(fn, bits, query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache, query_out,
                 interleaved, stream):
-    _token_rows(key, "key", (torch.float16, torch.bfloat16))
-    _token_rows(value, "value", (key.dtype,))
-    _cuda(positions, "positions", (torch.int64,))
-    _cuda(cos_sin, "cos_sin", (torch.float32,))
-    _cuda(slot_mapping, "slot_mapping", (torch.int64,))
-    _cuda(kv_cache, "kv_cache", (torch.uint8,))
-    if value.shape != key.shape:
+    kshape, kst = _token_rows(key, "key", _HALF_TYPES)
+    dtype = key.dtype
+    vshape, vst = _token_rows(value, "value", (dtype,))
+    _cuda(positions, "positions", _I64)
+    _cuda(cos_sin, "cos_sin", _F32)
+    _cuda(slot_mapping, "slot_mapping", _I64)
+    _cuda(kv_cache, "kv_cache", _U8)
+    if vshape != kshape:
         raise ValueError("key and value must both be [num_tokens, num_kv_heads, head_size]")
-    T, H, d = key.shape
-    if rht_signs is not None:
-        _cuda(rht_signs, "rht_signs", (torch.float32,))
+    T, H, d = kshape
+    signs = ()
+    if bits != 8:
+        _cuda(rht_signs, "rht_signs", _F32)
         if rht_signs.shape != (d,):
             raise ValueError("rht_signs must be [head_size]")
+        signs = (rht_signs.data_ptr(),)
     if slot_mapping.shape != (T,) or positions.shape != (T,):
         raise ValueError("positions and slot_mapping must be [num_tokens]")
-    if cos_sin.dim() != 2:
+    table = cos_sin.shape
+    if len(table) != 2:
         raise ValueError("cos_sin must be [max_position, rot_dim]")
-    if kv_cache.dim() != 5 or kv_cache.shape[1] != 2 or kv_cache.shape[3] != H or kv_cache.shape[4] != row_bytes(d):
-        raise ValueError(f"kv_cache must be (NB, 2, bs, {H}, {row_bytes(d)})")
-    Hq = 0
+    cshape, rb = kv_cache.shape, d * bits // 8 + 4
+    if len(cshape) != 5 or cshape[1] != 2 or cshape[3] != H or cshape[4] != rb:
+        raise ValueError(f"kv_cache must be (NB, 2, bs, {H}, {rb})")
+    Hq = qst = qost = 0
+    qptr = qoptr = None
     if query is not None:
-        _token_rows(query, "query", (key.dtype,))
-        if query.shape[0] != T or query.shape[2] != d:
+        qshape, qst = _token_rows(query, "query", (dtype,))
+        if qshape[0] != T or qshape[2] != d:
             raise ValueError("query must be [num_tokens, num_q_heads, head_size]")
-        Hq = query.shape[1]
+        Hq = qshape[1]
         if query_out is None:
-            query_out = torch.empty((T, Hq, d), dtype=query.dtype, device=query.device)
-        _token_rows(query_out, "query_out", (key.dtype,))
-        if query_out.shape != query.shape:
-            raise ValueError("query_out must have the query's shape")
+            query_out = torch.empty(qshape, dtype=dtype, device=query.device)
+            qost = Hq * d
+        else:
+            oshape, qost = _token_rows(query_out, "query_out", (dtype,))
+            if oshape != qshape:
+                raise ValueError("query_out must have the query's shape")
+        qptr, qoptr = query.data_ptr(), query_out.data_ptr()
     elif query_out is not None:
         raise ValueError("query_out needs a query")
-    with torch.cuda.device(_one_device(query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache,
-                                       query_out)):
-        signs = () if rht_signs is None else (rht_signs.data_ptr(),)
-        st = getattr(load(), fn)(query.data_ptr() if Hq else None, query.stride(0) if Hq else 0, Hq, key.data_ptr(),
-                                 key.stride(0), value.data_ptr(), value.stride(0), _DTYPES[key.dtype], T, H, d,
-                                 positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1],
-                                 int(bool(interleaved)), slot_mapping.data_ptr(), *signs,
-                                 query_out.data_ptr() if Hq else None, query_out.stride(0) if Hq else 0,
-                                 kv_cache.data_ptr(), kv_cache.shape[0], kv_cache.shape[2], _stream(stream))
-    _check(fn, st)
+    _call(fn, (query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache, query_out), stream,
+          qptr, qst, Hq, key.data_ptr(), kst, value.data_ptr(), vst, _DTYPES[dtype], T, H, d, positions.data_ptr(),
+          cos_sin.data_ptr(), table[0], table[1], 1 if interleaved else 0, slot_mapping.data_ptr(), *signs, qoptr, qost,
+          kv_cache.data_ptr(), cshape[0], cshape[2])
     return query_out
 
 
@@ -299,9 +343,7 @@ def kv_int4_rope_write(query, key: torch.Tensor, value: torch.Tensor, positions:
     (``query_out``, which may be ``query`` itself).  Query, key, value and query_out may have any stride
     between tokens, as the slices of a fused projection do.  A token whose position is outside the table
     is skipped: its ``query_out`` row is left as it was."""
-    if rht_signs is None:
-        raise ValueError("rht_signs must be a CUDA tensor")
-    return _rope_write("kv_int4_rope_write", kv_int4_row_bytes, query, key, value, positions, cos_sin, slot_mapping,
+    return _rope_write("kv_int4_rope_write", 4, query, key, value, positions, cos_sin, slot_mapping,
                        rht_signs, kv_cache, query_out, interleaved, stream)
 
 
@@ -309,7 +351,7 @@ def kv_int8_rope_write(query, key: torch.Tensor, value: torch.Tensor, positions:
                        slot_mapping: torch.Tensor, kv_cache: torch.Tensor, query_out=None, interleaved: bool = False,
                        stream=None):
     """kv_int4_rope_write into the INT8 comparator's cache (no signs)."""
-    return _rope_write("kv_int8_rope_write", kv_int8_row_bytes, query, key, value, positions, cos_sin, slot_mapping,
+    return _rope_write("kv_int8_rope_write", 8, query, key, value, positions, cos_sin, slot_mapping,
                        None, kv_cache, query_out, interleaved, stream)
 
 
@@ -317,39 +359,41 @@ def kv_int2_rope_write(query, key: torch.Tensor, value: torch.Tensor, positions:
                        slot_mapping: torch.Tensor, rht_signs: torch.Tensor, kv_cache: torch.Tensor, query_out=None,
                        interleaved: bool = False, stream=None):
     """kv_int4_rope_write into the INT2 Lloyd-Max cache."""
-    if rht_signs is None:
-        raise ValueError("rht_signs must be a CUDA tensor")
-    return _rope_write("kv_int2_rope_write", kv_int2_row_bytes, query, key, value, positions, cos_sin, slot_mapping,
+    return _rope_write("kv_int2_rope_write", 2, query, key, value, positions, cos_sin, slot_mapping,
                        rht_signs, kv_cache, query_out, interleaved, stream)
 
 
-def _read(fn, row_bytes, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, stream):
-    _cuda(kv_cache, "kv_cache", (torch.uint8,))
-    _cuda(slot_mapping, "slot_mapping", (torch.int64,))
-    if slot_mapping.dim() != 1:
+def _read(fn, bits, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, stream):
+    _cuda(kv_cache, "kv_cache", _U8)
+    _cuda(slot_mapping, "slot_mapping", _I64)
+    sshape, cshape = slot_mapping.shape, kv_cache.shape
+    if len(sshape) != 1:
         raise ValueError("slot_mapping must be [num_tokens]")
-    sizes = {row_bytes(d): d for d in (64, 128)}
-    if kv_cache.dim() != 5 or kv_cache.shape[1] != 2 or kv_cache.shape[4] not in sizes:
-        raise ValueError(f"kv_cache must be (NB, 2, bs, H, row bytes) with rows of {sorted(sizes)} bytes")
-    T, H, d = slot_mapping.shape[0], kv_cache.shape[3], sizes[kv_cache.shape[4]]
-    if rht_signs is not None:
-        _cuda(rht_signs, "rht_signs", (torch.float32,))
+    d = (cshape[-1] - 4) * 8 // bits if len(cshape) == 5 and cshape[1] == 2 else 0
+    if d not in (64, 128) or d * bits // 8 + 4 != cshape[4]:
+        raise ValueError(f"kv_cache must be (NB, 2, bs, H, row bytes) with rows of {8 * bits + 4} or {16 * bits + 4} bytes")
+    T, H = sshape[0], cshape[3]
+    signs = ()
+    if bits != 8:
+        _cuda(rht_signs, "rht_signs", _F32)
         if rht_signs.shape != (d,):
             raise ValueError("rht_signs must be [head_size]")
+        signs = (rht_signs.data_ptr(),)
+    shape = (T, H, d)
     if key_out is None:
-        key_out = torch.empty((T, H, d), dtype=dtype, device=kv_cache.device)
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype {dtype}, expected one of {tuple(_DTYPES)}")
+        key_out = torch.empty(shape, dtype=dtype, device=kv_cache.device)
+    else:
+        _cuda(key_out, "key_out", tuple(_DTYPES))
     if value_out is None:
-        value_out = torch.empty((T, H, d), dtype=key_out.dtype, device=kv_cache.device)
-    _cuda(key_out, "key_out", tuple(_DTYPES))
-    _cuda(value_out, "value_out", (key_out.dtype,))
-    if key_out.shape != (T, H, d) or value_out.shape != (T, H, d):
+        value_out = torch.empty(shape, dtype=key_out.dtype, device=kv_cache.device)
+    else:
+        _cuda(value_out, "value_out", (key_out.dtype,))
+    if key_out.shape != shape or value_out.shape != shape:
         raise ValueError(f"key_out and value_out must be [num_tokens, {H}, {d}]")
-    with torch.cuda.device(_one_device(kv_cache, slot_mapping, rht_signs, key_out, value_out)):
-        signs = () if rht_signs is None else (rht_signs.data_ptr(),)
-        st = getattr(load(), fn)(kv_cache.data_ptr(), kv_cache.shape[0], kv_cache.shape[2], H, d,
-                                 slot_mapping.data_ptr(), T, *signs, key_out.data_ptr(), value_out.data_ptr(),
-                                 _DTYPES[key_out.dtype], _stream(stream))
-    _check(fn, st)
+    _call(fn, (kv_cache, slot_mapping, rht_signs, key_out, value_out), stream, kv_cache.data_ptr(), cshape[0], cshape[2],
+          H, d, slot_mapping.data_ptr(), T, *signs, key_out.data_ptr(), value_out.data_ptr(), _DTYPES[key_out.dtype])
     return key_out, value_out
 
 
@@ -357,23 +401,19 @@ def kv_int4_read(kv_cache: torch.Tensor, slot_mapping: torch.Tensor, rht_signs: 
                  key_out=None, value_out=None, stream=None):
     """The keys and values [T, H, d] (``dtype``: fp16, bf16 or fp32, or that of ``key_out``) that the cached
     rows at ``slot_mapping`` stand for; negative slots give rows of zeros."""
-    if rht_signs is None:
-        raise ValueError("rht_signs must be a CUDA tensor")
-    return _read("kv_int4_read", kv_int4_row_bytes, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, stream)
+    return _read("kv_int4_read", 4, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, stream)
 
 
 def kv_int8_read(kv_cache: torch.Tensor, slot_mapping: torch.Tensor, dtype=torch.bfloat16, key_out=None, value_out=None,
                  stream=None):
     """kv_int4_read for the INT8 comparator's cache (no signs)."""
-    return _read("kv_int8_read", kv_int8_row_bytes, kv_cache, slot_mapping, None, dtype, key_out, value_out, stream)
+    return _read("kv_int8_read", 8, kv_cache, slot_mapping, None, dtype, key_out, value_out, stream)
 
 
 def kv_int2_read(kv_cache: torch.Tensor, slot_mapping: torch.Tensor, rht_signs: torch.Tensor, dtype=torch.bfloat16,
                  key_out=None, value_out=None, stream=None):
     """kv_int4_read for the INT2 Lloyd-Max cache."""
-    if rht_signs is None:
-        raise ValueError("rht_signs must be a CUDA tensor")
-    return _read("kv_int2_read", kv_int2_row_bytes, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, stream)
+    return _read("kv_int2_read", 2, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, stream)
 
 
 def kv_int4_attention_segment_len(num_seqs: int, max_seq_len: int, segment_len: int = 0) -> int:
@@ -587,41 +627,42 @@ def kv_int4_shared_prefix_attention(query: torch.Tensor, kv_cache: torch.Tensor,
     """kv_int4_paged_attention of a decode batch (one query token per sequence) whose first ``prefix_len``
     cached tokens are the same: their whole blocks are ``prefix_blocks`` (int32 [prefix_len // 16]), read once
     for the batch; the other arguments as there, ``block_tables`` and ``seq_lens`` counting the prefix."""
-    _cuda(query, "query", (torch.float16, torch.bfloat16))
-    _cuda(kv_cache, "kv_cache", (torch.uint8,))
-    _cuda(prefix_blocks, "prefix_blocks", (torch.int32,))
-    _cuda(block_tables, "block_tables", (torch.int32,))
-    _cuda(seq_lens, "seq_lens", (torch.int32,))
-    _cuda(query_start_loc, "query_start_loc", (torch.int32,))
-    _cuda(rht_signs, "rht_signs", (torch.float32,))
-    Nq, Hq, d = query.shape
-    NB, two, bs, H, rb = kv_cache.shape
+    _cuda(query, "query", _HALF_TYPES)
+    _cuda(kv_cache, "kv_cache", _U8)
+    _cuda(prefix_blocks, "prefix_blocks", _I32)
+    _cuda(block_tables, "block_tables", _I32)
+    _cuda(seq_lens, "seq_lens", _I32)
+    _cuda(query_start_loc, "query_start_loc", _I32)
+    _cuda(rht_signs, "rht_signs", _F32)
+    qshape, cshape, tshape = query.shape, kv_cache.shape, block_tables.shape
+    if len(qshape) != 3 or len(cshape) != 5 or seq_lens.dim() != 1:
+        raise ValueError("query must be [num_q_tokens, num_q_heads, head_size], kv_cache 5-D and seq_lens [num_seqs]")
+    Nq, Hq, d = qshape
+    NB, two, bs, H, rb = cshape
     S = seq_lens.shape[0]
-    if two != 2 or rb != kv_int4_row_bytes(d) or rht_signs.shape != (d,):
+    if two != 2 or rb != d // 2 + 4 or rht_signs.shape != (d,):
         raise ValueError("kv_cache / rht_signs do not match the query's head size")
-    if query_start_loc.shape != (S + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
+    if query_start_loc.shape != (S + 1,) or len(tshape) != 2 or tshape[0] != S:
         raise ValueError("block_tables must be [num_seqs, max_blocks] and query_start_loc [num_seqs + 1]")
     if prefix_blocks.dim() != 1 or prefix_blocks.shape[0] < prefix_len // bs:
         raise ValueError("prefix_blocks must hold the prefix's prefix_len // block_size block ids")
     if out is None:
-        out = torch.empty((Nq, Hq, d), dtype=out_dtype or query.dtype, device=query.device)
+        out = torch.empty(qshape, dtype=out_dtype or query.dtype, device=query.device)
     _cuda(out, "out", tuple(_DTYPES))
-    if out.shape != query.shape:
+    if out.shape != qshape:
         raise ValueError("out must have the query's shape")
-    need = kv_int4_shared_prefix_workspace_bytes(Nq, Hq, H, d, S, prefix_len, max_seq_len, segment_len)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+    if workspace is None:
+        need = (_lib or load()).kv_int4_shared_prefix_workspace_bytes(Nq, Hq, H, d, S, prefix_len, max_seq_len, segment_len)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    with torch.cuda.device(_one_device(query, kv_cache, prefix_blocks, block_tables, seq_lens, query_start_loc,
-                                       rht_signs, out, workspace)):
-        st = load().kv_int4_shared_prefix_attention(query.data_ptr(), _DTYPES[query.dtype], Nq, Hq, kv_cache.data_ptr(),
-                                                  NB, H, d, bs, prefix_blocks.data_ptr(), prefix_len,
-                                                  block_tables.data_ptr(), block_tables.shape[1], seq_lens.data_ptr(),
-                                                  query_start_loc.data_ptr(), S, 1, max_seq_len, float(softmax_scale),
-                                                  rht_signs.data_ptr(), segment_len, out.data_ptr(), _DTYPES[out.dtype],
-                                                  ws_ptr, ws_bytes, _stream(stream))
-    _check("kv_int4_shared_prefix_attention", st)
+    _call("kv_int4_shared_prefix_attention",
+          (query, kv_cache, prefix_blocks, block_tables, seq_lens, query_start_loc, rht_signs, out, workspace), stream,
+          query.data_ptr(), _DTYPES[query.dtype], Nq, Hq, kv_cache.data_ptr(), NB, H, d, bs, prefix_blocks.data_ptr(),
+          prefix_len, block_tables.data_ptr(), tshape[1], seq_lens.data_ptr(), query_start_loc.data_ptr(), S, 1,
+          max_seq_len, float(softmax_scale), rht_signs.data_ptr(), segment_len, out.data_ptr(), _DTYPES[out.dtype],
+          ws_ptr, ws_bytes)
     return out
 
 

@@ -9,9 +9,12 @@
 // staged and leave as one bulk store per row.
 //
 // INT4 and INT2: a lane pair per vector, thread t with the outputs of the stride-1 butterflies of
-// parity t, as the writes split it.  An INT4 row's butterflies run on the integers code - zp, which
-// stay within +-15 * 128: exact in fp16, two to a register, in any order of the strides; the one
-// rounding is the product with fp32(c s').  INT2 centroids are not integers: fp32.
+// parity t, as the writes split it.  An INT4 row's butterflies run on the integers code - zp, whose sums
+// stay within +-15 * 128: exact in fp16, two to a register, in any order of the strides; the one rounding
+// before the output's is the product with fp32(c s').  INT2 centroids are not integers: fp32.
+// What bounds it (65 536 tokens, 8 heads, d 128, bf16: 70 us, 4.9 TB/s, floor 51): 60 M warp-instructions at
+// 60-70% issue, half of them logic on the codes and the two-byte exchange of the pair's outputs.  Selects in
+// that exchange cost 8%; a warp's rows written by 16-byte stores instead of bulk copies cost 7%.
 // INT8: a thread per vector, code * s.
 #include "write_common.cuh"
 
@@ -35,6 +38,10 @@ struct ReadSmem {
     static constexpr int kBars = kWriteWarps * kPerWarp;       // two mbarriers per warp
     static constexpr int kMask = kBars + kWriteWarps * 16;     // [D / 2] sign bits of an output pair (15: even, 31: odd)
     static constexpr int kBytes = kMask + D * 2;
+    // Resident CTAs per SM, the grid's unit: what the shared memory leaves, up to 8 for INT4 (64 registers; 65 536
+    // tokens of 8 heads, d 128: 70 us, 72 with 5, 77 with 4) and 5 for the others (INT2 spills below 96).
+    static constexpr int kFit = 230000 / (kBytes + 1024);
+    static constexpr int kBlocks = BITS == 4 ? (kFit < 8 ? kFit : 8) : (kFit < 5 ? kFit : 5);
 };
 
 __device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
@@ -77,30 +84,41 @@ struct OutPair<float> {
 template <typename OT>
 __host__ __device__ constexpr int out_words(int n) { return n * (int)sizeof(OT) / 4; }
 
-// INT4: w the row's D/8 code words, then the scale word.
+// INT4: w the row's D/8 code words, then the scale word.  Byte m of the row holds elements 2m (low nibble)
+// and 2m + 1.  Thread t forms the outputs of parity t, then finishes the pairs m whose bit 4 is t: out[16 g + i]
+// is pair 32 g + 16 t + i (the two threads' 16-byte stores then fall in different banks).
 template <int D, typename OT>
 __device__ __forceinline__ void decode_half(const uint32_t* w, const uint32_t* mask, int t, float c, bool live,
                                             uint32_t (&out)[out_words<OT>(D / 2)]) {
-    constexpr int W = D / 8;   // code words; byte m of the row holds elements 2m (low nibble) and 2m + 1
+    constexpr int W = D / 8;   // code words
     const uint32_t sw = live ? w[W] : 0u;
     const uint32_t zp = sw & 15u;
     const float scale = __fmul_rn(__uint_as_float(sw & 0xFFFFFFF0u), c);   // dead rows: 0
-    // stride 1: u_m = e_2m + e_2m+1 - 2 zp (t = 0) or e_2m - e_2m+1 (t = 1; as e_2m + (15 - e_2m+1) - 15)
-    const uint32_t flip = t ? 0x0F0F0F0Fu : 0u;
-    const uint32_t bias = (0x6400u + (t ? 15u : 2u * zp)) * 0x10001u;
-    uint32_t u[2 * W];   // u[2w + i]: bytes 4w + 2i (low half) and 4w + 2i + 1
+    // stride 1: u_m = (e_2m - zp) + (e_2m+1 - zp) (t = 0) or e_2m - e_2m+1 (t = 1), from 1024 + e_2m and
+    // 1024 + 16 e_2m+1: every sum and product below is an exact small integer
+    const uint32_t sgn = t ? 0xBC00BC00u : 0x3C003C00u;                                     // +-1
+    const uint32_t nsgn = sgn ^ 0x80008000u;
+    const uint32_t sixteenth = t ? 0xAC00AC00u : 0x2C002C00u;                               // +-1/16
+    const uint32_t bias = t ? 0xE380E380u : hsub2(0xE440E440u, hadd2(zp_lo_half(zp) * 0x10001u, hadd2(zp_lo_half(zp) * 0x10001u, 0xE800E800u)));   // -960 or -1088 - 2 zp
+    uint32_t u[2 * W];   // u[2w + e]: pairs m = 4w + e (low half) and 4w + e + 2
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        const uint32_t x = w[i];
-        const uint32_t s = (x & 0x0F0F0F0Fu) + (((x >> 4) & 0x0F0F0F0Fu) ^ flip);   // bytes <= 30
-        u[2 * i] = hsub2(prmt(s, 0x64646464u, 0x4140u), bias);                      // 1024 + s - (1024 + bias)
-        u[2 * i + 1] = hsub2(prmt(s, 0x64646464u, 0x4342u), bias);
+        const uint32_t x = w[i], x8 = x >> 8;
+        u[2 * i] = hfma2(lop3_and_or(x, 0x00F000F0u, 0x64006400u), sixteenth, hadd2(lop3_and_or(x, 0x000F000Fu, 0x64006400u), bias));
+        u[2 * i + 1] = hfma2(lop3_and_or(x8, 0x00F000F0u, 0x64006400u), sixteenth, hadd2(lop3_and_or(x8, 0x000F000Fu, 0x64006400u), bias));
     }
-    // the byte index's bit 0 lies within a register, its other bits between registers
+    // bit 1 of m lies within a register
+    const __half2 pm = __halves2half2(__ushort_as_half(0x3C00), __ushort_as_half(0xBC00));   // (1, -1)
 #pragma unroll
-    for (int i = 0; i < 2 * W; ++i) u[i] = hfma2(u[i], 0xBC003C00u, prmt(u[i], u[i], 0x1032u));   // (a + b, a - b)
+    for (int i = 0; i < 2 * W; ++i) {
+        const __half2 v = *reinterpret_cast<const __half2*>(&u[i]);
+        const __half2 r = __hfma2(__high2half2(v), pm, __low2half2(v));   // (a + b, a - b)
+        u[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+    // bits 0, 2, 3 (and 5) between registers; bit 4 (register index bit 3) with the exchange below
 #pragma unroll
     for (int st = 1; st < 2 * W; st <<= 1) {
+        if (st == 8) continue;
 #pragma unroll
         for (int i = 0; i < 2 * W; ++i) {
             if (i & st) continue;
@@ -109,17 +127,27 @@ __device__ __forceinline__ void decode_half(const uint32_t* w, const uint32_t* m
             u[i + st] = hsub2(a, b);
         }
     }
-    // thread 0 finishes the row's first half, thread 1 the second: each sends what it holds of the other's
     const float2 s2 = make_float2(scale, scale);
+    const uint32_t sel_lo = t ? 0x1054u : 0x5410u, sel_hi = t ? 0x3276u : 0x7632u;   // (element 2m, element 2m + 1)
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const uint32_t other = __shfl_xor_sync(0xffffffffu, t ? u[i] : u[i + W], 1);
-        const uint32_t mine = t ? u[i + W] : u[i];
-        const uint32_t ev = t ? other : mine, od = t ? mine : other;   // elements 2m + 0 and 2m + 1, m = 2i, 2i + 1 (+ D/4)
-        const float2 a = mul_f32x2(half2_to_float2(prmt(ev, od, 0x5410u)), s2);
-        const float2 b = mul_f32x2(half2_to_float2(prmt(ev, od, 0x7632u)), s2);
-        OutPair<OT>::put(out, 2 * i, a, mask[2 * i]);
-        OutPair<OT>::put(out, 2 * i + 1, b, mask[2 * i + 1]);
+    for (int g = 0; g < W / 8; ++g) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {   // words 8 g + q and 8 g + q + 4
+            const uint4 mk = *reinterpret_cast<const uint4*>(mask + 32 * g + 16 * t + 4 * q);
+            uint32_t x[4];   // pairs 4 q .. 4 q + 3 of the group
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t a = u[16 * g + 2 * q + e], b = u[16 * g + 2 * q + 8 + e];
+                const uint32_t mine = hfma2(b, sgn, a);
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, hfma2(b, nsgn, a), 1);
+                x[e] = prmt(mine, other, sel_lo);
+                x[e + 2] = prmt(mine, other, sel_hi);
+            }
+            const uint32_t m4[4] = {mk.x, mk.y, mk.z, mk.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                OutPair<OT>::put(out, 16 * g + 4 * q + e, mul_f32x2(half2_to_float2(x[e]), s2), m4[e]);
+        }
     }
 }
 
@@ -167,7 +195,7 @@ __device__ __forceinline__ void decode_int8_words(const uint32_t* w, int first, 
 }
 
 template <int D, int BITS, typename OT>
-__global__ void __launch_bounds__(kWriteThreads) read_kernel(const __grid_constant__ ReadParams p) {
+__global__ void __launch_bounds__(kWriteThreads, ReadSmem<D, BITS, OT>::kBlocks) read_kernel(const __grid_constant__ ReadParams p) {
     using Sh = ReadShape<BITS>;
     using Sm = ReadSmem<D, BITS, OT>;
     constexpr int TPV = Sh::kTpv, TV = Sh::kTileVecs, RB = Sm::RB, RW = RB / 4;
@@ -276,12 +304,20 @@ __global__ void __launch_bounds__(kWriteThreads) read_kernel(const __grid_consta
         } else {
             constexpr int OWD = out_words<OT>(D / 2);
             uint32_t o[OWD];
-            if constexpr (BITS == 4) decode_half<D, OT>(row, mask + part * (D / 4), part, p.c, live, o);
+            if constexpr (BITS == 4) decode_half<D, OT>(row, mask, part, p.c, live, o);
             else decode_half_int2<D, OT>(row, mask + part * (D / 4), part, p.c, live, o);
             staging_free();
-            uint4* dst = reinterpret_cast<uint4*>(orow + part * (OWD * 4));
+            // INT4: groups of 16 pairs, the thread's in every second group; INT2: its half of the row
+            constexpr int kGroup = BITS == 4 ? out_words<OT>(32) : OWD;   // words
 #pragma unroll
-            for (int i = 0; i < OWD / 4; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int g = 0; g < OWD / kGroup; ++g) {
+                uint4* dst = reinterpret_cast<uint4*>(orow + (2 * g + part) * (kGroup * 4));
+#pragma unroll
+                for (int i = 0; i < kGroup / 4; ++i) {
+                    const uint32_t* q = o + g * kGroup + 4 * i;
+                    dst[i] = make_uint4(q[0], q[1], q[2], q[3]);
+                }
+            }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // staged rows -> bulk store
         __syncwarp();
@@ -305,9 +341,7 @@ cudaError_t launch_read_t(const ReadParams& p, cudaStream_t stream) {
     const int64_t blocks = (ntiles + kWriteWarps - 1) / kWriteWarps;
     cudaError_t err = opt_in_smem<read_kernel<D, BITS, OT>>(Sm::kBytes);
     if (err != cudaSuccess) return err;
-    int per_sm = (int)(230000 / (Sm::kBytes + 1024));
-    if (per_sm > 6) per_sm = 6;
-    const int64_t cap = (int64_t)num_sms() * per_sm;
+    const int64_t cap = (int64_t)num_sms() * Sm::kBlocks;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;

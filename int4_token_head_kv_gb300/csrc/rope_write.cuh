@@ -12,11 +12,16 @@
 // bit-exact with this definition followed by the plain write's.
 //
 // The work of one launch is two kinds of warp items: cache tiles (kTileVecs vectors, as the plain
-// write's, numbered plane by plane so that a tile is all keys or all values and a value tile skips the
-// rotation) and query items (one token, kRows heads).  A key vector's lane pair rotates the words it
-// reads on the fly: the partner words come from the same staged row, the table row through L1 (the
-// heads of a token share it).  A warp alternates the two kinds in proportion, because a cache tile is
-// bound by its instructions and a query item by memory.
+// write's, numbered plane by plane so that a tile is all keys or all values) and query items (one token,
+// kRows heads).  A warp alternates them in proportion, because a cache tile is bound by its instructions
+// and a query item by memory.
+//
+// A key tile is rotated by the whole warp before its vectors are encoded: a lane owns two words (pairs of
+// elements) of every row, holds their cosines and sines, signed with the Hadamard rotation's signs, in
+// registers for as long as the token lasts (its heads are neighbouring rows), and writes the rotated
+// elements as fp32 where the encoding lane pair reads them as the operands of its first butterflies.
+// (Rotated by the encoding threads themselves, each of a pair did the whole row: 64 table loads per thread
+// and tile, and 180 us for 65 536 tokens of 8 kv heads instead of 88.7 without a rotation.)
 #pragma once
 
 #include "write_common.cuh"
@@ -55,66 +60,132 @@ __device__ __forceinline__ void turn2(float2 a, float2 b, float2 c, float2 s, fl
 
 __device__ __forceinline__ float4 ldg4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
-// Words m0 .. m0 + 3 (pairs of elements) of a key row, rotated: x[e] = (x'_{2m}, x'_{2m+1}), m = m0 + e.
-// m0 is a multiple of 4 and rot of 16, so the four words and their partners lie on one side of every
-// border.  cs: the token's table row.
-template <typename T, bool INTER>
-__device__ __forceinline__ void roped_words(const uint32_t* row, int m0, const float* cs, int rot, float2 (&x)[4]) {
-    const uint4 own = *reinterpret_cast<const uint4*>(row + m0);
-    const uint32_t w[4] = {own.x, own.y, own.z, own.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = upcast_pair<T>(w[e]);
-    if (2 * m0 >= rot) return;
-    if constexpr (INTER) {
-        const float4 c = ldg4(cs + m0), s = ldg4(cs + (rot >> 1) + m0);
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 xc = mul_f32x2(x[e], make_float2(cc[e], cc[e])), xs = mul_f32x2(x[e], make_float2(ss[e], ss[e]));
-            x[e] = make_float2(__fsub_rn(xc.x, xs.y), __fadd_rn(xc.y, xs.x));
-        }
-    } else {
-        const int hw = rot >> 2;   // words of a half
-        const bool low = m0 < hw;
-        const int j = low ? m0 : m0 - hw;
-        const uint4 oth = *reinterpret_cast<const uint4*>(row + (low ? m0 + hw : j));
-        const uint32_t o[4] = {oth.x, oth.y, oth.z, oth.w};
-        const float4 c0 = ldg4(cs + 2 * j), c1 = ldg4(cs + 2 * j + 4);
-        const float4 s0 = ldg4(cs + (rot >> 1) + 2 * j), s1 = ldg4(cs + (rot >> 1) + 2 * j + 4);
-        const float2 c[4] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
-        const float2 s[4] = {{s0.x, s0.y}, {s0.z, s0.w}, {s1.x, s1.y}, {s1.z, s1.w}};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 xc = mul_f32x2(x[e], c[e]), ps = mul_f32x2(upcast_pair<T>(o[e]), s[e]);
-            x[e] = low ? diff_of_products(xc, ps) : sum_of_products(xc, ps);
-        }
-    }
-}
+// Rotated rows of a key tile, fp32, in shared memory: row r at r * kRopeRow<D> floats, in the order
+// [4k .. 4k + 3] = elements 2k, 2k + D/2, 2k + 1, 2k + 1 + D/2 (k < D/4): one 16-byte access holds the two
+// operand pairs of the encoder's stride-1 butterflies P[k].
+template <int D>
+constexpr int kRopeRow = D + 4;   // padded: 16-byte accesses of 8 rows hit distinct banks
+constexpr int kRopeRows = 16;     // rows staged at a time
 
-// One thread's stride-1 outputs of a key vector's Hadamard rotation, as rotate_half forms them, from
-// the position-rotated row.  fmask[m] (this thread's parity): bit 15 = sign of element 2m, bit 31 =
-// sign of element 2m + 1 times (t ? -1 : +1).
-template <int D, typename T, bool INTER>
-__device__ __forceinline__ void form_roped_half(const uint32_t* row, const uint32_t* fmask, const float* cs, int rot,
-                                                float2 (&P)[D / 4]) {
+// What a lane keeps of a token's table row: x' = x c + partner s for its two words.
+struct RopeTable {
+    float2 c[2], s[2];
+};
+
+// The lane's part of the table row of position pos (row 0 for one outside the table: its rows are not stored).
+template <int D, bool INTER>
+__device__ __forceinline__ RopeTable load_table(const RopeWriteParams& p, int64_t pos) {
     constexpr int Q = D / 4;
+    const int k = (threadIdx.x & 31) % Q, rot = p.rot, hw = rot >> 2;
+    const float* cs = p.cos_sin + (pos >= 0 && pos < p.max_position ? pos : 0) * rot;
+    RopeTable t;
 #pragma unroll
-    for (int k = 0; k < Q; k += 4) {
-        float2 lo[4], hi[4];
-        roped_words<T, INTER>(row, k, cs, rot, lo);
-        roped_words<T, INTER>(row, k + Q, cs, rot, hi);
-        const uint4 ml = *reinterpret_cast<const uint4*>(fmask + k), mh = *reinterpret_cast<const uint4*>(fmask + k + Q);
-        const uint32_t fl[4] = {ml.x, ml.y, ml.z, ml.w}, fh[4] = {mh.x, mh.y, mh.z, mh.w};
-        auto even = [](float x, uint32_t m) { return __uint_as_float(__float_as_uint(x) ^ ((m << 16) & 0x80000000u)); };
-        auto odd = [](float x, uint32_t m) { return __uint_as_float(__float_as_uint(x) ^ (m & 0x80000000u)); };
+    for (int i = 0; i < 2; ++i) {
+        const int m = k + i * Q;
+        t.c[i] = make_float2(1.0f, 1.0f);
+        t.s[i] = make_float2(0.0f, 0.0f);
+        if (2 * m < rot) {
+            if constexpr (INTER) {   // the sines' signs follow in rope_rows
+                t.c[i].x = __ldg(cs + m);
+                t.s[i].x = __ldg(cs + (rot >> 1) + m);
+            } else {
+                const int j = m < hw ? m : m - hw;
+                t.c[i] = __ldg(reinterpret_cast<const float2*>(cs + 2 * j));
+                t.s[i] = __ldg(reinterpret_cast<const float2*>(cs + (rot >> 1) + 2 * j));
+            }
+        }
+    }
+    return t;
+}
+
+// Rotate rows r0 .. r0 + nrows - 1 of the tile (vectors v0 + r of the key plane, staged at in + r * ROWPAD)
+// into stage rows 0 .. nrows - 1, nrows <= kRopeRows.  tab: the table row of the first row's token; pos: lane
+// r * TPV holds the position of row r's token.  fmask: per word m the signs to apply (bit 15: element 2m, bit
+// 31: 2m + 1), or nullptr for none.  All lanes call it.
+template <int D, typename T, bool INTER, int ROWPAD, int TPV>
+__device__ __forceinline__ void rope_rows(const RopeWriteParams& p, const uint8_t* in, float* stage, uint32_t v0, int r0,
+                                          int nrows, RopeTable tab, int64_t pos, const uint32_t* fmask) {
+    constexpr int Q = D / 4, kStep = 32 / Q;   // rows at once: a lane owns words k and k + Q of every kStep-th row
+    const int lane = threadIdx.x & 31, k = lane % Q, sub = lane / Q;
+    const uint32_t H = (uint32_t)p.w.H;
+    const int rot = p.rot, hw = rot >> 2;       // words of a half of the rotated elements
+    int pw[2];            // the partner word (split pairing)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            P[k + e] = add_f32x2(make_float2(even(lo[e].x, fl[e]), even(hi[e].x, fh[e])),
-                                 make_float2(odd(lo[e].y, fl[e]), odd(hi[e].y, fh[e])));
+    for (int i = 0; i < 2; ++i) {
+        const int m = k + i * Q;
+        pw[i] = INTER || 2 * m >= rot ? m : (m < hw ? m + hw : m - hw);
+    }
+    const bool full = !INTER && rot == D;   // the lane's two words are each other's partners
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(in + r0 * ROWPAD);
+    constexpr int kRowWords = ROWPAD / 4;
+    int r = 0, r_end = (int)(H - (v0 + r0) % H);   // rows of the first token
+    while (r < nrows) {
+        // a token's rows r .. r_end - 1, the next token's table row on its way
+        if (r_end > nrows) r_end = nrows;
+        RopeTable next = tab;
+        if (r_end < nrows) next = load_table<D, INTER>(p, __shfl_sync(0xffffffffu, pos, (r0 + r_end) * TPV));
+        float2 c[2], s[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int m = k + i * Q;
+            c[i] = tab.c[i];
+            s[i] = tab.s[i];
+            if (2 * m < rot) {
+                if constexpr (INTER) {
+                    c[i].y = c[i].x;
+                    s[i] = make_float2(-s[i].x, s[i].x);
+                } else if (m < hw) {
+                    s[i] = make_float2(-s[i].x, -s[i].y);
+                }
+            }
+            if (fmask != nullptr) {   // products with the signed values round as the plain ones
+                const uint32_t f = fmask[m], se = (f << 16) & 0x80000000u, so = f & 0x80000000u;
+                c[i] = make_float2(__uint_as_float(__float_as_uint(c[i].x) ^ se), __uint_as_float(__float_as_uint(c[i].y) ^ so));
+                s[i] = make_float2(__uint_as_float(__float_as_uint(s[i].x) ^ se), __uint_as_float(__float_as_uint(s[i].y) ^ so));
+            }
+        }
+        if (full) {
+#pragma unroll 4
+            for (int q = r + sub; q < r_end; q += kStep) {
+                const float2 x = upcast_pair<T>(src[q * kRowWords + k]), y = upcast_pair<T>(src[q * kRowWords + k + Q]);
+                const float2 a = sum_of_products(mul_f32x2(x, c[0]), mul_f32x2(y, s[0]));
+                const float2 b = sum_of_products(mul_f32x2(y, c[1]), mul_f32x2(x, s[1]));
+                *reinterpret_cast<float4*>(stage + q * kRopeRow<D> + 4 * k) = make_float4(a.x, b.x, a.y, b.y);
+            }
+        } else {
+#pragma unroll 2
+            for (int q = r + sub; q < r_end; q += kStep) {
+                float2 y[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float2 x = upcast_pair<T>(src[q * kRowWords + k + i * Q]);
+                    float2 o;
+                    if constexpr (INTER) o = make_float2(x.y, x.x);
+                    else o = upcast_pair<T>(src[q * kRowWords + pw[i]]);
+                    y[i] = sum_of_products(mul_f32x2(x, c[i]), mul_f32x2(o, s[i]));
+                }
+                *reinterpret_cast<float4*>(stage + q * kRopeRow<D> + 4 * k) = make_float4(y[0].x, y[1].x, y[0].y, y[1].y);
+            }
+        }
+        tab = next;
+        r = r_end;
+        r_end += (int)H;
     }
 }
 
-// The same for a value vector (no position rotation).
+// One thread's stride-1 outputs of a rotated key row (its signs are applied).
+template <int D>
+__device__ __forceinline__ void form_staged_half(const float* row, int t, float2 (&P)[D / 4]) {
+    const float2 ts = t ? make_float2(-1.0f, -1.0f) : make_float2(1.0f, 1.0f);
+#pragma unroll
+    for (int k = 0; k < D / 4; ++k) {
+        const float4 f = *reinterpret_cast<const float4*>(row + 4 * k);
+        P[k] = fma_f32x2(make_float2(f.z, f.w), ts, make_float2(f.x, f.y));   // the product with +-1 is exact
+    }
+}
+
+// The same for a value row as it comes.  fmask[m] (this thread's parity): bit 15 = sign of element 2m, bit
+// 31 = sign of element 2m + 1 times (t ? -1 : +1).
 template <int D, typename T>
 __device__ __forceinline__ void form_plain_half(const uint32_t* row, const uint32_t* fmask, float2 (&P)[D / 4]) {
     constexpr int Q = D / 4;
@@ -219,9 +290,23 @@ __device__ __forceinline__ void rotate_queries(const RopeWriteParams& p, uint32_
     }
 }
 
-// Resident CTAs per SM (register budget): the rotation needs more registers than the plain write.
+// Resident CTAs per SM (register and shared-memory budget).
 template <int BITS>
 constexpr int kRopeBlocks = BITS == 8 ? 3 : 4;
+
+// Shared memory of a warp: one tile of inputs, and the rotated rows, whose space holds the encoded rows once
+// the tile is in registers.
+template <int D, int BITS>
+struct RopeSmem {
+    static constexpr int TV = WriteShape<BITS>::kTileVecs;
+    static constexpr int kRowPad = 2 * D + 16;
+    static constexpr int kIn = TV * kRowPad;
+    static constexpr int kStage = kRopeRows * kRopeRow<D> * 4;
+    static_assert(TV * (D * BITS / 8 + 4) <= kStage, "encoded rows");
+    static constexpr int kPerWarp = kIn + kStage;
+    static constexpr int kBars = kWriteWarps * kPerWarp;   // one mbarrier per warp
+    static constexpr int kBytes = kBars + kWriteWarps * 16 + (int)sizeof(WriteSigns<D>);
+};
 
 template <int D, typename T, int BITS, bool INTER>
 __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
@@ -232,19 +317,20 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
     constexpr int RB = D * BITS / 8 + 4;             // cache row bytes
     constexpr int NW = RB / 4 - 1;                   // code words per row (then the scale)
     constexpr int OW = INT8 ? NW + 1 : NW / 2 + 1;   // words one thread stores (the last: the scale word)
-    using Sm = WriteSmem<D, TV>;
+    using Sm = RopeSmem<D, BITS>;
     extern __shared__ __align__(128) uint8_t smem[];
     // The previous kernel may produce any of the inputs.  Unlike the plain write, this kernel lets no
     // dependent start early: the attention that follows reads its queries before it waits.
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int vl = lane / TPV, part = lane % TPV;   // this thread's vector of the tile and its part
-    uint8_t* wbuf = smem + warp * Sm::kPerWarp;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::kBars) + warp * 2;   // this warp's [buffer]
-    WriteSigns<D>& sgn = *reinterpret_cast<WriteSigns<D>*>(smem + Sm::kBars + kWriteWarps * 2 * 8);
+    uint8_t* in = smem + warp * Sm::kPerWarp;
+    float* stage = reinterpret_cast<float*>(in + Sm::kIn);
+    uint8_t* obuf = in + Sm::kIn;
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Sm::kBars) + warp * 2;   // this warp's inputs have landed
+    WriteSigns<D>& sgn = *reinterpret_cast<WriteSigns<D>*>(smem + Sm::kBars + kWriteWarps * 16);
     if (lane == 0) {
-        mbar_init(&bars[0], 1);
-        mbar_init(&bars[1], 1);
+        mbar_init(bar, 1);
         fence_mbar_init();
     }
     for (int j = tid; j < (INT8 ? 0 : D / 2); j += kWriteThreads) {   // INT8 rows take no signs
@@ -283,7 +369,7 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
     uint32_t items_done = 0;
 
     // lane i < TV copies vector i of the tile (2D bytes) into row i of the buffer
-    auto prefetch = [&](uint32_t tile, uint8_t* buf, uint64_t* bar) {
+    auto prefetch = [&](uint32_t tile) {
         const uint32_t v0 = tile * TV;
         const uint32_t live_vecs = min((uint32_t)TV, nvec - v0);
         if (lane == 0) mbar_arrive_expect_tx(bar, live_vecs * (uint32_t)(D * 2));
@@ -292,69 +378,92 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
             uint32_t tok, h, pl;
             split(v0 + lane, tok, h, pl);
             const uint8_t* src = (pl ? vin + (int64_t)tok * vst : kin + (int64_t)tok * kst) + (int64_t)h * (D * 2);
-            bulk_copy_g2s(buf + lane * Sm::kRowPad, src, D * 2, bar, policy_evict_first());
+            bulk_copy_g2s(in + lane * Sm::kRowPad, src, D * 2, bar, policy_evict_first());
         }
     };
 
     uint32_t tile = gwarp;
     uint32_t it = 0;
     bool waited_out = false;
-    if (tile < ntiles) prefetch(tile, wbuf, &bars[0]);
+    // position and slot of this lane's vector of a tile (past the end: the tile's first vector), loaded one
+    // tile ahead with its rows
+    auto indices = [&](uint32_t tile, int64_t& pos, int64_t& slot) {
+        const uint32_t v = tile * TV + vl;
+        uint32_t tok, h, pl;
+        split(v < nvec ? v : tile * TV, tok, h, pl);
+        pos = __ldg(p.positions + tok);
+        slot = __ldg(p.w.slots + tok);
+    };
+    int64_t pos_next = 0, slot_next = 0;
+    if (my_tiles > 0) {
+        prefetch(tile);
+        indices(tile, pos_next, slot_next);
+    }
     for (; it < my_tiles; tile += nwarps, ++it) {
-        uint8_t* cur = wbuf + (it & 1) * Sm::kBuf;
-        uint8_t* nxt = wbuf + ((it + 1) & 1) * Sm::kBuf;
-        // the other buffer was last an output stage: its bulk stores must have read it
-        if (grouped) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-        __syncwarp();
-        if (it + 1 < my_tiles) prefetch(tile + nwarps, nxt, &bars[(it + 1) & 1]);
+        const int64_t pos = pos_next, slot = slot_next;
+        const uint32_t v0 = tile * TV, v = v0 + vl;
+        const bool live = v < nvec;
+        const int keys = v0 < nplane ? (int)min((uint32_t)TV, nplane - v0) : 0;   // key rows of the tile, its first ones
+        RopeTable tab = {};
+        if (keys > 0) tab = load_table<D, INTER>(p, __shfl_sync(0xffffffffu, pos, 0));
         // this tile's share of the query items
         const uint32_t until = (uint32_t)((uint64_t)my_items * (it + 1) / my_tiles);
         for (; items_done < until; ++items_done, item += nwarps) rotate_queries<D, T, INTER>(p, item, groups);
         __syncwarp();
-        // this tile's rows: use (it >> 1) of buffer it & 1
-        if (__any_sync(0xffffffffu, !mbar_wait(&bars[it & 1], (it >> 1) & 1u))) {
+        if (__any_sync(0xffffffffu, !mbar_wait(bar, it & 1u))) {
             if (lane == 0) count_status(p.w.status, 3);
             waited_out = true;
             break;
         }
-        const uint32_t v = tile * TV + vl;
-        const bool live = v < nvec;
+        // the previous tile's bulk stores have read the staged rows
+        if (grouped) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
         uint32_t tok = 0, h = 0, pl = 0;
-        split(live ? v : tile * TV, tok, h, pl);   // past the end: the tile's first vector, its words discarded
+        split(live ? v : v0, tok, h, pl);   // past the end: the tile's first vector, its words discarded
         // a token outside the table is skipped whole; a padding token (no slot, no position) is not counted
-        const int64_t pos = __ldg(p.positions + tok), slot = __ldg(p.w.slots + tok);
         const bool placed = pos >= 0 && pos < p.max_position;
         if (!placed && live && pl == 0 && h == 0 && part == 0 && (pos >= 0 || slot >= 0)) count_status(p.w.status, 5);
-        const float* cs = p.cos_sin + (placed ? pos : 0) * p.rot;
-        const uint8_t* rowb = cur + (live ? vl : 0) * Sm::kRowPad;
-        const uint32_t* row = reinterpret_cast<const uint32_t*>(rowb);
+        const int row = live ? vl : 0;
         uint32_t words[OW];
         if constexpr (INT8) {
             float u[D];
-            if (live) {
-                if (pl == 0) {
+            for (int r0 = 0; r0 < keys; r0 += kRopeRows) {
+                if (r0 > 0) tab = load_table<D, INTER>(p, __shfl_sync(0xffffffffu, pos, r0 * TPV));
+                rope_rows<D, T, INTER, Sm::kRowPad, TPV>(p, in, stage, v0, r0, min(kRopeRows, keys - r0), tab, pos, nullptr);
+                __syncwarp();
+                if (row >= r0 && row < min(r0 + kRopeRows, keys)) {
 #pragma unroll
-                    for (int m = 0; m < D / 2; m += 4) {
-                        float2 x[4];
-                        roped_words<T, INTER>(row, m, cs, p.rot, x);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            u[2 * (m + e)] = x[e].x;
-                            u[2 * (m + e) + 1] = x[e].y;
-                        }
+                    for (int k = 0; k < D / 4; ++k) {
+                        const float4 f = *reinterpret_cast<const float4*>(stage + (row - r0) * kRopeRow<D> + 4 * k);
+                        u[2 * k] = f.x;
+                        u[2 * k + D / 2] = f.y;
+                        u[2 * k + 1] = f.z;
+                        u[2 * k + 1 + D / 2] = f.w;
                     }
-                } else {
-                    load_vector_raw<D, T>(reinterpret_cast<const uint4*>(rowb), u);
                 }
+                __syncwarp();
             }
-            __syncwarp();   // the tile's inputs are in registers; its buffer becomes the output stage
+            if (row >= keys) load_vector_raw<D, T>(reinterpret_cast<const uint4*>(in + row * Sm::kRowPad), u);
+            __syncwarp();   // the tile is in registers
+            if (it + 1 < my_tiles) {
+                prefetch(tile + nwarps);
+                indices(tile + nwarps, pos_next, slot_next);
+            }
             if (live) encode_vector_int8<D>(u, words);
         } else {
             // every lane runs the encoder (it exchanges values within the lane pair)
             float2 P[D / 4];
-            if (pl == 0) form_roped_half<D, T, INTER>(row, sgn.xmask[part], cs, p.rot, P);
-            else form_plain_half<D, T>(row, sgn.xmask[part], P);
-            __syncwarp();   // the tile's inputs are consumed; its buffer becomes the output stage
+            if (keys > 0) {
+                rope_rows<D, T, INTER, Sm::kRowPad, TPV>(p, in, stage, v0, 0, keys, tab, pos, sgn.xmask[0]);
+                __syncwarp();
+            }
+            if (row < keys) form_staged_half<D>(stage + row * kRopeRow<D>, part, P);
+            else form_plain_half<D, T>(reinterpret_cast<const uint32_t*>(in + row * Sm::kRowPad), sgn.xmask[part], P);
+            __syncwarp();   // the tile is in registers
+            if (it + 1 < my_tiles) {
+                prefetch(tile + nwarps);
+                indices(tile + nwarps, pos_next, slot_next);
+            }
             butterflies_half<D>(p.w.c, P);
             if constexpr (BITS == 2) quantise_half_int2<D>(P, part, words);
             else quantise_half<D>(P, part, words);
@@ -368,7 +477,7 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
         const bool store = live && placed && slot >= 0 && in_range;
         const int64_t blk = slot / kBlockSize, off = slot % kBlockSize;
         if (grouped) {
-            uint32_t* orow = reinterpret_cast<uint32_t*>(cur + vl * RB) + w0;
+            uint32_t* orow = reinterpret_cast<uint32_t*>(obuf + vl * RB) + w0;
             if (live) {
 #pragma unroll
                 for (int wi = 0; wi < OW; ++wi)
@@ -378,7 +487,7 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
             __syncwarp();
             // the first thread of each row group stores the whole group
             if (store && h == 0 && part == 0)
-                bulk_store_s2g(p.w.cache + ((blk * 2 + pl) * kBlockSize + off) * (int64_t)group_bytes, cur + vl * RB, group_bytes);
+                bulk_store_s2g(p.w.cache + ((blk * 2 + pl) * kBlockSize + off) * (int64_t)group_bytes, obuf + vl * RB, group_bytes);
         } else if (store) {
             uint32_t* orow = reinterpret_cast<uint32_t*>(p.w.cache + (((blk * 2 + pl) * kBlockSize + off) * (int64_t)H + h) * RB) + w0;
 #pragma unroll
@@ -386,9 +495,7 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
                 if (wi < nw) orow[wi] = words[wi];
         }
     }
-    if (waited_out && it + 1 < my_tiles) {   // let the copy in flight land before the warp exits
-        (void)mbar_wait(&bars[(it + 1) & 1], ((it + 1) >> 1) & 1u);
-    }
+    if (waited_out) (void)mbar_wait(bar, it & 1u);   // let the copy in flight land before the warp exits
     for (; items_done < my_items; ++items_done, item += nwarps) rotate_queries<D, T, INTER>(p, item, groups);
     if (grouped) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
@@ -396,7 +503,7 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
 template <int D, typename T, int BITS, bool INTER>
 cudaError_t launch_rope_write_t(const RopeWriteParams& p, cudaStream_t stream) {
     using Sh = WriteShape<BITS>;
-    using Sm = WriteSmem<D, Sh::kTileVecs>;
+    using Sm = RopeSmem<D, BITS>;
     const int64_t ntiles = (p.w.num_tokens * p.w.H * 2 + Sh::kTileVecs - 1) / Sh::kTileVecs;
     const int64_t groups = (p.Hq + QueryItem<D>::kRows - 1) / QueryItem<D>::kRows;
     const int64_t blocks = (ntiles + p.w.num_tokens * groups + kWriteWarps - 1) / kWriteWarps;
