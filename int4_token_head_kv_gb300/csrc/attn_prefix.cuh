@@ -41,12 +41,13 @@ struct PxLayout {
     static constexpr uint32_t kRaw = Pf::kRaw;
     static constexpr uint32_t kChunks = Pf::kChunks, kWindow = Pf::kWindow;
     static constexpr uint32_t kPlane = kPfKeys * kWindow * 4;                    // one plane of a staged tile
-    static constexpr uint32_t kSk = kRaw + kPfRawStages * 2 * kPlane;            // [kring][128] f32 s'_K * k0 (0: no key)
-    static constexpr uint32_t kDeadF = kSk + kPfKRing * kPfKeys * 4;             // [kring][4] u32: a K warp saw a key with no row
+    static constexpr uint32_t kSk = kRaw + kPfRawStages * 2 * kPlane;            // [kring][128] f32 s'_K * k0
+    static constexpr uint32_t kDeadF = kSk + kPfKRing * kPfKeys * 4;             // [kring][4] u32: keys with no row, one bit each
     static constexpr uint32_t kSv = kDeadF + kPfKRing * 4 * 4;                   // [pairs][128] f32 s'_V
     static constexpr uint32_t kEblk = kSv + kPfPairs * kPfKeys * 4;              // [pairs][4] per-warp max V exponent
-    static constexpr uint32_t kQmax = kEblk + kPfPairs * 4 * 4;                  // u32: bits of the rows' largest |v|
-    static constexpr uint32_t kSignBits = kQmax + 16;                            // [D / 32] u32
+    static constexpr uint32_t kQexp = kEblk + kPfPairs * 4 * 4;                  // u32: first usable row and its exponent
+    static constexpr uint32_t kRs = kQexp + 16;                                  // [128] f32 2^-d of each row's own prescale
+    static constexpr uint32_t kSignBits = kRs + 128 * 4;                            // [D / 32] u32
     static constexpr uint32_t kBars = (kSignBits + D / 8 + 7u) & ~7u;
     // k_full[kring], k_free[pairs], v_full[pairs], v_free[pairs], pv_done[2], s_full[2], p_full[2], q_ready,
     // flush, q_tma, rot_in, rot_done, q_max, raw_full[plane][stages], raw_free[plane][stages]
@@ -61,6 +62,12 @@ __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
+}
+
+// The CTA's query prescale exponent from its first usable row (row << 8 | biased exponent of its largest
+// |v|; all ones: none): that row's to [2^7, 2^8), within the range a key's scale can take up.
+__device__ __forceinline__ int rows_exponent(uint32_t first) {
+    return first == 0xFFFFFFFFu ? 0 : max(-60, min(60, 7 + 127 - (int)(first & 0xFFu)));
 }
 
 // inverse of slot_of_column
@@ -110,13 +117,13 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     uint64_t* q_tma = flush + 1;                // the CTA's query rows in shared memory (bytes)
     uint64_t* rot_in = q_tma + 1;               // the rotation matrix in shared memory (256 arrivals)
     uint64_t* rot_done = rot_in + 1;            // the rotated queries in tensor memory (commit)
-    uint64_t* q_max = rot_done + 1;             // the rows' largest magnitude is known (256 arrivals)
+    uint64_t* q_max = rot_done + 1;             // the rows' exponent is known (256 arrivals)
     uint64_t* raw_full = q_max + 1;          // [plane][stages] packed rows of a key tile landed (32 lanes)
     uint64_t* raw_free = raw_full + 2 * kPfRawStages;   // [plane][stages] that plane converted (128 arrivals)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kFlags);
     uint32_t* deadf = reinterpret_cast<uint32_t*>(smem + Ly::kDeadF);
-    uint32_t* qmax = reinterpret_cast<uint32_t*>(smem + Ly::kQmax);
+    uint32_t* qexp = reinterpret_cast<uint32_t*>(smem + Ly::kQexp);
 
     if (threadIdx.x == 0) {
         for (int b = 0; b < kPfKRing; ++b) mbar_init(&k_full[b], 128);
@@ -136,7 +143,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         mbar_init(rot_in, kPfSoftmaxThreads);
         mbar_init(rot_done, 1);
         mbar_init(q_max, kPfSoftmaxThreads);
-        *qmax = 0u;
+        *qexp = 0xFFFFFFFFu;
         for (int i = 0; i < 2 * kPfRawStages; ++i) {
             mbar_init(&raw_full[i], 32);
             mbar_init(&raw_free[i], 128);
@@ -243,9 +250,13 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         if (none_a) vis_a = p.px_len;
         if (none_b) vis_b = p.px_len;
         const bool idle = __all_sync(0xffffffffu, none_a && none_b);
-        // ---- one power-of-two prescale 2^e for the CTA's rows, bringing the largest |v| into [2^14, 2^15), and
-        // fp16 high + low halves into tensor memory.  (A row 2^16 smaller than the largest still keeps 22
-        // bits; with one exponent, 2^-e goes into the keys' scales instead of a factor per row.)
+        // ---- a power-of-two prescale of the rows, then fp16 high + low halves into tensor memory.  One exponent
+        // serves the CTA, so that 2^-e sits in the keys' scales and not in a factor per row: it brings the first
+        // usable row's max |v| (finite, not zero, of a row that sees keys) to [2^7, 2^8).  A row whose largest value
+        // then lies in [2^-2, 2^15) keeps 22 bits; any other (2^9 away, infinite) takes a further power of two of
+        // its own, so no row's values reach another's results.
+        float* rs = reinterpret_cast<float*>(smem + Ly::kRs);   // what a row's S is multiplied with
+        bool own_a = false, own_b = false;
         bool ok = wait(rot_done, 0);
         if (__all_sync(0xffffffffu, ok)) {
             tc_fence_after();
@@ -253,24 +264,46 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 64) tmem_ld_q8(trow + Tm::kS0 + c0, reinterpret_cast<uint32_t*>(v) + c0 / 2);
             tmem_ld_wait();
-            float mx = 0.0f;
+            // the rows' largest magnitudes by their bits (a NaN's are above infinity's)
+            uint32_t mxa = 0u, mxb = 0u;
 #pragma unroll
-            for (int i = 0; i < D / 4; ++i) mx = max3(mx, fabsf(v[2 * i]), fabsf(v[2 * i + 1]));
-            const uint32_t wmx = __reduce_max_sync(0xffffffffu, __float_as_uint(mx));   // non-negative floats order like their bits
-            if (lane == 0) atomicMax(qmax, wmx);
+            for (int i = 0; i < D / 8; ++i) {
+                mxa = max(mxa, max(__float_as_uint(v[4 * i]) & 0x7FFFFFFFu, __float_as_uint(v[4 * i + 1]) & 0x7FFFFFFFu));
+                mxb = max(mxb, max(__float_as_uint(v[4 * i + 2]) & 0x7FFFFFFFu, __float_as_uint(v[4 * i + 3]) & 0x7FFFFFFFu));
+            }
+            mxa = max(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
+            mxb = max(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
+            mxa = max(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
+            mxb = max(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
+            const int xa = (int)(mxa >> 23), xb = (int)(mxb >> 23);   // biased exponents
+            if (t4 == 0) {
+                if (!none_a && xa > 0 && xa < 255) atomicMin(qexp, (uint32_t)ra << 8 | (uint32_t)xa);
+                if (!none_b && xb > 0 && xb < 255) atomicMin(qexp, (uint32_t)rb << 8 | (uint32_t)xb);
+            }
             __syncwarp();
             mbar_arrive(q_max);
             ok = __all_sync(0xffffffffu, wait(q_max, 0));
-            const float sc = exp2i(prescale_exponent(__uint_as_float(*reinterpret_cast<volatile uint32_t*>(qmax))));
+            const int e = rows_exponent(*reinterpret_cast<volatile uint32_t*>(qexp));
+            auto own = [&](int x) -> int {   // a row's further exponent
+                const int y = x - 127 + e;
+                return x == 0 || (y >= -2 && y <= 14) ? 0 : max(-126 - e, min(127 - e, 7 - y));
+            };
+            const int da = own(xa), db = own(xb);
+            own_a = da != 0;
+            own_b = db != 0;
+            if (t4 == 0) {
+                rs[ra] = exp2f((float)-da);
+                rs[rb] = exp2f((float)-db);
+            }
+            __syncwarp();
+            const float sca = exp2i(e + da), scb = exp2i(e + db);
 #pragma unroll
             for (int q = 0; q < D / 16; ++q) {
                 uint32_t hw[4], lw[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int i = 2 * q + e;
-#pragma unroll
-                    for (int rr = 0; rr < 2; ++rr)
-                        split_f16x2(v[4 * i + 2 * rr] * sc, v[4 * i + 2 * rr + 1] * sc, hw[2 * rr + e], lw[2 * rr + e]);
+                for (int i = 2 * q; i < 2 * q + 2; ++i) {
+                    split_f16x2(v[4 * i] * sca, v[4 * i + 1] * sca, hw[i & 1], lw[i & 1]);
+                    split_f16x2(v[4 * i + 2] * scb, v[4 * i + 3] * scb, hw[2 + (i & 1)], lw[2 + (i & 1)]);
                 }
                 tmem_st_q1(trow + Tm::kQh + 8 * q, hw);
                 tmem_st_q1(trow + Tm::kQl + 8 * q, lw);
@@ -281,6 +314,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         }
         tc_fence_before();
         mbar_arrive(q_ready);
+        // Keys below this one need no mask; rows with a prescale of their own (rare) go with the masked ones.
+        const int plain_vis = own_a || own_b ? 0 : min(vis_a, vis_b);
         // ---- the key tiles
         // Reference maxima m (log2 units) as the exponents' offsets off = 127 - E - m; m = 0 and E = 127 until a
         // row has a key (any).
@@ -311,14 +346,14 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             tmem_ld_q8(scol, s);
             tmem_ld_q8(scol + 64, s + 32);
             tmem_ld_wait();
-            // Exponents e = S s'_K k0 2^-e - m + 127 - E (one FMA; scale 0: no key) against the references as they
+            // Exponents e = S s'_K k0 2^-e - m + 127 - E (one FMA) against the references as they
             // are, and their row maxima; a reference that moves is added to them afterwards, which is rare.
             const int key0 = (kt0 + j) * kPfKeys;
             const float4* skb = reinterpret_cast<const float4*>(sk + kr * kPfKeys) + t4;   // columns 16q + (2t, 2t + 1, 8 + 2t, 9 + 2t)
             const bool clean = (deadf[kr * 4] | deadf[kr * 4 + 1] | deadf[kr * 4 + 2] | deadf[kr * 4 + 3]) == 0u &&
-                               key0 + kPfKeys <= min(vis_a, vis_b);
+                               key0 + kPfKeys <= plain_vis;
             float bma = -INFINITY, bmb = -INFINITY;
-            if (__all_sync(0xffffffffu, clean)) {   // every key live and visible to both rows
+            if (__all_sync(0xffffffffu, clean)) {   // every key live and visible to both rows, rs 1
                 const float2 moa2 = make_float2(off_a, off_a), mob2 = make_float2(off_b, off_b);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -334,6 +369,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                     bmb = max3(bmb, eb.x, eb.y);
                 }
             } else {
+                const float rs_a = rs[ra], rs_b = rs[rb];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float4 k4 = skb[4 * (i / 2)];
@@ -342,8 +378,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                     for (int e = 0; e < 2; ++e) {
                         const float kk = e ? k2.y : k2.x;
                         const int key = key0 + 8 * i + 2 * t4 + e;
-                        const float ea = kk > 0.0f && key < vis_a ? fmaf(__uint_as_float(s[4 * i + e]), kk, off_a) : -INFINITY;
-                        const float eb = kk > 0.0f && key < vis_b ? fmaf(__uint_as_float(s[4 * i + 2 + e]), kk, off_b) : -INFINITY;
+                        const bool live = ((deadf[kr * 4 + i / 4] >> (8 * (i % 4) + 2 * t4 + e)) & 1u) == 0u;
+                        const float ea = live && key < vis_a ? fmaf(__uint_as_float(s[4 * i + e]) * rs_a, kk, off_a) : -INFINITY;
+                        const float eb = live && key < vis_b ? fmaf(__uint_as_float(s[4 * i + 2 + e]) * rs_b, kk, off_b) : -INFINITY;
                         s[4 * i + e] = __float_as_uint(ea);
                         s[4 * i + 2 + e] = __float_as_uint(eb);
                         bma = fmaxf(bma, ea);
@@ -535,7 +572,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                 if (j == 0) {   // the rows' prescale
                     ok = wait(q_max, 0);
                     if (!__all_sync(0xffffffffu, ok)) break;
-                    k0 *= exp2i(-prescale_exponent(__uint_as_float(*reinterpret_cast<volatile uint32_t*>(qmax))));
+                    k0 *= exp2i(-rows_exponent(*reinterpret_cast<volatile uint32_t*>(qexp)));
                 }
                 sk[(j % kPfKRing) * kPfKeys + slot_of_column(k)] = __uint_as_float(kw[Gm::KW] & 0xFFFFFFF0u) * k0;
                 const uint32_t nodead = __ballot_sync(0xffffffffu, kw[Gm::KW] == 0u);

@@ -200,8 +200,9 @@ __global__ void __launch_bounds__(kWriteThreads, ReadSmem<D, BITS, OT>::kBlocks)
     using Sm = ReadSmem<D, BITS, OT>;
     constexpr int TPV = Sh::kTpv, TV = Sh::kTileVecs, RB = Sm::RB, RW = RB / 4;
     extern __shared__ __align__(128) uint8_t smem[];
-    griddep_wait();   // the cache and the slots may come from the previous kernel
-    griddep_launch_dependents();
+    // The cache and the slots may come from the previous kernel.  No dependent starts early: it might take
+    // the rows read here as the queries it looks at before it waits.
+    griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int vl = lane / TPV, part = lane % TPV;
     uint8_t* wbuf = smem + warp * Sm::kPerWarp;

@@ -175,10 +175,37 @@ def test_bad_prefix_block_is_counted_and_skipped():
 
 
 def test_queries_of_very_different_magnitudes():
-    """One prescale serves a CTA's 128 rows: rows 2^12 apart, and rows of zeros."""
-    b = Batch(2048, _lens(2048, 12, 20, 3), 8, 2, 128, seed=15, outliers=False)
-    b.q *= (2.0 ** torch.tensor([0, -12, 0, -6, 0, 2, -12, -3, 0, 0, 1, -9], device="cuda")).to(b.q.dtype)[:, None, None]
+    """A CTA's rows share one prescale where they can: rows up to 2^100 apart, and rows of zeros."""
+    b = Batch(2048, _lens(2048, 14, 20, 3), 8, 2, 128, seed=15, outliers=False)
+    e = [0, -12, 0, -6, 0, 2, -12, -3, 0, 0, 1, -9, -100, -30]
+    b.q *= (2.0 ** torch.tensor(e, device="cuda")).to(b.q.dtype)[:, None, None]
     b.q[8] = 0
+    _check(b)
+    b.q[0] *= 2.0 ** -70   # the row the shared exponent comes from
+    _check(b)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 3e38])
+@pytest.mark.parametrize("where", [0, 5])
+def test_a_sequence_of_garbage_leaves_the_others_alone(where, bad):
+    """A query that is not finite, or huge, reaches only its own sequence's output; a padding row's reaches none."""
+    from gpu_helpers import assert_attention_close
+    b = Batch(2048, _lens(2048, 12, 20, 4), 8, 2, 128, seed=16)
+    ref = b.oracle()
+    b.q[where, :, ::3] = bad
+    got = b.shared()
+    keep = [i for i in range(12) if i != where]
+    assert_attention_close(got[keep], ref[keep])
+    b.lens[where] = 0
+    got = b.shared()
+    assert_attention_close(got[keep], ref[keep])
+    assert not got[where].any()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.05, 1e-30, 3.0])
+def test_softmax_scales(scale):
+    b = Batch(2030, [2031, 2040, 1000, 2029, 5, 2032, 2050, 1999, 2047], 8, 2, 64, seed=17, outliers=False)
+    b.scale = scale
     _check(b)
 
 
