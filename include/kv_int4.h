@@ -382,6 +382,7 @@ kv_int4_status kv_int4_paged_attention_ex(const void* q, kv_int4_dtype q_dtype, 
  * prefix_len     0 .. 16 max_blocks_per_seq + 15.
  * max_query_len  1 (a larger value returns KV_INT4_EUNSUPPORTED and launches nothing).
  * workspace      >= kv_int4_shared_prefix_workspace_bytes(...) bytes.
+ * options        as kv_int4_paged_attention_ex, or NULL.
  * Other arguments, alignment, supported sizes, clamping and error behaviour as kv_int4_paged_attention.
  */
 kv_int4_status kv_int4_shared_prefix_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens,
@@ -393,7 +394,8 @@ kv_int4_status kv_int4_shared_prefix_attention(const void* q, kv_int4_dtype q_dt
                                                int32_t num_seqs, int32_t max_query_len, int32_t max_seq_len,
                                                float softmax_scale, const float* rht_signs, int32_t segment_len,
                                                void* out, kv_int4_dtype out_dtype, void* workspace,
-                                               size_t workspace_bytes, kv_int4_stream_t stream);
+                                               size_t workspace_bytes, kv_int4_stream_t stream,
+                                               const kv_int4_attn_options* options);
 
 /*
  * Bytes of workspace kv_int4_shared_prefix_attention needs for these sizes: the decode path's for the

@@ -94,7 +94,8 @@ def _load():
     lib.kv_int2_paged_attention.argtypes = lib.kv_int4_paged_attention.argtypes
     lib.kv_int2_paged_attention.restype = ctypes.c_int
     lib.kv_int4_shared_prefix_attention.argtypes = [vp, ctypes.c_int, i64, i32, vp, i64, i32, i32, i32, vp, i32, vp, i32,
-                                                    vp, vp, i32, i32, i32, f32, vp, i32, vp, ctypes.c_int, vp, szt, vp]
+                                                    vp, vp, i32, i32, i32, f32, vp, i32, vp, ctypes.c_int, vp, szt, vp,
+                                                    ctypes.POINTER(AttnOptions)]
     lib.kv_int4_shared_prefix_attention.restype = ctypes.c_int
     lib.kv_int4_shared_prefix_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, i32, i32]
     lib.kv_int4_shared_prefix_workspace_bytes.restype = szt
@@ -241,9 +242,9 @@ except AttributeError:
         return torch.cuda.current_stream(device).cuda_stream
 
 
-def _call(fn: str, tensors, stream, *args) -> None:
-    """Call the library's ``fn`` with ``args`` and the stream on the device that all ``tensors`` (None entries
-    skipped) are on."""
+def _call(fn: str, tensors, stream, tail, *args) -> None:
+    """Call the library's ``fn`` with ``args``, the stream and ``tail`` (a tuple) on the device that all
+    ``tensors`` (None entries skipped) are on."""
     dev = -1
     for t in tensors:
         if t is not None:
@@ -258,10 +259,10 @@ def _call(fn: str, tensors, stream, *args) -> None:
         stream = stream.cuda_stream
     f = getattr(_lib or load(), fn)
     if dev == torch.cuda.current_device():
-        st = f(*args, stream)
+        st = f(*args, stream, *tail)
     else:
         with torch.cuda.device(dev):
-            st = f(*args, stream)
+            st = f(*args, stream, *tail)
     if st != 0:
         _check(fn, st)
 
@@ -326,7 +327,7 @@ def _rope_write(fn, bits, query, key, value, positions, cos_sin, slot_mapping, r
         qptr, qoptr = query.data_ptr(), query_out.data_ptr()
     elif query_out is not None:
         raise ValueError("query_out needs a query")
-    _call(fn, (query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache, query_out), stream,
+    _call(fn, (query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache, query_out), stream, (),
           qptr, qst, Hq, key.data_ptr(), kst, value.data_ptr(), vst, _DTYPES[dtype], T, H, d, positions.data_ptr(),
           cos_sin.data_ptr(), table[0], table[1], 1 if interleaved else 0, slot_mapping.data_ptr(), *signs, qoptr, qost,
           kv_cache.data_ptr(), cshape[0], cshape[2])
@@ -392,8 +393,8 @@ def _read(fn, bits, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out
         _cuda(value_out, "value_out", (key_out.dtype,))
     if key_out.shape != shape or value_out.shape != shape:
         raise ValueError(f"key_out and value_out must be [num_tokens, {H}, {d}]")
-    _call(fn, (kv_cache, slot_mapping, rht_signs, key_out, value_out), stream, kv_cache.data_ptr(), cshape[0], cshape[2],
-          H, d, slot_mapping.data_ptr(), T, *signs, key_out.data_ptr(), value_out.data_ptr(), _DTYPES[key_out.dtype])
+    _call(fn, (kv_cache, slot_mapping, rht_signs, key_out, value_out), stream, (), kv_cache.data_ptr(), cshape[0],
+          cshape[2], H, d, slot_mapping.data_ptr(), T, *signs, key_out.data_ptr(), value_out.data_ptr(), _DTYPES[key_out.dtype])
     return key_out, value_out
 
 
@@ -623,10 +624,12 @@ def kv_int4_shared_prefix_attention(query: torch.Tensor, kv_cache: torch.Tensor,
                                     prefix_len: int, block_tables: torch.Tensor, seq_lens: torch.Tensor,
                                     query_start_loc: torch.Tensor, softmax_scale: float, rht_signs: torch.Tensor,
                                     max_seq_len: int, out=None, out_dtype=None, segment_len: int = 0, workspace=None,
-                                    stream=None) -> torch.Tensor:
+                                    stream=None, window_left: int = -1, softcap: float = 0.0, alibi_slopes=None,
+                                    qq_bias=None) -> torch.Tensor:
     """kv_int4_paged_attention of a decode batch (one query token per sequence) whose first ``prefix_len``
     cached tokens are the same: their whole blocks are ``prefix_blocks`` (int32 [prefix_len // 16]), read once
-    for the batch; the other arguments as there, ``block_tables`` and ``seq_lens`` counting the prefix."""
+    for the batch; the other arguments and the options as there, ``block_tables`` and ``seq_lens`` counting
+    the prefix."""
     _cuda(query, "query", _HALF_TYPES)
     _cuda(kv_cache, "kv_cache", _U8)
     _cuda(prefix_blocks, "prefix_blocks", _I32)
@@ -657,8 +660,12 @@ def kv_int4_shared_prefix_attention(query: torch.Tensor, kv_cache: torch.Tensor,
             workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    opts = None
+    if window_left >= 0 or softcap != 0.0 or alibi_slopes is not None or qq_bias is not None:
+        opts = ctypes.byref(_options(Hq, 1, window_left, softcap, alibi_slopes, qq_bias))
     _call("kv_int4_shared_prefix_attention",
-          (query, kv_cache, prefix_blocks, block_tables, seq_lens, query_start_loc, rht_signs, out, workspace), stream,
+          (query, kv_cache, prefix_blocks, block_tables, seq_lens, query_start_loc, rht_signs, out, workspace,
+           alibi_slopes, qq_bias), stream, (opts,),
           query.data_ptr(), _DTYPES[query.dtype], Nq, Hq, kv_cache.data_ptr(), NB, H, d, bs, prefix_blocks.data_ptr(),
           prefix_len, block_tables.data_ptr(), tshape[1], seq_lens.data_ptr(), query_start_loc.data_ptr(), S, 1,
           max_seq_len, float(softmax_scale), rht_signs.data_ptr(), segment_len, out.data_ptr(), _DTYPES[out.dtype],

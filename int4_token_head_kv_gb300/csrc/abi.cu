@@ -447,7 +447,8 @@ kv_int4_status paged_attention_impl(int bits, const void* q, kv_int4_dtype q_dty
     const int32_t seg = kv_int4_attention_segment_len(num_seqs, walk_len, segment_len);
     if (seg <= 0) return KV_INT4_EINVAL;
     const int64_t len_cap = std::min<int64_t>(max_seq_len, (int64_t)max_blocks_per_seq * kBlockSize);
-    const int64_t max_blocks_total = (int64_t)num_seqs * ((len_cap + kBlockSize - 1) / kBlockSize);
+    const int64_t walk_cap = std::max<int64_t>(0, len_cap - px.len);
+    const int64_t max_blocks_total = (int64_t)num_seqs * ((walk_cap + kBlockSize - 1) / kBlockSize);
     if (max_blocks_total >= ((int64_t)1 << 31)) return KV_INT4_EUNSUPPORTED;   // 32-bit block positions
     WsLayout w;
     if (!ws_layout(num_q_heads, num_kv_heads, head_size, num_seqs, walk_len, seg, &w)) return KV_INT4_EINVAL;
@@ -612,7 +613,8 @@ kv_int4_status kv_int4_shared_prefix_attention(const void* q, kv_int4_dtype q_dt
                                                int32_t num_seqs, int32_t max_query_len, int32_t max_seq_len,
                                                float softmax_scale, const float* rht_signs, int32_t segment_len,
                                                void* out, kv_int4_dtype out_dtype, void* workspace,
-                                               size_t workspace_bytes, kv_int4_stream_t stream) {
+                                               size_t workspace_bytes, kv_int4_stream_t stream,
+                                               const kv_int4_attn_options* options) {
     if (prefix_len < 0 || max_query_len < 0) return KV_INT4_EINVAL;
     if (max_query_len > 1) return KV_INT4_EUNSUPPORTED;   // decode batches
     if (num_q_tokens > 0 && num_seqs > 0 && prefix_len >= kBlockSize && !prefix_blocks) return KV_INT4_EINVAL;
@@ -621,7 +623,7 @@ kv_int4_status kv_int4_shared_prefix_attention(const void* q, kv_int4_dtype q_dt
     return paged_attention_impl(4, q, q_dtype, num_q_tokens, num_q_heads, cache, num_blocks, num_kv_heads, head_size,
                                 block_size, block_tables, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs,
                                 max_query_len, max_seq_len, softmax_scale, rht_signs, segment_len, out, out_dtype,
-                                workspace, workspace_bytes, stream, nullptr, prefix_blocks, prefix_len);
+                                workspace, workspace_bytes, stream, options, prefix_blocks, prefix_len);
 }
 
 kv_int4_status kv_int8_paged_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens,

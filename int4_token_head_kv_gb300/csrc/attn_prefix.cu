@@ -21,10 +21,17 @@ int prefix_splits(int64_t row_tiles, int num_kv_heads, int prefix_len) {
     return (int)best;
 }
 
+namespace {
+template <int D, typename QT>
+cudaError_t prefix_by_options(const AttnParams& p, cudaStream_t stream) {
+    return p.opts != 0 ? launch_prefix_t<D, QT, true>(p, stream) : launch_prefix_t<D, QT, false>(p, stream);
+}
+}  // namespace
+
 cudaError_t launch_prefix(const AttnParams& p, int head_size, DType q_dt, cudaStream_t stream) {
     if (head_size == 128)
-        return q_dt == DType::BF16 ? launch_prefix_t<128, __nv_bfloat16>(p, stream) : launch_prefix_t<128, __half>(p, stream);
-    return q_dt == DType::BF16 ? launch_prefix_t<64, __nv_bfloat16>(p, stream) : launch_prefix_t<64, __half>(p, stream);
+        return q_dt == DType::BF16 ? prefix_by_options<128, __nv_bfloat16>(p, stream) : prefix_by_options<128, __half>(p, stream);
+    return q_dt == DType::BF16 ? prefix_by_options<64, __nv_bfloat16>(p, stream) : prefix_by_options<64, __half>(p, stream);
 }
 
 }  // namespace kvi4

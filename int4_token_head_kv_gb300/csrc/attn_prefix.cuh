@@ -12,13 +12,20 @@
 // Grid: (row tiles of 128 / G tokens) x kv heads x splits of the prefix's 128-key tiles, one CTA per SM.
 // The splits fill the SMs when the batch alone does not (prefix_splits).
 //
-// Warp roles (640 threads): warps 0-7 own the rows (rotation, softmax, epilogue), warps 8-11 dequantise
-// the K rows and warps 12-15 the V rows of a tile (one row per thread), warp 16 issues the MMAs, warps
-// 17-18 stage packed rows four tiles ahead, warp 19 is idle (it completes the last warpgroup, which the
-// register split needs).  The prefill dequantises with four warps, K then V, and is bound by that chain
-// (3 200 of its 3 500 cycles per tile); two plane groups halve it, and the registers they need come from
-// a setmaxnreg split: 136 for the rows, 72 for the dequantisation, 64 for the rest, together what 640
-// threads are launched with at 96.
+// Warp roles (640 threads): warps 0-7 own the rows (rotation, softmax, partials), warps 8-11 dequantise the K
+// rows and warps 12-15 the V rows of a tile (one row per thread), warp 16 issues the MMAs, warps 17-18 stage
+// packed rows four tiles ahead, warp 19 is idle (it completes the last warpgroup, which the register split
+// needs).  The registers come from a setmaxnreg split: 136 for the rows, 72 for the dequantisation, 64 for the
+// rest, together what 640 threads are launched with at 96.
+//
+// What bounds it (clock stamps in an instrumented copy, cycles per 128-key tile, d 128): 2 500-2 900 a tile.
+// Its 24 MMAs take 66 each, the softmax of a tile about 1 750 and the conversion of its K and V rows 700 and 900
+// beside it; the schedulers issue 0.6 instructions a cycle, so it is the instructions that count (1 850 per
+// scheduler and tile: 670 softmax, 540 dequantisation).  What the steps gave on 128 sequences, 131 072 shared
+// tokens, 64 q / 8 kv heads (961 us at first): block ids looked up four tiles ahead and copies without a spilled
+// table, descriptors in uniform registers: 812; one prescale per CTA, so that one FMA forms the exponent, and
+// a fixed MMA order: 775.  Tried and dropped: forming the weights before the maxima are known (no gain), 16
+// softmax warps with half of the keys each (923), output rows staged for bulk stores (no gain).
 #pragma once
 
 #include "attn_prefill.cuh"
@@ -47,7 +54,7 @@ struct PxLayout {
     static constexpr uint32_t kEblk = kSv + kPfPairs * kPfKeys * 4;              // [pairs][4] per-warp max V exponent
     static constexpr uint32_t kQexp = kEblk + kPfPairs * 4 * 4;                  // u32: first usable row and its exponent
     static constexpr uint32_t kRs = kQexp + 16;                                  // [128] f32 2^-d of each row's own prescale
-    static constexpr uint32_t kSignBits = kRs + 128 * 4;                            // [D / 32] u32
+    static constexpr uint32_t kSignBits = kRs + 128 * 4;                         // [D / 32] u32
     static constexpr uint32_t kBars = (kSignBits + D / 8 + 7u) & ~7u;
     // k_full[kring], k_free[pairs], v_full[pairs], v_free[pairs], pv_done[2], s_full[2], p_full[2], q_ready,
     // flush, q_tma, rot_in, rot_done, q_max, raw_full[plane][stages], raw_free[plane][stages]
@@ -82,7 +89,8 @@ __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.
 template <int REGS>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
 
-template <int D, typename QT>
+// OPTS: the call has logit options; every tile then takes the masked path, which applies them.
+template <int D, typename QT, bool OPTS>
 __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap) {
     using Gm = Geo<D>;
     using Ly = PxLayout<D>;
@@ -118,7 +126,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     uint64_t* rot_in = q_tma + 1;               // the rotation matrix in shared memory (256 arrivals)
     uint64_t* rot_done = rot_in + 1;            // the rotated queries in tensor memory (commit)
     uint64_t* q_max = rot_done + 1;             // the rows' exponent is known (256 arrivals)
-    uint64_t* raw_full = q_max + 1;          // [plane][stages] packed rows of a key tile landed (32 lanes)
+    uint64_t* raw_full = q_max + 1;             // [plane][stages] packed rows of a key tile landed (32 lanes)
     uint64_t* raw_free = raw_full + 2 * kPfRawStages;   // [plane][stages] that plane converted (128 arrivals)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kFlags);
@@ -166,8 +174,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         meta_a = row_meta(qt0 + r / G);
         meta_b = row_meta(qt0 + (r + 8) / G);
     }
-    // keys [0, n) of the prefix that a query token sees
-    auto visible = [&](int tok, const RowMeta& mt) -> int {
+    // cached tokens of a query token's sequence
+    auto context = [&](int tok, const RowMeta& mt) -> int {
         if ((int64_t)tok >= p.num_q_tokens) return 0;
         int len = mt.len;
         if (tok >= p.num_seqs || mt.q0 != tok || mt.q1 != tok + 1) {   // some sequences have no query: search
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             if (__ldg(p.qsl + lo) != tok || __ldg(p.qsl + lo + 1) != tok + 1) return 0;
             len = __ldg(p.seq_lens + lo);
         }
-        return max(0, min(min(len, p.len_cap), p.px_len));
+        return max(0, min(len, p.len_cap));
     };
     uint32_t* signbits = reinterpret_cast<uint32_t*>(smem + Ly::kSignBits);
     if (threadIdx.x < D) {   // whole warps (D is a multiple of 32)
@@ -245,7 +253,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         // A row that sees none (a padding row, or one past the batch) goes along as if it saw all, so that it
         // does not put its warp on the masked path, and its partial is empty at the end; a warp of such rows
         // leaves its weights unwritten.
-        int vis_a = visible(qt0 + ra / G, meta_a), vis_b = visible(qt0 + rb / G, meta_b);
+        const int len_a = context(qt0 + ra / G, meta_a), len_b = context(qt0 + rb / G, meta_b);
+        int vis_a = min(len_a, p.px_len), vis_b = min(len_b, p.px_len);
         const bool none_a = vis_a == 0, none_b = vis_b == 0;
         if (none_a) vis_a = p.px_len;
         if (none_b) vis_b = p.px_len;
@@ -353,7 +362,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             const bool clean = (deadf[kr * 4] | deadf[kr * 4 + 1] | deadf[kr * 4 + 2] | deadf[kr * 4 + 3]) == 0u &&
                                key0 + kPfKeys <= plain_vis;
             float bma = -INFINITY, bmb = -INFINITY;
-            if (__all_sync(0xffffffffu, clean)) {   // every key live and visible to both rows, rs 1
+            if (!OPTS && __all_sync(0xffffffffu, clean)) {   // every key live and visible to both rows, rs 1
                 const float2 moa2 = make_float2(off_a, off_a), mob2 = make_float2(off_b, off_b);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -370,6 +379,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                 }
             } else {
                 const float rs_a = rs[ra], rs_b = rs[rb];
+                const bool alibi = OPTS && (p.opts & kOptAlibi);
+                const float sl_a = alibi ? __ldg(p.alibi + h * G + ra % G) * kLog2e : 0.0f;
+                const float sl_b = alibi ? __ldg(p.alibi + h * G + rb % G) * kLog2e : 0.0f;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float4 k4 = skb[4 * (i / 2)];
@@ -379,8 +391,16 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                         const float kk = e ? k2.y : k2.x;
                         const int key = key0 + 8 * i + 2 * t4 + e;
                         const bool live = ((deadf[kr * 4 + i / 4] >> (8 * (i % 4) + 2 * t4 + e)) & 1u) == 0u;
-                        const float ea = live && key < vis_a ? fmaf(__uint_as_float(s[4 * i + e]) * rs_a, kk, off_a) : -INFINITY;
-                        const float eb = live && key < vis_b ? fmaf(__uint_as_float(s[4 * i + 2 + e]) * rs_b, kk, off_b) : -INFINITY;
+                        float ea, eb;
+                        if constexpr (OPTS) {   // on the log2 logit
+                            ea = live && key < vis_a ? __uint_as_float(s[4 * i + e]) * rs_a * kk : -INFINITY;
+                            eb = live && key < vis_b ? __uint_as_float(s[4 * i + 2 + e]) * rs_b * kk : -INFINITY;
+                            ea = apply_opts(ea, key, len_a - 1, sl_a, p, len_a - 1) + off_a;
+                            eb = apply_opts(eb, key, len_b - 1, sl_b, p, len_b - 1) + off_b;
+                        } else {
+                            ea = live && key < vis_a ? fmaf(__uint_as_float(s[4 * i + e]) * rs_a, kk, off_a) : -INFINITY;
+                            eb = live && key < vis_b ? fmaf(__uint_as_float(s[4 * i + 2 + e]) * rs_b, kk, off_b) : -INFINITY;
+                        }
                         s[4 * i + e] = __float_as_uint(ea);
                         s[4 * i + 2 + e] = __float_as_uint(eb);
                         bma = fmaxf(bma, ea);
@@ -732,16 +752,16 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     griddep_wait();
 }
 
-template <int D, typename QT>
+template <int D, typename QT, bool OPTS>
 cudaError_t launch_prefix_t(const AttnParams& p, cudaStream_t stream) {
     const size_t smem = PxLayout<D>::kBytes;
-    cudaError_t err = opt_in_smem<prefix_kernel<D, QT>>(smem);
+    cudaError_t err = opt_in_smem<prefix_kernel<D, QT, OPTS>>(smem);
     if (err != cudaSuccess) return err;
     // the register split waits for registers the launch did not give out if this does not hold
     static std::atomic<int> regs{0};
     if (regs.load(std::memory_order_acquire) == 0) {
         cudaFuncAttributes fa;
-        err = cudaFuncGetAttributes(&fa, prefix_kernel<D, QT>);
+        err = cudaFuncGetAttributes(&fa, prefix_kernel<D, QT, OPTS>);
         if (err != cudaSuccess) return err;
         regs.store(fa.numRegs, std::memory_order_release);
     }
@@ -760,7 +780,7 @@ cudaError_t launch_prefix_t(const AttnParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefix_kernel<D, QT>, p, qmap);
+    return cudaLaunchKernelEx(&cfg, prefix_kernel<D, QT, OPTS>, p, qmap);
 }
 
 }  // namespace

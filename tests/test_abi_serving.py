@@ -67,13 +67,17 @@ def test_shared_prefix(lib):
     f = lib.kv_int4_shared_prefix_attention
     f.restype = ctypes.c_int
     f.argtypes = [vp, ctypes.c_int, i64, i32, vp, i64, i32, i32, i32, vp, i32, vp, i32, vp, vp, i32, i32, i32, f32, vp,
-                  i32, vp, ctypes.c_int, vp, szt, vp]
+                  i32, vp, ctypes.c_int, vp, szt, vp, vp]
     base = dict(q=FAKE, qd=1, nq=4, hq=32, cache=FAKE, nb=64, h=8, d=128, bs=16, pb=FAKE, pl=4096, bt=FAKE, mb=260, sl=FAKE,
-                qsl=FAKE, ns=4, mql=1, msl=4160, scale=0.088, signs=FAKE, seg=0, out=FAKE, od=2, ws=None, wsb=0, st=None)
+                qsl=FAKE, ns=4, mql=1, msl=4160, scale=0.088, signs=FAKE, seg=0, out=FAKE, od=2, ws=None, wsb=0, st=None, opts=None)
 
     def call(**kw):
         return f(*dict(base, **kw).values())
 
+    from int4_token_head_kv_gb300 import AttnOptions
+    for bad in (AttnOptions(-1, -1.0, None, None, 0), AttnOptions(-1, float("nan"), None, None, 0),
+                AttnOptions(-1, 0.0, None, FAKE, 0)):
+        assert call(opts=ctypes.addressof(bad)) == 1
     assert call(mql=2) == 2 and call(h=3, hq=24) == 2 and call(d=80) == 2 and call(seg=24) == 2 and call(od=5) == 2
     assert call(pl=-1) == 1 and call(pb=None) == 1 and call(pl=16 * 261) == 1 and call(q=None) == 1 and call(signs=None) == 1
     assert call(out=FAKE + 4) == 3

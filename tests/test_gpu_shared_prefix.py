@@ -209,6 +209,27 @@ def test_softmax_scales(scale):
     _check(b)
 
 
+@pytest.mark.parametrize("opts", [dict(softcap=5.0), dict(window_left=900), dict(window_left=10), dict(alibi=True),
+                                  dict(qq=True), dict(softcap=3.0, window_left=1500, alibi=True, qq=True)])
+@pytest.mark.parametrize("Hq, H, d", [(8, 2, 128), (8, 1, 64)])
+def test_options(Hq, H, d, opts):
+    from gpu_helpers import assert_attention_close
+    b = Batch(2030, [2031, 2040, 1000, 2029, 0, 2032, 2050, 1999, 2047, 15], Hq, H, d, seed=18, outliers=False)
+    assert b.is_shared()
+    o = {k: v for k, v in opts.items() if k in ("softcap", "window_left")}
+    g = dict(o)
+    if "alibi" in opts:
+        o["alibi_slopes"] = np.float32(2.0) ** -np.arange(1, Hq + 1, dtype=np.float32)
+        g["alibi_slopes"] = torch.from_numpy(o["alibi_slopes"]).cuda()
+    if "qq" in opts:
+        o["qq_bias"] = np.full((1, 1), 1.5, np.float32)
+        g["qq_bias"] = torch.from_numpy(o["qq_bias"]).cuda()
+    ref = oracle.paged_attention(b.q, b.cache.cpu().numpy(), b.tables, b.lens, b.qsl, b.scale, b.signs, **o)
+    assert_attention_close(b.shared(**g), ref, str(opts))
+    small = Batch(256, [260, 300, 257], Hq, H, d, seed=19)
+    assert not small.is_shared() and torch.equal(small.shared(**g), small.plain(**g))
+
+
 def test_heavy_tails_and_large_scales():
     b = Batch(2000, _lens(2000, 9, 90, 7), 16, 2, 128, seed=7)
     assert b.is_shared()
