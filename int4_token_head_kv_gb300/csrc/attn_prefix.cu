@@ -24,7 +24,8 @@ int prefix_splits(int64_t row_tiles, int num_kv_heads, int prefix_len) {
 namespace {
 template <int D, typename QT>
 cudaError_t prefix_by_options(const AttnParams& p, cudaStream_t stream) {
-    return p.opts != 0 ? launch_prefix_t<D, QT, true>(p, stream) : launch_prefix_t<D, QT, false>(p, stream);
+    if (p.opts != 0) return launch_prefix_t<D, QT, true, true>(p, stream);
+    return p.px_two ? launch_prefix_t<D, QT, false, true>(p, stream) : launch_prefix_t<D, QT, false, false>(p, stream);
 }
 }  // namespace
 

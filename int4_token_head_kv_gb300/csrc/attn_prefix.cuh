@@ -90,7 +90,10 @@ template <int REGS>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
 
 // OPTS: the call has logit options; every tile then takes the masked path, which applies them.
-template <int D, typename QT, bool OPTS>
+// TWO: the weights too are carried as high + low halves (the low ones over S's last 64 columns).  One fp16
+// weight per key errs by up to 2^-11, as much as the rounding of an fp16 output: results were 1.4-1.7 times
+// as far off as that rounding alone.  A bf16 output does not show it, and is spared the 5-8% of the call.
+template <int D, typename QT, bool OPTS, bool TWO>
 __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap) {
     using Gm = Geo<D>;
     using Ly = PxLayout<D>;
@@ -478,7 +481,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             float2 lsa = make_float2(0.0f, 0.0f), lsb = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                uint32_t pw[4];
+                uint32_t pw[4], pl[4];
                 const float4 v4 = svb[4 * q];
 #pragma unroll
                 for (int i = 2 * q; i < 2 * q + 2; ++i) {
@@ -489,10 +492,16 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                     lsb = add_f32x2(lsb, pb);
                     const float2 wa = mul_f32x2(pa, v2), wb = mul_f32x2(pb, v2);
                     const int e = i & 1;
-                    pw[e] = pack_f16x2(wa.x, wa.y);
-                    pw[2 + e] = pack_f16x2(wb.x, wb.y);
+                    if constexpr (TWO) {
+                        split_f16x2(wa.x, wa.y, pw[e], pl[e]);
+                        split_f16x2(wb.x, wb.y, pw[2 + e], pl[2 + e]);
+                    } else {
+                        pw[e] = pack_f16x2(wa.x, wa.y);
+                        pw[2 + e] = pack_f16x2(wb.x, wb.y);
+                    }
                 }
                 tmem_st_q1(scol + 8 * q, pw);
+                if constexpr (TWO) tmem_st_q1(scol + 64 + 8 * q, pl);
             }
             l_a += lsa.x + lsa.y;
             l_b += lsb.x + lsb.y;
@@ -712,8 +721,10 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                 const uint64_t vd = (t & 1) ? vd1 : vd0;
                 if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < kPfKeys / 16; ++kk)   // P of keys 16 kk .. 16 kk + 15 (in contraction order)
+                    for (int kk = 0; kk < kPfKeys / 16; ++kk) {   // P of keys 16 kk .. 16 kk + 15 (in contraction order)
                         mma_ts(tmem + Tm::kO, pcol + 8u * kk, vd + ((kk * 16 * 128) >> 4), idPV, t > 0 || kk > 0);
+                        if constexpr (TWO) mma_ts(tmem + Tm::kO, pcol + 64u + 8u * kk, vd + ((kk * 16 * 128) >> 4), idPV, true);
+                    }
                     mma_commit(&pv_done[t & 1]);
                     mma_commit(&v_free[t % kPfPairs]);
                 }
@@ -752,16 +763,16 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     griddep_wait();
 }
 
-template <int D, typename QT, bool OPTS>
+template <int D, typename QT, bool OPTS, bool TWO>
 cudaError_t launch_prefix_t(const AttnParams& p, cudaStream_t stream) {
     const size_t smem = PxLayout<D>::kBytes;
-    cudaError_t err = opt_in_smem<prefix_kernel<D, QT, OPTS>>(smem);
+    cudaError_t err = opt_in_smem<prefix_kernel<D, QT, OPTS, TWO>>(smem);
     if (err != cudaSuccess) return err;
     // the register split waits for registers the launch did not give out if this does not hold
     static std::atomic<int> regs{0};
     if (regs.load(std::memory_order_acquire) == 0) {
         cudaFuncAttributes fa;
-        err = cudaFuncGetAttributes(&fa, prefix_kernel<D, QT, OPTS>);
+        err = cudaFuncGetAttributes(&fa, prefix_kernel<D, QT, OPTS, TWO>);
         if (err != cudaSuccess) return err;
         regs.store(fa.numRegs, std::memory_order_release);
     }
@@ -780,7 +791,7 @@ cudaError_t launch_prefix_t(const AttnParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefix_kernel<D, QT, OPTS>, p, qmap);
+    return cudaLaunchKernelEx(&cfg, prefix_kernel<D, QT, OPTS, TWO>, p, qmap);
 }
 
 }  // namespace

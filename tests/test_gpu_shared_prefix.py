@@ -260,6 +260,21 @@ def test_larger_batches_match_the_plain_call(S, prefix, Hq, H, d):
     assert not any(status().values())
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_finer_than_bf16_are_not_rounded_by_the_weights(d, dtype):
+    """fp16 and fp32 outputs carry the weights in two halves: the error against 64 bits, in the 2-norm, stays
+    near the output's own rounding.  (fp32: Q' and the weights keep 22 bits, the products' sums are fp32 over
+    128 dimensions and some thousand keys; a single fp16 weight would give about 2e-4.)"""
+    b = Batch(2100, _lens(2100, 10, 30, 6), 8, 2, d, dtype=dtype, seed=20)
+    assert b.is_shared()
+    ref = torch.from_numpy(b.oracle())
+    err = lambda out: float((out.double().cpu() - ref).norm() / ref.norm())
+    assert err(b.shared(torch.float32)) < 2e-5
+    # half a step is 2^-11 at most, its root mean square over the mantissas and signs about 0.42 of it
+    assert err(b.shared(torch.float16)) < 0.5 * 2.0 ** -11
+
+
 def test_same_bits_again_and_captured():
     b = Batch(1000, [1001 + 9 * i for i in range(20)], 32, 8, 128, seed=8)
     first = b.shared(out_dtype=torch.bfloat16)
