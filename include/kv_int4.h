@@ -189,8 +189,8 @@ kv_int4_status kv_int2_write(const void* k, const void* v, kv_int4_dtype dtype, 
  * cos_sin        [max_position, rot_dim] fp32, 16-B aligned.  rot_dim: a multiple of 16, 16..head_size.
  * slot_mapping   as kv_int4_write; a token with a negative slot still has its query rotated.  Slots
  *                that are not negative must be distinct within the call.
- * q_out          may be q itself with the same stride (rotation in place); otherwise it must not
- *                overlap q, k or v.
+ * q_out          may be q itself with the same stride (rotation in place; with another one
+ *                KV_INT4_EINVAL); otherwise it must not overlap q, k or v.
  * Other arguments, limits and errors as kv_int4_write.
  */
 kv_int4_status kv_int4_rope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
@@ -379,7 +379,7 @@ kv_int4_status kv_int4_paged_attention_ex(const void* q, kv_int4_dtype q_dtype, 
  * so a sequence's output may differ in the last bits between batches; the same call gives the same bits.
  *
  * prefix_blocks  [prefix_len / 16] int32, may be NULL when prefix_len < 16.
- * prefix_len     0 .. 16 max_blocks_per_seq + 15.
+ * prefix_len     0 .. 16 max_blocks_per_seq + 15, at most 2^30.
  * max_query_len  1 (a larger value returns KV_INT4_EUNSUPPORTED and launches nothing).
  * workspace      >= kv_int4_shared_prefix_workspace_bytes(...) bytes.
  * options        as kv_int4_paged_attention_ex, or NULL.

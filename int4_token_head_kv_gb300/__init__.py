@@ -242,9 +242,24 @@ except AttributeError:
         return torch.cuda.current_stream(device).cuda_stream
 
 
-def _call(fn: str, tensors, stream, tail, *args) -> None:
-    """Call the library's ``fn`` with ``args``, the stream and ``tail`` (a tuple) on the device that all
-    ``tensors`` (None entries skipped) are on."""
+def _current(stream, tensor: torch.Tensor):
+    """A context with ``stream`` (a torch stream, or a raw handle on the tensor's device) as the current one.
+    The serving calls run whole inside it, so that what they allocate belongs to the stream that uses it:
+    memory from another stream's pool could be in use there, or be handed out again while this one runs."""
+    if not isinstance(tensor, torch.Tensor) or not tensor.is_cuda:
+        raise ValueError("the call's tensors must be CUDA tensors")
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        stream = (torch.cuda.ExternalStream(handle, device=tensor.device) if handle else
+                  torch.cuda.default_stream(tensor.device))
+    elif stream.device != tensor.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {tensor.device}")
+    return torch.cuda.stream(stream)
+
+
+def _call(fn: str, tensors, tail, *args) -> None:
+    """Call the library's ``fn`` with ``args``, the current stream and ``tail`` (a tuple) on the device that
+    all ``tensors`` (None entries skipped) are on."""
     dev = -1
     for t in tensors:
         if t is not None:
@@ -253,10 +268,7 @@ def _call(fn: str, tensors, stream, tail, *args) -> None:
                 if dev >= 0:
                     _one_device(*tensors)   # raises
                 dev = i
-    if stream is None:
-        stream = _raw_stream(dev)
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
+    stream = _raw_stream(dev)
     f = getattr(_lib or load(), fn)
     if dev == torch.cuda.current_device():
         st = f(*args, stream, *tail)
@@ -286,6 +298,10 @@ _I64, _F32, _U8, _I32 = (torch.int64,), (torch.float32,), (torch.uint8,), (torch
 
 def _rope_write(fn, bits, query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache, query_out,
                 interleaved, stream):
+    if stream is not None:
+        with _current(stream, key):
+            return _rope_write(fn, bits, query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache,
+                               query_out, interleaved, None)
     kshape, kst = _token_rows(key, "key", _HALF_TYPES)
     dtype = key.dtype
     vshape, vst = _token_rows(value, "value", (dtype,))
@@ -327,7 +343,7 @@ def _rope_write(fn, bits, query, key, value, positions, cos_sin, slot_mapping, r
         qptr, qoptr = query.data_ptr(), query_out.data_ptr()
     elif query_out is not None:
         raise ValueError("query_out needs a query")
-    _call(fn, (query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache, query_out), stream, (),
+    _call(fn, (query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache, query_out), (),
           qptr, qst, Hq, key.data_ptr(), kst, value.data_ptr(), vst, _DTYPES[dtype], T, H, d, positions.data_ptr(),
           cos_sin.data_ptr(), table[0], table[1], 1 if interleaved else 0, slot_mapping.data_ptr(), *signs, qoptr, qost,
           kv_cache.data_ptr(), cshape[0], cshape[2])
@@ -365,6 +381,9 @@ def kv_int2_rope_write(query, key: torch.Tensor, value: torch.Tensor, positions:
 
 
 def _read(fn, bits, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, stream):
+    if stream is not None:
+        with _current(stream, kv_cache):
+            return _read(fn, bits, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, None)
     _cuda(kv_cache, "kv_cache", _U8)
     _cuda(slot_mapping, "slot_mapping", _I64)
     sshape, cshape = slot_mapping.shape, kv_cache.shape
@@ -393,7 +412,7 @@ def _read(fn, bits, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out
         _cuda(value_out, "value_out", (key_out.dtype,))
     if key_out.shape != shape or value_out.shape != shape:
         raise ValueError(f"key_out and value_out must be [num_tokens, {H}, {d}]")
-    _call(fn, (kv_cache, slot_mapping, rht_signs, key_out, value_out), stream, (), kv_cache.data_ptr(), cshape[0],
+    _call(fn, (kv_cache, slot_mapping, rht_signs, key_out, value_out), (), kv_cache.data_ptr(), cshape[0],
           cshape[2], H, d, slot_mapping.data_ptr(), T, *signs, key_out.data_ptr(), value_out.data_ptr(), _DTYPES[key_out.dtype])
     return key_out, value_out
 
@@ -630,6 +649,12 @@ def kv_int4_shared_prefix_attention(query: torch.Tensor, kv_cache: torch.Tensor,
     cached tokens are the same: their whole blocks are ``prefix_blocks`` (int32 [prefix_len // 16]), read once
     for the batch; the other arguments and the options as there, ``block_tables`` and ``seq_lens`` counting
     the prefix."""
+    if stream is not None:
+        with _current(stream, query):
+            return kv_int4_shared_prefix_attention(query, kv_cache, prefix_blocks, prefix_len, block_tables, seq_lens,
+                                                   query_start_loc, softmax_scale, rht_signs, max_seq_len, out,
+                                                   out_dtype, segment_len, workspace, None, window_left, softcap,
+                                                   alibi_slopes, qq_bias)
     _cuda(query, "query", _HALF_TYPES)
     _cuda(kv_cache, "kv_cache", _U8)
     _cuda(prefix_blocks, "prefix_blocks", _I32)
@@ -647,7 +672,7 @@ def kv_int4_shared_prefix_attention(query: torch.Tensor, kv_cache: torch.Tensor,
         raise ValueError("kv_cache / rht_signs do not match the query's head size")
     if query_start_loc.shape != (S + 1,) or len(tshape) != 2 or tshape[0] != S:
         raise ValueError("block_tables must be [num_seqs, max_blocks] and query_start_loc [num_seqs + 1]")
-    if prefix_blocks.dim() != 1 or prefix_blocks.shape[0] < prefix_len // bs:
+    if prefix_blocks.dim() != 1 or prefix_blocks.shape[0] < prefix_len // max(bs, 1):
         raise ValueError("prefix_blocks must hold the prefix's prefix_len // block_size block ids")
     if out is None:
         out = torch.empty(qshape, dtype=out_dtype or query.dtype, device=query.device)
@@ -665,7 +690,7 @@ def kv_int4_shared_prefix_attention(query: torch.Tensor, kv_cache: torch.Tensor,
         opts = ctypes.byref(_options(Hq, 1, window_left, softcap, alibi_slopes, qq_bias))
     _call("kv_int4_shared_prefix_attention",
           (query, kv_cache, prefix_blocks, block_tables, seq_lens, query_start_loc, rht_signs, out, workspace,
-           alibi_slopes, qq_bias), stream, (opts,),
+           alibi_slopes, qq_bias), (opts,),
           query.data_ptr(), _DTYPES[query.dtype], Nq, Hq, kv_cache.data_ptr(), NB, H, d, bs, prefix_blocks.data_ptr(),
           prefix_len, block_tables.data_ptr(), tshape[1], seq_lens.data_ptr(), query_start_loc.data_ptr(), S, 1,
           max_seq_len, float(softmax_scale), rht_signs.data_ptr(), segment_len, out.data_ptr(), _DTYPES[out.dtype],

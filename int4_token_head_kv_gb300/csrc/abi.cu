@@ -213,6 +213,8 @@ kv_int4_status rope_write_impl(int bits, const void* q, int64_t q_token_stride, 
     if (num_q_heads > 0 && (!aligned16(q) || !aligned16(q_out) ||
                             (num_tokens > 1 && (q_token_stride % 8 != 0 || q_out_token_stride % 8 != 0))))
         return KV_INT4_EALIGN;
+    // in place only with one stride: with two, a token's result could land on another's query
+    if (num_tokens > 1 && num_q_heads > 0 && q == q_out && q_token_stride != q_out_token_stride) return KV_INT4_EINVAL;
     RopeWriteParams p;
     p.w.k = k;
     p.w.v = v;
@@ -594,8 +596,8 @@ kv_int4_status kv_int4_paged_attention_ex(const void* q, kv_int4_dtype q_dtype, 
 size_t kv_int4_shared_prefix_workspace_bytes(int64_t num_q_tokens, int32_t num_q_heads, int32_t num_kv_heads,
                                              int32_t head_size, int32_t num_seqs, int32_t prefix_len,
                                              int32_t max_seq_len, int32_t segment_len) {
-    if (num_seqs <= 0 || max_seq_len < 0 || num_q_tokens <= 0 || prefix_len < 0 || num_kv_heads <= 0 || num_q_heads <= 0 ||
-        num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > kPrefillRows)
+    if (num_seqs <= 0 || max_seq_len < 0 || num_q_tokens <= 0 || prefix_len < 0 || prefix_len > (1 << 30) ||
+        num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > kPrefillRows)
         return 0;
     const PrefixLayout px = prefix_layout(num_q_tokens, num_q_heads, num_kv_heads, head_size, num_seqs, prefix_len);
     const int32_t walk_len = std::max(0, max_seq_len - px.len);
@@ -618,6 +620,7 @@ kv_int4_status kv_int4_shared_prefix_attention(const void* q, kv_int4_dtype q_dt
                                                const kv_int4_attn_options* options) {
     if (prefix_len < 0 || max_query_len < 0) return KV_INT4_EINVAL;
     if (max_query_len > 1) return KV_INT4_EUNSUPPORTED;   // decode batches
+    if (prefix_len > (1 << 30)) return KV_INT4_EUNSUPPORTED;   // 32-bit key indices, rounded up to tiles
     if (num_q_tokens > 0 && num_seqs > 0 && prefix_len >= kBlockSize && !prefix_blocks) return KV_INT4_EINVAL;
     // the prefix's blocks are the first of every sequence's table
     if (prefix_len / kBlockSize > max_blocks_per_seq) return KV_INT4_EINVAL;

@@ -19,12 +19,12 @@
 // rest, together what 640 threads are launched with at 96.
 //
 // What bounds it (clock stamps in an instrumented copy, cycles per 128-key tile, d 128): 2 500-2 900 a tile.
-// Its 24 MMAs take 66 each, the softmax of a tile about 1 750 and the conversion of its K and V rows 700 and 900
+// Its 24 MMAs (32 with the weights in two halves) take 66 each, the softmax of a tile about 1 750 and the conversion of its K and V rows 700 and 900
 // beside it; the schedulers issue 0.6 instructions a cycle, so it is the instructions that count (1 850 per
 // scheduler and tile: 670 softmax, 540 dequantisation).  What the steps gave on 128 sequences, 131 072 shared
 // tokens, 64 q / 8 kv heads (961 us at first): block ids looked up four tiles ahead and copies without a spilled
 // table, descriptors in uniform registers: 812; one prescale per CTA, so that one FMA forms the exponent, and
-// a fixed MMA order: 775.  Tried and dropped: forming the weights before the maxima are known (no gain), 16
+// a fixed MMA order: 775; a walker grid for the tokens behind the prefix alone: 729.  Tried and dropped: forming the weights before the maxima are known (no gain), 16
 // softmax warps with half of the keys each (923), output rows staged for bulk stores (no gain).
 #pragma once
 

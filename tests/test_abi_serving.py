@@ -101,3 +101,16 @@ def test_shared_prefix(lib):
     assert w(4, 32, 8, 128, 4, 4080, 4160, 0) == plain(32, 8, 128, 4, 4160, 0)  # below 16 384 tokens in all
     assert w(2, 8, 2, 128, 2, 4096, 4160, 0) > plain(8, 2, 128, 2, 64, 0)       # 8 192 with few kv heads
     assert w(0, 32, 8, 128, 4, 256, 320, 0) == 0 and w(4, 30, 8, 128, 4, 256, 320, 0) == 0 and w(4, 32, 8, 128, 0, 256, 320, 0) == 0
+    assert call(pl=(1 << 30) + 1, mb=1 << 27) == 2            # 32-bit key indices
+    assert w(4, 32, 8, 128, 4, (1 << 30) + 1, 1 << 30, 0) == 0
+
+
+@pytest.mark.parametrize("name", ["kv_int4_rope_write", "kv_int8_rope_write", "kv_int2_rope_write"])
+def test_rope_write_in_place_needs_one_stride(lib, name):
+    f = getattr(lib, name)
+    f.restype = ctypes.c_int
+    signs = [vp] if "8" not in name else []
+    f.argtypes = [vp, i64, i32, vp, i64, vp, i64, ctypes.c_int, i64, i32, i32, vp, vp, i64, i32, i32, vp] + signs + \
+        [vp, i64, vp, i64, i32, vp]
+    head = (FAKE, 1024, 8, FAKE, 256, FAKE, 256, 1, 4, 2, 128, FAKE, FAKE, 64, 128, 0, FAKE) + (FAKE,) * len(signs)
+    assert f(*head, FAKE, 2048, FAKE, 8, 16, None) == 1

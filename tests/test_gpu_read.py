@@ -161,3 +161,25 @@ def test_write_then_read_keeps_the_vectors(bits):
             assert bool((err < x.norm(dim=-1)).all())   # sigma and the centroids keep less than the norm lost
         else:
             assert bool((err <= 128 ** 0.5 * step).all())
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_belong_to_the_stream_that_writes_them(raw):
+    """Outputs allocated by a call on another stream and dropped while it has yet to run: the current stream
+    must not be handed their memory."""
+    kv = _kv()
+    cache = torch.from_numpy(_random_cache(4, 4, 2, 64, seed=6)).cuda()
+    signs, slots = torch.ones(64, device="cuda"), torch.arange(64, device="cuda").repeat(200)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(50_000_000)
+    out = kv.kv_int4_read(cache, slots, signs, dtype=torch.float32, stream=s.cuda_stream if raw else s)
+    shape = out[0].shape
+    del out
+    a, b = torch.zeros(shape, device="cuda"), torch.zeros(shape, device="cuda")
+    torch.cuda.synchronize()
+    assert not a.any() and not b.any()
+    got = kv.kv_int4_read(cache, slots, signs, dtype=torch.float32, stream=0)   # the default stream's handle
+    want = kv.kv_int4_read(cache, slots, signs, dtype=torch.float32)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -350,3 +350,45 @@ def test_a_serving_step_as_it_runs():
         assert_attention_close(outs[i], ref, f"step {i}")
         want = oracle.decode_rows(cache[slots[i] // 16, 0, slots[i] % 16].reshape(S * H, -1), b.signs).reshape(S, H, d)
         assert np.allclose(rows[i][0].cpu().numpy(), want, rtol=1e-6, atol=1e-9)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace, overlap and keep their bits."""
+    a, b = Batch(4096, _lens(4096, 40, 300, 1), 32, 8, 128, seed=11), Batch(3000, _lens(3000, 30, 200, 2), 8, 1, 64, seed=12)
+    want = a.shared(), b.shared()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    args = [(x.q, x.cache, torch.from_numpy(x.prefix_blocks).cuda(), x.prefix) + x._args() + (x.scale, x.gsigns, x.max_len)
+            for x in (a, b)]   # alive until both streams are done
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            got[i].append(_kv().kv_int4_shared_prefix_attention(*args[i], out_dtype=torch.float32, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+def test_blocks_past_32_bit_offsets():
+    """A cache of more than 4 GiB whose last blocks hold everything: rotary write, read-back and attention at
+    byte offsets past 32 bits give the bits of the same rows in a small cache."""
+    kv = _kv()
+    b = Batch(1024, _lens(1024, 20, 30, 3), 32, 8, 128, seed=13)
+    assert b.is_shared()
+    small, nb = b.cache, b.cache.shape[0]
+    far = (1 << 32) // (small.stride(0)) + 100
+    big = torch.zeros((far + nb,) + tuple(small.shape[1:]), dtype=torch.uint8, device="cuda")
+    assert far * small.stride(0) > 1 << 32
+    r = np.random.default_rng(4)
+    x = torch.from_numpy(r.standard_normal((nb * 16, 48, 128)).astype(np.float32)).bfloat16().cuda()
+    tab = torch.from_numpy(r.uniform(-1, 1, (64, 128)).astype(np.float32)).cuda()
+    pos, slots = torch.arange(nb * 16, device="cuda") % 64, torch.arange(nb * 16, device="cuda")
+    for cache, off in ((small, 0), (big, far)):
+        kv.kv_int4_rope_write(x[:, :32], x[:, 32:40], x[:, 40:], pos, tab, slots + 16 * off, b.gsigns, cache)
+    assert torch.equal(big[far:], small) and not big[:far].any()
+    want = kv.kv_int4_read(small, slots, b.gsigns)
+    got = kv.kv_int4_read(big, slots + 16 * far, b.gsigns)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    want = b.shared()
+    b.cache, b.tables, b.prefix_blocks = big, b.tables + np.int32(far), b.prefix_blocks + np.int32(far)
+    assert torch.equal(b.shared(), want)
