@@ -18,14 +18,19 @@
 // needs).  The registers come from a setmaxnreg split: 136 for the rows, 72 for the dequantisation, 64 for the
 // rest, together what 640 threads are launched with at 96.
 //
-// What bounds it (clock stamps in an instrumented copy, cycles per 128-key tile, d 128): 2 500-2 900 a tile.
-// Its 24 MMAs (32 with the weights in two halves) take 66 each, the softmax of a tile about 1 750 and the conversion of its K and V rows 700 and 900
-// beside it; the schedulers issue 0.6 instructions a cycle, so it is the instructions that count (1 850 per
-// scheduler and tile: 670 softmax, 540 dequantisation).  What the steps gave on 128 sequences, 131 072 shared
-// tokens, 64 q / 8 kv heads (961 us at first): block ids looked up four tiles ahead and copies without a spilled
-// table, descriptors in uniform registers: 812; one prescale per CTA, so that one FMA forms the exponent, and
-// a fixed MMA order: 775; a walker grid for the tokens behind the prefix alone: 729.  Tried and dropped: forming the weights before the maxima are known (no gain), 16
-// softmax warps with half of the keys each (923), output rows staged for bulk stores (no gain).
+// What bounds it (clock stamps in an instrumented copy, cycles per 128-key tile, d 128): about 3 000 a tile, of
+// which the tensor pipe computes 1 600 (24 MMAs of 66; 32 with the weights in two halves).  A tile goes round the
+// chain S (1 230 to issue) -> softmax (1 970, among the dequantisation's instructions) -> P.V (600) -> the S after
+// next, which takes the same of the two S buffers, and each hand-over costs 300-700 until the MMAs issued have
+// run and the other side is awake; tensor memory is full (two S, O, the queries' halves), so there is no third
+// buffer.  Beside it K's and V's rows of a tile take 700 and 1 000.  What the steps gave on 128 sequences, 131 072
+// shared tokens, 64 q / 8 kv heads (961 us at first): block ids looked up four tiles ahead and copies without a
+// spilled table, descriptors in uniform registers: 812; one prescale per CTA, so that one FMA forms the
+// exponent, and a fixed MMA order: 775; a walker grid for the tokens behind the prefix alone: 729; packed rows by
+// TMA boxes instead of 16-byte copies: 696; polling in the chain's waits: 665.  Tried and dropped: forming the
+// weights before the maxima are known (no gain), 16 softmax warps with half of the keys each (923), output rows
+// staged for bulk stores (no gain), S as two products of 64 keys, so that one of them need not wait for P.V (713
+// against 683), weights handed over in two halves (674 against 665).
 #pragma once
 
 #include "attn_prefill.cuh"
@@ -37,6 +42,7 @@ constexpr int kPxDequantWarp = kPfSoftmaxWarps;          // K group, then the V 
 constexpr int kPxMmaWarp = kPxDequantWarp + 8;
 constexpr int kPxLoadWarp = kPxMmaWarp + 1;              // one per plane (K, V)
 constexpr int kPxThreads = (kPxMmaWarp + 4) * 32;
+constexpr int kPxPolls = 128;                            // about 4 000 cycles, a tile and a bit
 constexpr int kPxLaunchRegs = 96, kPxRowRegs = 136, kPxDequantRegs = 72, kPxOtherRegs = 64;
 static_assert(kPxRowRegs * 256 + kPxDequantRegs * 256 + kPxOtherRegs * 128 == kPxLaunchRegs * kPxThreads, "register split");
 
@@ -84,6 +90,13 @@ __host__ __device__ constexpr int column_of_slot(int s) {
 static_assert(column_of_slot(slot_of_column(2)) == 2 && column_of_slot(slot_of_column(9)) == 9 &&
               column_of_slot(slot_of_column(30)) == 30, "inverse");
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
 template <int REGS>
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS)); }
 template <int REGS>
@@ -94,7 +107,8 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 // weight per key errs by up to 2^-11, as much as the rounding of an fp16 output: results were 1.4-1.7 times
 // as far off as that rounding alone.  A bf16 output does not show it, and is spared the 5-8% of the call.
 template <int D, typename QT, bool OPTS, bool TWO>
-__global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap) {
+__global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap,
+                                                                  const __grid_constant__ CUtensorMap cmap) {
     using Gm = Geo<D>;
     using Ly = PxLayout<D>;
     using Tm = PfTmem<D>;
@@ -110,6 +124,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     const int split = blockIdx.y;
     const int tiles_all = (p.px_len + kPfKeys - 1) / kPfKeys;
     const int kt0 = (int)((int64_t)tiles_all * split / p.px_splits), kt1 = (int)((int64_t)tiles_all * (split + 1) / p.px_splits);
+    const bool boxes = H % 4 == 0;   // rows of a multiple of 16 bytes: TMA loads packed rows (see the loaders)
     const int nkt = kt1 - kt0;   // at least one: the host takes no more splits than tiles
 
     float* sk = reinterpret_cast<float*>(smem + Ly::kSk);
@@ -129,7 +144,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     uint64_t* rot_in = q_tma + 1;               // the rotation matrix in shared memory (256 arrivals)
     uint64_t* rot_done = rot_in + 1;            // the rotated queries in tensor memory (commit)
     uint64_t* q_max = rot_done + 1;             // the rows' exponent is known (256 arrivals)
-    uint64_t* raw_full = q_max + 1;             // [plane][stages] packed rows of a key tile landed (32 lanes)
+    uint64_t* raw_full = q_max + 1;             // [plane][stages] packed rows of a key tile landed (bytes, or 32 lanes)
     uint64_t* raw_free = raw_full + 2 * kPfRawStages;   // [plane][stages] that plane converted (128 arrivals)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kFlags);
@@ -156,7 +171,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         mbar_init(q_max, kPfSoftmaxThreads);
         *qexp = 0xFFFFFFFFu;
         for (int i = 0; i < 2 * kPfRawStages; ++i) {
-            mbar_init(&raw_full[i], 32);
+            mbar_init(&raw_full[i], boxes ? 1 : 32);
             mbar_init(&raw_free[i], 128);
         }
         *abort_flag = 0;
@@ -217,6 +232,13 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         if (mbar_wait(bar, parity)) return true;
         if (atomicExch(const_cast<int*>(abort_flag), 1) == 0) count_status(p.status, 3);
         return false;
+    };
+    // the same in the chain S -> weights -> P.V -> next S, where waking a suspended warp would add to every tile:
+    // polled first
+    auto soon = [&](uint64_t* bar, uint32_t parity) -> bool {
+        for (int i = 0; i < kPxPolls; ++i)
+            if (mbar_test_wait(bar, parity)) return true;
+        return wait(bar, parity);
     };
 
     if (warp < kPfSoftmaxWarps) {
@@ -346,7 +368,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             const int b = j & 1;
             const uint32_t ph = (uint32_t)(j >> 1) & 1u;
             const int kb = j % kPfPairs, kr = j % kPfKRing;
-            ok = wait(&s_full[b], ph) && wait(&k_full[kr], (uint32_t)(j / kPfKRing) & 1u) &&
+            ok = soon(&s_full[b], ph) && wait(&k_full[kr], (uint32_t)(j / kPfKRing) & 1u) &&
                  wait(&v_full[kb], (uint32_t)(j / kPfPairs) & 1u);
             if (__any_sync(0xffffffffu, !ok)) {
                 ok = false;
@@ -558,7 +580,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         const int k = pl ? column_of_slot(i128) : i128;
         constexpr int NW = D / 8 + 1;                     // words of a row: codes, then the scale word
         float k0 = p.c * p.softmax_scale * kLog2e;        // raw score -> log2 logit, with 2^-e once it is known
-        // word offset of this key's rows in their windows (the prefill's rule)
+        // Word offset of this key's rows in their windows (the prefill's rule).  With 4 or 8 kv heads it is h % 4 for
+        // the whole CTA, but a copy of the loop for each offset, without the 35 selects among a row's 270
+        // instructions, made the large batch below 9% slower (762 us against 696).
         const int row_off = ((k % kBlockSize) * H + h) & 3;
         const uint32_t trow = (uint32_t)i128;
         for (int j = 0; j < nkt; ++j) {
@@ -618,8 +642,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         fewer_registers<kPxOtherRegs>();
         if (warp == kPxLoadWarp || warp == kPxLoadWarp + 1) {
             // ============================================================ loads of packed rows
-            // As the prefill's loaders: 16-byte copies of each row's aligned window, keys past the prefix
-            // or in a block outside the cache zero-filled (scale word 0: no key).
+            // Each row's 16-byte-aligned window, keys past the prefix or in a block outside the cache zero-filled
+            // (scale word 0: no key).  With 4 or 8 kv heads a token's rows are a multiple of 16 bytes and TMA
+            // takes a block's windows at once; with 1 or 2 they are not, and the windows are 16-byte copies.
             // A pass moves kKeys whole windows (C lanes each; 30 of 32 lanes), so that a lane keeps its chunk
             // and the offsets are a few integer operations: a precomputed table of them spilled in this
             // warp's 64 registers and made a tile's copies 2 500 cycles.
@@ -642,6 +667,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             };
             int blk_next = lookup(0), blkv = -1;
             bool ok = true;
+            int issued = 0;
             for (int j = 0; j < nkt && ok; ++j) {
                 const int st = j % kPfRawStages;
                 if ((j & 3) == 0) {
@@ -655,6 +681,18 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                 if (j >= kPfRawStages) ok = wait(&raw_free[pl * kPfRawStages + st], (uint32_t)(j / kPfRawStages - 1) & 1u);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 const uint32_t dst = smem_u32(smem + Ly::kRaw + (uint32_t)(st * 2 + pl) * Ly::kPlane);
+                if (boxes) {
+                    // one box [16 tokens][window bytes] per block; block -1 lies outside the tensor and reads as
+                    // zeros, as do a last head's bytes past its token's rows
+                    uint64_t* full = &raw_full[pl * kPfRawStages + st];
+                    const int blk = __shfl_sync(0xffffffffu, blkv, (j & 3) * 8 + (lane & 7));
+                    if (lane == 0) mbar_arrive_expect_tx(full, Ly::kPlane);
+                    __syncwarp();
+                    if (lane < kPfKeys / kBlockSize)
+                        tma_load_4d(dst + (uint32_t)lane * (kBlockSize * Ly::kWindow * 4), &cmap, (h * Gm::RB) & ~15, 0, pl, blk, full);
+                    issued = j + 1;
+                    continue;
+                }
 #pragma unroll
                 for (int t = 0; t < kPasses; ++t) {
                     const int key = t * kKeys + ck;
@@ -666,7 +704,10 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                 }
                 cp_async_arrive_noinc(&raw_full[pl * kPfRawStages + st]);
             }
-            cp_async_wait_all();   // no copy outlives the CTA
+            // no copy outlives the CTA
+            cp_async_wait_all();
+            for (int j = max(0, issued - kPfRawStages); j < issued; ++j)
+                (void)mbar_wait(&raw_full[pl * kPfRawStages + j % kPfRawStages], (uint32_t)(j / kPfRawStages) & 1u);
         } else if (warp == kPxMmaWarp) {
             // ============================================================ the MMA issuer
             // S of tile t (its K tile dequantised, its S buffer read by P.V of tile t - 2), then P.V of tile t - 1
@@ -734,14 +775,14 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             bool ok = __all_sync(0xffffffffu, nkt == 0 || wait(q_ready, 0));
             for (int t = 0; t <= nkt && ok; ++t) {
                 if (t < nkt) {
-                    ok = wait(&k_full[t % kPfKRing], (uint32_t)(t / kPfKRing) & 1u) &&
-                         (t < 2 || wait(&pv_done[t & 1], (uint32_t)((t - 2) >> 1) & 1u));
+                    ok = soon(&k_full[t % kPfKRing], (uint32_t)(t / kPfKRing) & 1u) &&
+                         (t < 2 || soon(&pv_done[t & 1], (uint32_t)((t - 2) >> 1) & 1u));
                     if (!__all_sync(0xffffffffu, ok)) break;
                     tc_fence_after();
                     issue_s(t);
                 }
                 if (t > 0) {
-                    ok = wait(&p_full[(t - 1) & 1], (uint32_t)((t - 1) >> 1) & 1u);
+                    ok = soon(&p_full[(t - 1) & 1], (uint32_t)((t - 1) >> 1) & 1u);
                     if (!__all_sync(0xffffffffu, ok)) break;
                     tc_fence_after();
                     issue_pv(t - 1);
@@ -763,6 +804,24 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     griddep_wait();
 }
 
+// The cache as bytes [block][plane][token][heads' rows], in boxes of one block's windows of one head (4 or 8 kv
+// heads).  Block ids are int32, so a larger cache has no block past 2^31 that could be named.
+template <int D>
+cudaError_t cache_map(const AttnParams& p, CUtensorMap* map) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t row = (cuuint64_t)p.H * Geo<D>::RB;
+    const cuuint64_t blocks = (cuuint64_t)std::min<int64_t>(std::max<int64_t>(p.num_blocks, 1), (int64_t)1 << 31);
+    const cuuint64_t dims[4] = {row, kBlockSize, 2, blocks};
+    const cuuint64_t strides[3] = {row, row * kBlockSize, row * kBlockSize * 2};
+    const cuuint32_t box[4] = {PxLayout<D>::kWindow * 4, kBlockSize, 1, 1};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(p.cache), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int D, typename QT, bool OPTS, bool TWO>
 cudaError_t launch_prefix_t(const AttnParams& p, cudaStream_t stream) {
     const size_t smem = PxLayout<D>::kBytes;
@@ -777,9 +836,15 @@ cudaError_t launch_prefix_t(const AttnParams& p, cudaStream_t stream) {
         regs.store(fa.numRegs, std::memory_order_release);
     }
     if (regs.load(std::memory_order_acquire) != kPxLaunchRegs) return cudaErrorInvalidKernelImage;
-    CUtensorMap qmap;
+    CUtensorMap qmap, cmap;
     err = query_map<D, QT>(p, &qmap);
     if (err != cudaSuccess) return err;
+    if (p.H % 4 == 0) {
+        err = cache_map<D>(p, &cmap);
+        if (err != cudaSuccess) return err;
+    } else {
+        cmap = qmap;   // not used
+    }
     const int64_t bq = kPfRows / p.G, tiles = (p.num_q_tokens + bq - 1) / bq;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -791,7 +856,7 @@ cudaError_t launch_prefix_t(const AttnParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefix_kernel<D, QT, OPTS, TWO>, p, qmap);
+    return cudaLaunchKernelEx(&cfg, prefix_kernel<D, QT, OPTS, TWO>, p, qmap, cmap);
 }
 
 }  // namespace
