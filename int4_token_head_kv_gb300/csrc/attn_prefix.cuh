@@ -23,11 +23,13 @@
 // chain S (1 230 to issue) -> softmax (1 970, among the dequantisation's instructions) -> P.V (600) -> the S after
 // next, which takes the same of the two S buffers, and each hand-over costs 300-700 until the MMAs issued have
 // run and the other side is awake; tensor memory is full (two S, O, the queries' halves), so there is no third
-// buffer.  Beside it K's and V's rows of a tile take 700 and 1 000.  What the steps gave on 128 sequences, 131 072
+// buffer.  Beside it K's and V's rows of a tile take 700 and 1 000.  Shared memory is what makes the MMAs run late:
+// its data pipe is 84% busy (28% the MMAs' operands, 55% loads and stores: per tile 512 cycles of scales for the
+// softmax, 512 of converted rows, 320 of packed ones).  What the steps gave on 128 sequences, 131 072
 // shared tokens, 64 q / 8 kv heads (961 us at first): block ids looked up four tiles ahead and copies without a
 // spilled table, descriptors in uniform registers: 812; one prescale per CTA, so that one FMA forms the
 // exponent, and a fixed MMA order: 775; a walker grid for the tokens behind the prefix alone: 729; packed rows by
-// TMA boxes instead of 16-byte copies: 696; polling in the chain's waits: 665.  Tried and dropped: forming the
+// TMA boxes instead of 16-byte copies: 696; polling in the chain's waits: 665; V rows read without bank conflicts: 661.  Tried and dropped: forming the
 // weights before the maxima are known (no gain), 16 softmax warps with half of the keys each (923), output rows
 // staged for bulk stores (no gain), S as two products of 64 keys, so that one of them need not wait for P.V (713
 // against 683), weights handed over in two halves (674 against 665).
@@ -83,12 +85,24 @@ __device__ __forceinline__ int rows_exponent(uint32_t first) {
     return first == 0xFFFFFFFFu ? 0 : max(-60, min(60, 7 + 127 - (int)(first & 0xFFu)));
 }
 
-// inverse of slot_of_column
-__host__ __device__ constexpr int column_of_slot(int s) {
-    return (s & ~15) + 2 * ((s >> 2) & 3) + 8 * ((s >> 1) & 1) + (s & 1);
+// Key of V thread i (see the dequantisation): of a group of 16 keys 8a + 2b + c (rows 4b + 2a + c), the first
+// eight threads take a = b / 2, the others the other half.
+__host__ __device__ constexpr int v_key(int i) {
+    const int b = (i >> 1) & 3, a = (b >> 1) ^ ((i >> 3) & 1);
+    return (i & ~15) + 8 * a + 2 * b + (i & 1);
 }
-static_assert(column_of_slot(slot_of_column(2)) == 2 && column_of_slot(slot_of_column(9)) == 9 &&
-              column_of_slot(slot_of_column(30)) == 30, "inverse");
+constexpr bool v_keys_spread() {
+    for (int i = 0; i < 128; i += 8) {
+        unsigned keys = 0, rows = 0;
+        for (int j = i; j < i + 8; ++j) {
+            keys |= 1u << (v_key(j) & 7);
+            rows |= 1u << (slot_of_column(v_key(j)) & 7);
+        }
+        if (keys != 255u || rows != 255u) return false;
+    }
+    return true;
+}
+static_assert(v_keys_spread(), "eight neighbours, eight remainders");
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
     asm volatile(
@@ -573,18 +587,18 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         fewer_registers<kPxDequantRegs>();
         // ================================================================ dequantisation of key tiles
         const int pl = (warp - kPxDequantWarp) >> 2;      // 0: K rows, 1: V rows
-        // This thread's key of every tile.  A V tile keeps its rows in the order the weights are laid out
-        // in, and a V thread takes the key of row i (its index in the group), so that eight neighbouring
-        // threads store eight neighbouring swizzled rows (by key they hit four of them twice).
+        // This thread's key of every tile.  A V tile keeps its rows in the order the weights are laid out in, and V
+        // threads take their keys in an order in which eight neighbours have keys, and rows, of eight different
+        // remainders mod 8: the windows' reads and the swizzled rows' stores then hit no bank twice.
         const int i128 = (threadIdx.x - kPfSoftmaxThreads) & 127;
-        const int k = pl ? column_of_slot(i128) : i128;
+        const int k = pl ? v_key(i128) : i128;
+        const uint32_t trow = (uint32_t)(pl ? slot_of_column(k) : k);
         constexpr int NW = D / 8 + 1;                     // words of a row: codes, then the scale word
         float k0 = p.c * p.softmax_scale * kLog2e;        // raw score -> log2 logit, with 2^-e once it is known
         // Word offset of this key's rows in their windows (the prefill's rule).  With 4 or 8 kv heads it is h % 4 for
         // the whole CTA, but a copy of the loop for each offset, without the 35 selects among a row's 270
         // instructions, made the large batch below 9% slower (762 us against 696).
         const int row_off = ((k % kBlockSize) * H + h) & 3;
-        const uint32_t trow = (uint32_t)i128;
         for (int j = 0; j < nkt; ++j) {
             const int kb = j % kPfPairs, st = j % kPfRawStages;
             bool ok = wait(&raw_full[pl * kPfRawStages + st], (uint32_t)(j / kPfRawStages) & 1u);
