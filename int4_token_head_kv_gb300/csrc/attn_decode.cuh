@@ -162,7 +162,8 @@ __device__ __forceinline__ uint32_t pack_halves(__half lo, __half hi) {
 
 // ------------------------------------------------------------------ 0. query rotation
 
-// One CTA per sequence; only decode sequences (one query token) are rotated.  Record of a sequence
+// One CTA per sequence, or per share of its kv heads while the grid is small (qrot_groups); only decode
+// sequences (one query token) are rotated.  Record of a sequence
 // (32-bit words): for kv head h, 32-dimension group j and lane, the QW fp16x2 words that lane feeds
 // to the score mma; then alpha[Hq rounded up to 4] (raw score -> log2-domain logit, before the
 // key's scale) and qsum[Hq rounded up to 4] (sum of the stored high + low halves of each vector).
@@ -170,30 +171,37 @@ template <int D, bool WIDE, int BITS, typename QT>
 __global__ void __launch_bounds__(256) qrot_kernel(const __grid_constant__ AttnParams p) {
     constexpr int QW = WIDE ? 8 : 4, KWPT = D / 32;
     extern __shared__ __align__(128) uint8_t smem[];
-    griddep_launch_dependents();   // the walker's set-up reads only metadata
     const int seq = blockIdx.x;
+    const int HC = p.H / (int)gridDim.y, h0 = (int)blockIdx.y * HC;   // this CTA's kv heads
     const int q0 = __ldg(p.qsl + seq);
     const bool decode = __ldg(p.qsl + seq + 1) - q0 == 1 && q0 >= 0 && (int64_t)q0 < p.num_q_tokens;
     if (decode) {   // uniform over the CTA
         const int H = p.H, G = p.G, Hq = p.Hq, Hq4 = (Hq + 3) & ~3;
+        const int NV = HC * G, NV4 = (NV + 3) & ~3, first = h0 * G;   // its query vectors: first .. first + NV - 1
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
         float* sgn = reinterpret_cast<float*>(smem);
         float* alpha = sgn + D;
-        float* qsum = alpha + Hq4;
-        __half* qh = reinterpret_cast<__half*>(qsum + Hq4);
-        __half* ql = qh + Hq * D;
+        float* qsum = alpha + NV4;
+        __half* qh = reinterpret_cast<__half*>(qsum + NV4);
+        __half* ql = qh + NV * D;
         // INT8 queries are not rotated (sign +1, no transform, no 1/sqrt(d) of the transform)
         for (int i = threadIdx.x; i < D; i += blockDim.x) sgn[i] = BITS != 8 && p.signs[i] < 0.0f ? -1.0f : 1.0f;
+        // The previous kernel may be a combine, which lets this one start while it still reads its partials and
+        // stores its outputs: the records below may lie over those partials (another call's workspace layout),
+        // and the queries may be those outputs.  The walker starts once this grid is past the wait, so nothing
+        // before this call is running when its set-up reads the metadata.
+        griddep_wait();
+        griddep_launch_dependents();
         __syncthreads();
         const float lsc = (BITS != 8 ? p.c : 1.0f) * p.softmax_scale * kLog2e;
-        for (int v0 = warp; v0 < Hq; v0 += 4 * 8) {   // four vectors per warp at a time
+        for (int v0 = warp; v0 < NV; v0 += 4 * 8) {   // four vectors per warp at a time
             float x[4][D / 32];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const int v = v0 + 8 * k;
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j)
-                    x[k][j] = v < Hq ? load_elem<QT>(p.q, ((int64_t)q0 * Hq + v) * D + lane + 32 * j) * sgn[lane + 32 * j]
+                    x[k][j] = v < NV ? load_elem<QT>(p.q, ((int64_t)q0 * Hq + first + v) * D + lane + 32 * j) * sgn[lane + 32 * j]
                                      : 0.0f;
             }
             // v = H_d D q; a power-of-two prescale brings max|v| into [2^14, 2^15) for the halves
@@ -223,12 +231,12 @@ __global__ void __launch_bounds__(256) qrot_kernel(const __grid_constant__ AttnP
                     const __half hi = __float2half_rn(y);
                     const __half lo = __float2half_rn(y - __half2float(hi));
                     sum[k] += __half2float(hi) + __half2float(lo);
-                    if (v < Hq) {
+                    if (v < NV) {
                         qh[v * D + lane + 32 * j] = hi;
                         ql[v * D + lane + 32 * j] = lo;
                     }
                 }
-                if (lane == 0 && v < Hq) alpha[v] = lsc * exp2i(-e);
+                if (lane == 0 && v < NV) alpha[v] = lsc * exp2i(-e);
             }
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) {
@@ -237,7 +245,7 @@ __global__ void __launch_bounds__(256) qrot_kernel(const __grid_constant__ AttnP
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (lane == 0 && v0 + 8 * k < Hq) qsum[v0 + 8 * k] = sum[k];
+                if (lane == 0 && v0 + 8 * k < NV) qsum[v0 + 8 * k] = sum[k];
         }
         __syncthreads();
         // Score-mma B fragments.  Lane (g, t) of kv head h's warp feeds, for the group W = t + 4 j of
@@ -247,7 +255,7 @@ __global__ void __launch_bounds__(256) qrot_kernel(const __grid_constant__ AttnP
         // halves follow as a second tile); otherwise head g >> 1, the high half for even g and the
         // low half for odd g.
         uint32_t* rec = p.ws_q + (size_t)seq * p.qrec_words;
-        for (int idx = threadIdx.x; idx < H * KWPT * 32; idx += blockDim.x) {
+        for (int idx = threadIdx.x; idx < HC * KWPT * 32; idx += blockDim.x) {
             const int ln = idx & 31, j = (idx >> 5) % KWPT, h = idx / (32 * KWPT);
             const int g = ln >> 2, t = ln & 3;
             const int head = WIDE ? g : (g >> 1);
@@ -270,19 +278,21 @@ __global__ void __launch_bounds__(256) qrot_kernel(const __grid_constant__ AttnP
                     w[5 + 2 * hh] = live ? pack_halves(__hmul(qv2[d0 + s2], od), __hmul(qv2[d0 + s2 + s1], od)) : 0u;
                 }
             }
-            uint4* dst = reinterpret_cast<uint4*>(rec) + (size_t)idx * (QW / 4);
+            uint4* dst = reinterpret_cast<uint4*>(rec) + (size_t)(h0 * KWPT * 32 + idx) * (QW / 4);
             dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
             if constexpr (WIDE) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
         float* ralpha = reinterpret_cast<float*>(rec + (size_t)H * D * QW);
-        for (int v = threadIdx.x; v < Hq4; v += blockDim.x) {
-            ralpha[v] = v < Hq ? alpha[v] : 0.0f;
-            ralpha[Hq4 + v] = v < Hq ? qsum[v] : 0.0f;
+        const int last = first + NV == Hq ? Hq4 - first : NV;   // the last CTA pads the lists
+        for (int v = threadIdx.x; v < last; v += blockDim.x) {
+            ralpha[first + v] = v < NV ? alpha[v] : 0.0f;
+            ralpha[Hq4 + first + v] = v < NV ? qsum[v] : 0.0f;
         }
     }
-    // Complete only after the previous kernel of the stream (the cache write, typically) has:
-    // whoever waits for this kernel then also sees that kernel's results.
+    // With no record to write as well, complete only after the previous kernel of the stream (the cache write,
+    // typically) has: whoever waits for this kernel then also sees that kernel's results.
     griddep_wait();
+    griddep_launch_dependents();
 }
 
 // ------------------------------------------------------------------ 1. split-KV unit walker
@@ -319,9 +329,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
     int* run_seq = run_first + kMaxUnits;                // that sequence
     int* tbl = run_seq + kMaxUnits;                      // block ids of the CTA's first kTableWin blocks
 
-    // Launched as a programmatic dependent (of the cache write, typically): everything up to
-    // griddep_wait() below reads only the host-provided metadata (query_start_loc, seq_lens, block
-    // tables, signs) and writes only shared memory.  The combine may be scheduled right away: it
+    // Launched as a programmatic dependent of the query rotation, which lets it start once everything
+    // before the call has completed: up to griddep_wait() below it reads only the metadata
+    // (query_start_loc, seq_lens, block tables) and writes only shared memory.  The combine may be scheduled right away: it
     // waits for this grid before reading anything, and its CTAs become resident as walker CTAs
     // retire.  The shared-prefix kernel reads the queries and the cache without waiting for this grid, so
     // in front of it the trigger comes after the wait below.
@@ -1227,6 +1237,15 @@ __global__ void __launch_bounds__(kCombineWarps * 32) combine_kernel(const __gri
 
 // ------------------------------------------------------------------ launchers
 
+// CTAs per sequence of the query rotation: its kv heads are shared out (a power of two divides them) as long as a
+// CTA keeps 32 vectors, which it turns at once (four per warp), and the grid stays within two CTAs per SM.  The
+// rotation waits for the previous kernel, so a CTA's second round of vectors holds the walker up.
+inline unsigned qrot_groups(const AttnParams& p) {
+    unsigned n = 1;
+    while (2 * n <= (unsigned)p.H && (unsigned)p.Hq / (2 * n) >= 32u && (int64_t)p.num_seqs * 2 * n <= 2ll * num_sms()) n *= 2;
+    return n;
+}
+
 template <int D, bool WIDE, int BITS, typename QT, typename OT>
 cudaError_t launch_decode_t(const AttnParams& p, int num_ctas, cudaStream_t stream) {
     const DecodeSmem lay = decode_smem_layout<D, WIDE, BITS>(p.H, p.Hq);
@@ -1241,9 +1260,11 @@ cudaError_t launch_decode_t(const AttnParams& p, int num_ctas, cudaStream_t stre
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    const size_t qsm = D * 4 + 2 * (size_t)((p.Hq + 3) & ~3) * 4 + 2 * (size_t)p.Hq * D * 2;
+    const unsigned qgroups = qrot_groups(p);
+    const size_t nv = (size_t)p.Hq / qgroups;   // query vectors of a CTA
+    const size_t qsm = D * 4 + 2 * ((nv + 3) & ~(size_t)3) * 4 + 2 * nv * D * 2;
     cudaLaunchConfig_t qcfg = {};
-    qcfg.gridDim = dim3((unsigned)p.num_seqs);
+    qcfg.gridDim = dim3((unsigned)p.num_seqs, qgroups);
     qcfg.blockDim = dim3(256);
     qcfg.dynamicSmemBytes = qsm;
     qcfg.stream = stream;

@@ -200,8 +200,7 @@ __global__ void __launch_bounds__(kWriteThreads, ReadSmem<D, BITS, OT>::kBlocks)
     using Sm = ReadSmem<D, BITS, OT>;
     constexpr int TPV = Sh::kTpv, TV = Sh::kTileVecs, RB = Sm::RB, RW = RB / 4;
     extern __shared__ __align__(128) uint8_t smem[];
-    // The cache and the slots may come from the previous kernel.  No dependent starts early: it might take
-    // the rows read here as the queries it looks at before it waits.
+    // The cache and the slots may come from the previous kernel.  No dependent starts early.
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int vl = lane / TPV, part = lane % TPV;

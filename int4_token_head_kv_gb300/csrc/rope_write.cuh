@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
     using Sm = RopeSmem<D, BITS>;
     extern __shared__ __align__(128) uint8_t smem[];
     // The previous kernel may produce any of the inputs.  Unlike the plain write, this kernel lets no
-    // dependent start early: the attention that follows reads its queries before it waits.
+    // dependent start early.
     griddep_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int vl = lane / TPV, part = lane % TPV;   // this thread's vector of the tile and its part

@@ -392,3 +392,65 @@ def test_blocks_past_32_bit_offsets():
     want = b.shared()
     b.cache, b.tables, b.prefix_blocks = big, b.tables + np.int32(far), b.prefix_blocks + np.int32(far)
     assert torch.equal(b.shared(), want)
+
+
+def test_calls_of_different_shapes_follow_each_other_on_one_workspace():
+    """Shared and plain calls of different batch sizes and head layouts take turns on one stream with one
+    workspace and nothing between them: each keeps the bits of a call by itself."""
+    kv = _kv()
+    batches = [Batch(1024, _lens(1024, 32, 300, 21), 32, 8, 128, seed=21), Batch(900, _lens(900, 64, 200, 22), 64, 8, 128, seed=22),
+               Batch(2048, _lens(2048, 12, 900, 23), 8, 1, 64, seed=23), Batch(400, _lens(400, 200, 60, 24), 16, 4, 64, seed=24),
+               Batch(64, _lens(64, 700, 30, 25), 4, 4, 64, seed=25)]
+    calls = []
+    for b in batches:
+        t, l, q = b._args()
+        pb = torch.from_numpy(b.prefix_blocks).cuda()
+        calls.append(lambda ws, out, b=b, t=t, l=l, q=q, pb=pb: kv.kv_int4_shared_prefix_attention(
+            b.q, b.cache, pb, b.prefix, t, l, q, b.scale, b.gsigns, max_seq_len=b.max_len, out=out, workspace=ws))
+        calls.append(lambda ws, out, b=b, t=t, l=l, q=q: kv.kv_int4_paged_attention(
+            b.q, b.cache, t, l, q, b.scale, b.gsigns, 1, b.max_len, out=out, workspace=ws))
+    need = 0
+    for b in batches:
+        S, Hq, d, H = len(b.lens), b.q.shape[1], b.q.shape[2], b.cache.shape[3]
+        need = max(need, kv.kv_int4_attention_workspace_bytes(Hq, H, d, S, b.max_len),
+                   kv.kv_int4_shared_prefix_workspace_bytes(S, Hq, H, d, S, b.prefix, b.max_len))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(b.q) for b in batches for _ in range(2)]
+    want = []
+    for f, o in zip(calls, outs):
+        torch.cuda.synchronize()
+        want.append(f(ws, o).clone())
+        torch.cuda.synchronize()
+    order = list(np.random.default_rng(0).permutation(len(calls) * 8) % len(calls))
+    got = [torch.empty_like(outs[i]) for i in order]
+    torch.cuda.synchronize()
+    for i, o in zip(order, got):
+        calls[i](ws, o)
+    torch.cuda.synchronize()
+    bad = [(k, i) for k, (i, o) in enumerate(zip(order, got)) if not torch.equal(o, want[i])]
+    assert not bad, bad
+
+
+def test_outputs_are_the_next_calls_queries():
+    """A call's output fed to the next call as its queries, with nothing between them on the stream."""
+    b = Batch(1024, _lens(1024, 32, 200, 31), 32, 8, 128, seed=31)
+    t, l, q = b._args()
+    pb = torch.from_numpy(b.prefix_blocks).cuda()
+    kv = _kv()
+
+    def chain(sync):
+        outs, x = [], b.q
+        for i in range(12):
+            if i % 3 == 2:
+                x = kv.kv_int4_paged_attention(x, b.cache, t, l, q, b.scale, b.gsigns, 1, b.max_len)
+            else:
+                x = kv.kv_int4_shared_prefix_attention(x, b.cache, pb, b.prefix, t, l, q, b.scale, b.gsigns, max_seq_len=b.max_len)
+            outs.append(x)
+            if sync:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs
+
+    want = chain(True)
+    for _ in range(5):
+        assert all(torch.equal(x, y) for x, y in zip(chain(False), want))
