@@ -110,10 +110,12 @@ __device__ __forceinline__ void rope_rows(const RopeWriteParams& p, const uint8_
     const uint32_t H = (uint32_t)p.w.H;
     const int rot = p.rot, hw = rot >> 2;       // words of a half of the rotated elements
     int pw[2];            // the partner word (split pairing)
+    bool turned[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int m = k + i * Q;
-        pw[i] = INTER || 2 * m >= rot ? m : (m < hw ? m + hw : m - hw);
+        turned[i] = 2 * m < rot;
+        pw[i] = INTER || !turned[i] ? m : (m < hw ? m + hw : m - hw);
     }
     const bool full = !INTER && rot == D;   // the lane's two words are each other's partners
     const uint32_t* src = reinterpret_cast<const uint32_t*>(in + r0 * ROWPAD);
@@ -130,7 +132,7 @@ __device__ __forceinline__ void rope_rows(const RopeWriteParams& p, const uint8_
             const int m = k + i * Q;
             c[i] = tab.c[i];
             s[i] = tab.s[i];
-            if (2 * m < rot) {
+            if (turned[i]) {
                 if constexpr (INTER) {
                     c[i].y = c[i].x;
                     s[i] = make_float2(-s[i].x, s[i].x);
@@ -162,7 +164,9 @@ __device__ __forceinline__ void rope_rows(const RopeWriteParams& p, const uint8_
                     float2 o;
                     if constexpr (INTER) o = make_float2(x.y, x.x);
                     else o = upcast_pair<T>(src[q * kRowWords + pw[i]]);
-                    y[i] = sum_of_products(mul_f32x2(x, c[i]), mul_f32x2(o, s[i]));
+                    // c holds an unrotated word's signs; a product with its sine of 0 would make NaN of an infinity
+                    const float2 xc = mul_f32x2(x, c[i]), z = sum_of_products(xc, mul_f32x2(o, s[i]));
+                    y[i] = turned[i] ? z : xc;
                 }
                 *reinterpret_cast<float4*>(stage + q * kRopeRow<D> + 4 * k) = make_float4(y[0].x, y[1].x, y[0].y, y[1].y);
             }

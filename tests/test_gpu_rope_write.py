@@ -179,3 +179,37 @@ def test_python_checks():
         kv.kv_int4_rope_write(**{**ok, "cos_sin": tab[:, :24].contiguous()})   # 24 rotated dimensions
     assert e.value.status == 2
     assert not cache.any()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d, rot", [(128, 64), (64, 16), (128, 112)])
+@pytest.mark.parametrize("bits", [4, 8, 2])
+def test_dimensions_behind_the_rotated_ones_stay_whatever_they_hold(bits, d, rot, dtype, inter):
+    """Infinities and NaN among them: at position 0, where the others are left too, the bytes are the plain
+    write's; at any position an infinite element gives its row an infinite scale, as the definition does."""
+    kv = _kv()
+    c = _case(21, 4, 2, d, rot, dtype, seed=rot + bits)
+    x = c["x"]
+    plus, minus, nan = float("inf"), float("-inf"), float("nan")
+    # (token, head of key or value, element): neighbours, first, last and several in one row
+    for t, h, i, val in ((0, 4, rot, plus), (1, 5, rot + 1, minus), (2, 4, d - 1, plus), (3, 5, rot, nan), (4, 4, rot + 2, plus),
+                         (4, 4, rot + 3, minus), (5, 6, rot, plus), (6, 2, rot + 5, plus), (7, 3, d - 2, nan)):
+        x[t, h, i] = val
+    gx, slots, signs = x.cuda(), torch.from_numpy(c["slots"]).cuda(), torch.from_numpy(c["signs"]).cuda()
+    k, v = gx[:, 4:6].contiguous(), gx[:, 6:].contiguous()
+    shape = {4: kv.kv_int4_cache_shape, 8: kv.kv_int8_cache_shape, 2: kv.kv_int2_cache_shape}[bits](c["nb"], 16, 2, d)
+    want, got = (torch.full(shape, 0xA5, dtype=torch.uint8, device="cuda") for _ in range(2))
+    if bits == 8:
+        kv.kv_int8_write(k, v, slots, want)
+    else:
+        (kv.kv_int4_write if bits == 4 else kv.kv_int2_write)(k, v, slots, signs, want)
+    tab = torch.from_numpy(c["tab"]).cuda()
+    q = _call(bits, gx[:, :4], k, v, torch.zeros(21, dtype=torch.int64, device="cuda"), tab, slots, signs, got, interleaved=inter)
+    assert torch.equal(got, want)
+    assert torch.equal(q.contiguous().view(torch.int16), gx[:, :4].contiguous().view(torch.int16))
+    pos = torch.from_numpy(c["pos"]).cuda()
+    _call(bits, None, k, v, pos, tab, slots, signs, got, interleaved=inter)
+    at = slots[[0, 1, 2]]
+    scale = got[at // 16, 0, at % 16, torch.tensor([0, 1, 0], device="cuda"), -4:].contiguous().view(torch.int32)
+    assert bool(((scale & ~15) == 0x7F800000).all())
