@@ -186,7 +186,8 @@ kv_int4_status kv_int2_write(const void* k, const void* v, kv_int4_dtype dtype, 
  *                whole (its cache row and its q_out row are left as they were) and counted
  *                (KV_INT4_STAT_POSITION_OUT_OF_RANGE), unless its slot and its position are both
  *                negative: a padding token, not counted.
- * cos_sin        [max_position, rot_dim] fp32, 16-B aligned.  rot_dim: a multiple of 16, 16..head_size.
+ * cos_sin        [max_position, rot_dim] fp32, 16-B aligned, max_position >= 1 (unless num_tokens is 0).
+ *                rot_dim: a multiple of 16, 16..head_size.
  * slot_mapping   as kv_int4_write; a token with a negative slot still has its query rotated.  Slots
  *                that are not negative must be distinct within the call.
  * q_out          may be q itself with the same stride (rotation in place; with another one

@@ -203,6 +203,7 @@ kv_int4_status rope_write_impl(int bits, const void* q, int64_t q_token_stride, 
     if (!k || !v || !positions || !cos_sin || !slot_mapping || (bits != 8 && !rht_signs) || !cache ||
         (num_q_heads > 0 && (!q || !q_out)))
         return KV_INT4_EINVAL;
+    if (max_position == 0) return KV_INT4_EINVAL;   // the kernels look at row 0 for a position outside the table
     const int64_t kv_row = (int64_t)num_kv_heads * head_size, q_row = (int64_t)num_q_heads * head_size;
     // rows of different tokens must not overlap (a single token needs no stride)
     if (num_tokens > 1 && (k_token_stride < kv_row || v_token_stride < kv_row ||

@@ -114,3 +114,19 @@ def test_rope_write_in_place_needs_one_stride(lib, name):
         [vp, i64, vp, i64, i32, vp]
     head = (FAKE, 1024, 8, FAKE, 256, FAKE, 256, 1, 4, 2, 128, FAKE, FAKE, 64, 128, 0, FAKE) + (FAKE,) * len(signs)
     assert f(*head, FAKE, 2048, FAKE, 8, 16, None) == 1
+
+
+@pytest.mark.parametrize("name", ["kv_int4_rope_write", "kv_int8_rope_write", "kv_int2_rope_write"])
+def test_rope_write_needs_a_table_row(lib, name):
+    """A table of no rows is refused whatever its pointer, unless there is no token either."""
+    f = getattr(lib, name)
+    f.restype = ctypes.c_int
+    signs = [vp] if "8" not in name else []
+    f.argtypes = [vp, i64, i32, vp, i64, vp, i64, ctypes.c_int, i64, i32, i32, vp, vp, i64, i32, i32, vp] + signs + \
+        [vp, i64, vp, i64, i32, vp]
+
+    def call(n):
+        return f(FAKE, 1024, 8, FAKE, 256, FAKE, 256, 1, n, 2, 128, FAKE, FAKE, 0, 128, 0, FAKE, *(FAKE,) * len(signs), FAKE, 1024,
+                 FAKE, 8, 16, None)
+
+    assert call(4) == 1 and call(1) == 1 and call(0) == 0
