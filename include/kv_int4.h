@@ -374,9 +374,10 @@ kv_int4_status kv_int4_paged_attention_ex(const void* q, kv_int4_dtype q_dtype, 
  *
  * Computation: one kernel takes every query row of the batch against the prefix's keys, split among the
  * SMs, as the prefill does (tcgen05), the decode path takes the tokens behind the prefix, and the
- * combine merges both in a fixed order.  With one sequence, or where num_seqs x
- * the shared tokens is below 16 384 (8 192 with up to 4 kv heads and 4096 shared tokens), the extra launch
- * would cost more than it saves, and it is the plain call.  The prefix's split depends on the batch's size,
+ * combine merges both in a fixed order.  With one sequence, where num_seqs x the shared tokens is below
+ * 16 384 (8 192 with up to 4 kv heads and 4096 shared tokens), or with fewer shared tokens than 32 per query
+ * head of a kv head (216 + 40 num_kv_heads with eight of them), the extra launch would cost more than it
+ * saves, and it is the plain call.  The prefix's split depends on the batch's size,
  * so a sequence's output may differ in the last bits between batches; the same call gives the same bits.
  *
  * prefix_blocks  [prefix_len / 16] int32, may be NULL when prefix_len < 16.

@@ -397,13 +397,23 @@ bool ws_layout(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size, int
 // 256..65 536 tokens, seven head layouts) this is within 0.6% of the faster one in the mean and 16% at worst:
 // 32 x 1024 tokens, 32 q / 8 kv heads, d 128: shared 20.4 us, plain 27.2; 8 x 1024: 17.8 and 12.5; 4 x 4096:
 // 20.8 and 18.3; 2 x 4096 with 8 q / 1 kv heads, d 64: 18.0 and 41.3.
+//
+// However many sequences there are, a short prefix is not worth a row's partial and its merge, whose cost goes
+// by the query heads per kv head: the walk of 32 tokens a head, or with eight heads, where the walk is cheaper,
+// of 216 + 40 per kv head.  (Over 592 shapes of 64..4096 sequences, 16..640 tokens, ten layouts, no shared call
+// is then more than 30% slower than the plain one, and with 256 sequences and more none more than 14%; without
+// this they were up to three times slower.  512 x 64 tokens, 32 q / 8 kv heads, d 128: 56.6 us shared, 46.1
+// plain; 128 tokens: 55.8 and 54.6; 256: 56.9 and 72.4.  64 q / 8 kv heads: 384 tokens 134 and 119, 480: 137 and
+// 133, 640: 140 and 158.)
 PrefixLayout prefix_layout(int64_t num_q_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
                            int32_t num_seqs, int32_t prefix_len) {
     PrefixLayout x = {};
     const int32_t len = prefix_len / kBlockSize * kBlockSize;
     const int64_t walk = (int64_t)num_seqs * len;
+    const int G = num_q_heads / num_kv_heads;
+    if (len < (G < 8 ? 32 * G : 216 + 40 * num_kv_heads)) return x;
     if (num_seqs < 2 || walk < (num_kv_heads <= 4 && len >= 4096 ? 8192 : 16384)) return x;
-    const int64_t bq = kPrefillRows / (num_q_heads / num_kv_heads);
+    const int64_t bq = kPrefillRows / G;
     x.len = len;
     x.splits = prefix_splits((num_q_tokens + bq - 1) / bq, num_kv_heads, len);
     const size_t rows = (size_t)x.splits * (size_t)num_q_tokens * (size_t)num_q_heads;

@@ -130,3 +130,19 @@ def test_rope_write_needs_a_table_row(lib, name):
                  FAKE, 8, 16, None)
 
     assert call(4) == 1 and call(1) == 1 and call(0) == 0
+
+
+def test_short_prefixes_take_the_plain_walk(lib):
+    """However many sequences share them: the workspace is the plain call's."""
+    w = lib.kv_int4_shared_prefix_workspace_bytes
+    w.restype = szt
+    w.argtypes = [i64, i32, i32, i32, i32, i32, i32, i32]
+    plain = lib.kv_int4_attention_workspace_bytes
+    plain.restype = szt
+    plain.argtypes = [i32] * 6
+    for Hq, H, least in ((8, 8, 32), (16, 8, 64), (32, 8, 128), (8, 1, 256), (32, 4, 384), (64, 8, 544)):
+        for S in (1024, 8192):
+            assert w(S, Hq, H, 128, S, least - 1, least + 100, 0) == plain(Hq, H, 128, S, least + 100, 0)
+            shared = w(S, Hq, H, 128, S, least, least + 100, 0)
+            assert shared > plain(Hq, H, 128, S, 100, 0) and shared != plain(Hq, H, 128, S, least + 100, 0)
+    assert w(1024, 32, 8, 128, 1024, 16, 80, 0) == plain(32, 8, 128, 1024, 80, 0)
