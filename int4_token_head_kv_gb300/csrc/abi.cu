@@ -528,7 +528,7 @@ kv_int4_status paged_attention_impl(int bits, const void* q, kv_int4_dtype q_dty
     p.px_ml = reinterpret_cast<float*>(ws + px_at + px.ml);
     p.px_len = px.len;
     p.px_splits = px.splits;
-    p.px_two = out_dtype != KV_INT4_BF16;
+    p.px_two = out_dtype != KV_INT4_BF16 || G < 8;   // at least the walker's weights, whose second half G = 8 has no room for
     if (options) {
         if (options->window_left >= 0) {
             p.opts |= kOptWindow;

@@ -117,9 +117,11 @@ template <int REGS>
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS)); }
 
 // OPTS: the call has logit options; every tile then takes the masked path, which applies them.
-// TWO: the weights too are carried as high + low halves (the low ones over S's last 64 columns).  One fp16
-// weight per key errs by up to 2^-11, as much as the rounding of an fp16 output: results were 1.4-1.7 times
-// as far off as that rounding alone.  A bf16 output does not show it, and is spared the 5-8% of the call.
+// TWO: the weights too are carried as high + low halves (the low ones over S's last 64 columns), as the walker
+// carries them with up to four query heads per kv head.  One fp16 weight per key errs by up to 2^-11, as much
+// as the rounding of an fp16 output: results were 1.4-1.7 times as far off as that rounding alone.  With eight
+// heads per kv head the walker has one half, and so has this kernel then for a bf16 output, whose error against
+// 64 bits it raises by a hundredth (0.00167 to 0.00169 in the 2-norm); the second half costs 5-8% of the call.
 template <int D, typename QT, bool OPTS, bool TWO>
 __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap,
                                                                   const __grid_constant__ CUtensorMap cmap) {

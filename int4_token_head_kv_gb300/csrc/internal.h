@@ -109,7 +109,7 @@ struct AttnParams {
     float* px_ml;             // [px_splits][num_q_tokens * Hq][2] partial (max in log2 units, sum)
     int px_len;               // tokens, a multiple of 16
     int px_splits;
-    int px_two;               // 1: weights as two fp16 halves (outputs finer than bf16)
+    int px_two;               // 1: weights as two fp16 halves
 };
 constexpr int kOptWindow = 1, kOptSoftcap = 2, kOptAlibi = 4, kOptQQ = 8;
 

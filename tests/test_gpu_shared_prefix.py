@@ -454,3 +454,36 @@ def test_outputs_are_the_next_calls_queries():
     want = chain(True)
     for _ in range(5):
         assert all(torch.equal(x, y) for x, y in zip(chain(False), want))
+
+
+@pytest.mark.parametrize("Hq, H, d", [(8, 8, 64), (8, 4, 128), (8, 2, 128), (32, 8, 64)])
+def test_bf16_outputs_are_the_fp32_ones_rounded(Hq, H, d):
+    """With up to four query heads per kv head the weights keep two halves whatever the output, as the plain
+    call's do: a bf16 output is the fp32 one with its last rounding."""
+    b = Batch(2100, _lens(2100, 10, 30, 6), Hq, H, d, seed=32)
+    assert b.is_shared()
+    assert torch.equal(b.shared(torch.bfloat16), b.shared(torch.float32).bfloat16())
+
+
+def test_bf16_outputs_of_eight_heads_stay_within_their_rounding():
+    """Eight query heads per kv head and a bf16 output: one fp16 weight per key, as in the plain call.  Half a step
+    of bf16 is 2^-8 at most, its root mean square about 0.42 of it; the weights' 2e-4 hardly adds to that."""
+    b = Batch(2100, _lens(2100, 10, 30, 6), 16, 2, 128, seed=33)
+    assert b.is_shared()
+    ref = torch.from_numpy(b.oracle())
+    assert float((b.shared(torch.bfloat16).double().cpu() - ref).norm() / ref.norm()) < 0.5 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("Hq, H, d", [(8, 2, 64), (32, 8, 128)])
+def test_calls_agree_closely(Hq, H, d):
+    """The two calls' fp32 outputs differ by the rounding of 22-bit weights and queries and of fp32 sums alone."""
+    b = Batch(2000, _lens(2000, 40, 300, 34), Hq, H, d, seed=34, outliers=False)
+    assert b.is_shared()
+    x, y = b.shared().double(), b.plain().double()
+    assert float((x - y).norm() / y.norm()) < 4e-5   # 2e-5 each, see the test of finer outputs
+
+
+def test_more_than_512_sequences():
+    b = Batch(300, [0 if i % 97 == 5 else 1 + i % 300 if i % 31 == 7 else 301 + i % 40 for i in range(700)], 8, 2, 64, seed=35)
+    _check(b, seqs=range(0, 700, 23))
+    _check(b, seqs=[5, 7, 38, 699])
