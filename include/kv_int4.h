@@ -370,7 +370,8 @@ kv_int4_status kv_int4_paged_attention_ex(const void* q, kv_int4_dtype q_dtype, 
  * entries of its block_tables row name the same blocks (entry i of a row is the sequence's tokens 16 i ..
  * 16 i + 15, as in the plain call); the library reads either.  A row whose sequence ends inside the prefix
  * needs no more entries than its tokens: it sees its first seq_lens[b] tokens of the prefix; seq_lens 0 (a
- * padding row) yields zeros.
+ * padding row) yields zeros.  A row that was never written (zeros) counts as in the plain call: a key of logit
+ * 0 and a value of 0.
  *
  * Computation: one kernel takes every query row of the batch against the prefix's keys, split among the
  * SMs, as the prefill does (tcgen05), the decode path takes the tokens behind the prefix, and the

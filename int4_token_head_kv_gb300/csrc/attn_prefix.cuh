@@ -57,11 +57,12 @@ struct PxLayout {
     static constexpr uint32_t kChunks = Pf::kChunks, kWindow = Pf::kWindow;
     static constexpr uint32_t kPlane = kPfKeys * kWindow * 4;                    // one plane of a staged tile
     static constexpr uint32_t kSk = kRaw + kPfRawStages * 2 * kPlane;            // [kring][128] f32 s'_K * k0
-    static constexpr uint32_t kDeadF = kSk + kPfKRing * kPfKeys * 4;             // [kring][4] u32: keys with no row, one bit each
+    static constexpr uint32_t kDeadF = kSk + kPfKRing * kPfKeys * 4;             // [kring][4] u32: positions with no key, one bit each
     static constexpr uint32_t kSv = kDeadF + kPfKRing * 4 * 4;                   // [pairs][128] f32 s'_V
     static constexpr uint32_t kEblk = kSv + kPfPairs * kPfKeys * 4;              // [pairs][4] per-warp max V exponent
     static constexpr uint32_t kQexp = kEblk + kPfPairs * 4 * 4;                  // u32: first usable row and its exponent
-    static constexpr uint32_t kRs = kQexp + 16;                                  // [128] f32 2^-d of each row's own prescale
+    static constexpr uint32_t kHeld = kQexp + 16;                                // [stages] u32: blocks of a staged tile that hold keys
+    static constexpr uint32_t kRs = kHeld + kPfRawStages * 4;                    // [128] f32 2^-d of each row's own prescale
     static constexpr uint32_t kSignBits = kRs + 128 * 4;                         // [D / 32] u32
     static constexpr uint32_t kBars = (kSignBits + D / 8 + 7u) & ~7u;
     // k_full[kring], k_free[pairs], v_full[pairs], v_free[pairs], pv_done[2], s_full[2], p_full[2], q_ready,
@@ -160,12 +161,13 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
     uint64_t* rot_in = q_tma + 1;               // the rotation matrix in shared memory (256 arrivals)
     uint64_t* rot_done = rot_in + 1;            // the rotated queries in tensor memory (commit)
     uint64_t* q_max = rot_done + 1;             // the rows' exponent is known (256 arrivals)
-    uint64_t* raw_full = q_max + 1;             // [plane][stages] packed rows of a key tile landed (bytes, or 32 lanes)
+    uint64_t* raw_full = q_max + 1;             // [plane][stages] packed rows of a key tile landed (one arrival and bytes, or and 32 lanes)
     uint64_t* raw_free = raw_full + 2 * kPfRawStages;   // [plane][stages] that plane converted (128 arrivals)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kFlags);
     uint32_t* deadf = reinterpret_cast<uint32_t*>(smem + Ly::kDeadF);
     uint32_t* qexp = reinterpret_cast<uint32_t*>(smem + Ly::kQexp);
+    uint32_t* held = reinterpret_cast<uint32_t*>(smem + Ly::kHeld);
 
     if (threadIdx.x == 0) {
         for (int b = 0; b < kPfKRing; ++b) mbar_init(&k_full[b], 128);
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         mbar_init(q_max, kPfSoftmaxThreads);
         *qexp = 0xFFFFFFFFu;
         for (int i = 0; i < 2 * kPfRawStages; ++i) {
-            mbar_init(&raw_full[i], boxes ? 1 : 32);
+            mbar_init(&raw_full[i], boxes ? 1 : 33);
             mbar_init(&raw_free[i], 128);
         }
         *abort_flag = 0;
@@ -557,7 +559,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         const bool good = __all_sync(0xffffffffu, ok) && nkt > 0;
         if (none_a) any_a = false;
         if (none_b) any_b = false;
-        const float es = good && E ? __uint_as_float(E << 23) : 0.0f;   // 2^(E - 127)
+        const float es = good ? __uint_as_float((E ? E : 127u) << 23) : 0.0f;   // 2^(E - 127); E none: only rows of zeros
         const float eoff = (float)(127 - (int)(E ? E : 127u));
         const float m_a = any_a ? eoff - off_a : kNegBig, m_b = any_b ? eoff - off_b : kNegBig;
         const int64_t rows = p.num_q_tokens * Hq;
@@ -622,6 +624,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
 #pragma unroll
                 for (int w = 0; w < NW; ++w) kw[w] = (row_off & 1) ? wv[w + 1] : wv[w];
             }
+            const uint32_t blocks = pl == 0 ? held[st] : 0u;
             mbar_arrive(&raw_free[pl * kPfRawStages + st]);
             ok = j != 1 || wait(q_ready, 0);        // the query rows and the rotation matrix sat on pair 1
             if (ok && j >= kPfPairs) ok = wait(pl ? &v_free[kb] : &k_free[kb], (uint32_t)(j / kPfPairs - 1) & 1u);
@@ -644,8 +647,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                     k0 *= exp2i(-rows_exponent(*reinterpret_cast<volatile uint32_t*>(qexp)));
                 }
                 sk[(j % kPfKRing) * kPfKeys + slot_of_column(k)] = __uint_as_float(kw[Gm::KW] & 0xFFFFFFF0u) * k0;
-                const uint32_t nodead = __ballot_sync(0xffffffffu, kw[Gm::KW] == 0u);
-                if (lane == 0) deadf[(j % kPfKRing) * 4 + (warp & 3)] = nodead;
+                const uint32_t nokey = __ballot_sync(0xffffffffu, ((blocks >> (k / kBlockSize)) & 1u) == 0u);   // a row of zeros is a key, of logit 0
+                if (lane == 0) deadf[(j % kPfKRing) * 4 + (warp & 3)] = nokey;
             } else {
                 sv[kb * kPfKeys + (int)trow] = __uint_as_float(kw[Gm::KW] & 0xFFFFFFF0u);
                 const uint32_t wmax = __reduce_max_sync(0xffffffffu, kw[Gm::KW]);   // positive floats order like their bits
@@ -658,8 +661,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         fewer_registers<kPxOtherRegs>();
         if (warp == kPxLoadWarp || warp == kPxLoadWarp + 1) {
             // ============================================================ loads of packed rows
-            // Each row's 16-byte-aligned window, keys past the prefix or in a block outside the cache zero-filled
-            // (scale word 0: no key).  With 4 or 8 kv heads a token's rows are a multiple of 16 bytes and TMA
+            // Each row's 16-byte-aligned window, keys past the prefix or in a block outside the cache zero-filled;
+            // which blocks hold keys goes along with the K rows.  With 4 or 8 kv heads a token's rows are a multiple of 16 bytes and TMA
             // takes a block's windows at once; with 1 or 2 they are not, and the windows are 16-byte copies.
             // A pass moves kKeys whole windows (C lanes each; 30 of 32 lanes), so that a lane keeps its chunk
             // and the offsets are a few integer operations: a precomputed table of them spilled in this
@@ -682,6 +685,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                 return blk;
             };
             int blk_next = lookup(0), blkv = -1;
+            uint32_t blocks = 0;
             bool ok = true;
             int issued = 0;
             for (int j = 0; j < nkt && ok; ++j) {
@@ -693,10 +697,12 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                         if (pl == 0 && h == 0 && qt0 == 0) count_status(p.status, 1);
                         blkv = -1;
                     }
+                    blocks = __ballot_sync(0xffffffffu, blkv >= 0);
                 }
                 if (j >= kPfRawStages) ok = wait(&raw_free[pl * kPfRawStages + st], (uint32_t)(j / kPfRawStages - 1) & 1u);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 const uint32_t dst = smem_u32(smem + Ly::kRaw + (uint32_t)(st * 2 + pl) * Ly::kPlane);
+                if (pl == 0 && lane == 0) held[st] = blocks >> (8 * (j & 3));   // this tile's: the low 8 bits; before the arrival below
                 if (boxes) {
                     // one box [16 tokens][window bytes] per block; block -1 lies outside the tensor and reads as
                     // zeros, as do a last head's bytes past its token's rows
@@ -719,6 +725,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                     if (mine && key < kPfKeys) cp_async16_zfill(dst + 16u * (uint32_t)(key * C + cc), src, live);
                 }
                 cp_async_arrive_noinc(&raw_full[pl * kPfRawStages + st]);
+                if (lane == 0) mbar_arrive(&raw_full[pl * kPfRawStages + st]);
             }
             // no copy outlives the CTA
             cp_async_wait_all();

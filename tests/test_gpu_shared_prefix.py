@@ -487,3 +487,22 @@ def test_more_than_512_sequences():
     b = Batch(300, [0 if i % 97 == 5 else 1 + i % 300 if i % 31 == 7 else 301 + i % 40 for i in range(700)], 8, 2, 64, seed=35)
     _check(b, seqs=range(0, 700, 23))
     _check(b, seqs=[5, 7, 38, 699])
+
+
+@pytest.mark.parametrize("Hq, H", [(8, 8), (8, 4), (8, 2), (8, 1)])
+def test_rows_never_written_count_as_in_the_plain_call(Hq, H):
+    """A row of zeros (its token was skipped) is a key of logit 0 and a value of 0, whichever kernel reads it."""
+    from gpu_helpers import assert_attention_close
+    b = Batch(2048, [2049, 2100, 2048, 40, 16, 700, 2060, 2070, 33], Hq, H, 64, seed=36, outliers=False)
+    assert b.is_shared()
+    r = np.random.default_rng(36)
+    tok = np.concatenate([np.arange(40), 40 + r.permutation(2008)[:900]])   # the first 40: all that some rows see
+    blk = torch.from_numpy(b.prefix_blocks[tok // 16].astype(np.int64)).cuda()
+    b.cache[blk, :, torch.from_numpy(tok % 16).cuda()] = 0
+    b.cache[int(b.prefix_blocks[60]), 0, 3, H - 1] = 0        # a key alone, a value alone
+    b.cache[int(b.prefix_blocks[61]), 1, 4, 0] = 0
+    got, ref = b.shared(), b.oracle()
+    assert_attention_close(got, ref)
+    assert not got[[3, 4, 8]].any()
+    c = b.plain().double()
+    assert float((got.double() - c).norm() / c.norm()) < 1e-3
