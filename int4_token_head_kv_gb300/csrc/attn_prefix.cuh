@@ -675,15 +675,12 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             const uint8_t* base = p.cache + (int64_t)pl * kBlockSize * tok_stride;
             const int ck = lane / C, cc = lane - ck * C;   // this lane's key of a pass and its chunk
             const bool mine = ck < kKeys;
-            // Block ids of four tiles at a time, lane l's those of tile (group) + l / 8, block l % 8 of it
-            // (-1: none), loaded a group ahead: one tile ahead, the load's latency bounded every tile (the
+            // Block ids of four tiles at a time, lane l's that of tile (group) + l / 8, block l % 8 of it
+            // (-1: none, or not in the cache), loaded a group ahead: one tile ahead, the load's latency bounded every tile (the
             // K rows' wait was 2 100 of 3 600 cycles).
             const int nblocks = p.px_len / kBlockSize;
-            auto lookup = [&](int j) -> int {
-                const int i = (kt0 + j) * (kPfKeys / kBlockSize) + lane;
-                int blk = j + lane / 8 < nkt && i < nblocks ? __ldg(table + i) : -1;
-                return blk;
-            };
+            auto inside = [&](int j) -> bool { return j + lane / 8 < nkt && (kt0 + j) * (kPfKeys / kBlockSize) + lane < nblocks; };
+            auto lookup = [&](int j) -> int { return inside(j) ? __ldg(table + (kt0 + j) * (kPfKeys / kBlockSize) + lane) : -1; };
             int blk_next = lookup(0), blkv = -1;
             uint32_t blocks = 0;
             bool ok = true;
@@ -693,8 +690,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                 if ((j & 3) == 0) {
                     blkv = blk_next;
                     blk_next = lookup(j + 4);
-                    if (blkv != -1 && (blkv < 0 || (int64_t)blkv >= p.num_blocks)) {
-                        if (pl == 0 && h == 0 && qt0 == 0) count_status(p.status, 1);
+                    if (blkv < 0 || (int64_t)blkv >= p.num_blocks) {
+                        if (pl == 0 && h == 0 && qt0 == 0 && inside(j)) count_status(p.status, 1);
                         blkv = -1;
                     }
                     blocks = __ballot_sync(0xffffffffu, blkv >= 0);

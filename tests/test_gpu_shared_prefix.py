@@ -506,3 +506,17 @@ def test_rows_never_written_count_as_in_the_plain_call(Hq, H):
     assert not got[[3, 4, 8]].any()
     c = b.plain().double()
     assert float((got.double() - c).norm() / c.norm()) < 1e-3
+
+
+@pytest.mark.parametrize("bad", [-1, -2 ** 31, 2 ** 31 - 1])
+@pytest.mark.parametrize("Hq, H", [(8, 4), (8, 2)])
+def test_any_block_id_outside_the_cache_is_counted(Hq, H, bad):
+    from gpu_helpers import status
+    b = Batch(2048, _lens(2048, 9, 40, 37), Hq, H, 64, seed=37)
+    assert b.is_shared()
+    good = b.shared()
+    assert not any(status().values())
+    b.prefix_blocks[100] = bad
+    got = b.shared()
+    assert status()["block_out_of_range"] > 0
+    assert not torch.equal(got, good) and bool(torch.isfinite(got).all())
