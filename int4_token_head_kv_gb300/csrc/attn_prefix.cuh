@@ -4,10 +4,10 @@
 //
 // The mathematics is the chunked prefill's (attn_prefill.cuh: rotated queries as fp16 high + low halves,
 // S = Q' (K - zp)^T, logit = S s'_K k0 2^-e, weights 2^(logit - m + 127 - E) s'_V, O += P_w (V - zp), all
-// accumulated in fp32), with two differences: a row is one (query token, q head) of any sequence and sees
+// accumulated in fp32), with these differences: a row is one (query token, q head) of any sequence and sees
 // the prefix keys below its own limit (its sequence's length, when that ends inside the prefix; a padding
 // row sees none), and a CTA writes its key range's partial (reference maximum m in log2 units, sum l,
-// unnormalised O, still rotated), which the combine merges with the suffix's.
+// unnormalised O, still rotated), which the combine merges with the suffix's; the weights are raised (kPxRaise).
 //
 // Grid: (row tiles of 128 / G tokens) x kv heads x splits of the prefix's 128-key tiles, one CTA per SM.
 // The splits fill the SMs when the batch alone does not (prefix_splits).
@@ -45,6 +45,14 @@ constexpr int kPxMmaWarp = kPxDequantWarp + 8;
 constexpr int kPxLoadWarp = kPxMmaWarp + 1;              // one per plane (K, V)
 constexpr int kPxThreads = (kPxMmaWarp + 4) * 32;
 constexpr int kPxPolls = 128;                            // about 4 000 cycles, a tile and a bit
+// Binades that a row's largest V scale may pass its reference exponent by, and the power of two the weights are
+// raised by: w < 2^(kPfLazyMax + 0 + 1 + 6), half of fp16's range.  fp16's smallest step then stands for 2^-30 of
+// the reference's weight.  (Without the raise it was 2^-24, and the weights of 2^16 keys some 25 binades below a
+// dominant one, together 2^-9 of the sum, were lost from the output: a CTA's range can be the whole prefix, and it
+// has one reference.)  A maximum that may trail less, 4 binades for a raise of 10, moves more often: 12% of the
+// large calls with strong key channels.
+constexpr uint32_t kPxLazyExp = 0;
+constexpr int kPxRaise = 6;
 constexpr int kPxLaunchRegs = 96, kPxRowRegs = 136, kPxDequantRegs = 72, kPxOtherRegs = 64;
 static_assert(kPxRowRegs * 256 + kPxDequantRegs * 256 + kPxOtherRegs * 128 == kPxLaunchRegs * kPxThreads, "register split");
 
@@ -369,11 +377,11 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         // Keys below this one need no mask; rows with a prescale of their own (rare) go with the masked ones.
         const int plain_vis = own_a || own_b ? 0 : min(vis_a, vis_b);
         // ---- the key tiles
-        // Reference maxima m (log2 units) as the exponents' offsets off = 127 - E - m; m = 0 and E = 127 until a
-        // row has a key (any).
+        // Reference maxima m (log2 units) as the exponents' offsets off = 127 + raise - E - m; E = 127 and off = 0
+        // until a row has a key (any).
         float off_a = 0.0f, off_b = 0.0f;
         bool any_a = false, any_b = false;
-        float l_a = 0.0f, l_b = 0.0f;           // this thread's part of the sums of 2^(127-E) p
+        float l_a = 0.0f, l_b = 0.0f;           // this thread's part of the sums of 2^(127+raise-E) p
         uint32_t E = 0;                         // reference biased exponent of the V scales (0: none yet)
         if (idle) {   // a loop of its own: the test in the loop below cost 3% of the whole call
             for (int j = 0; j < nkt && ok; ++j) {
@@ -398,7 +406,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             tmem_ld_q8(scol, s);
             tmem_ld_q8(scol + 64, s + 32);
             tmem_ld_wait();
-            // Exponents e = S s'_K k0 2^-e - m + 127 - E (one FMA) against the references as they
+            // Exponents e = S s'_K k0 2^-e - m + 127 + raise - E (one FMA) against the references as they
             // are, and their row maxima; a reference that moves is added to them afterwards, which is rare.
             const int key0 = (kt0 + j) * kPfKeys;
             const float4* skb = reinterpret_cast<const float4*>(sk + kr * kPfKeys) + t4;   // columns 16q + (2t, 2t + 1, 8 + 2t, 9 + 2t)
@@ -458,8 +466,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             // the four threads of a row take the same decisions; a row without a reference takes the first one
             const uint32_t* eb4 = eblkw + kb * 4;
             const uint32_t eb = max(max(eb4[0], eb4[1]), max(eb4[2], eb4[3]));
-            const float eoff0 = (float)(127 - (int)(E ? E : 127u));
-            const bool newE = E == 0u ? eb > 0u : eb > E + kPfLazyExp;
+            const float eoff0 = (float)(127 + kPxRaise - (int)(E ? E : 127u));
+            const bool newE = E == 0u ? eb > 0u : eb > E + kPxLazyExp;
             const bool up_a = any_a ? bma > eoff0 + kPfLazyMax : bma > -INFINITY;
             const bool up_b = any_b ? bmb > eoff0 + kPfLazyMax : bmb > -INFINITY;
             if (__any_sync(0xffffffffu, up_a || up_b || newE)) {
@@ -549,7 +557,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             tc_fence_before();
             mbar_arrive(&p_full[b]);
         }
-        // ---- the partial: (m, l 2^(E - 127), O 2^(E - 127)), O's columns in the tile's dimension order
+        // ---- the partial: (m, l 2^(E - 127 - raise), O 2^(E - 127 - raise)), O's columns in the tile's dimension order
         if (ok && nkt > 0) ok = wait(&pv_done[(nkt - 1) & 1], (uint32_t)((nkt - 1) >> 1) & 1u);
         tc_fence_after();
         l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
@@ -559,8 +567,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         const bool good = __all_sync(0xffffffffu, ok) && nkt > 0;
         if (none_a) any_a = false;
         if (none_b) any_b = false;
-        const float es = good ? __uint_as_float((E ? E : 127u) << 23) : 0.0f;   // 2^(E - 127); E none: only rows of zeros
-        const float eoff = (float)(127 - (int)(E ? E : 127u));
+        // 2^(E - 127 - raise); E none: only rows of zeros
+        const float es = good ? __uint_as_float((E ? E : 127u) << 23) * exp2i(-kPxRaise) : 0.0f;
+        const float eoff = (float)(127 + kPxRaise - (int)(E ? E : 127u));
         const float m_a = any_a ? eoff - off_a : kNegBig, m_b = any_b ? eoff - off_b : kNegBig;
         const int64_t rows = p.num_q_tokens * Hq;
         auto record = [&](int r) -> int64_t { return (int64_t)split * rows + (int64_t)(qt0 + r / G) * Hq + h * G + r % G; };

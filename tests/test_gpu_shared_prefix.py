@@ -520,3 +520,37 @@ def test_any_block_id_outside_the_cache_is_counted(Hq, H, bad):
     got = b.shared()
     assert status()["block_out_of_range"] > 0
     assert not torch.equal(got, good) and bool(torch.isfinite(got).all())
+
+
+def test_a_dominant_key_leaves_the_small_weights_their_share():
+    """65 536 keys some 24.5 binades below one of the first: 2^-8.5 of the softmax's mass, and all of the output,
+    because the dominant key's value is zero.  A CTA's range holds all of them (19 row tiles of 8 kv heads are 152
+    CTAs).  Each weight errs by half of fp16's smallest step at most, 2^-25, where the reference has 2^6: 2^16 keys
+    together by 2^-15 of the value's size; a weight is the value's scale of 15 steps times its share."""
+    S, P, Hq, H, d = 304, 65536, 64, 8, 64
+    b = Batch(P, [P + 1 + i % 16 for i in range(S)], Hq, H, d, seed=38)
+    kv, n = _kv(), b.cache.shape[0] * 16
+    rows = S * Hq * (d * 4 + 8)   # bytes of one split's partials
+    need = kv.kv_int4_shared_prefix_workspace_bytes(S, Hq, H, d, S, P, b.max_len)
+    splits = (need - kv.kv_int4_attention_workspace_bytes(Hq, H, d, S, b.max_len - P)) // rows
+    assert splits == 1 or torch.cuda.get_device_properties(0).multi_processor_count != 152
+    g = torch.Generator(device="cuda").manual_seed(38)
+    slot = int(b.prefix_blocks[0]) * 16 + 5
+    k = torch.zeros(n, H, d, dtype=torch.bfloat16, device="cuda")
+    k[slot] = 4.0
+    v = (1.0 + 0.1 * torch.randn(n, H, d, generator=g, device="cuda")).bfloat16()
+    v[slot] = 0.0
+    kv.kv_int4_write(k, v, torch.arange(n, device="cuda"), b.gsigns, b.cache)
+    b.q = torch.full_like(b.q, 24.5 / (4.0 * d * b.scale * 1.4427))
+    got = b.shared().double()
+    size = float(v.float().norm(dim=-1).max())
+    for i in (0, 77, 303):
+        tok = np.arange(int(b.lens[i]))
+        slots = torch.from_numpy(b.tables[i, tok // 16].astype(np.int64) * 16 + tok % 16).cuda()
+        kr, vr = (x.double() for x in kv.kv_int4_read(b.cache, slots, b.gsigns, dtype=torch.float32))
+        for h in (0, 7):
+            x = b.scale * kr[:, h] @ b.q[i, h * 8].double()
+            assert 24.0 < float(x[5] - x[6]) * 1.442695 < 25.5
+            ref = torch.softmax(x, 0) @ vr[:, h]
+            err = float((got[i, h * 8] - ref).norm())
+            assert err < 2.0 ** -15 * 2 * size + 2e-5 * float(ref.norm()), (err, float(ref.norm()))
