@@ -382,7 +382,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         float off_a = 0.0f, off_b = 0.0f;
         bool any_a = false, any_b = false;
         float l_a = 0.0f, l_b = 0.0f;           // this thread's part of the sums of 2^(127+raise-E) p
-        uint32_t E = 0;                         // reference biased exponent of the V scales (0: none yet)
+        // Reference biased exponents of the V scales that the rows see (0: none yet).  Each row has its own: a key
+        // behind its sequence's end, infinite perhaps, must not move it.
+        uint32_t E_a = 0, E_b = 0;
         if (idle) {   // a loop of its own: the test in the loop below cost 3% of the whole call
             for (int j = 0; j < nkt && ok; ++j) {
                 ok = wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u);
@@ -413,6 +415,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             const bool clean = (deadf[kr * 4] | deadf[kr * 4 + 1] | deadf[kr * 4 + 2] | deadf[kr * 4 + 3]) == 0u &&
                                key0 + kPfKeys <= plain_vis;
             float bma = -INFINITY, bmb = -INFINITY;
+            const uint32_t* eb4 = eblkw + kb * 4;
+            const float4* svb = reinterpret_cast<const float4*>(sv + kb * kPfKeys) + t4;
+            uint32_t eb_a = max(max(eb4[0], eb4[1]), max(eb4[2], eb4[3])), eb_b = eb_a;
             if (!OPTS && __all_sync(0xffffffffu, clean)) {   // every key live and visible to both rows, rs 1
                 const float2 moa2 = make_float2(off_a, off_a), mob2 = make_float2(off_b, off_b);
 #pragma unroll
@@ -458,37 +463,60 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                         bmb = fmaxf(bmb, eb);
                     }
                 }
+                if (__any_sync(0xffffffffu, key0 + kPfKeys > min(vis_a, vis_b))) {   // the V scales of the visible keys alone
+                    uint32_t ma = 0u, mb = 0u;
+#pragma unroll 1
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 v4 = svb[4 * q];
+                        const float v[4] = {v4.x, v4.y, v4.z, v4.w};   // keys 16q + (2t, 2t + 1, 8 + 2t, 9 + 2t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0 + 16 * q + 8 * (e >> 1) + 2 * t4 + (e & 1);
+                            const uint32_t bits = __float_as_uint(v[e]) + 1u;   // the largest finite value stands for infinity
+                            if (key < vis_a) ma = max(ma, bits);
+                            if (key < vis_b) mb = max(mb, bits);
+                        }
+                    }
+#pragma unroll
+                    for (int off = 1; off < 4; off <<= 1) {
+                        ma = max(ma, __shfl_xor_sync(0xffffffffu, ma, off));
+                        mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, off));
+                    }
+                    eb_a = ma >> 23;
+                    eb_b = mb >> 23;
+                }
             }
             bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 1));
             bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 1));
             bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 2));
             bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 2));
             // the four threads of a row take the same decisions; a row without a reference takes the first one
-            const uint32_t* eb4 = eblkw + kb * 4;
-            const uint32_t eb = max(max(eb4[0], eb4[1]), max(eb4[2], eb4[3]));
-            const float eoff0 = (float)(127 + kPxRaise - (int)(E ? E : 127u));
-            const bool newE = E == 0u ? eb > 0u : eb > E + kPxLazyExp;
-            const bool up_a = any_a ? bma > eoff0 + kPfLazyMax : bma > -INFINITY;
-            const bool up_b = any_b ? bmb > eoff0 + kPfLazyMax : bmb > -INFINITY;
-            if (__any_sync(0xffffffffu, up_a || up_b || newE)) {
-                const float da = up_a ? eoff0 - bma : 0.0f, db = up_b ? eoff0 - bmb : 0.0f;   // old reference - new one
+            const float eoff_a = (float)(127 + kPxRaise - (int)(E_a ? E_a : 127u)), eoff_b = (float)(127 + kPxRaise - (int)(E_b ? E_b : 127u));
+            const bool newE_a = E_a == 0u ? eb_a > 0u : eb_a > E_a + kPxLazyExp;
+            const bool newE_b = E_b == 0u ? eb_b > 0u : eb_b > E_b + kPxLazyExp;
+            const bool up_a = any_a ? bma > eoff_a + kPfLazyMax : bma > -INFINITY;
+            const bool up_b = any_b ? bmb > eoff_b + kPfLazyMax : bmb > -INFINITY;
+            if (__any_sync(0xffffffffu, up_a || up_b || newE_a || newE_b)) {
+                const float da = up_a ? eoff_a - bma : 0.0f, db = up_b ? eoff_b - bmb : 0.0f;   // old reference - new one
                 const float fm_a = up_a ? (any_a ? fast_exp2(da) : 0.0f) : 1.0f, fm_b = up_b ? (any_b ? fast_exp2(db) : 0.0f) : 1.0f;
                 any_a = any_a || up_a;
                 any_b = any_b || up_b;
-                const uint32_t Eeff = E ? E : 127u;
-                float fe = 1.0f, de = 0.0f;
-                if (newE) {
-                    // rebase from 2^(127 - Eeff) to 2^(127 - eb); 0 when the jump underflows
+                // rebase from 2^(127 - E) to 2^(127 - eb); 0 when the jump underflows
+                auto rebase = [](uint32_t& E, uint32_t eb, float& fe, float& de) {
+                    const uint32_t Eeff = E ? E : 127u;
                     fe = eb > Eeff + 126u ? 0.0f : __uint_as_float((127u + Eeff - eb) << 23);
                     de = (float)((int)Eeff - (int)eb);
                     E = eb;
-                }
-                const float f_a = fm_a * fe, f_b = fm_b * fe;
+                };
+                float fe_a = 1.0f, fe_b = 1.0f, de_a = 0.0f, de_b = 0.0f;
+                if (newE_a) rebase(E_a, eb_a, fe_a, de_a);
+                if (newE_b) rebase(E_b, eb_b, fe_b, de_b);
+                const float f_a = fm_a * fe_a, f_b = fm_b * fe_b;
                 l_a *= f_a;
                 l_b *= f_b;
-                off_a += da + de;
-                off_b += db + de;
-                const float2 da2 = make_float2(da + de, da + de), db2 = make_float2(db + de, db + de);
+                off_a += da + de_a;
+                off_b += db + de_b;
+                const float2 da2 = make_float2(da + de_a, da + de_a), db2 = make_float2(db + de_b, db + de_b);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float2 ea = add_f32x2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), da2);
@@ -525,7 +553,6 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             }
             // p' = 2^e, w = p' s'_V as fp16 pairs over the first 64 S columns: the pair of columns 8i + 2t, + 1
             // goes to column 8 (i / 2) + 2t + i % 2 (the V tile holds its rows in the matching order)
-            const float4* svb = reinterpret_cast<const float4*>(sv + kb * kPfKeys) + t4;
             float2 lsa = make_float2(0.0f, 0.0f), lsb = make_float2(0.0f, 0.0f);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -567,16 +594,17 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         const bool good = __all_sync(0xffffffffu, ok) && nkt > 0;
         if (none_a) any_a = false;
         if (none_b) any_b = false;
-        // 2^(E - 127 - raise); E none: only rows of zeros
-        const float es = good ? __uint_as_float((E ? E : 127u) << 23) * exp2i(-kPxRaise) : 0.0f;
-        const float eoff = (float)(127 + kPxRaise - (int)(E ? E : 127u));
-        const float m_a = any_a ? eoff - off_a : kNegBig, m_b = any_b ? eoff - off_b : kNegBig;
+        E_a = E_a ? E_a : 127u;   // none: only rows of zeros
+        E_b = E_b ? E_b : 127u;
+        const float es_a = __uint_as_float(E_a << 23) * exp2i(-kPxRaise), es_b = __uint_as_float(E_b << 23) * exp2i(-kPxRaise);
+        const float m_a = any_a ? (float)(127 + kPxRaise - (int)E_a) - off_a : kNegBig;
+        const float m_b = any_b ? (float)(127 + kPxRaise - (int)E_b) - off_b : kNegBig;
         const int64_t rows = p.num_q_tokens * Hq;
         auto record = [&](int r) -> int64_t { return (int64_t)split * rows + (int64_t)(qt0 + r / G) * Hq + h * G + r % G; };
         auto in_batch = [&](int r) -> bool { return (int64_t)(qt0 + r / G) < p.num_q_tokens; };
         if (t4 == 0) {
-            if (in_batch(ra)) reinterpret_cast<float2*>(p.px_ml)[record(ra)] = any_a && good ? make_float2(m_a, l_a * es) : make_float2(kNegBig, 0.0f);
-            if (in_batch(rb)) reinterpret_cast<float2*>(p.px_ml)[record(rb)] = any_b && good ? make_float2(m_b, l_b * es) : make_float2(kNegBig, 0.0f);
+            if (in_batch(ra)) reinterpret_cast<float2*>(p.px_ml)[record(ra)] = any_a && good ? make_float2(m_a, l_a * es_a) : make_float2(kNegBig, 0.0f);
+            if (in_batch(rb)) reinterpret_cast<float2*>(p.px_ml)[record(rb)] = any_b && good ? make_float2(m_b, l_b * es_b) : make_float2(kNegBig, 0.0f);
         }
         const bool full_a = good && any_a, full_b = good && any_b, in_a = in_batch(ra), in_b = in_batch(rb);
         float* oa_row = p.px_o + (in_a ? record(ra) : 0) * D + 2 * t4;
@@ -590,8 +618,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 oa = full_a ? make_float2(__uint_as_float(o[4 * i]) * es, __uint_as_float(o[4 * i + 1]) * es) : make_float2(0.0f, 0.0f);
-                const float2 ob = full_b ? make_float2(__uint_as_float(o[4 * i + 2]) * es, __uint_as_float(o[4 * i + 3]) * es) : make_float2(0.0f, 0.0f);
+                const float2 oa = full_a ? make_float2(__uint_as_float(o[4 * i]) * es_a, __uint_as_float(o[4 * i + 1]) * es_a) : make_float2(0.0f, 0.0f);
+                const float2 ob = full_b ? make_float2(__uint_as_float(o[4 * i + 2]) * es_b, __uint_as_float(o[4 * i + 3]) * es_b) : make_float2(0.0f, 0.0f);
                 if (in_a) *reinterpret_cast<float2*>(oa_row + c0 + 8 * i) = oa;
                 if (in_b) *reinterpret_cast<float2*>(ob_row + c0 + 8 * i) = ob;
             }
@@ -659,7 +687,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
                 const uint32_t nokey = __ballot_sync(0xffffffffu, ((blocks >> (k / kBlockSize)) & 1u) == 0u);   // a row of zeros is a key, of logit 0
                 if (lane == 0) deadf[(j % kPfKRing) * 4 + (warp & 3)] = nokey;
             } else {
-                sv[kb * kPfKeys + (int)trow] = __uint_as_float(kw[Gm::KW] & 0xFFFFFFF0u);
+                // finite, so that a weight of 0 stays one; an infinite scale shows in the exponent
+                sv[kb * kPfKeys + (int)trow] = fminf(__uint_as_float(kw[Gm::KW] & 0xFFFFFFF0u), 3.4028234664e38f);
                 const uint32_t wmax = __reduce_max_sync(0xffffffffu, kw[Gm::KW]);   // positive floats order like their bits
                 if (lane == 0) eblkw[kb * 4 + (warp & 3)] = (wmax >> 23) & 0xFFu;
             }

@@ -554,3 +554,29 @@ def test_a_dominant_key_leaves_the_small_weights_their_share():
             ref = torch.softmax(x, 0) @ vr[:, h]
             err = float((got[i, h * 8] - ref).norm())
             assert err < 2.0 ** -15 * 2 * size + 2e-5 * float(ref.norm()), (err, float(ref.norm()))
+
+
+@pytest.mark.parametrize("value", [float("inf"), 1e30, 1e6])
+@pytest.mark.parametrize("Hq, H", [(8, 4), (8, 1)])
+def test_values_behind_a_sequences_end_stay_out_of_it(Hq, H, value):
+    """Sequences that end inside the prefix, before a token whose value vector is infinite or huge: in its tile and
+    before it."""
+    from gpu_helpers import assert_attention_close
+    lens = [2041, 1500, 1499, 1490, 1409, 1408, 1400, 130, 2100, 1, 1501]
+    b = Batch(2040, lens, Hq, H, 128, seed=39, outliers=False)
+    assert b.is_shared()
+    kv = _kv()
+    at = torch.tensor([int(b.prefix_blocks[1500 // 16]) * 16 + 1500 % 16], device="cuda")
+    x = torch.randn(1, H, 128, device="cuda").bfloat16()
+    y = x.clone()
+    y[:, :, 7] = value
+    kv.kv_int4_write(x, y, at, b.gsigns, b.cache)
+    before = [i for i, l in enumerate(lens) if l <= 1500]
+    ref = b.oracle(seqs=before)
+    for o in (torch.float32, torch.bfloat16):
+        got, plain = b.shared(out_dtype=o), b.plain(out_dtype=o)
+        assert_attention_close(got[before], ref[before])
+        assert torch.equal(torch.isfinite(got), torch.isfinite(plain))
+    for opts in (dict(window_left=1200), dict(softcap=30.0)):
+        got, plain = b.shared(**opts), b.plain(**opts)
+        assert_attention_close(got[before], plain[before].double().cpu().numpy())
