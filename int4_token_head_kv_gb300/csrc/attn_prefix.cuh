@@ -592,8 +592,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
         l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
         const bool good = __all_sync(0xffffffffu, ok) && nkt > 0;
-        if (none_a) any_a = false;
-        if (none_b) any_b = false;
+        // a row that met only NaN (its query or the keys are not finite) shows it: no maximum tells
+        any_a = (any_a || l_a != l_a) && !none_a;
+        any_b = (any_b || l_b != l_b) && !none_b;
         E_a = E_a ? E_a : 127u;   // none: only rows of zeros
         E_b = E_b ? E_b : 127u;
         const float es_a = __uint_as_float(E_a << 23) * exp2i(-kPxRaise), es_b = __uint_as_float(E_b << 23) * exp2i(-kPxRaise);

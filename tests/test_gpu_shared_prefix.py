@@ -580,3 +580,30 @@ def test_values_behind_a_sequences_end_stay_out_of_it(Hq, H, value):
     for opts in (dict(window_left=1200), dict(softcap=30.0)):
         got, plain = b.shared(**opts), b.plain(**opts)
         assert_attention_close(got[before], plain[before].double().cpu().numpy())
+
+
+@pytest.mark.parametrize("opts", [{}, dict(softcap=20.0)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite_shows(bad, opts):
+    """Its outputs are not finite, wherever its sequence ends, as the plain call's are not."""
+    b = Batch(2048, [2049, 100, 2048, 2100, 1500, 0, 16, 2060, 2070], 8, 2, 128, seed=40, outliers=False)
+    assert b.is_shared()
+    for i in range(9):
+        b.q[i, :, 5 * i] = bad
+    b.q[7] = 1.0
+    got, plain = b.shared(**opts), b.plain(**opts)
+    assert torch.equal(torch.isfinite(got), torch.isfinite(plain))
+    assert not torch.isfinite(got[[0, 1, 2, 3, 4, 6, 8]]).any() and bool((got[5] == 0).all())
+
+
+def test_a_key_that_is_not_finite_shows():
+    """An infinite key of the prefix makes the outputs of the sequences that see it NaN, and no other's."""
+    b = Batch(2048, [2049, 100, 2048, 2100, 700, 1500, 701, 2060, 2070], 8, 2, 128, seed=41, outliers=False)
+    assert b.is_shared()
+    at = torch.tensor([int(b.prefix_blocks[700 // 16]) * 16 + 700 % 16], device="cuda")
+    x = torch.randn(1, 2, 128, device="cuda").bfloat16()
+    x[:, 1, 9] = float("inf")
+    _kv().kv_int4_write(x, x.nan_to_num(0, 0, 0), at, b.gsigns, b.cache)
+    got, plain = b.shared(), b.plain()
+    assert torch.equal(torch.isfinite(got), torch.isfinite(plain))
+    assert bool(torch.isfinite(got[[1, 4]]).all()) and not torch.isfinite(got[0, 4:]).any()
