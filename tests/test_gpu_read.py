@@ -183,3 +183,22 @@ def test_outputs_belong_to_the_stream_that_writes_them(raw):
     got = kv.kv_int4_read(cache, slots, signs, dtype=torch.float32, stream=0)   # the default stream's handle
     want = kv.kv_int4_read(cache, slots, signs, dtype=torch.float32)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_int4_rows_come_back_within_their_own_step():
+    """A stored INT4 vector comes back within half a step of its row's own scale s' in every rotated dimension:
+    code = N(y / s' + zp), and with elements of both signs no y / s' + zp lies further than half outside 0..15 (s' is
+    short of (max - min) / 15 by less than 2^-19 of it).  So within sqrt(d) s' / 2 in the 2-norm, with 1e-4 for that
+    and the fp32 butterflies; a read-back of zeros would not be."""
+    kv = _kv()
+    wl = workloads.random_write(60, 4, 128, seed=22)
+    signs, slots = torch.from_numpy(wl.signs).cuda(), torch.from_numpy(wl.slot_mapping).cuda()
+    k, v = wl.key.cuda(), wl.value.cuda()
+    cache = torch.zeros(kv.kv_int4_cache_shape(wl.num_blocks, 16, 4, 128), dtype=torch.uint8, device="cuda")
+    kv.kv_int4_write(k, v, slots, signs, cache)
+    words = cache[slots // 16, :, slots % 16, :, -4:].contiguous().view(torch.int32)[..., 0]   # [T, 2, H]
+    step = (words & -16).view(torch.float32)
+    for p, (g, x) in enumerate(zip(kv.kv_int4_read(cache, slots, signs, dtype=torch.float32), (k.float(), v.float()))):
+        bound = 128 ** 0.5 / 2 * step[:, p] * (1 + 1e-4)
+        assert bool(((g - x).norm(dim=-1) <= bound).all())
+        assert bool((x.norm(dim=-1) > bound).all())
