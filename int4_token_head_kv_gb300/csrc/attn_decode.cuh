@@ -573,6 +573,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2) decode_kernel(const __grid_
             ub += fast_div((uint32_t)(own_info(b - b0, false).x + S - 1), (uint32_t)S, p.seg_rcp);
         }
         if (threadIdx.x == 0) p.ws_meta[N] = (int)U;
+        __syncthreads();   // the first copies below land where every thread has just read its sequences' lengths
     }
     if (threadIdx.x == 0) {   // the first query rows, then the first blocks
         for (int r = 0; r < min(nq, nruns); ++r) produce_q(r);

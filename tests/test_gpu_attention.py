@@ -349,3 +349,16 @@ def test_options_together():
     wl.query = (wl.query.float() * 4.0).to(wl.query.dtype)
     _run_opts(wl, window_left=150, softcap=8.0, slopes=[0.03 * (i + 1) for i in range(32)],
               qq_bias=np.random.default_rng(36).uniform(-2, 2, (200, 200)))
+
+
+def test_many_sequences_give_the_same_bits_every_time():
+    """More sequences than the combine counts for itself (512): it takes their first segments from memory, where
+    the walker's first CTA leaves them while its own first copies start."""
+    from gpu_helpers import assert_attention_close, dev, gpu_attention, oracle_attention, oracle_cache
+    r = np.random.default_rng(12)
+    wl = workloads.make_attention_workload("many_sequences", [int(n) for n in r.integers(1, 260, 900)], [1] * 900, 8, 2, 64, seed=12)
+    cache = torch.from_numpy(oracle_cache(wl)).to(dev())
+    first = gpu_attention(wl, cache)
+    assert_attention_close(first, oracle_attention(wl, cache.cpu().numpy(), seqs=range(0, 900, 90)))
+    for _ in range(40):
+        assert torch.equal(gpu_attention(wl, cache), first)
