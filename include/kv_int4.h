@@ -362,9 +362,9 @@ kv_int4_status kv_int4_paged_attention_ex(const void* q, kv_int4_dtype q_dtype, 
 
 /*
  * kv_int4_shared_prefix_attention -- kv_int4_paged_attention for a decode batch whose sequences start
- * with the same cached tokens (samples of one prompt, questions on one document): the same result, with
- * the shared tokens read and dequantised once for up to 128 / (num_q_heads / num_kv_heads) sequences
- * instead of once for each.
+ * with the same cached tokens (samples of one prompt, questions on one document): the same result, up to
+ * rounding, with the shared tokens read and dequantised once for up to 128 / (num_q_heads / num_kv_heads)
+ * sequences instead of once for each.
  *
  * The first prefix_len / 16 (rounded down) blocks of every sequence are prefix_blocks, and the first
  * entries of its block_tables row name the same blocks (entry i of a row is the sequence's tokens 16 i ..
@@ -378,8 +378,10 @@ kv_int4_status kv_int4_paged_attention_ex(const void* q, kv_int4_dtype q_dtype, 
  * combine merges both in a fixed order.  With one sequence, where num_seqs x the shared tokens is below
  * 16 384 (8 192 with up to 4 kv heads and 4096 shared tokens), or with fewer shared tokens than 32 per query
  * head of a kv head (216 + 40 num_kv_heads with eight of them), the extra launch would cost more than it
- * saves, and it is the plain call.  The prefix's split depends on the batch's size,
- * so a sequence's output may differ in the last bits between batches; the same call gives the same bits.
+ * saves, and it is the plain call.  The prefix's split depends on the batch's size, and the rows of a tile share
+ * a power-of-two prescale, so a sequence's output may differ in the last bits between batches; the same call
+ * gives the same bits.  Queries and sums keep 22 bits and more, the softmax weights 22 (11 with eight query heads
+ * per kv head and a bf16 output), as in the plain call (11 with eight heads).
  *
  * prefix_blocks  [prefix_len / 16] int32, may be NULL when prefix_len < 16.
  * prefix_len     0 .. 16 max_blocks_per_seq + 15, at most 2^30.

@@ -393,8 +393,8 @@ bool ws_layout(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size, int
 // The shared-prefix rule.  The prefix kernel adds a launch and its start-up (10 us or so), and saves the
 // repeated reads of the plain walk, whose time goes by the tokens walked in all and, with few kv heads, by a
 // long context's many partials.  So the prefix is shared from num_seqs x tokens = 16 384 on, and with up to 4
-// kv heads and 4096 tokens or more from 8 192 on.  Measured over 210 shapes (2..128 sequences, prefixes of
-// 256..65 536 tokens, seven head layouts) this is within 0.6% of the faster one in the mean and 16% at worst:
+// kv heads and 4096 tokens or more from 8 192 on.  Over 210 shapes (2..128 sequences, prefixes of 256..65 536
+// tokens, seven head layouts) this was within 0.6% of the faster one in the mean and 16% at worst:
 // 32 x 1024 tokens, 32 q / 8 kv heads, d 128: shared 20.4 us, plain 27.2; 8 x 1024: 17.8 and 12.5; 4 x 4096:
 // 20.8 and 18.3; 2 x 4096 with 8 q / 1 kv heads, d 64: 18.0 and 41.3.
 //

@@ -24,15 +24,17 @@
 // next, which takes the same of the two S buffers, and each hand-over costs 300-700 until the MMAs issued have
 // run and the other side is awake; tensor memory is full (two S, O, the queries' halves), so there is no third
 // buffer.  Beside it K's and V's rows of a tile take 700 and 1 000.  Shared memory is what makes the MMAs run late:
-// its data pipe is 84% busy (28% the MMAs' operands, 55% loads and stores: per tile 512 cycles of scales for the
+// its data pipe is 83% busy (29% the MMAs' operands, 54% loads and stores: per tile 512 cycles of scales for the
 // softmax, 512 of converted rows, 320 of packed ones).  What the steps gave on 128 sequences, 131 072
 // shared tokens, 64 q / 8 kv heads (961 us at first): block ids looked up four tiles ahead and copies without a
 // spilled table, descriptors in uniform registers: 812; one prescale per CTA, so that one FMA forms the
 // exponent, and a fixed MMA order: 775; a walker grid for the tokens behind the prefix alone: 729; packed rows by
-// TMA boxes instead of 16-byte copies: 696; polling in the chain's waits: 665; V rows read without bank conflicts: 661.  Tried and dropped: forming the
-// weights before the maxima are known (no gain), 16 softmax warps with half of the keys each (923), output rows
-// staged for bulk stores (no gain), S as two products of 64 keys, so that one of them need not wait for P.V (713
-// against 683), weights handed over in two halves (674 against 665).
+// TMA boxes instead of 16-byte copies: 696; polling in the chain's waits: 665; V rows read without bank conflicts:
+// 661.  Since then blocks that hold keys are told from rows of zeros, the weights are raised and each row has its
+// own V exponent: 679.  Tried and dropped: forming the weights before the maxima are known (no gain), 16 softmax
+// warps with half of the keys each (923), output rows staged for bulk stores (no gain), S as two products of 64
+// keys, so that one of them need not wait for P.V (713 against 683), weights handed over in two halves (674 against
+// 665).
 #pragma once
 
 #include "attn_prefill.cuh"
@@ -130,7 +132,8 @@ __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec
 // carries them with up to four query heads per kv head.  One fp16 weight per key errs by up to 2^-11, as much
 // as the rounding of an fp16 output: results were 1.4-1.7 times as far off as that rounding alone.  With eight
 // heads per kv head the walker has one half, and so has this kernel then for a bf16 output, whose error against
-// 64 bits it raises by a hundredth (0.00167 to 0.00169 in the 2-norm); the second half costs 5-8% of the call.
+// 64 bits it raises by a hundredth (0.00167 to 0.00169 in the 2-norm).  The second half costs 11% (four heads per
+// kv head) or 14% (eight) of a large call.
 template <int D, typename QT, bool OPTS, bool TWO>
 __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap qmap,
                                                                   const __grid_constant__ CUtensorMap cmap) {
@@ -313,8 +316,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) prefix_kernel(const __grid_cons
         // ---- a power-of-two prescale of the rows, then fp16 high + low halves into tensor memory.  One exponent
         // serves the CTA, so that 2^-e sits in the keys' scales and not in a factor per row: it brings the first
         // usable row's max |v| (finite, not zero, of a row that sees keys) to [2^7, 2^8).  A row whose largest value
-        // then lies in [2^-2, 2^15) keeps 22 bits; any other (2^9 away, infinite) takes a further power of two of
-        // its own, so no row's values reach another's results.
+        // then lies in [2^-2, 2^15) keeps 22 bits of it (its elements err by 2^-25 at most, or 2^-23 relative); any
+        // other (2^9 away, infinite) takes a further power of two of its own.  So a row's values reach another's
+        // results in the last bits alone.
         float* rs = reinterpret_cast<float*>(smem + Ly::kRs);   // what a row's S is multiplied with
         bool own_a = false, own_b = false;
         bool ok = wait(rot_done, 0);
