@@ -12,6 +12,7 @@
  *   kv_int2_write            the INT2 per-(token, head) Lloyd-Max cache write;
  *   kv_int2_paged_attention  decode attention over the INT2 cache;
  *   kv_int{4,8,2}_rope_write the writes with the rotary position embedding of queries and keys;
+ *   kv_int{4,8,2}_mrope_write  the same with positions on several axes;
  *   kv_int{4,8,2}_read       cached rows back as the keys and values they stand for;
  *   kv_int4_shared_prefix_attention  decode attention of a batch that shares a cached prefix.
  *
@@ -219,6 +220,47 @@ kv_int4_status kv_int2_rope_write(const void* q, int64_t q_token_stride, int32_t
                                   int32_t rot_dim, int32_t interleaved, const int64_t* slot_mapping,
                                   const float* rht_signs, void* q_out, int64_t q_out_token_stride, uint8_t* cache,
                                   int64_t num_blocks, int32_t block_size, kv_int4_stream_t stream);
+
+/*
+ * kv_int4_mrope_write -- kv_int4_rope_write with positions on several axes, as images and videos have them (time,
+ * height, width): pair i takes its cosine and sine from the table row of its own axis,
+ *   c_i = cos_sin[positions[pair_axis[i]][t]][i],  s_i = cos_sin[positions[pair_axis[i]][t]][rot_dim/2 + i],
+ * and everything else is as there, bit for bit.
+ *
+ * positions      [num_axes, num_tokens] int64.  A token with a position outside [0, max_position) on any axis is
+ *                skipped whole and counted once, unless its slot and all its positions are negative: a padding token.
+ * num_axes       1..4.
+ * pair_axis      HOST array [rot_dim / 2], read during the call: the axis of every pair, 0 .. num_axes - 1.
+ * Other arguments, limits and errors as kv_int4_rope_write.
+ */
+kv_int4_status kv_int4_mrope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                                   int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                                   int64_t num_tokens, int32_t num_kv_heads, int32_t head_size,
+                                   const int64_t* positions, int32_t num_axes, const uint8_t* pair_axis,
+                                   const float* cos_sin, int64_t max_position, int32_t rot_dim, int32_t interleaved,
+                                   const int64_t* slot_mapping, const float* rht_signs, void* q_out,
+                                   int64_t q_out_token_stride, uint8_t* cache, int64_t num_blocks, int32_t block_size,
+                                   kv_int4_stream_t stream);
+
+/* kv_int8_mrope_write -- the same into the INT8 comparator's cache (rows as kv_int8_write; no signs). */
+kv_int4_status kv_int8_mrope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                                   int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                                   int64_t num_tokens, int32_t num_kv_heads, int32_t head_size,
+                                   const int64_t* positions, int32_t num_axes, const uint8_t* pair_axis,
+                                   const float* cos_sin, int64_t max_position, int32_t rot_dim, int32_t interleaved,
+                                   const int64_t* slot_mapping, void* q_out,
+                                   int64_t q_out_token_stride, uint8_t* cache, int64_t num_blocks, int32_t block_size,
+                                   kv_int4_stream_t stream);
+
+/* kv_int2_mrope_write -- the same into the INT2 Lloyd-Max cache (rows as kv_int2_write). */
+kv_int4_status kv_int2_mrope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                                   int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                                   int64_t num_tokens, int32_t num_kv_heads, int32_t head_size,
+                                   const int64_t* positions, int32_t num_axes, const uint8_t* pair_axis,
+                                   const float* cos_sin, int64_t max_position, int32_t rot_dim, int32_t interleaved,
+                                   const int64_t* slot_mapping, const float* rht_signs, void* q_out,
+                                   int64_t q_out_token_stride, uint8_t* cache, int64_t num_blocks, int32_t block_size,
+                                   kv_int4_stream_t stream);
 
 /*
  * kv_int4_read -- the keys and values that cached rows stand for: the inverse of kv_int4_write, for

@@ -9,6 +9,7 @@ ImportError when the library has not been built (``python int4_token_head_kv_gb3
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -67,6 +68,11 @@ def _load():
     lib.kv_int8_rope_write.restype = ctypes.c_int
     lib.kv_int2_rope_write.argtypes = lib.kv_int4_rope_write.argtypes
     lib.kv_int2_rope_write.restype = ctypes.c_int
+    for name, signs in (("kv_int4_mrope_write", [vp]), ("kv_int8_mrope_write", []), ("kv_int2_mrope_write", [vp])):
+        f = getattr(lib, name)
+        f.argtypes = [vp, i64, i32, vp, i64, vp, i64, ctypes.c_int, i64, i32, i32, vp, i32, ctypes.c_char_p, vp, i64, i32,
+                      i32, vp] + signs + [vp, i64, vp, i64, i32, vp]
+        f.restype = ctypes.c_int
     lib.kv_int4_read.argtypes = [vp, i64, i32, i32, i32, vp, i64, vp, vp, vp, ctypes.c_int, vp]
     lib.kv_int4_read.restype = ctypes.c_int
     lib.kv_int8_read.argtypes = [vp, i64, i32, i32, i32, vp, i64, vp, vp, ctypes.c_int, vp]
@@ -296,12 +302,24 @@ _HALF_TYPES = (torch.float16, torch.bfloat16)
 _I64, _F32, _U8, _I32 = (torch.int64,), (torch.float32,), (torch.uint8,), (torch.int32,)
 
 
+@functools.lru_cache(maxsize=256)
+def _pair_axes(sections: tuple, mixed: bool) -> bytes:
+    """The axis of every rotated pair, one byte each: the sections one after another, or dealt out in turn while
+    they last when ``mixed``."""
+    if not sections or len(sections) > 4 or any(not isinstance(n, int) or n < 0 for n in sections):
+        raise ValueError("sections must be one to four counts of pairs, one for each axis")
+    if not mixed:
+        return bytes(a for a, n in enumerate(sections) for _ in range(n))
+    turns = range(max(sections))
+    return bytes(a for i in turns for a, n in enumerate(sections) if i < n)
+
+
 def _rope_write(fn, bits, query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache, query_out,
-                interleaved, stream):
+                interleaved, stream, sections=None, mixed=False):
     if stream is not None:
         with _current(stream, key):
             return _rope_write(fn, bits, query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache,
-                               query_out, interleaved, None)
+                               query_out, interleaved, None, sections, mixed)
     kshape, kst = _token_rows(key, "key", _HALF_TYPES)
     dtype = key.dtype
     vshape, vst = _token_rows(value, "value", (dtype,))
@@ -318,11 +336,20 @@ def _rope_write(fn, bits, query, key, value, positions, cos_sin, slot_mapping, r
         if rht_signs.shape != (d,):
             raise ValueError("rht_signs must be [head_size]")
         signs = (rht_signs.data_ptr(),)
-    if slot_mapping.shape != (T,) or positions.shape != (T,):
-        raise ValueError("positions and slot_mapping must be [num_tokens]")
     table = cos_sin.shape
     if len(table) != 2:
         raise ValueError("cos_sin must be [max_position, rot_dim]")
+    axes = ()
+    if sections is None:
+        if slot_mapping.shape != (T,) or positions.shape != (T,):
+            raise ValueError("positions and slot_mapping must be [num_tokens]")
+    else:
+        pairs = _pair_axes(tuple(sections), bool(mixed))
+        if 2 * len(pairs) != table[1]:
+            raise ValueError("the sections must sum to rot_dim / 2 pairs")
+        if slot_mapping.shape != (T,) or positions.shape != (len(sections), T):
+            raise ValueError("positions must be [num_axes, num_tokens], one row for each section, and slot_mapping [num_tokens]")
+        axes = (len(sections), pairs)
     cshape, rb = kv_cache.shape, d * bits // 8 + 4
     if len(cshape) != 5 or cshape[1] != 2 or cshape[3] != H or cshape[4] != rb:
         raise ValueError(f"kv_cache must be (NB, 2, bs, {H}, {rb})")
@@ -345,7 +372,7 @@ def _rope_write(fn, bits, query, key, value, positions, cos_sin, slot_mapping, r
         raise ValueError("query_out needs a query")
     _call(fn, (query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache, query_out), (),
           qptr, qst, Hq, key.data_ptr(), kst, value.data_ptr(), vst, _DTYPES[dtype], T, H, d, positions.data_ptr(),
-          cos_sin.data_ptr(), table[0], table[1], 1 if interleaved else 0, slot_mapping.data_ptr(), *signs, qoptr, qost,
+          *axes, cos_sin.data_ptr(), table[0], table[1], 1 if interleaved else 0, slot_mapping.data_ptr(), *signs, qoptr, qost,
           kv_cache.data_ptr(), cshape[0], cshape[2])
     return query_out
 
@@ -378,6 +405,33 @@ def kv_int2_rope_write(query, key: torch.Tensor, value: torch.Tensor, positions:
     """kv_int4_rope_write into the INT2 Lloyd-Max cache."""
     return _rope_write("kv_int2_rope_write", 2, query, key, value, positions, cos_sin, slot_mapping,
                        rht_signs, kv_cache, query_out, interleaved, stream)
+
+
+def kv_int4_mrope_write(query, key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                        sections, slot_mapping: torch.Tensor, rht_signs: torch.Tensor, kv_cache: torch.Tensor,
+                        query_out=None, interleaved: bool = False, mixed_sections: bool = False, stream=None):
+    """kv_int4_rope_write with positions on several axes (time, height, width): ``positions`` is int64 [axes, T] and
+    ``sections`` the number of rotated pairs of each axis (one to four axes, summing to rot_dim / 2).  The axes'
+    pairs follow one another, or are dealt out in turn while they last when ``mixed_sections`` (sections (3, 2, 2):
+    axes 0 1 2 0 1 2 0).  Pair i takes column i of its own axis's row ``cos_sin[positions[axis]]``."""
+    return _rope_write("kv_int4_mrope_write", 4, query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache,
+                       query_out, interleaved, stream, sections, mixed_sections)
+
+
+def kv_int8_mrope_write(query, key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                        sections, slot_mapping: torch.Tensor, kv_cache: torch.Tensor, query_out=None,
+                        interleaved: bool = False, mixed_sections: bool = False, stream=None):
+    """kv_int4_mrope_write into the INT8 comparator's cache (no signs)."""
+    return _rope_write("kv_int8_mrope_write", 8, query, key, value, positions, cos_sin, slot_mapping, None, kv_cache,
+                       query_out, interleaved, stream, sections, mixed_sections)
+
+
+def kv_int2_mrope_write(query, key: torch.Tensor, value: torch.Tensor, positions: torch.Tensor, cos_sin: torch.Tensor,
+                        sections, slot_mapping: torch.Tensor, rht_signs: torch.Tensor, kv_cache: torch.Tensor,
+                        query_out=None, interleaved: bool = False, mixed_sections: bool = False, stream=None):
+    """kv_int4_mrope_write into the INT2 Lloyd-Max cache."""
+    return _rope_write("kv_int2_mrope_write", 2, query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache,
+                       query_out, interleaved, stream, sections, mixed_sections)
 
 
 def _read(fn, bits, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, stream):

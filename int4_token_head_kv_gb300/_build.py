@@ -17,7 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIB_DIR, "libkv_int4.so")
-SOURCES = ["abi.cu", "write.cu", "rope_write.cu", "rope_write_int8.cu", "rope_write_int2.cu", "read.cu",
+SOURCES = ["abi.cu", "write.cu", "rope_write.cu", "rope_write_int8.cu", "rope_write_int2.cu",
+           "mrope_write.cu", "mrope_write_int8.cu", "mrope_write_int2.cu", "read.cu",
            "attn_decode.cu", "attn_decode_int8.cu", "attn_decode_int2.cu", "attn_prefill.cu",
            "attn_prefill_opts.cu", "attn_prefix.cu", "noalloc.cu"]
 HEADERS = ["device.cuh", "write_common.cuh", "rope_write.cuh", "attn_common.cuh", "attn_decode.cuh", "attn_prefill.cuh",

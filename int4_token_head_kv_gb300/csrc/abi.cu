@@ -182,20 +182,29 @@ kv_int4_status kv_int2_write(const void* k, const void* v, kv_int4_dtype dtype, 
 
 namespace {
 
-// The checks and the launch that the rotary writes of the three modes share (bits 4, 8 or 2).
+// The checks and the launch that the rotary writes of the three modes share (bits 4, 8 or 2).  num_axes 0: one
+// position per token; otherwise positions is [num_axes][num_tokens] and pair_axis (host) the axis of every pair.
 kv_int4_status rope_write_impl(int bits, const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
                                int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
                                int64_t num_tokens, int32_t num_kv_heads, int32_t head_size, const int64_t* positions,
                                const float* cos_sin, int64_t max_position, int32_t rot_dim, int32_t interleaved,
                                const int64_t* slot_mapping, const float* rht_signs, void* q_out,
                                int64_t q_out_token_stride, uint8_t* cache, int64_t num_blocks, int32_t block_size,
-                               kv_int4_stream_t stream) {
+                               kv_int4_stream_t stream, int32_t num_axes = 0, const uint8_t* pair_axis = nullptr) {
     if (num_tokens < 0 || num_blocks < 0 || num_kv_heads <= 0 || num_q_heads < 0 || max_position < 0 || rot_dim < 0)
         return KV_INT4_EINVAL;
     if (head_size != 64 && head_size != 128) return KV_INT4_EUNSUPPORTED;
     if (block_size != kBlockSize || num_kv_heads > 64 || num_q_heads > 1024 || !valid_dtype_16(dtype))
         return KV_INT4_EUNSUPPORTED;
     if (rot_dim == 0 || rot_dim > head_size || rot_dim % 16 != 0) return KV_INT4_EUNSUPPORTED;
+    uint32_t axis_bits[4] = {};
+    if (num_axes > 0) {
+        if (!pair_axis) return KV_INT4_EINVAL;
+        for (int i = 0; i < rot_dim / 2; ++i) {
+            if (pair_axis[i] >= num_axes) return KV_INT4_EINVAL;
+            axis_bits[i / 16] |= (uint32_t)pair_axis[i] << (2 * (i % 16));
+        }
+    }
     if (num_tokens == 0) return KV_INT4_OK;
     // 32-bit vector and item indices
     if (num_tokens >= ((int64_t)1 << 31) / (2 * num_kv_heads) || (num_q_heads > 0 && num_tokens >= ((int64_t)1 << 31) / num_q_heads))
@@ -238,9 +247,15 @@ kv_int4_status rope_write_impl(int bits, const void* q, int64_t q_token_stride, 
     p.qo_stride = q_out_token_stride;
     p.Hq = num_q_heads;
     p.rot = rot_dim;
+    p.axes = num_axes;
+    for (int i = 0; i < 4; ++i) p.pair_axis[i] = axis_bits[i];
     const DType dt = dtype == KV_INT4_BF16 ? DType::BF16 : DType::F16;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool inter = interleaved != 0;
+    if (num_axes > 0)
+        return from_cuda(bits == 8   ? launch_mrope_write_int8(p, head_size, dt, inter, s)
+                         : bits == 2 ? launch_mrope_write_int2(p, head_size, dt, inter, s)
+                                     : launch_mrope_write(p, head_size, dt, inter, s));
     return from_cuda(bits == 8   ? launch_rope_write_int8(p, head_size, dt, inter, s)
                      : bits == 2 ? launch_rope_write_int2(p, head_size, dt, inter, s)
                                  : launch_rope_write(p, head_size, dt, inter, s));
@@ -310,6 +325,54 @@ kv_int4_status kv_int2_rope_write(const void* q, int64_t q_token_stride, int32_t
     return rope_write_impl(2, q, q_token_stride, num_q_heads, k, k_token_stride, v, v_token_stride, dtype, num_tokens,
                            num_kv_heads, head_size, positions, cos_sin, max_position, rot_dim, interleaved, slot_mapping,
                            rht_signs, q_out, q_out_token_stride, cache, num_blocks, block_size, stream);
+}
+
+kv_int4_status kv_int4_mrope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                                   int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                                   int64_t num_tokens, int32_t num_kv_heads, int32_t head_size,
+                                   const int64_t* positions, int32_t num_axes, const uint8_t* pair_axis,
+                                   const float* cos_sin, int64_t max_position, int32_t rot_dim, int32_t interleaved,
+                                   const int64_t* slot_mapping, const float* rht_signs, void* q_out,
+                                   int64_t q_out_token_stride, uint8_t* cache, int64_t num_blocks, int32_t block_size,
+                                   kv_int4_stream_t stream) {
+    if (num_axes < 1) return KV_INT4_EINVAL;
+    if (num_axes > 4) return KV_INT4_EUNSUPPORTED;
+    return rope_write_impl(4, q, q_token_stride, num_q_heads, k, k_token_stride, v, v_token_stride, dtype, num_tokens,
+                           num_kv_heads, head_size, positions, cos_sin, max_position, rot_dim, interleaved, slot_mapping,
+                           rht_signs, q_out, q_out_token_stride, cache, num_blocks, block_size, stream, num_axes,
+                           pair_axis);
+}
+
+kv_int4_status kv_int8_mrope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                                   int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                                   int64_t num_tokens, int32_t num_kv_heads, int32_t head_size,
+                                   const int64_t* positions, int32_t num_axes, const uint8_t* pair_axis,
+                                   const float* cos_sin, int64_t max_position, int32_t rot_dim, int32_t interleaved,
+                                   const int64_t* slot_mapping, void* q_out,
+                                   int64_t q_out_token_stride, uint8_t* cache, int64_t num_blocks, int32_t block_size,
+                                   kv_int4_stream_t stream) {
+    if (num_axes < 1) return KV_INT4_EINVAL;
+    if (num_axes > 4) return KV_INT4_EUNSUPPORTED;
+    return rope_write_impl(8, q, q_token_stride, num_q_heads, k, k_token_stride, v, v_token_stride, dtype, num_tokens,
+                           num_kv_heads, head_size, positions, cos_sin, max_position, rot_dim, interleaved, slot_mapping,
+                           nullptr, q_out, q_out_token_stride, cache, num_blocks, block_size, stream, num_axes,
+                           pair_axis);
+}
+
+kv_int4_status kv_int2_mrope_write(const void* q, int64_t q_token_stride, int32_t num_q_heads, const void* k,
+                                   int64_t k_token_stride, const void* v, int64_t v_token_stride, kv_int4_dtype dtype,
+                                   int64_t num_tokens, int32_t num_kv_heads, int32_t head_size,
+                                   const int64_t* positions, int32_t num_axes, const uint8_t* pair_axis,
+                                   const float* cos_sin, int64_t max_position, int32_t rot_dim, int32_t interleaved,
+                                   const int64_t* slot_mapping, const float* rht_signs, void* q_out,
+                                   int64_t q_out_token_stride, uint8_t* cache, int64_t num_blocks, int32_t block_size,
+                                   kv_int4_stream_t stream) {
+    if (num_axes < 1) return KV_INT4_EINVAL;
+    if (num_axes > 4) return KV_INT4_EUNSUPPORTED;
+    return rope_write_impl(2, q, q_token_stride, num_q_heads, k, k_token_stride, v, v_token_stride, dtype, num_tokens,
+                           num_kv_heads, head_size, positions, cos_sin, max_position, rot_dim, interleaved, slot_mapping,
+                           rht_signs, q_out, q_out_token_stride, cache, num_blocks, block_size, stream, num_axes,
+                           pair_axis);
 }
 
 kv_int4_status kv_int4_read(const uint8_t* cache, int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,

@@ -41,6 +41,9 @@ struct RopeWriteParams {
     int64_t q_stride, k_stride, v_stride, qo_stride;   // elements from one token to the next
     int Hq;                 // 0: no queries
     int rot;                // rotated dimensions, a multiple of 16
+    // several position axes (the kernels built for them): positions is [axes][num_tokens]
+    int axes;               // 1..4
+    uint32_t pair_axis[4];  // the axis of pair i: bits 2 (i % 16), 2 (i % 16) + 1 of word i / 16
 };
 
 struct ReadParams {
@@ -123,6 +126,10 @@ cudaError_t launch_write_int2(const WriteParams& p, int head_size, DType dt, cud
 cudaError_t launch_rope_write(const RopeWriteParams& p, int head_size, DType dt, bool interleaved, cudaStream_t stream);
 cudaError_t launch_rope_write_int8(const RopeWriteParams& p, int head_size, DType dt, bool interleaved, cudaStream_t stream);
 cudaError_t launch_rope_write_int2(const RopeWriteParams& p, int head_size, DType dt, bool interleaved, cudaStream_t stream);
+// The same with several position axes.
+cudaError_t launch_mrope_write(const RopeWriteParams& p, int head_size, DType dt, bool interleaved, cudaStream_t stream);
+cudaError_t launch_mrope_write_int8(const RopeWriteParams& p, int head_size, DType dt, bool interleaved, cudaStream_t stream);
+cudaError_t launch_mrope_write_int2(const RopeWriteParams& p, int head_size, DType dt, bool interleaved, cudaStream_t stream);
 // Cached rows back as the values they stand for (bits 4, 8 or 2).
 cudaError_t launch_read(const ReadParams& p, int bits, int head_size, DType out_dt, cudaStream_t stream);
 // Decode path: query rotation, the split-KV segment walker, and the combine that finishes every

@@ -22,6 +22,9 @@
 // elements as fp32 where the encoding lane pair reads them as the operands of its first butterflies.
 // (Rotated by the encoding threads themselves, each of a pair did the whole row: 64 table loads per thread
 // and tile, and 180 us for 65 536 tokens of 8 kv heads instead of 88.7 without a rotation.)
+//
+// AXES: positions on several axes (time, height, width).  Pair i takes its cosine and sine from the table row of
+// its own axis's position; the axis of every pair is two bits of a kernel parameter.  Everything else is the same.
 #pragma once
 
 #include "write_common.cuh"
@@ -72,6 +75,54 @@ struct RopeTable {
     float2 c[2], s[2];
 };
 
+// The axis of pair i.
+__device__ __forceinline__ int axis_of(const RopeWriteParams& p, int i) { return (int)((p.pair_axis[i >> 4] >> (2 * (i & 15))) & 3u); }
+
+// The table row of token tok on one axis (row 0 for a position outside the table: its rows are not stored).
+__device__ __forceinline__ const float* axis_row(const RopeWriteParams& p, uint32_t tok, int axis) {
+    const int64_t pos = __ldg(p.positions + (int64_t)axis * p.w.num_tokens + tok);
+    return p.cos_sin + (pos >= 0 && pos < p.max_position ? pos : 0) * p.rot;
+}
+
+// One position that stands for a token's positions on all axes: in the table when all of them are, negative when
+// all of them are, else behind the table.
+__device__ __forceinline__ int64_t joint_position(const RopeWriteParams& p, uint32_t tok) {
+    bool inside = true, negative = true;
+    for (int a = 0; a < p.axes; ++a) {
+        const int64_t pos = __ldg(p.positions + (int64_t)a * p.w.num_tokens + tok);
+        inside = inside && pos >= 0 && pos < p.max_position;
+        negative = negative && pos < 0;
+    }
+    return inside ? 0 : negative ? -1 : p.max_position;
+}
+
+// The lane's part of token tok's table rows.
+template <int D, bool INTER>
+__device__ __forceinline__ RopeTable load_axes(const RopeWriteParams& p, uint32_t tok) {
+    constexpr int Q = D / 4;
+    const int k = (threadIdx.x & 31) % Q, rot = p.rot, hw = rot >> 2, half = rot >> 1;
+    RopeTable t;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int m = k + i * Q;
+        t.c[i] = make_float2(1.0f, 1.0f);
+        t.s[i] = make_float2(0.0f, 0.0f);
+        if (2 * m < rot) {
+            if constexpr (INTER) {
+                const float* cs = axis_row(p, tok, axis_of(p, m));
+                t.c[i].x = __ldg(cs + m);
+                t.s[i].x = __ldg(cs + half + m);
+            } else {
+                const int j = 2 * (m < hw ? m : m - hw);   // pairs j and j + 1
+                const float *ca = axis_row(p, tok, axis_of(p, j)), *cb = axis_row(p, tok, axis_of(p, j + 1));
+                t.c[i] = make_float2(__ldg(ca + j), __ldg(cb + j + 1));
+                t.s[i] = make_float2(__ldg(ca + half + j), __ldg(cb + half + j + 1));
+            }
+        }
+    }
+    return t;
+}
+
 // The lane's part of the table row of position pos (row 0 for one outside the table: its rows are not stored).
 template <int D, bool INTER>
 __device__ __forceinline__ RopeTable load_table(const RopeWriteParams& p, int64_t pos) {
@@ -100,9 +151,9 @@ __device__ __forceinline__ RopeTable load_table(const RopeWriteParams& p, int64_
 
 // Rotate rows r0 .. r0 + nrows - 1 of the tile (vectors v0 + r of the key plane, staged at in + r * ROWPAD)
 // into stage rows 0 .. nrows - 1, nrows <= kRopeRows.  tab: the table row of the first row's token; pos: lane
-// r * TPV holds the position of row r's token.  fmask: per word m the signs to apply (bit 15: element 2m, bit
+// r * TPV holds the position of row r's token (unused with AXES).  fmask: per word m the signs to apply (bit 15: element 2m, bit
 // 31: 2m + 1), or nullptr for none.  All lanes call it.
-template <int D, typename T, bool INTER, int ROWPAD, int TPV>
+template <int D, typename T, bool INTER, bool AXES, int ROWPAD, int TPV>
 __device__ __forceinline__ void rope_rows(const RopeWriteParams& p, const uint8_t* in, float* stage, uint32_t v0, int r0,
                                           int nrows, RopeTable tab, int64_t pos, const uint32_t* fmask) {
     constexpr int Q = D / 4, kStep = 32 / Q;   // rows at once: a lane owns words k and k + Q of every kStep-th row
@@ -125,7 +176,10 @@ __device__ __forceinline__ void rope_rows(const RopeWriteParams& p, const uint8_
         // a token's rows r .. r_end - 1, the next token's table row on its way
         if (r_end > nrows) r_end = nrows;
         RopeTable next = tab;
-        if (r_end < nrows) next = load_table<D, INTER>(p, __shfl_sync(0xffffffffu, pos, (r0 + r_end) * TPV));
+        if (r_end < nrows) {
+            if constexpr (AXES) next = load_axes<D, INTER>(p, (v0 + (uint32_t)(r0 + r_end)) / H);
+            else next = load_table<D, INTER>(p, __shfl_sync(0xffffffffu, pos, (r0 + r_end) * TPV));
+        }
         float2 c[2], s[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -216,12 +270,12 @@ struct QueryItem {
     static constexpr int kRows = kPassRows * kPasses;
 };
 
-template <int D, typename T, bool INTER>
+template <int D, typename T, bool INTER, bool AXES>
 __device__ __forceinline__ void rotate_queries(const RopeWriteParams& p, uint32_t item, uint32_t groups) {
     using Qi = QueryItem<D>;
     const int lane = threadIdx.x & 31, c = lane % Qi::kSlots, r = lane / Qi::kSlots;
     const uint32_t tok = item / groups, head0 = (item - tok * groups) * Qi::kRows;
-    const int64_t pos = __ldg(p.positions + tok);
+    const int64_t pos = AXES ? joint_position(p, tok) : __ldg(p.positions + tok);
     if (pos < 0 || pos >= p.max_position) return;   // the cache tiles count it
     const int rot = p.rot;
     const bool turned = 16 * c < rot;
@@ -249,7 +303,15 @@ __device__ __forceinline__ void rotate_queries(const RopeWriteParams& p, uint32_
         }
     }
     float2 cv[4], sv[4];
-    if (turned) {
+    if (AXES && turned) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = 8 * c + 2 * e, half = rot >> 1;   // pairs j and j + 1
+            const float *ra = axis_row(p, tok, axis_of(p, j)), *rb = axis_row(p, tok, axis_of(p, j + 1));
+            cv[e] = make_float2(__ldg(ra + j), __ldg(rb + j + 1));
+            sv[e] = make_float2(__ldg(ra + half + j), __ldg(rb + half + j + 1));
+        }
+    } else if (turned) {
         const float* cs = p.cos_sin + pos * rot;
         const float4 c0 = ldg4(cs + 8 * c), c1 = ldg4(cs + 8 * c + 4);
         const float4 s0 = ldg4(cs + (rot >> 1) + 8 * c), s1 = ldg4(cs + (rot >> 1) + 8 * c + 4);
@@ -312,7 +374,7 @@ struct RopeSmem {
     static constexpr int kBytes = kBars + kWriteWarps * 16 + (int)sizeof(WriteSigns<D>);
 };
 
-template <int D, typename T, int BITS, bool INTER>
+template <int D, typename T, int BITS, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
     rope_write_kernel(const __grid_constant__ RopeWriteParams p) {
     using Sh = WriteShape<BITS>;
@@ -395,8 +457,14 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
         const uint32_t v = tile * TV + vl;
         uint32_t tok, h, pl;
         split(v < nvec ? v : tile * TV, tok, h, pl);
-        pos = __ldg(p.positions + tok);
+        if constexpr (AXES) pos = joint_position(p, tok);
+        else pos = __ldg(p.positions + tok);
         slot = __ldg(p.w.slots + tok);
+    };
+    // the lane's table entries of vector v of the key plane; pos: lane src holds its token's position
+    auto table_of = [&](uint32_t v, int64_t pos, int src) -> RopeTable {
+        if constexpr (AXES) return load_axes<D, INTER>(p, v / H);
+        else return load_table<D, INTER>(p, __shfl_sync(0xffffffffu, pos, src));
     };
     int64_t pos_next = 0, slot_next = 0;
     if (my_tiles > 0) {
@@ -409,10 +477,10 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
         const bool live = v < nvec;
         const int keys = v0 < nplane ? (int)min((uint32_t)TV, nplane - v0) : 0;   // key rows of the tile, its first ones
         RopeTable tab = {};
-        if (keys > 0) tab = load_table<D, INTER>(p, __shfl_sync(0xffffffffu, pos, 0));
+        if (keys > 0) tab = table_of(v0, pos, 0);
         // this tile's share of the query items
         const uint32_t until = (uint32_t)((uint64_t)my_items * (it + 1) / my_tiles);
-        for (; items_done < until; ++items_done, item += nwarps) rotate_queries<D, T, INTER>(p, item, groups);
+        for (; items_done < until; ++items_done, item += nwarps) rotate_queries<D, T, INTER, AXES>(p, item, groups);
         __syncwarp();
         if (__any_sync(0xffffffffu, !mbar_wait(bar, it & 1u))) {
             if (lane == 0) count_status(p.w.status, 3);
@@ -432,8 +500,8 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
         if constexpr (INT8) {
             float u[D];
             for (int r0 = 0; r0 < keys; r0 += kRopeRows) {
-                if (r0 > 0) tab = load_table<D, INTER>(p, __shfl_sync(0xffffffffu, pos, r0 * TPV));
-                rope_rows<D, T, INTER, Sm::kRowPad, TPV>(p, in, stage, v0, r0, min(kRopeRows, keys - r0), tab, pos, nullptr);
+                if (r0 > 0) tab = table_of(v0 + (uint32_t)r0, pos, r0 * TPV);
+                rope_rows<D, T, INTER, AXES, Sm::kRowPad, TPV>(p, in, stage, v0, r0, min(kRopeRows, keys - r0), tab, pos, nullptr);
                 __syncwarp();
                 if (row >= r0 && row < min(r0 + kRopeRows, keys)) {
 #pragma unroll
@@ -458,7 +526,7 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
             // every lane runs the encoder (it exchanges values within the lane pair)
             float2 P[D / 4];
             if (keys > 0) {
-                rope_rows<D, T, INTER, Sm::kRowPad, TPV>(p, in, stage, v0, 0, keys, tab, pos, sgn.xmask[0]);
+                rope_rows<D, T, INTER, AXES, Sm::kRowPad, TPV>(p, in, stage, v0, 0, keys, tab, pos, sgn.xmask[0]);
                 __syncwarp();
             }
             if (row < keys) form_staged_half<D>(stage + row * kRopeRow<D>, part, P);
@@ -500,11 +568,11 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
         }
     }
     if (waited_out) (void)mbar_wait(bar, it & 1u);   // let the copy in flight land before the warp exits
-    for (; items_done < my_items; ++items_done, item += nwarps) rotate_queries<D, T, INTER>(p, item, groups);
+    for (; items_done < my_items; ++items_done, item += nwarps) rotate_queries<D, T, INTER, AXES>(p, item, groups);
     if (grouped) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-template <int D, typename T, int BITS, bool INTER>
+template <int D, typename T, int BITS, bool INTER, bool AXES>
 cudaError_t launch_rope_write_t(const RopeWriteParams& p, cudaStream_t stream) {
     using Sh = WriteShape<BITS>;
     using Sm = RopeSmem<D, BITS>;
@@ -512,7 +580,7 @@ cudaError_t launch_rope_write_t(const RopeWriteParams& p, cudaStream_t stream) {
     const int64_t groups = (p.Hq + QueryItem<D>::kRows - 1) / QueryItem<D>::kRows;
     const int64_t blocks = (ntiles + p.w.num_tokens * groups + kWriteWarps - 1) / kWriteWarps;
     const int64_t cap = (int64_t)num_sms() * kRopeBlocks<BITS>;
-    cudaError_t err = opt_in_smem<rope_write_kernel<D, T, BITS, INTER>>(Sm::kBytes);
+    cudaError_t err = opt_in_smem<rope_write_kernel<D, T, BITS, INTER, AXES>>(Sm::kBytes);
     if (err != cudaSuccess) return err;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -524,22 +592,24 @@ cudaError_t launch_rope_write_t(const RopeWriteParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rope_write_kernel<D, T, BITS, INTER>, p);
+    return cudaLaunchKernelEx(&cfg, rope_write_kernel<D, T, BITS, INTER, AXES>, p);
 }
 
 // Every (head size, type, pairing) instantiation of one cache mode.
-template <int BITS>
+template <int BITS, bool AXES = false>
 cudaError_t launch_rope_write_mode(const RopeWriteParams& p, int head_size, DType dt, bool inter, cudaStream_t s) {
     if (head_size == 128) {
         if (dt == DType::BF16)
-            return inter ? launch_rope_write_t<128, __nv_bfloat16, BITS, true>(p, s)
-                         : launch_rope_write_t<128, __nv_bfloat16, BITS, false>(p, s);
-        return inter ? launch_rope_write_t<128, __half, BITS, true>(p, s) : launch_rope_write_t<128, __half, BITS, false>(p, s);
+            return inter ? launch_rope_write_t<128, __nv_bfloat16, BITS, true, AXES>(p, s)
+                         : launch_rope_write_t<128, __nv_bfloat16, BITS, false, AXES>(p, s);
+        return inter ? launch_rope_write_t<128, __half, BITS, true, AXES>(p, s)
+                     : launch_rope_write_t<128, __half, BITS, false, AXES>(p, s);
     }
     if (dt == DType::BF16)
-        return inter ? launch_rope_write_t<64, __nv_bfloat16, BITS, true>(p, s)
-                     : launch_rope_write_t<64, __nv_bfloat16, BITS, false>(p, s);
-    return inter ? launch_rope_write_t<64, __half, BITS, true>(p, s) : launch_rope_write_t<64, __half, BITS, false>(p, s);
+        return inter ? launch_rope_write_t<64, __nv_bfloat16, BITS, true, AXES>(p, s)
+                     : launch_rope_write_t<64, __nv_bfloat16, BITS, false, AXES>(p, s);
+    return inter ? launch_rope_write_t<64, __half, BITS, true, AXES>(p, s)
+                 : launch_rope_write_t<64, __half, BITS, false, AXES>(p, s);
 }
 
 }  // namespace

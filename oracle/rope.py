@@ -31,3 +31,25 @@ def rotate(x, positions, cos_sin: np.ndarray, interleaved: bool = False) -> np.n
     y[..., ia] = (a * c).astype(np.float32) - (b * s).astype(np.float32)
     y[..., ib] = (b * c).astype(np.float32) + (a * s).astype(np.float32)
     return y
+
+
+def pair_axes(sections, mixed: bool = False) -> np.ndarray:
+    """The axis of every rotated pair: the sections one after another, or dealt out in turn while they last."""
+    if not mixed:
+        return np.repeat(np.arange(len(sections)), sections)
+    left, out = list(sections), []
+    while any(left):
+        for a in range(len(left)):
+            if left[a]:
+                left[a] -= 1
+                out.append(a)
+    return np.array(out)
+
+
+def rotate_axes(x, positions, cos_sin: np.ndarray, sections, mixed: bool = False, interleaved: bool = False) -> np.ndarray:
+    """rotate() with positions [axes, T]: pair i takes column i of its own axis's table row."""
+    half = cos_sin.shape[1] // 2
+    at = np.asarray(positions)[pair_axes(sections, mixed)].T          # [T, pairs]
+    i = np.arange(half)
+    own = np.concatenate([cos_sin[at, i], cos_sin[at, half + i]], axis=1)   # every token's own table row
+    return rotate(x, np.arange(at.shape[0]), own, interleaved)
