@@ -14,7 +14,8 @@
  *   kv_int{4,8,2}_rope_write the writes with the rotary position embedding of queries and keys;
  *   kv_int{4,8,2}_mrope_write  the same with positions on several axes;
  *   kv_int{4,8,2}_read       cached rows back as the keys and values they stand for;
- *   kv_int4_shared_prefix_attention  decode attention of a batch that shares a cached prefix.
+ *   kv_int4_shared_prefix_attention  decode attention of a batch that shares a cached prefix;
+ *   kv_int{4,8,2}_span_attention  attention of chunks and single tokens, every query on a span of keys.
  *
  * The caller owns every buffer.  The library never allocates device or host memory: the
  * attention's split-KV partials live in a caller-provided workspace whose size
@@ -561,6 +562,77 @@ kv_int4_status kv_int4_paged_attention_noalloc_ex(const void* q, kv_int4_dtype q
                                                   const float* rht_signs, int32_t segment_len, void* out,
                                                   kv_int4_dtype out_dtype, kv_int4_stream_t stream,
                                                   const kv_int4_attn_options* options);
+
+/*
+ * kv_int4_span_attention -- attention in which every query row sees the cached keys of a span of its own, over the
+ * INT4 cache: the documents of a packed prompt, a prefix that sees itself whole, images whose tokens see each other,
+ * sliding windows, and plain causal attention, for chunks of any length and for single tokens.
+ *
+ * Sequence b has L = seq_lens[b] cached tokens (this step's among them) and the query rows query_start_loc[b] ..
+ * query_start_loc[b+1]-1; its t-th query sits at position pos = L - q_len + t.  Query row r sees the keys
+ *   max(0, key_begin[r]) <= j < min(L, key_end[r])     (key_begin NULL: 0; key_end NULL: pos + 1),
+ * which may lie before, around or behind its own position.  With x_K, x_V the cached rows as kv_int4_read gives
+ * them and g the query head, on the visible keys and in this order:
+ *   s_j = softmax_scale * q . x_K,j
+ *   softcap > 0            s_j <- softcap * tanh(s_j / softcap)
+ *   alibi_slopes != NULL   s_j <- s_j - alibi_slopes[g] * |pos - j|
+ *   out = sum_j softmax(s)_j x_V,j;  zeros for an empty span.
+ * Document mask: key_begin = the first position of the query's document.  Prefix mask: key_end = max(pos + 1, prefix
+ * length).  An image's tokens: key_end = the image's end.  Sliding window: key_begin = pos - window.
+ * What a row does not see does not reach it: its keys and values may be infinite or NaN.  A visible row of zeros
+ * (never written) is a key of logit 0 and a value of 0.
+ *
+ * key_begin, key_end  [num_q_tokens] int32 or NULL.
+ * softcap             0: none; negative or not finite: KV_INT4_EINVAL.
+ * alibi_slopes        [num_q_heads] fp32 or NULL.
+ * max_query_len       host int: max over b of q_len_b.  Queries past it are left as they were (counted as bad metadata).
+ * max_seq_len         host int: >= max over b of seq_lens[b].  Longer contexts are clamped to it, and to the block
+ *                     table (and counted as bad metadata).
+ * out                 [num_q_tokens, num_q_heads, head_size]; rows of no sequence are left as they were.
+ * workspace           >= kv_int4_span_workspace_bytes(...) bytes, 16-B aligned (NULL when that is 0).  Overlapping
+ *                     calls must not share a workspace.
+ * A block id outside [0, num_blocks) hides its keys and is counted; a chunk longer than its sequence is counted, but
+ * for a sequence of no tokens (a padding row), which gives zeros.
+ * Other arguments, alignment, supported sizes and error behaviour as kv_int4_paged_attention.
+ */
+kv_int4_status kv_int4_span_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens, int32_t num_q_heads,
+                                      const uint8_t* cache, int64_t num_blocks, int32_t num_kv_heads,
+                                      int32_t head_size, int32_t block_size, const int32_t* block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                      const int32_t* query_start_loc, int32_t num_seqs, int32_t max_query_len,
+                                      int32_t max_seq_len, float softmax_scale, const float* rht_signs,
+                                      const int32_t* key_begin, const int32_t* key_end, float softcap,
+                                      const float* alibi_slopes, void* out, kv_int4_dtype out_dtype, void* workspace,
+                                      size_t workspace_bytes, kv_int4_stream_t stream);
+
+/* kv_int8_span_attention -- the same over the INT8 comparator's cache (rows as kv_int8_write; no signs). */
+kv_int4_status kv_int8_span_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens, int32_t num_q_heads,
+                                      const uint8_t* cache, int64_t num_blocks, int32_t num_kv_heads,
+                                      int32_t head_size, int32_t block_size, const int32_t* block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                      const int32_t* query_start_loc, int32_t num_seqs, int32_t max_query_len,
+                                      int32_t max_seq_len, float softmax_scale,
+                                      const int32_t* key_begin, const int32_t* key_end, float softcap,
+                                      const float* alibi_slopes, void* out, kv_int4_dtype out_dtype, void* workspace,
+                                      size_t workspace_bytes, kv_int4_stream_t stream);
+
+/* kv_int2_span_attention -- the same over the INT2 Lloyd-Max cache (rows as kv_int2_write). */
+kv_int4_status kv_int2_span_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens, int32_t num_q_heads,
+                                      const uint8_t* cache, int64_t num_blocks, int32_t num_kv_heads,
+                                      int32_t head_size, int32_t block_size, const int32_t* block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                      const int32_t* query_start_loc, int32_t num_seqs, int32_t max_query_len,
+                                      int32_t max_seq_len, float softmax_scale, const float* rht_signs,
+                                      const int32_t* key_begin, const int32_t* key_end, float softcap,
+                                      const float* alibi_slopes, void* out, kv_int4_dtype out_dtype, void* workspace,
+                                      size_t workspace_bytes, kv_int4_stream_t stream);
+
+/*
+ * Bytes of workspace the kv_int{4,8,2}_span_attention calls need for these sizes (the same for the three caches).  0
+ * when none is needed, or when the arguments are invalid or num_seqs or num_q_tokens is 0.
+ */
+size_t kv_int4_span_workspace_bytes(int64_t num_q_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                                    int32_t num_seqs, int32_t max_query_len, int32_t max_seq_len);
 
 /*
  * Copy the current device's status counters (KV_INT4_STAT_COUNT uint32 values) to the HOST array

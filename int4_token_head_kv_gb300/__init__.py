@@ -105,6 +105,13 @@ def _load():
     lib.kv_int4_shared_prefix_attention.restype = ctypes.c_int
     lib.kv_int4_shared_prefix_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, i32, i32]
     lib.kv_int4_shared_prefix_workspace_bytes.restype = szt
+    for name, signs in (("kv_int4_span_attention", [vp]), ("kv_int8_span_attention", []), ("kv_int2_span_attention", [vp])):
+        f = getattr(lib, name)
+        f.argtypes = [vp, ctypes.c_int, i64, i32, vp, i64, i32, i32, i32, vp, i32, vp, vp, i32, i32, i32, f32] + signs + [
+            vp, vp, f32, vp, vp, ctypes.c_int, vp, szt, vp]
+        f.restype = ctypes.c_int
+    lib.kv_int4_span_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32, i32]
+    lib.kv_int4_span_workspace_bytes.restype = szt
     lib.kv_int4_read_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), vp]
     lib.kv_int4_read_device_status.restype = ctypes.c_int
     lib.kv_int4_clear_device_status.argtypes = [vp]
@@ -750,6 +757,107 @@ def kv_int4_shared_prefix_attention(query: torch.Tensor, kv_cache: torch.Tensor,
           max_seq_len, float(softmax_scale), rht_signs.data_ptr(), segment_len, out.data_ptr(), _DTYPES[out.dtype],
           ws_ptr, ws_bytes)
     return out
+
+
+def kv_int4_span_workspace_bytes(num_q_tokens: int, num_q_heads: int, num_kv_heads: int, head_size: int, num_seqs: int,
+                                 max_query_len: int, max_seq_len: int) -> int:
+    return int(load().kv_int4_span_workspace_bytes(num_q_tokens, num_q_heads, num_kv_heads, head_size, num_seqs,
+                                                   max_query_len, max_seq_len))
+
+
+def _span_attention(fn, bits, query, kv_cache, block_tables, seq_lens, query_start_loc, softmax_scale, rht_signs,
+                    max_query_len, max_seq_len, key_begin, key_end, softcap, alibi_slopes, out, out_dtype, workspace, stream):
+    if stream is not None:
+        with _current(stream, query):
+            return _span_attention(fn, bits, query, kv_cache, block_tables, seq_lens, query_start_loc, softmax_scale,
+                                   rht_signs, max_query_len, max_seq_len, key_begin, key_end, softcap, alibi_slopes, out,
+                                   out_dtype, workspace, None)
+    _cuda(query, "query", _HALF_TYPES)
+    _cuda(kv_cache, "kv_cache", _U8)
+    _cuda(block_tables, "block_tables", _I32)
+    _cuda(seq_lens, "seq_lens", _I32)
+    _cuda(query_start_loc, "query_start_loc", _I32)
+    qshape, cshape, tshape = query.shape, kv_cache.shape, block_tables.shape
+    if len(qshape) != 3 or len(cshape) != 5 or seq_lens.dim() != 1:
+        raise ValueError("query must be [num_q_tokens, num_q_heads, head_size], kv_cache 5-D and seq_lens [num_seqs]")
+    Nq, Hq, d = qshape
+    NB, two, bs, H, rb = cshape
+    S = seq_lens.shape[0]
+    signs = ()
+    if bits != 8:
+        _cuda(rht_signs, "rht_signs", _F32)
+        if rht_signs.shape != (d,):
+            raise ValueError("rht_signs must be [head_size]")
+        signs = (rht_signs.data_ptr(),)
+    if two != 2 or rb != d * bits // 8 + 4:
+        raise ValueError("kv_cache does not match the query's head size")
+    if query_start_loc.shape != (S + 1,) or len(tshape) != 2 or tshape[0] != S:
+        raise ValueError("block_tables must be [num_seqs, max_blocks] and query_start_loc [num_seqs + 1]")
+    begin = end = slopes = None
+    if key_begin is not None:
+        if _cuda(key_begin, "key_begin", _I32).shape != (Nq,):
+            raise ValueError("key_begin must be [num_q_tokens]")
+        begin = key_begin.data_ptr()
+    if key_end is not None:
+        if _cuda(key_end, "key_end", _I32).shape != (Nq,):
+            raise ValueError("key_end must be [num_q_tokens]")
+        end = key_end.data_ptr()
+    if alibi_slopes is not None:
+        if _cuda(alibi_slopes, "alibi_slopes", _F32).shape != (Hq,):
+            raise ValueError("alibi_slopes must be [num_q_heads]")
+        slopes = alibi_slopes.data_ptr()
+    if out is None:
+        out = torch.empty(qshape, dtype=out_dtype or query.dtype, device=query.device)
+    _cuda(out, "out", tuple(_DTYPES))
+    if out.shape != qshape:
+        raise ValueError("out must have the query's shape")
+    if workspace is None:
+        need = (_lib or load()).kv_int4_span_workspace_bytes(Nq, Hq, H, d, S, max_query_len, max_seq_len)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
+    ws_ptr = workspace.data_ptr() if workspace is not None else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _call(fn, (query, kv_cache, block_tables, seq_lens, query_start_loc, rht_signs, key_begin, key_end, alibi_slopes, out,
+               workspace), (),
+          query.data_ptr(), _DTYPES[query.dtype], Nq, Hq, kv_cache.data_ptr(), NB, H, d, bs, block_tables.data_ptr(),
+          tshape[1], seq_lens.data_ptr(), query_start_loc.data_ptr(), S, max_query_len, max_seq_len, float(softmax_scale),
+          *signs, begin, end, float(softcap), slopes, out.data_ptr(), _DTYPES[out.dtype], ws_ptr, ws_bytes)
+    return out
+
+
+def kv_int4_span_attention(query: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                           query_start_loc: torch.Tensor, softmax_scale: float, rht_signs: torch.Tensor, max_query_len: int,
+                           max_seq_len: int, key_begin=None, key_end=None, softcap: float = 0.0, alibi_slopes=None, out=None,
+                           out_dtype=None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention of ``query`` [Nq, Hq, d] over the INT4 cache in which query row r sees the cached keys
+    ``key_begin[r] <= j < key_end[r]`` of its sequence (int32 [Nq]; by default from 0, and up to its own position):
+    document masks of packed prompts, prefixes and images that see themselves whole, windows, or plain causal
+    attention, for chunks of any length and single tokens.  ``softcap`` > 0 caps the scaled scores by a tanh,
+    ``alibi_slopes`` (fp32 [Hq]) takes slope * |pos - j| off them.  A row whose span is empty gives zeros.  The other
+    arguments as kv_int4_paged_attention's; the workspace is sized by kv_int4_span_workspace_bytes."""
+    return _span_attention("kv_int4_span_attention", 4, query, kv_cache, block_tables, seq_lens, query_start_loc,
+                           softmax_scale, rht_signs, max_query_len, max_seq_len, key_begin, key_end, softcap, alibi_slopes,
+                           out, out_dtype, workspace, stream)
+
+
+def kv_int8_span_attention(query: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                           query_start_loc: torch.Tensor, softmax_scale: float, max_query_len: int, max_seq_len: int,
+                           key_begin=None, key_end=None, softcap: float = 0.0, alibi_slopes=None, out=None, out_dtype=None,
+                           workspace=None, stream=None) -> torch.Tensor:
+    """kv_int4_span_attention over the INT8 comparator's cache (no signs)."""
+    return _span_attention("kv_int8_span_attention", 8, query, kv_cache, block_tables, seq_lens, query_start_loc,
+                           softmax_scale, None, max_query_len, max_seq_len, key_begin, key_end, softcap, alibi_slopes, out,
+                           out_dtype, workspace, stream)
+
+
+def kv_int2_span_attention(query: torch.Tensor, kv_cache: torch.Tensor, block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                           query_start_loc: torch.Tensor, softmax_scale: float, rht_signs: torch.Tensor, max_query_len: int,
+                           max_seq_len: int, key_begin=None, key_end=None, softcap: float = 0.0, alibi_slopes=None, out=None,
+                           out_dtype=None, workspace=None, stream=None) -> torch.Tensor:
+    """kv_int4_span_attention over the INT2 Lloyd-Max cache."""
+    return _span_attention("kv_int2_span_attention", 2, query, kv_cache, block_tables, seq_lens, query_start_loc,
+                           softmax_scale, rht_signs, max_query_len, max_seq_len, key_begin, key_end, softcap, alibi_slopes,
+                           out, out_dtype, workspace, stream)
 
 
 def kv_int4_read_device_status(stream=None) -> dict:

@@ -733,6 +733,120 @@ kv_int4_status kv_int2_paged_attention(const void* q, kv_int4_dtype q_dtype, int
                                 workspace, workspace_bytes, stream, nullptr);
 }
 
+}  // extern "C"
+
+namespace {
+
+// The checks and the launch that the span attentions of the three caches share (bits 4, 8 or 2).
+kv_int4_status span_attention_impl(int bits, const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens, int32_t num_q_heads,
+                                   const uint8_t* cache, int64_t num_blocks, int32_t num_kv_heads, int32_t head_size,
+                                   int32_t block_size, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* seq_lens, const int32_t* query_start_loc, int32_t num_seqs,
+                                   int32_t max_query_len, int32_t max_seq_len, float softmax_scale,
+                                   const float* rht_signs, const int32_t* key_begin, const int32_t* key_end, float softcap,
+                                   const float* alibi_slopes, void* out, kv_int4_dtype out_dtype, void* workspace,
+                                   size_t workspace_bytes, kv_int4_stream_t stream) {
+    if (num_q_tokens < 0 || num_seqs < 0 || num_blocks < 0 || max_query_len < 0 || max_seq_len < 0 || max_blocks_per_seq < 0)
+        return KV_INT4_EINVAL;
+    if (head_size != 64 && head_size != 128) return KV_INT4_EUNSUPPORTED;
+    if (block_size != kBlockSize) return KV_INT4_EUNSUPPORTED;
+    if (!is_pow2_in(num_kv_heads, 1, 8) || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0) return KV_INT4_EUNSUPPORTED;
+    const int G = num_q_heads / num_kv_heads;
+    if (!is_pow2_in(G, 1, 8)) return KV_INT4_EUNSUPPORTED;
+    if (!valid_dtype_16(q_dtype) || !(valid_dtype_16(out_dtype) || out_dtype == KV_INT4_F32)) return KV_INT4_EUNSUPPORTED;
+    if (num_seqs > 65535 || num_q_tokens >= ((int64_t)1 << 31)) return KV_INT4_EUNSUPPORTED;
+    if (!(softmax_scale == softmax_scale) || !(softcap >= 0.0f && softcap <= 3.0e38f)) return KV_INT4_EINVAL;
+    if (num_q_tokens == 0 || num_seqs == 0) return KV_INT4_OK;
+    if (!q || !cache || !block_tables || !seq_lens || !query_start_loc || (bits != 8 && !rht_signs) || !out) return KV_INT4_EINVAL;
+    if (max_query_len < 1 || max_blocks_per_seq < 1) return KV_INT4_EINVAL;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(cache)) return KV_INT4_EALIGN;
+    const size_t need = kv_int4_span_workspace_bytes(num_q_tokens, num_q_heads, num_kv_heads, head_size, num_seqs, max_query_len,
+                                                     max_seq_len);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KV_INT4_EWORKSPACE;
+    if (need > 0 && !aligned16(workspace)) return KV_INT4_EALIGN;
+    SpanParams p;
+    p.q = q;
+    p.cache = cache;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.qsl = query_start_loc;
+    p.key_begin = key_begin;
+    p.key_end = key_end;
+    p.alibi = alibi_slopes;
+    p.signs = bits != 8 ? rht_signs : nullptr;
+    p.out = out;
+    p.status = status_ptr();
+    p.num_blocks = num_blocks;
+    p.num_q_tokens = num_q_tokens;
+    p.num_seqs = num_seqs;
+    p.max_query_len = max_query_len;
+    p.H = num_kv_heads;
+    p.G = G;
+    p.Hq = num_q_heads;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.len_cap = (int)std::min<int64_t>(max_seq_len, (int64_t)max_blocks_per_seq * kBlockSize);
+    p.softmax_scale = softmax_scale;
+    p.c = bits != 8 ? (float)(1.0 / std::sqrt((double)head_size)) : 1.0f;
+    p.softcap = softcap;
+    const DType qd = q_dtype == KV_INT4_BF16 ? DType::BF16 : DType::F16;
+    const DType od = out_dtype == KV_INT4_BF16 ? DType::BF16 : (out_dtype == KV_INT4_F16 ? DType::F16 : DType::F32);
+    return from_cuda(launch_span(p, bits, head_size, qd, od, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kv_int4_span_workspace_bytes(int64_t num_q_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+                                    int32_t num_seqs, int32_t max_query_len, int32_t max_seq_len) {
+    return 0;
+}
+
+kv_int4_status kv_int4_span_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens, int32_t num_q_heads,
+                                      const uint8_t* cache, int64_t num_blocks, int32_t num_kv_heads,
+                                      int32_t head_size, int32_t block_size, const int32_t* block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                      const int32_t* query_start_loc, int32_t num_seqs, int32_t max_query_len,
+                                      int32_t max_seq_len, float softmax_scale, const float* rht_signs,
+                                      const int32_t* key_begin, const int32_t* key_end, float softcap,
+                                      const float* alibi_slopes, void* out, kv_int4_dtype out_dtype, void* workspace,
+                                      size_t workspace_bytes, kv_int4_stream_t stream) {
+    return span_attention_impl(4, q, q_dtype, num_q_tokens, num_q_heads, cache, num_blocks, num_kv_heads, head_size,
+                               block_size, block_tables, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs,
+                               max_query_len, max_seq_len, softmax_scale, rht_signs, key_begin, key_end, softcap,
+                               alibi_slopes, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
+kv_int4_status kv_int8_span_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens, int32_t num_q_heads,
+                                      const uint8_t* cache, int64_t num_blocks, int32_t num_kv_heads,
+                                      int32_t head_size, int32_t block_size, const int32_t* block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                      const int32_t* query_start_loc, int32_t num_seqs, int32_t max_query_len,
+                                      int32_t max_seq_len, float softmax_scale,
+                                      const int32_t* key_begin, const int32_t* key_end, float softcap,
+                                      const float* alibi_slopes, void* out, kv_int4_dtype out_dtype, void* workspace,
+                                      size_t workspace_bytes, kv_int4_stream_t stream) {
+    return span_attention_impl(8, q, q_dtype, num_q_tokens, num_q_heads, cache, num_blocks, num_kv_heads, head_size,
+                               block_size, block_tables, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs,
+                               max_query_len, max_seq_len, softmax_scale, nullptr, key_begin, key_end, softcap,
+                               alibi_slopes, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
+kv_int4_status kv_int2_span_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens, int32_t num_q_heads,
+                                      const uint8_t* cache, int64_t num_blocks, int32_t num_kv_heads,
+                                      int32_t head_size, int32_t block_size, const int32_t* block_tables,
+                                      int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                      const int32_t* query_start_loc, int32_t num_seqs, int32_t max_query_len,
+                                      int32_t max_seq_len, float softmax_scale, const float* rht_signs,
+                                      const int32_t* key_begin, const int32_t* key_end, float softcap,
+                                      const float* alibi_slopes, void* out, kv_int4_dtype out_dtype, void* workspace,
+                                      size_t workspace_bytes, kv_int4_stream_t stream) {
+    return span_attention_impl(2, q, q_dtype, num_q_tokens, num_q_heads, cache, num_blocks, num_kv_heads, head_size,
+                               block_size, block_tables, max_blocks_per_seq, seq_lens, query_start_loc, num_seqs,
+                               max_query_len, max_seq_len, softmax_scale, rht_signs, key_begin, key_end, softcap,
+                               alibi_slopes, out, out_dtype, workspace, workspace_bytes, stream);
+}
+
 kv_int4_status kv_int4_selftest_wait_timeout(uint64_t timeout_ns, kv_int4_stream_t stream) {
     uint32_t* ptr = status_ptr();
     if (!ptr) return KV_INT4_ECUDA;

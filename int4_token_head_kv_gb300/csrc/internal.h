@@ -116,6 +116,31 @@ struct AttnParams {
 };
 constexpr int kOptWindow = 1, kOptSoftcap = 2, kOptAlibi = 4, kOptQQ = 8;
 
+// Attention in which every query row sees the keys of a span of its own.
+struct SpanParams {
+    const void* q;
+    const uint8_t* cache;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    const int32_t* qsl;         // query_start_loc
+    const int32_t* key_begin;   // [num_q_tokens] or nullptr: 0
+    const int32_t* key_end;     // [num_q_tokens] or nullptr: the query's position + 1
+    const float* alibi;         // [Hq] slopes or nullptr
+    const float* signs;         // nullptr for INT8 rows
+    void* out;
+    uint32_t* status;
+    int64_t num_blocks;
+    int64_t num_q_tokens;
+    int num_seqs;
+    int max_query_len;
+    int H, G, Hq;
+    int max_blocks_per_seq;
+    int len_cap;                // contexts are clamped to this (max_seq_len, block table)
+    float softmax_scale;
+    float c;                    // fp32(1 / sqrt(head_size)); 1 for INT8 rows
+    float softcap;              // 0: none
+};
+
 // Launchers (return cudaSuccess or the launch error).
 cudaError_t launch_write(const WriteParams& p, int head_size, DType dt, cudaStream_t stream);
 // INT8 per-(token, head) comparator rows (D codes + fp32 scale); p.signs and p.c are not used.
@@ -169,6 +194,9 @@ cudaError_t launch_prefix(const AttnParams& p, int head_size, DType q_dt, cudaSt
 // Splits of the prefix's keys for a batch of row_tiles 128-row tiles per kv head.
 int prefix_splits(int64_t row_tiles, int num_kv_heads, int prefix_len);
 constexpr int kMaxPrefixSplits = 64;
+
+// Attention over key spans (bits 4, 8 or 2).
+cudaError_t launch_span(const SpanParams& p, int bits, int head_size, DType q_dt, DType out_dt, cudaStream_t stream);
 
 int num_sms();
 

@@ -41,3 +41,39 @@ def test_mrope_write(lib, name):
         assert call(**{x: FAKE + 8}) == 3, x
     assert call(n=1 << 29) == 2   # 32-bit vector index
     assert call(n=0, q=None, k=None, v=None) == 0
+
+
+@pytest.mark.parametrize("name", ["kv_int4_span_attention", "kv_int8_span_attention", "kv_int2_span_attention"])
+def test_span_attention(lib, name):
+    f, signs = getattr(lib, name), "8" not in name
+    f.restype = ctypes.c_int
+    f.argtypes = [vp, ctypes.c_int, i64, i32, vp, i64, i32, i32, i32, vp, i32, vp, vp, i32, i32, i32, f32] + \
+        ([vp] if signs else []) + [vp, vp, f32, vp, vp, ctypes.c_int, vp, szt, vp]
+    base = dict(q=FAKE, qdt=1, n=12, hq=8, cache=FAKE, nb=8, h=2, d=128, bs=16, bt=FAKE, mb=4, lens=FAKE, qsl=FAKE, ns=3, mq=4,
+                ms=64, scale=0.1, signs=FAKE, kb=FAKE, ke=None, cap=0.0, al=None, out=FAKE, odt=2, ws=FAKE, wsb=1 << 30, st=None)
+    if not signs:
+        del base["signs"]
+
+    def call(**kw):
+        return f(*dict(base, **kw).values())
+
+    assert call(d=96) == 2 and call(bs=32) == 2 and call(qdt=2) == 2 and call(odt=3) == 2 and call(h=3, hq=6) == 2
+    assert call(hq=6) == 2 and call(hq=32) == 2 and call(h=16, hq=16) == 2 and call(ns=65536) == 2 and call(n=1 << 31) == 2
+    for x in ("n", "ns", "nb", "mq", "ms", "mb"):
+        assert call(**{x: -1}) == 1, x
+    assert call(cap=-1.0) == 1 and call(cap=float("inf")) == 1 and call(cap=float("nan")) == 1 and call(scale=float("nan")) == 1
+    for x in ("q", "cache", "bt", "lens", "qsl", "out") + (("signs",) if signs else ()):
+        assert call(**{x: None}) == 1, x
+    assert call(mq=0) == 1 and call(mb=0) == 1
+    for x in ("q", "cache", "out"):
+        assert call(**{x: FAKE + 8}) == 3, x
+    assert call(n=0, q=None) == 0 and call(ns=0) == 0
+
+
+def test_span_workspace(lib):
+    f = lib.kv_int4_span_workspace_bytes
+    f.restype, f.argtypes = szt, [i64, i32, i32, i32, i32, i32, i32]
+    for bad in ((0, 8, 2, 128, 3, 4, 64), (12, 8, 2, 128, 0, 4, 64), (12, 8, 0, 128, 3, 4, 64), (12, 0, 2, 128, 3, 4, 64),
+                (12, 7, 2, 128, 3, 4, 64), (12, 8, 2, 0, 3, 4, 64), (-1, 8, 2, 128, 3, 4, 64), (12, 8, 2, 128, 3, -1, 64),
+                (12, 8, 2, 128, 3, 4, -1)):
+        assert f(*bad) == 0, bad
