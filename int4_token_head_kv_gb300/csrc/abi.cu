@@ -737,6 +737,50 @@ kv_int4_status kv_int2_paged_attention(const void* q, kv_int4_dtype q_dtype, int
 
 namespace {
 
+// Grid and workspace of the span attention.
+struct SpanLayout {
+    int tiles;      // row tiles per kv head: of the batch (tiled), or of its longest chunk
+    bool tiled;
+    int splits;
+    size_t ml, total;   // workspace: partial outputs, then at ml their (max, sum) pairs
+};
+
+// Row tiles hold 128 / G tokens of one sequence.  One grid slice per sequence, unless that is much more than a bound
+// on the batch's tiles (a few chunks among many single tokens).  The keys of a tile are split among CTAs so that
+// the estimated time is least: rounds of one CTA per SM, each the tile's key tiles and about five of them for its
+// start and end, and three for the combine.
+bool span_layout(int64_t num_q_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size, int32_t num_seqs,
+                 int32_t max_query_len, int32_t max_seq_len, SpanLayout* x) {
+    if (num_q_tokens <= 0 || num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 ||
+        head_size <= 0 || max_query_len <= 0 || max_seq_len < 0)
+        return false;
+    const int G = num_q_heads / num_kv_heads;
+    if (G > kPrefillRows) return false;
+    const int64_t bq = kPrefillRows / G;
+    const int64_t per_seq = ((int64_t)max_query_len + bq - 1) / bq, with = std::min<int64_t>(num_seqs, num_q_tokens);
+    const int64_t bound = std::min((num_q_tokens + with * (bq - 1)) / bq, with * per_seq), sliced = (int64_t)num_seqs * per_seq;
+    if (bound * num_kv_heads >= ((int64_t)1 << 31) || per_seq * num_kv_heads >= ((int64_t)1 << 31)) return false;
+    x->tiled = sliced > bound + bound / 4;
+    x->tiles = (int)(x->tiled ? bound : per_seq);
+    const int64_t ctas = bound * num_kv_heads, sms = num_sms(), keys = ((int64_t)max_seq_len + 127) / 128;
+    double best = 0.0;
+    x->splits = 1;
+    for (int s = 1; s <= kMaxSpanSplits && s <= std::max<int64_t>(keys, 1); ++s) {
+        const double cost = (double)((ctas * s + sms - 1) / sms) * (double)((keys + s - 1) / s + 5) + (s > 1 ? 3.0 + 0.05 * s : 0.0);
+        if (s == 1 || cost < best) {
+            best = cost;
+            x->splits = s;
+        }
+    }
+    x->ml = x->total = 0;
+    if (x->splits > 1) {
+        const size_t rows = (size_t)num_q_tokens * (size_t)num_q_heads * (size_t)x->splits;
+        x->ml = align256(rows * (size_t)head_size * 4);
+        x->total = x->ml + rows * 8;
+    }
+    return true;
+}
+
 // The checks and the launch that the span attentions of the three caches share (bits 4, 8 or 2).
 kv_int4_status span_attention_impl(int bits, const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens, int32_t num_q_heads,
                                    const uint8_t* cache, int64_t num_blocks, int32_t num_kv_heads, int32_t head_size,
@@ -760,10 +804,11 @@ kv_int4_status span_attention_impl(int bits, const void* q, kv_int4_dtype q_dtyp
     if (!q || !cache || !block_tables || !seq_lens || !query_start_loc || (bits != 8 && !rht_signs) || !out) return KV_INT4_EINVAL;
     if (max_query_len < 1 || max_blocks_per_seq < 1) return KV_INT4_EINVAL;
     if (!aligned16(q) || !aligned16(out) || !aligned16(cache)) return KV_INT4_EALIGN;
-    const size_t need = kv_int4_span_workspace_bytes(num_q_tokens, num_q_heads, num_kv_heads, head_size, num_seqs, max_query_len,
-                                                     max_seq_len);
-    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return KV_INT4_EWORKSPACE;
-    if (need > 0 && !aligned16(workspace)) return KV_INT4_EALIGN;
+    SpanLayout lay;
+    if (!span_layout(num_q_tokens, num_q_heads, num_kv_heads, head_size, num_seqs, max_query_len, max_seq_len, &lay))
+        return KV_INT4_EUNSUPPORTED;
+    if (lay.total > 0 && (workspace == nullptr || workspace_bytes < lay.total)) return KV_INT4_EWORKSPACE;
+    if (lay.total > 0 && !aligned16(workspace)) return KV_INT4_EALIGN;
     SpanParams p;
     p.q = q;
     p.cache = cache;
@@ -788,9 +833,16 @@ kv_int4_status span_attention_impl(int bits, const void* q, kv_int4_dtype q_dtyp
     p.softmax_scale = softmax_scale;
     p.c = bits != 8 ? (float)(1.0 / std::sqrt((double)head_size)) : 1.0f;
     p.softcap = softcap;
-    const DType qd = q_dtype == KV_INT4_BF16 ? DType::BF16 : DType::F16;
-    const DType od = out_dtype == KV_INT4_BF16 ? DType::BF16 : (out_dtype == KV_INT4_F16 ? DType::F16 : DType::F32);
-    return from_cuda(launch_span(p, bits, head_size, qd, od, reinterpret_cast<cudaStream_t>(stream)));
+    p.cap_l2 = (float)((double)softcap * 1.4426950408889634);
+    p.cap_in = softcap > 0.0f ? 2.0f / softcap : 0.0f;
+    p.out_dt = out_dtype == KV_INT4_BF16 ? DType::BF16 : (out_dtype == KV_INT4_F16 ? DType::F16 : DType::F32);
+    p.q_bf16 = q_dtype == KV_INT4_BF16;
+    p.tiles = lay.tiles;
+    p.tiled = lay.tiled;
+    p.splits = lay.splits;
+    p.part_o = reinterpret_cast<float*>(workspace);
+    p.part_ml = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + lay.ml);
+    return from_cuda(launch_span(p, bits, head_size, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace
@@ -799,7 +851,8 @@ extern "C" {
 
 size_t kv_int4_span_workspace_bytes(int64_t num_q_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
                                     int32_t num_seqs, int32_t max_query_len, int32_t max_seq_len) {
-    return 0;
+    SpanLayout x;
+    return span_layout(num_q_tokens, num_q_heads, num_kv_heads, head_size, num_seqs, max_query_len, max_seq_len, &x) ? x.total : 0;
 }
 
 kv_int4_status kv_int4_span_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens, int32_t num_q_heads,

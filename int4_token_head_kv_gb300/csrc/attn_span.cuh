@@ -1,0 +1,1148 @@
+// Attention in which every query row sees the cached keys of a span of its own, over the INT4, INT8 and INT2
+// caches, for chunks of queries and single tokens.  For the query at position pos of its sequence, over its keys
+// lo <= j < hi:
+//   s_j = scale q . x_Kj,  s_j <- softcap tanh(s_j / softcap),  s_j <- s_j - slope |pos - j|,
+//   out = sum_j softmax(s)_j x_Vj   (0 for an empty span).
+//
+// The products run on the fifth-generation tensor cores with the rows left in the domain they are stored in
+// (rotated, but for INT8): S = Q' N_K^T with the stored numbers N exact in fp16 (INT4 code - zp, INT8 code, INT2
+// centroid) and the rotated queries Q' as fp16 high + low halves, logit = S s_K k0 2^-e, one pass over the keys with
+// a running reference maximum m and a reference exponent E of the V scales per row, weights
+// w = 2^(logit - m + 127 + raise - E) s_V in fp16 (two halves but for a bf16 output), O += w N_V, everything
+// accumulated in fp32, out = O / l un-rotated.
+//
+// A CTA takes 128 rows (128 / G query tokens of one sequence x the G query heads of a kv head) against the keys that
+// some of them see, 128 at a time; tiles outside that range are not touched, so a document mask costs what its
+// documents hold.  With few row tiles the range is split among CTAs and span_combine_kernel joins the partials.
+// Tiles that every row of a warp sees whole take no mask; tiles that none of them sees take no arithmetic.
+#pragma once
+
+#include "attn_prefix.cuh"
+
+namespace kvi4 {
+namespace {
+
+// Warp roles (640 threads, the shared-prefix kernel's): warps 0-7 own the rows, 8-11 convert K rows, 12-15 V rows,
+// 16 issues the MMAs, 17-18 load packed rows, 19 completes the last warpgroup for the register split.
+
+// Shared memory: [K 0][V 0][K 1][V 1] fp16 tiles (as the prefill's), then staged packed rows, records, barriers.
+template <int D, int BITS>
+struct SpLayout {
+    static constexpr uint32_t kRowBytes = D * BITS / 8 + 4;
+    static constexpr uint32_t kRowWords = kRowBytes / 4;                          // codes, then the scale word
+    static constexpr uint32_t kChunks = (kRowWords + 3 + 3) / 4;                  // 16-byte chunks of a row's aligned window
+    static constexpr uint32_t kWindow = 4 * kChunks;
+    static constexpr int kStages = kRowWords > 20 ? 2 : 4;                        // packed tiles staged ahead
+    static constexpr uint32_t kTile = (D / 64) * kPfKeys * 128;
+    static constexpr uint32_t kPlane = kPfKeys * kWindow * 4;                     // one plane of a staged tile
+    static constexpr uint32_t kRaw = 2 * kPfPairs * kTile;
+    static constexpr uint32_t kSk = kRaw + kStages * 2 * kPlane;                  // [kring][128] f32 s_K k0 2^-e
+    static constexpr uint32_t kDeadF = kSk + kPfKRing * kPfKeys * 4;              // [kring][4] u32: positions with no key
+    static constexpr uint32_t kSv = kDeadF + kPfKRing * 4 * 4;                    // [pairs][128] f32 s_V
+    static constexpr uint32_t kEblk = kSv + kPfPairs * kPfKeys * 4;               // [pairs][4] per-warp largest V exponent
+    static constexpr uint32_t kQexp = kEblk + kPfPairs * 4 * 4;                   // u32: first usable row and its exponent
+    static constexpr uint32_t kWhere = kQexp + 4;                                 // i32: sequence, query tile, first key, end of the keys
+    static constexpr uint32_t kHeld = kWhere + 16;                                // [stages] u32: blocks of a staged tile that hold keys
+    static constexpr uint32_t kScan = kHeld + kStages * 4;                        // [20] u32
+    static constexpr uint32_t kRs = kScan + 20 * 4;                               // [128] f32 2^-d of each row's own prescale
+    static constexpr uint32_t kFin = kRs + 128 * 4;                               // [128] f32 what a row's O is multiplied with
+    static constexpr uint32_t kSignBits = kFin + 128 * 4;                         // [4] u32
+    static constexpr uint32_t kBars = (kSignBits + 16 + 7u) & ~7u;
+    // k_full[kring], k_free[pairs], v_full[pairs], v_free[pairs], pv_done[2], s_full[2], p_full[2], q_ready,
+    // flush, q_tma, rot_in, rot_done, q_max, epi[2], raw_full[plane][stages], raw_free[plane][stages]
+    static constexpr int kNumBars = kPfKRing + 3 * kPfPairs + 6 + 6 + 2 + 4 * kStages;
+    static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
+    static constexpr uint32_t kFlags = kTmemSlot + 4;
+    static constexpr uint32_t kBytes = kFlags + 4 + 1024;                         // + alignment slack
+    static_assert(kBytes <= 232448, "shared memory");
+    static_assert(kPfRows * D * 4 <= 4 * kTile, "output exchange");
+};
+
+// The INT2 centroids as the tiles hold them are 1.0002228 a and 1.0002134 b in fp16; with 1 / 1.0002181 in the scales both are
+// within 5e-6.
+constexpr float kU2Scale = 0.99978195f;
+
+// The dimension a tile column holds.
+template <int BITS>
+__host__ __device__ constexpr int span_dim(int c) { return BITS == 8 ? c : dim_of_column(c); }
+
+// 32 lanes x 32 columns: thread i gets row (lane) i of the address's lanes, 32 consecutive columns.
+__device__ __forceinline__ void tmem_ld_row32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// Store n (a multiple of 8) consecutive values of a row, 16 bytes at a time; at is a multiple of 8.
+template <int N>
+__device__ __forceinline__ void store_values(void* out, DType dt, int64_t at, const float* x) {
+    if (dt == DType::F32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) o[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        return;
+    }
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
+    const bool bf = dt == DType::BF16;
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = x[8 * i + 2 * e], b = x[8 * i + 2 * e + 1];
+            if (bf) {
+                const __nv_bfloat162 y = __floats2bfloat162_rn(a, b);
+                w[e] = *reinterpret_cast<const uint32_t*>(&y);
+            } else {
+                w[e] = pack_f16x2(a, b);
+            }
+        }
+        o[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// The options on a visible key's logit x (log2 units): the cap, then the distance bias.
+__device__ __forceinline__ float span_opts(float x, float dist, float slope_l2, const SpanParams& p) {
+    if (p.softcap > 0.0f) {   // C tanh(x / C) = C - 2 C / (e^(2 x / C) + 1)
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(x * p.cap_in) + 1.0f));
+        x = fmaf(-2.0f * p.cap_l2, r, p.cap_l2);
+    }
+    return fmaf(-slope_l2, dist, x);
+}
+
+// Where a query row's keys are: lo <= j < hi (none: an empty span, or no row).
+struct Span {
+    int lo, hi;
+};
+
+// OPTS: the call caps its scores or has a distance bias.  TWO: the weights as fp16 high + low halves.
+template <int D, int BITS, bool OPTS, bool TWO>
+__global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_constant__ SpanParams p, const __grid_constant__ CUtensorMap qmap,
+                                                             const __grid_constant__ CUtensorMap cmap) {
+    using Ly = SpLayout<D, BITS>;
+    using Tm = PfTmem<D>;
+    constexpr int KSTEPS = D / 16, RB = (int)Ly::kRowBytes, kStages = Ly::kStages;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    griddep_wait();   // the previous kernel may produce any of the inputs
+    if (p.splits > 1) griddep_launch_dependents();   // the combine, which waits for this grid before it reads anything
+
+    const int G = p.G, Hq = p.Hq, H = p.H;
+    const int BQ = kPfRows / G;
+    const int h = (int)(blockIdx.x % (unsigned)H), split = (int)blockIdx.y;
+    const bool boxes = H % 4 == 0;   // rows of a multiple of 16 bytes: TMA loads packed rows (see the loaders)
+    volatile int* where = reinterpret_cast<volatile int*>(smem + Ly::kWhere);
+
+    // ---- the CTA's sequence and query tile, the last tiles (the longest causal rows) first
+    auto tiles_of = [&](int b) -> int {
+        const int ql = min(__ldg(p.qsl + b + 1) - __ldg(p.qsl + b), p.max_query_len);
+        return ql > 0 ? (ql + BQ - 1) / BQ : 0;
+    };
+    int seq, qtile;
+    if (p.tiled) {   // tile v of the batch's: its sequence by a scan over the sequences' tile counts
+        const int v = (int)(blockIdx.x / (unsigned)H), per = (p.num_seqs + kPxThreads - 1) / kPxThreads;
+        const int b0 = min(p.num_seqs, (int)threadIdx.x * per), b1 = min(p.num_seqs, b0 + per);
+        int mine = 0;
+        for (int b = b0; b < b1; ++b) mine += tiles_of(b);
+        int x = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        int* scan = reinterpret_cast<int*>(smem + Ly::kScan);
+        if (lane == 31) scan[warp] = x;
+        if (threadIdx.x == 0) where[0] = -1;
+        __syncthreads();
+        int before = x - mine;
+        for (int w = 0; w < warp; ++w) before += scan[w];
+        if (v >= before && v < before + mine) {
+            int b = b0, left = v - before;
+            for (int n = tiles_of(b); left >= n; n = tiles_of(b)) {
+                left -= n;
+                ++b;
+            }
+            where[0] = b;
+            where[1] = tiles_of(b) - 1 - left;
+        }
+        __syncthreads();
+        seq = where[0];
+        qtile = where[1];
+        if (seq < 0) return;   // past the batch's last tile
+    } else {
+        seq = (int)blockIdx.z;
+        qtile = tiles_of(seq) - 1 - (int)(blockIdx.x / (unsigned)H);
+        if (qtile < 0) return;
+    }
+    const int q0 = __ldg(p.qsl + seq);
+    const int qlen = __ldg(p.qsl + seq + 1) - q0, qcount = min(qlen, p.max_query_len);
+    const int qt0 = qtile * BQ;
+    const int len = __ldg(p.seq_lens + seq), L = max(0, min(len, p.len_cap)), pos0 = len - qlen;
+    const bool outside = q0 < 0 || (int64_t)q0 + qlen > p.num_q_tokens;
+    if (qtile == 0 && h == 0 && split == 0 && threadIdx.x == 0 &&
+        (outside || len > p.len_cap || (qlen > len && len != 0) || qlen > p.max_query_len))
+        count_status(p.status, 2);
+    if (outside) return;
+    auto span_of = [&](int qt) -> Span {
+        if (qt >= qcount) return Span{0, 0};
+        const int r = q0 + qt;
+        return Span{p.key_begin ? max(0, __ldg(p.key_begin + r)) : 0, min(L, p.key_end ? __ldg(p.key_end + r) : pos0 + qt + 1)};
+    };
+
+    float* sk = reinterpret_cast<float*>(smem + Ly::kSk);
+    float* sv = reinterpret_cast<float*>(smem + Ly::kSv);
+    uint32_t* eblkw = reinterpret_cast<uint32_t*>(smem + Ly::kEblk);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::kBars);
+    uint64_t* k_full = bars;                    // [kring] K tile and scales of tile j (128 arrivals)
+    uint64_t* k_free = k_full + kPfKRing;       // [pairs] K tile j % 2 read by S of tile j (commit)
+    uint64_t* v_full = k_free + kPfPairs;       // [pairs] V tile and scales of tile j (128 arrivals)
+    uint64_t* v_free = v_full + kPfPairs;       // [pairs] V tile j % 2 read by P.V of tile j (commit)
+    uint64_t* pv_done = v_free + kPfPairs;      // [2] P.V of tile j done (commit): S buffer j % 2 and O free
+    uint64_t* s_full = pv_done + 2;             // [2] S of the tile in tensor memory (commit)
+    uint64_t* p_full = s_full + 2;              // [2] P of the tile in tensor memory (256 arrivals)
+    uint64_t* q_ready = p_full + 2;             // queries in tensor memory, staging free (256 arrivals)
+    uint64_t* flush = q_ready + 1;              // the MMA thread's last commit (teardown)
+    uint64_t* q_tma = flush + 1;                // the CTA's query rows in shared memory (bytes)
+    uint64_t* rot_in = q_tma + 1;               // the rotation matrix in shared memory (256 arrivals)
+    uint64_t* rot_done = rot_in + 1;            // the rotated queries in tensor memory (commit)
+    uint64_t* q_max = rot_done + 1;             // the rows' exponent is known (256 arrivals)
+    uint64_t* epi = q_max + 1;                  // [2] the row threads meet (256 arrivals)
+    uint64_t* raw_full = epi + 2;               // [plane][stages] packed rows of a key tile landed (one arrival and bytes, or and 32 lanes)
+    uint64_t* raw_free = raw_full + 2 * kStages;   // [plane][stages] that plane converted (128 arrivals)
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::kTmemSlot);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kFlags);
+    uint32_t* deadf = reinterpret_cast<uint32_t*>(smem + Ly::kDeadF);
+    uint32_t* qexp = reinterpret_cast<uint32_t*>(smem + Ly::kQexp);
+    uint32_t* held = reinterpret_cast<uint32_t*>(smem + Ly::kHeld);
+    float* fin = reinterpret_cast<float*>(smem + Ly::kFin);
+
+    if (warp == 0) {   // the keys that some row sees
+        int lo = 0x7FFFFFFF, hi = 0;
+        for (int t = lane; t < BQ; t += 32) {
+            const Span s = span_of(qt0 + t);
+            if (s.hi > s.lo) {
+                lo = min(lo, s.lo);
+                hi = max(hi, s.hi);
+            }
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) {
+            where[2] = lo;
+            where[3] = hi;
+        }
+    }
+    if (threadIdx.x == 32) {
+        for (int b = 0; b < kPfKRing; ++b) mbar_init(&k_full[b], 128);
+        for (int b = 0; b < kPfPairs; ++b) {
+            mbar_init(&k_free[b], 1);
+            mbar_init(&v_full[b], 128);
+            mbar_init(&v_free[b], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&pv_done[b], 1);
+            mbar_init(&s_full[b], 1);
+            mbar_init(&p_full[b], kPfSoftmaxThreads);
+            mbar_init(&epi[b], kPfSoftmaxThreads);
+        }
+        mbar_init(q_ready, kPfSoftmaxThreads);
+        mbar_init(flush, 1);
+        mbar_init(q_tma, 1);
+        mbar_init(rot_in, kPfSoftmaxThreads);
+        mbar_init(rot_done, 1);
+        mbar_init(q_max, kPfSoftmaxThreads);
+        *qexp = 0xFFFFFFFFu;
+        for (int i = 0; i < 2 * kStages; ++i) {
+            mbar_init(&raw_full[i], boxes ? 1 : 33);
+            mbar_init(&raw_free[i], 128);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    uint32_t* signbits = reinterpret_cast<uint32_t*>(smem + Ly::kSignBits);
+    if (BITS != 8 && warp >= 4 && warp < 4 + D / 32) {
+        const float s = p.signs[(warp - 4) * 32 + lane];
+        const uint32_t m = __ballot_sync(0xffffffffu, s < 0.0f);
+        if (lane == 0) signbits[warp - 4] = m;
+    }
+    if (warp == kPxMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                     "n"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // this split's 128-key tiles, counted from the first key's block
+    const int key_base = where[2] / kBlockSize * kBlockSize, key_end = where[3];
+    const int tiles_all = key_end > where[2] ? (key_end - key_base + kPfKeys - 1) / kPfKeys : 0;
+    const int kt0 = (int)((int64_t)tiles_all * split / p.splits), kt1 = (int)((int64_t)tiles_all * (split + 1) / p.splits);
+    const int nkt = kt1 - kt0;
+    uint8_t* tiles = smem;   // [K0][V0][K1][V1]
+    auto ktile = [&](int b) { return tiles + (uint32_t)b * 2u * Ly::kTile; };
+    auto vtile = [&](int b) { return tiles + (uint32_t)b * 2u * Ly::kTile + Ly::kTile; };
+    // a wait that runs out counts once and winds the CTA down
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (*abort_flag) return false;
+        if (mbar_wait(bar, parity)) return true;
+        if (atomicExch(const_cast<int*>(abort_flag), 1) == 0) count_status(p.status, 3);
+        return false;
+    };
+    // the same in the chain S -> weights -> P.V -> next S, where waking a suspended warp would add to every tile:
+    // polled first
+    auto soon = [&](uint64_t* bar, uint32_t parity) -> bool {
+        for (int i = 0; i < kPxPolls; ++i)
+            if (mbar_test_wait(bar, parity)) return true;
+        return wait(bar, parity);
+    };
+
+    if (nkt == 0) {
+        // no keys: nothing below waits for any copy or product; the rows are written at the end
+    } else if (warp < kPfSoftmaxWarps) {
+        more_registers<kPxRowRegs>();
+        // ================================================================ rows: softmax + output
+        // Warp w owns the 16 rows 32 (w % 4) + 16 (w / 4) .. in the 16-lane tensor-memory layout: thread (g, t) holds
+        // rows ra = rbase + g and rb = ra + 8 and, of every group of 8 columns, columns 2t and 2t + 1.
+        const int rbase = 32 * (warp & 3) + 16 * (warp >> 2);
+        const int t4 = lane & 3;
+        const int ra = rbase + (lane >> 2), rb = ra + 8;
+        const uint32_t trow = tmem + ((uint32_t)rbase << 16);
+        // ---- the rotation matrix B[p][k] = sign_k (-1)^popcount(n(p) & k) (INT8: the identity) in pair 1's V tile
+        {
+            constexpr int kRowChunks = D / 8, kThreadsPerRow = kPfSoftmaxThreads / D, kChunksPerThread = kRowChunks / kThreadsPerRow;
+            uint8_t* qb = vtile(1);
+            const uint32_t one = p.q_bf16 ? 0x3F80u : 0x3C00u;
+            const int prow = threadIdx.x / kThreadsPerRow;
+            const int n = span_dim<BITS>(slot_of_column(prow));
+            uint32_t par8 = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) par8 |= ((uint32_t)__popc(n & j) & 1u) << j;
+#pragma unroll
+            for (int it = 0; it < kChunksPerThread; ++it) {
+                const int k8 = (threadIdx.x % kThreadsPerRow) * kChunksPerThread + it;
+                uint32_t w[4];
+                if constexpr (BITS == 8) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = n / 2 == 4 * k8 + e ? one << (16 * (n & 1)) : 0u;
+                } else {
+                    const uint32_t sb = (signbits[k8 / 4] >> (8 * (k8 % 4))) & 0xFFu;
+                    const uint32_t neg = par8 ^ sb ^ ((__popc(n & (8 * k8)) & 1) ? 0xFFu : 0u);
+                    pm1_words(neg, one, w);
+                }
+                *reinterpret_cast<uint4*>(qb + (uint32_t)(k8 / 8) * (uint32_t)(D * 128) + swz128((uint32_t)prow, (uint32_t)(k8 % 8))) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // generic writes -> tensor core reads
+            mbar_arrive(rot_in);
+        }
+        // ---- each row's keys.  A row that sees none goes along as if it saw all, so that it does not put its warp on
+        // the masked path, and is zero at the end; a warp of such rows leaves its weights unwritten.
+        Span sa = span_of(qt0 + ra / G), sb = span_of(qt0 + rb / G);
+        const bool none_a = sa.hi <= sa.lo, none_b = sb.hi <= sb.lo;
+        if (none_a) sa = Span{0, 0x7FFFFFFF};
+        if (none_b) sb = Span{0, 0x7FFFFFFF};
+        const bool idle = __all_sync(0xffffffffu, none_a && none_b);
+        // the keys that all, and that any, of the warp's rows see
+        const int all_lo = __reduce_max_sync(0xffffffffu, max(sa.lo, sb.lo)), all_hi = __reduce_min_sync(0xffffffffu, min(sa.hi, sb.hi));
+        const int any_lo = __reduce_min_sync(0xffffffffu, min(none_a ? 0x7FFFFFFF : sa.lo, none_b ? 0x7FFFFFFF : sb.lo));
+        const int any_hi = __reduce_max_sync(0xffffffffu, max(none_a ? 0 : sa.hi, none_b ? 0 : sb.hi));
+        // ---- a power-of-two prescale of the rows, then fp16 high + low halves into tensor memory, by the shared-prefix
+        // kernel's rule: one exponent serves the CTA, so that 2^-e sits in the keys' scales; a row whose largest value
+        // then lies outside [2^-2, 2^15) takes a further power of two of its own.
+        float* rs = reinterpret_cast<float*>(smem + Ly::kRs);   // what a row's S is multiplied with
+        bool own_any = false;
+        bool ok = wait(rot_done, 0);
+        if (__all_sync(0xffffffffu, ok)) {
+            tc_fence_after();
+            float v[D / 2];   // v[4i], v[4i + 1]: row a, columns 8i + 2t, + 1; v[4i + 2], v[4i + 3]: row b
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 64) tmem_ld_q8(trow + Tm::kS0 + c0, reinterpret_cast<uint32_t*>(v) + c0 / 2);
+            tmem_ld_wait();
+            // the rows' largest magnitudes by their bits (a NaN's are above infinity's)
+            uint32_t mxa = 0u, mxb = 0u;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                mxa = max(mxa, max(__float_as_uint(v[4 * i]) & 0x7FFFFFFFu, __float_as_uint(v[4 * i + 1]) & 0x7FFFFFFFu));
+                mxb = max(mxb, max(__float_as_uint(v[4 * i + 2]) & 0x7FFFFFFFu, __float_as_uint(v[4 * i + 3]) & 0x7FFFFFFFu));
+            }
+            mxa = max(mxa, __shfl_xor_sync(0xffffffffu, mxa, 1));
+            mxb = max(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
+            mxa = max(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
+            mxb = max(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
+            const int xa = (int)(mxa >> 23), xb = (int)(mxb >> 23);   // biased exponents
+            if (t4 == 0) {
+                if (!none_a && xa > 0 && xa < 255) atomicMin(qexp, (uint32_t)ra << 8 | (uint32_t)xa);
+                if (!none_b && xb > 0 && xb < 255) atomicMin(qexp, (uint32_t)rb << 8 | (uint32_t)xb);
+            }
+            __syncwarp();
+            mbar_arrive(q_max);
+            ok = __all_sync(0xffffffffu, wait(q_max, 0));
+            const int e = rows_exponent(*reinterpret_cast<volatile uint32_t*>(qexp));
+            auto own = [&](int x) -> int {   // a row's further exponent
+                const int y = x - 127 + e;
+                return x == 0 || (y >= -2 && y <= 14) ? 0 : max(-126 - e, min(127 - e, 7 - y));
+            };
+            const int da = own(xa), db = own(xb);
+            own_any = __any_sync(0xffffffffu, da != 0 || db != 0);
+            if (t4 == 0) {
+                rs[ra] = exp2f((float)-da);
+                rs[rb] = exp2f((float)-db);
+            }
+            __syncwarp();
+            const float sca = exp2i(e + da), scb = exp2i(e + db);
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+                uint32_t hw[4], lw[4];
+#pragma unroll
+                for (int i = 2 * q; i < 2 * q + 2; ++i) {
+                    split_f16x2(v[4 * i] * sca, v[4 * i + 1] * sca, hw[i & 1], lw[i & 1]);
+                    split_f16x2(v[4 * i + 2] * scb, v[4 * i + 3] * scb, hw[2 + (i & 1)], lw[2 + (i & 1)]);
+                }
+                tmem_st_q1(trow + Tm::kQh + 8 * q, hw);
+                tmem_st_q1(trow + Tm::kQl + 8 * q, lw);
+            }
+            tmem_st_wait();
+        } else {
+            ok = false;
+        }
+        tc_fence_before();
+        mbar_arrive(q_ready);
+        // ---- the key tiles
+        // Reference maxima m (log2 units) as the exponents' offsets off = 127 + raise - E - m; E = 127 and off = 0
+        // until a row has a key (any).
+        float off_a = 0.0f, off_b = 0.0f;
+        bool any_a = false, any_b = false;
+        float l_a = 0.0f, l_b = 0.0f;           // this thread's part of the sums of 2^(127+raise-E) p
+        uint32_t E_a = 0, E_b = 0;              // reference biased exponents of the V scales that the rows see (0: none yet)
+        const float pos_a = (float)(pos0 + qt0 + ra / G), pos_b = (float)(pos0 + qt0 + rb / G);
+        float sl_a = 0.0f, sl_b = 0.0f;
+        if (OPTS && p.alibi) {
+            sl_a = __ldg(p.alibi + h * G + ra % G) * kLog2e;
+            sl_b = __ldg(p.alibi + h * G + rb % G) * kLog2e;
+        }
+        if (idle) {
+            for (int j = 0; j < nkt && ok; ++j) {
+                ok = wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) mbar_arrive(&p_full[j & 1]);
+            }
+        }
+        for (int j = idle ? nkt : 0; j < nkt && ok; ++j) {
+            const int b = j & 1;
+            const uint32_t ph = (uint32_t)(j >> 1) & 1u;
+            const int kb = j % kPfPairs, kr = j % kPfKRing;
+            ok = soon(&s_full[b], ph) && wait(&k_full[kr], (uint32_t)(j / kPfKRing) & 1u) &&
+                 wait(&v_full[kb], (uint32_t)(j / kPfPairs) & 1u);
+            if (__any_sync(0xffffffffu, !ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t scol = trow + (b ? Tm::kS1 : Tm::kS0);
+            const int key0 = key_base + (kt0 + j) * kPfKeys;
+            if (key0 >= any_hi || key0 + kPfKeys <= any_lo) {   // none of the warp's rows sees any of it
+                const uint32_t zero[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int q = 0; q < (TWO ? 16 : 8); ++q) tmem_st_q1(scol + 8 * q, zero);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&p_full[b]);
+                continue;
+            }
+            uint32_t s[64];   // s[4i], s[4i + 1]: row a, columns 8i + 2t, + 1; s[4i + 2], s[4i + 3]: row b
+            tmem_ld_q8(scol, s);
+            tmem_ld_q8(scol + 64, s + 32);
+            tmem_ld_wait();
+            // Exponents e = S s_K k0 2^-e - m + 127 + raise - E (one FMA) against the references as they
+            // are, and their row maxima; a reference that moves is added to them afterwards, which is rare.
+            const float4* skb = reinterpret_cast<const float4*>(sk + kr * kPfKeys) + t4;   // columns 16q + (2t, 2t + 1, 8 + 2t, 9 + 2t)
+            const uint32_t dead = deadf[kr * 4] | deadf[kr * 4 + 1] | deadf[kr * 4 + 2] | deadf[kr * 4 + 3];
+            const bool clean = dead == 0u && !own_any && key0 >= all_lo && key0 + kPfKeys <= all_hi;   // warp-uniform
+            float bma = -INFINITY, bmb = -INFINITY;
+            const uint32_t* eb4 = eblkw + kb * 4;
+            const float4* svb = reinterpret_cast<const float4*>(sv + kb * kPfKeys) + t4;
+            uint32_t eb_a = max(max(eb4[0], eb4[1]), max(eb4[2], eb4[3])), eb_b = eb_a;
+            if (!OPTS && clean) {   // every key live and visible to both rows, rs 1
+                const float2 moa2 = make_float2(off_a, off_a), mob2 = make_float2(off_b, off_b);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 k4 = skb[4 * (i / 2)];
+                    const float2 k2 = (i & 1) ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
+                    const float2 ea = fma_f32x2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), k2, moa2);
+                    const float2 eb = fma_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k2, mob2);
+                    s[4 * i] = __float_as_uint(ea.x);
+                    s[4 * i + 1] = __float_as_uint(ea.y);
+                    s[4 * i + 2] = __float_as_uint(eb.x);
+                    s[4 * i + 3] = __float_as_uint(eb.y);
+                    bma = max3(bma, ea.x, ea.y);
+                    bmb = max3(bmb, eb.x, eb.y);
+                }
+            } else {
+                const float rs_a = rs[ra], rs_b = rs[rb];
+                const float da0 = pos_a - (float)key0 - (float)(2 * t4), db0 = pos_b - (float)key0 - (float)(2 * t4);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 k4 = skb[4 * (i / 2)];
+                    const float2 k2 = (i & 1) ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float kk = e ? k2.y : k2.x;
+                        const int key = key0 + 8 * i + 2 * t4 + e;
+                        float ea, eb;
+                        if constexpr (OPTS) {   // on the log2 logit
+                            ea = span_opts(__uint_as_float(s[4 * i + e]) * rs_a * kk, fabsf(da0 - (float)(8 * i + e)), sl_a, p) + off_a;
+                            eb = span_opts(__uint_as_float(s[4 * i + 2 + e]) * rs_b * kk, fabsf(db0 - (float)(8 * i + e)), sl_b, p) + off_b;
+                        } else {
+                            ea = fmaf(__uint_as_float(s[4 * i + e]) * rs_a, kk, off_a);
+                            eb = fmaf(__uint_as_float(s[4 * i + 2 + e]) * rs_b, kk, off_b);
+                        }
+                        if (!clean) {
+                            const bool live = ((deadf[kr * 4 + i / 4] >> (8 * (i % 4) + 2 * t4 + e)) & 1u) == 0u;
+                            ea = live && key >= sa.lo && key < sa.hi ? ea : -INFINITY;
+                            eb = live && key >= sb.lo && key < sb.hi ? eb : -INFINITY;
+                        }
+                        s[4 * i + e] = __float_as_uint(ea);
+                        s[4 * i + 2 + e] = __float_as_uint(eb);
+                        bma = fmaxf(bma, ea);
+                        bmb = fmaxf(bmb, eb);
+                    }
+                }
+                if (!clean) {   // the V scales of the visible keys alone
+                    uint32_t ma = 0u, mb = 0u;
+#pragma unroll 1
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 v4 = svb[4 * q];
+                        const float v[4] = {v4.x, v4.y, v4.z, v4.w};   // keys 16q + (2t, 2t + 1, 8 + 2t, 9 + 2t)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0 + 16 * q + 8 * (e >> 1) + 2 * t4 + (e & 1);
+                            const uint32_t bits = (__float_as_uint(v[e]) & 0x7FFFFFFFu) + 1u;   // the largest finite value stands for infinity
+                            if (key >= sa.lo && key < sa.hi) ma = max(ma, bits);
+                            if (key >= sb.lo && key < sb.hi) mb = max(mb, bits);
+                        }
+                    }
+#pragma unroll
+                    for (int off = 1; off < 4; off <<= 1) {
+                        ma = max(ma, __shfl_xor_sync(0xffffffffu, ma, off));
+                        mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, off));
+                    }
+                    eb_a = ma >> 23;
+                    eb_b = mb >> 23;
+                }
+            }
+            bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 1));
+            bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 1));
+            bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 2));
+            bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 2));
+            // the four threads of a row take the same decisions; a row without a reference takes the first one
+            const float eoff_a = (float)(127 + kPxRaise - (int)(E_a ? E_a : 127u)), eoff_b = (float)(127 + kPxRaise - (int)(E_b ? E_b : 127u));
+            const bool newE_a = E_a == 0u ? eb_a > 0u : eb_a > E_a + kPxLazyExp;
+            const bool newE_b = E_b == 0u ? eb_b > 0u : eb_b > E_b + kPxLazyExp;
+            const bool up_a = any_a ? bma > eoff_a + kPfLazyMax : bma > -INFINITY;
+            const bool up_b = any_b ? bmb > eoff_b + kPfLazyMax : bmb > -INFINITY;
+            if (__any_sync(0xffffffffu, up_a || up_b || newE_a || newE_b)) {
+                const float da = up_a ? eoff_a - bma : 0.0f, db = up_b ? eoff_b - bmb : 0.0f;   // old reference - new one
+                const float fm_a = up_a ? (any_a ? fast_exp2(da) : 0.0f) : 1.0f, fm_b = up_b ? (any_b ? fast_exp2(db) : 0.0f) : 1.0f;
+                any_a = any_a || up_a;
+                any_b = any_b || up_b;
+                // rebase from 2^(127 - E) to 2^(127 - eb); 0 when the jump underflows
+                auto rebase = [](uint32_t& E, uint32_t eb, float& fe, float& de) {
+                    const uint32_t Eeff = E ? E : 127u;
+                    fe = eb > Eeff + 126u ? 0.0f : __uint_as_float((127u + Eeff - eb) << 23);
+                    de = (float)((int)Eeff - (int)eb);
+                    E = eb;
+                };
+                float fe_a = 1.0f, fe_b = 1.0f, de_a = 0.0f, de_b = 0.0f;
+                if (newE_a) rebase(E_a, eb_a, fe_a, de_a);
+                if (newE_b) rebase(E_b, eb_b, fe_b, de_b);
+                const float f_a = fm_a * fe_a, f_b = fm_b * fe_b;
+                l_a *= f_a;
+                l_b *= f_b;
+                off_a += da + de_a;
+                off_b += db + de_b;
+                const float2 da2 = make_float2(da + de_a, da + de_a), db2 = make_float2(db + de_b, db + de_b);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 ea = add_f32x2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), da2);
+                    const float2 eb2 = add_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), db2);
+                    s[4 * i] = __float_as_uint(ea.x);
+                    s[4 * i + 1] = __float_as_uint(ea.y);
+                    s[4 * i + 2] = __float_as_uint(eb2.x);
+                    s[4 * i + 3] = __float_as_uint(eb2.y);
+                }
+                if (j > 0 && __any_sync(0xffffffffu, f_a != 1.0f || f_b != 1.0f)) {
+                    // O must hold P.V of the previous tile before it is rescaled
+                    ok = wait(&pv_done[(j - 1) & 1], (uint32_t)((j - 1) >> 1) & 1u);
+                    if (__any_sync(0xffffffffu, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const float2 fa2 = make_float2(f_a, f_a), fb2 = make_float2(f_b, f_b);
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 8) {
+                        uint32_t o[4];
+                        tmem_ld_q1(trow + Tm::kO + c0, o);
+                        tmem_ld_wait();
+                        const float2 oa = mul_f32x2(make_float2(__uint_as_float(o[0]), __uint_as_float(o[1])), fa2);
+                        const float2 ob = mul_f32x2(make_float2(__uint_as_float(o[2]), __uint_as_float(o[3])), fb2);
+                        o[0] = __float_as_uint(oa.x);
+                        o[1] = __float_as_uint(oa.y);
+                        o[2] = __float_as_uint(ob.x);
+                        o[3] = __float_as_uint(ob.y);
+                        tmem_st_q1(trow + Tm::kO + c0, o);
+                    }
+                    tmem_st_wait();
+                }
+            }
+            // p' = 2^e, w = p' s_V as fp16 pairs over the first 64 S columns: the pair of columns 8i + 2t, + 1
+            // goes to column 8 (i / 2) + 2t + i % 2 (the V tile holds its rows in the matching order)
+            float2 lsa = make_float2(0.0f, 0.0f), lsb = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                uint32_t pw[4], pl[4];
+                const float4 v4 = svb[4 * q];
+#pragma unroll
+                for (int i = 2 * q; i < 2 * q + 2; ++i) {
+                    const float2 v2 = (i & 1) ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y);
+                    const float2 pa = make_float2(fast_exp2(__uint_as_float(s[4 * i])), fast_exp2(__uint_as_float(s[4 * i + 1])));
+                    const float2 pb = make_float2(fast_exp2(__uint_as_float(s[4 * i + 2])), fast_exp2(__uint_as_float(s[4 * i + 3])));
+                    lsa = add_f32x2(lsa, pa);
+                    lsb = add_f32x2(lsb, pb);
+                    const float2 wa = mul_f32x2(pa, v2), wb = mul_f32x2(pb, v2);
+                    const int e = i & 1;
+                    if constexpr (TWO) {
+                        split_f16x2(wa.x, wa.y, pw[e], pl[e]);
+                        split_f16x2(wb.x, wb.y, pw[2 + e], pl[2 + e]);
+                    } else {
+                        pw[e] = pack_f16x2(wa.x, wa.y);
+                        pw[2 + e] = pack_f16x2(wb.x, wb.y);
+                    }
+                }
+                tmem_st_q1(scol + 8 * q, pw);
+                if constexpr (TWO) tmem_st_q1(scol + 64 + 8 * q, pl);
+            }
+            l_a += lsa.x + lsa.y;
+            l_b += lsb.x + lsb.y;
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&p_full[b]);
+        }
+        // ---- the output, or the split's partial: (m, l 2^(E - 127 - raise)) and O / l
+        if (ok) ok = wait(&pv_done[(nkt - 1) & 1], (uint32_t)((nkt - 1) >> 1) & 1u);
+        l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
+        l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
+        l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
+        l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
+        // a row that met only NaN (its query or the keys are not finite) shows it: no maximum tells
+        any_a = (any_a || l_a != l_a) && !none_a;
+        any_b = (any_b || l_b != l_b) && !none_b;
+        if (t4 == 0) {
+            fin[ra] = any_a && l_a != 0.0f ? 1.0f / l_a : 0.0f;
+            fin[rb] = any_b && l_b != 0.0f ? 1.0f / l_b : 0.0f;
+            if (p.splits > 1) {
+                auto partial = [&](int r, bool any, float l, float off, uint32_t E) {
+                    const int qt = qt0 + r / G;
+                    if (qt >= qcount) return;
+                    E = E ? E : 127u;   // none: only rows of zeros
+                    const float m = (float)(127 + kPxRaise - (int)E) - off, es = __uint_as_float(E << 23) * exp2i(-kPxRaise);
+                    reinterpret_cast<float2*>(p.part_ml)[((int64_t)(q0 + qt) * Hq + h * G + r % G) * p.splits + split] =
+                        any && ok ? make_float2(m, l * es) : make_float2(kNegBig, 0.0f);
+                };
+                partial(ra, any_a, l_a, off_a, E_a);
+                partial(rb, any_b, l_b, off_b, E_b);
+            }
+        }
+        __syncwarp();
+        // Two threads per row from here on, the other layout: warp w takes the 32 rows 32 (w % 4) .. and column half w / 4.
+        auto rows_meet = [&](uint64_t* bar) -> bool {
+            mbar_arrive(bar);
+            return __all_sync(0xffffffffu, wait(bar, 0));
+        };
+        const bool met = rows_meet(&epi[0]);
+        ok = __all_sync(0xffffffffu, ok) && met;
+        tc_fence_after();
+        constexpr int HD = D / 2;   // this thread's dimensions: half * HD ..
+        const int row = 32 * (warp & 3) + lane, half = warp >> 2;
+        const int qt = qt0 + row / G;
+        const bool stored = qt < qcount;
+        const int64_t orow = (int64_t)(q0 + (stored ? qt : 0)) * Hq + h * G + row % G;
+        float x[HD];
+        if (ok) {
+            uint32_t o[HD];
+#pragma unroll
+            for (int c = 0; c < HD; c += 32) tmem_ld_row32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + Tm::kO + half * HD + c, o + c);
+            tmem_ld_wait();
+            const float f = fin[row];
+#pragma unroll
+            for (int c = 0; c < HD; ++c) x[span_dim<BITS>(c)] = f == 0.0f ? 0.0f : __uint_as_float(o[c]) * f;
+        } else {
+#pragma unroll
+            for (int c = 0; c < HD; ++c) x[c] = 0.0f;
+        }
+        if (p.splits > 1) {
+            if (stored) store_values<HD>(p.part_o, DType::F32, (orow * p.splits + split) * D + half * HD, x);
+        } else {
+            if constexpr (BITS != 8) {
+                // out = c D H x: the butterflies of this half in registers, those between the halves through shared
+                // memory (the last P.V is done, so nothing reads the tiles)
+#pragma unroll
+                for (int w = 1; w < HD; w <<= 1) {
+#pragma unroll
+                    for (int i = 0; i < HD; ++i) {
+                        if (i & w) continue;
+                        const float a = x[i], c = x[i + w];
+                        x[i] = a + c;
+                        x[i + w] = a - c;
+                    }
+                }
+                float* xch = reinterpret_cast<float*>(tiles) + row;
+#pragma unroll
+                for (int i = 0; i < HD; ++i) xch[(half * HD + i) * kPfRows] = x[i];
+                ok = rows_meet(&epi[1]);
+                const float sg = half ? -1.0f : 1.0f;
+#pragma unroll
+                for (int i = 0; i < HD; ++i) {
+                    const float y = fmaf(sg, x[i], xch[((half ^ 1) * HD + i) * kPfRows]);   // half 0: x + other, half 1: other - x
+                    x[i] = ((signbits[(half * HD + i) / 32] >> ((half * HD + i) % 32)) & 1u) ? -p.c * y : p.c * y;
+                }
+            }
+            if (stored && ok) store_values<HD>(p.out, p.out_dt, orow * D + half * HD, x);
+        }
+    } else if (warp < kPxMmaWarp) {
+        fewer_registers<kPxDequantRegs>();
+        // ================================================================ conversion of key tiles
+        const int pl = (warp - kPxDequantWarp) >> 2;      // 0: K rows, 1: V rows
+        // This thread's key of every tile.  A V tile keeps its rows in the order the weights are laid out in, and V
+        // threads take their keys in an order in which eight neighbours have keys, and rows, of eight different
+        // remainders mod 8: the windows' reads and the swizzled rows' stores then hit no bank twice.
+        const int i128 = (threadIdx.x - kPfSoftmaxThreads) & 127;
+        const int k = pl ? v_key(i128) : i128;
+        const uint32_t trow = (uint32_t)(pl ? slot_of_column(k) : k);
+        constexpr int NW = (int)Ly::kRowWords;            // words of a row: codes, then the scale word
+        float k0 = p.c * p.softmax_scale * kLog2e;        // raw score -> log2 logit, with 2^-e once it is known
+        const int row_off = ((k % kBlockSize) * H + h) & 3;   // the row's first word in its window (row bytes are 4 mod 16)
+        for (int j = 0; j < nkt; ++j) {
+            const int kb = j % kPfPairs, st = j % kStages;
+            bool ok = wait(&raw_full[pl * kStages + st], (uint32_t)(j / kStages) & 1u);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const uint4* win4 = reinterpret_cast<const uint4*>(smem + Ly::kRaw + (uint32_t)(st * 2 + pl) * Ly::kPlane) + k * Ly::kChunks;
+            const uint32_t blocks = pl == 0 ? held[st] : 0u;
+            uint8_t* t = pl ? vtile(kb) : ktile(kb);
+            auto tile_free = [&]() -> bool {
+                bool f = j != 1 || wait(q_ready, 0);        // the query rows and the rotation matrix sat on pair 1
+                if (f && j >= kPfPairs) f = wait(pl ? &v_free[kb] : &k_free[kb], (uint32_t)(j / kPfPairs - 1) & 1u);
+                return __all_sync(0xffffffffu, f);
+            };
+            auto put = [&](int w, const uint32_t (&o)[4]) {   // dimensions 8w .. 8w + 7 in the tile's order
+                *reinterpret_cast<uint4*>(t + (uint32_t)(w / 8) * (kPfKeys * 128u) + swz128(trow, (uint32_t)(w % 8))) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            };
+            uint32_t scale;   // the scale word
+            if constexpr (NW > 20) {   // long rows: a chunk of 16 numbers at a time
+                ok = tile_free();
+                if (!ok) break;
+                uint4 c0 = win4[0];
+#pragma unroll
+                for (int c = 0; c < (NW - 1) / 4; ++c) {
+                    const uint4 c1 = win4[c + 1];
+                    const uint32_t u[6] = {(row_off & 2) ? c0.z : c0.x, (row_off & 2) ? c0.w : c0.y, (row_off & 2) ? c1.x : c0.z,
+                                           (row_off & 2) ? c1.y : c0.w, (row_off & 2) ? c1.z : c1.x, 0u};
+                    uint32_t w[4], o[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = (row_off & 1) ? u[e + 1] : u[e];
+                    unpack_i8(w[0], w[1], o);
+                    put(2 * c, o);
+                    unpack_i8(w[2], w[3], o);
+                    put(2 * c + 1, o);
+                    c0 = c1;
+                }
+                scale = row_off == 0 ? c0.x : row_off == 1 ? c0.y : row_off == 2 ? c0.z : c0.w;
+                mbar_arrive(&raw_free[pl * kStages + st]);
+            } else {
+                uint32_t kw[NW];
+                {
+                    uint32_t wv[Ly::kWindow];
+#pragma unroll
+                    for (int c = 0; c < (int)Ly::kChunks; ++c) {
+                        const uint4 v = win4[c];
+                        wv[4 * c] = v.x;
+                        wv[4 * c + 1] = v.y;
+                        wv[4 * c + 2] = v.z;
+                        wv[4 * c + 3] = v.w;
+                    }
+#pragma unroll
+                    for (int w = 0; w < NW + 1; ++w) wv[w] = (row_off & 2) ? wv[w + 2] : wv[w];
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) kw[w] = (row_off & 1) ? wv[w + 1] : wv[w];
+                }
+                mbar_arrive(&raw_free[pl * kStages + st]);
+                ok = tile_free();
+                if (!ok) break;
+                scale = kw[NW - 1];
+                if constexpr (BITS == 4) {
+                    const uint32_t zp = scale & 15u, zl = zp_lo_half(zp) * 0x10001u, zh = zp_hi_half(zp) * 0x10001u;
+                    scale &= 0xFFFFFFF0u;
+#pragma unroll
+                    for (int w = 0; w < NW - 1; ++w) {
+                        uint32_t o[4];
+                        unpack_word(kw[w], zl, zh, o);
+                        put(w, o);
+                    }
+                } else if constexpr (BITS == 8) {
+#pragma unroll
+                    for (int w = 0; w < (NW - 1) / 2; ++w) {
+                        uint32_t o[4];
+                        unpack_i8(kw[2 * w], kw[2 * w + 1], o);
+                        put(w, o);
+                    }
+                } else {
+#pragma unroll
+                    for (int w = 0; w < NW - 1; ++w) {
+                        uint32_t oa[4], ob[4];
+                        unpack_u2_x2(kw[w], oa, ob);
+                        put(2 * w, oa);
+                        put(2 * w + 1, ob);
+                    }
+                }
+            }
+            const float sc = BITS == 2 ? __uint_as_float(scale) * kU2Scale : __uint_as_float(scale);
+            if (pl == 0) {
+                if (j == 0) {   // the rows' prescale
+                    ok = wait(q_max, 0);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    k0 *= exp2i(-rows_exponent(*reinterpret_cast<volatile uint32_t*>(qexp)));
+                }
+                sk[(j % kPfKRing) * kPfKeys + slot_of_column(k)] = sc * k0;
+                const uint32_t nokey = __ballot_sync(0xffffffffu, ((blocks >> (k / kBlockSize)) & 1u) == 0u);   // a row of zeros is a key, of logit 0
+                if (lane == 0) deadf[(j % kPfKRing) * 4 + (warp & 3)] = nokey;
+            } else {
+                // finite, so that a weight of 0 stays one; an infinite scale shows in the exponent
+                sv[kb * kPfKeys + (int)trow] = fmaxf(fminf(sc, 3.4028234664e38f), -3.4028234664e38f);
+                const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(sc) & 0x7FFFFFFFu);   // magnitudes order like their bits
+                if (lane == 0) eblkw[kb * 4 + (warp & 3)] = (wmax >> 23) & 0xFFu;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // generic writes -> tensor core reads
+            mbar_arrive(pl ? &v_full[kb] : &k_full[j % kPfKRing]);
+        }
+    } else {
+        fewer_registers<kPxOtherRegs>();
+        if (warp == kPxLoadWarp || warp == kPxLoadWarp + 1) {
+            // ============================================================ loads of packed rows
+            // Each row's 16-byte-aligned window, keys in a block outside the cache or past the last key's block
+            // zero-filled; which blocks hold keys goes along with the K rows.  With 4 or 8 kv heads a token's rows
+            // are a multiple of 16 bytes and TMA takes a block's windows at once; with 1 or 2 they are not, and
+            // the windows are 16-byte copies, kKeys whole windows (C lanes each) a pass.
+            constexpr int C = Ly::kChunks, kKeys = 32 / C, kPasses = (kPfKeys + kKeys - 1) / kKeys;
+            const int pl = warp - kPxLoadWarp;
+            const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq + key_base / kBlockSize;
+            const int tok_stride = H * RB;
+            const int64_t blk_stride = 2 * kBlockSize * (int64_t)tok_stride;
+            const uint8_t* base = p.cache + (int64_t)pl * kBlockSize * tok_stride;
+            const int ck = lane / C, cc = lane - ck * C;   // this lane's key of a pass and its chunk
+            const bool mine = ck < kKeys;
+            // Block ids of four tiles at a time, lane l's that of tile (group) + l / 8, block l % 8 of it
+            // (-1: none, or not in the cache), loaded a group ahead.
+            const int nblocks = (key_end + kBlockSize - 1) / kBlockSize - key_base / kBlockSize;
+            auto inside = [&](int j) -> bool { return j + lane / 8 < nkt && (kt0 + j) * (kPfKeys / kBlockSize) + lane < nblocks; };
+            auto lookup = [&](int j) -> int { return inside(j) ? __ldg(table + (kt0 + j) * (kPfKeys / kBlockSize) + lane) : -1; };
+            int blk_next = lookup(0), blkv = -1;
+            uint32_t blocks = 0;
+            bool ok = true;
+            int issued = 0;
+            for (int j = 0; j < nkt && ok; ++j) {
+                const int st = j % kStages;
+                if ((j & 3) == 0) {
+                    blkv = blk_next;
+                    blk_next = lookup(j + 4);
+                    if (blkv < 0 || (int64_t)blkv >= p.num_blocks) {
+                        if (pl == 0 && h == 0 && inside(j)) count_status(p.status, 1);
+                        blkv = -1;
+                    }
+                    blocks = __ballot_sync(0xffffffffu, blkv >= 0);
+                }
+                if (j >= kStages) ok = wait(&raw_free[pl * kStages + st], (uint32_t)(j / kStages - 1) & 1u);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                const uint32_t dst = smem_u32(smem + Ly::kRaw + (uint32_t)(st * 2 + pl) * Ly::kPlane);
+                if (pl == 0 && lane == 0) held[st] = blocks >> (8 * (j & 3));   // this tile's: the low 8 bits; before the arrival below
+                if (boxes) {
+                    // one box [16 tokens][window bytes] per block; block -1 lies outside the tensor and reads as
+                    // zeros, as do a last head's bytes past its token's rows
+                    uint64_t* full = &raw_full[pl * kStages + st];
+                    const int blk = __shfl_sync(0xffffffffu, blkv, (j & 3) * 8 + (lane & 7));
+                    if (lane == 0) mbar_arrive_expect_tx(full, Ly::kPlane);
+                    __syncwarp();
+                    if (lane < kPfKeys / kBlockSize)
+                        tma_load_4d(dst + (uint32_t)lane * (kBlockSize * Ly::kWindow * 4), &cmap, (h * RB) & ~15, 0, pl, blk, full);
+                    issued = j + 1;
+                    continue;
+                }
+#pragma unroll
+                for (int t = 0; t < kPasses; ++t) {
+                    const int key = t * kKeys + ck;
+                    const int blk = __shfl_sync(0xffffffffu, blkv, (j & 3) * 8 + ((key / kBlockSize) & 7));
+                    const bool live = blk >= 0;
+                    const uint32_t row = (uint32_t)(h * RB + (key % kBlockSize) * tok_stride);
+                    const uint8_t* src = base + (int64_t)(live ? blk : 0) * blk_stride + ((row & ~15u) + 16u * (uint32_t)cc);
+                    if (mine && key < kPfKeys) cp_async16_zfill(dst + 16u * (uint32_t)(key * C + cc), src, live);
+                }
+                cp_async_arrive_noinc(&raw_full[pl * kStages + st]);
+                if (lane == 0) mbar_arrive(&raw_full[pl * kStages + st]);
+            }
+            // no copy outlives the CTA
+            cp_async_wait_all();
+            for (int j = max(0, issued - kStages); j < issued; ++j)
+                (void)mbar_wait(&raw_full[pl * kStages + j % kStages], (uint32_t)(j / kStages) & 1u);
+        } else if (warp == kPxMmaWarp) {
+            // ============================================================ the MMA issuer
+            // S of tile t (its K tile converted, its S buffer read by P.V of tile t - 2), then P.V of tile t - 1
+            // (its weights in tensor memory).  The whole warp runs the loop with uniform values and one elected
+            // lane issues, so that the descriptors sit in uniform registers.
+            constexpr uint32_t idS = idesc_f16(kPfKeys, 0), idPV = idesc_f16(D, 1);
+            const bool leader = elect_one();
+            const uint64_t kd0 = smem_desc_sw128(smem_u32(ktile(0)), 16u, 1024u), kd1 = smem_desc_sw128(smem_u32(ktile(1)), 16u, 1024u);
+            const uint64_t vd0 = smem_desc_sw128(smem_u32(vtile(0)), kPfKeys * 128u, 1024u);
+            const uint64_t vd1 = smem_desc_sw128(smem_u32(vtile(1)), kPfKeys * 128u, 1024u);
+            {
+                if (leader) {
+                    mbar_arrive_expect_tx(q_tma, Ly::kTile);
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c)
+                        tma_load_3d(ktile(1) + c * (kPfRows * 128), &qmap, 64 * c, h * G, q0 + qt0, q_tma);
+                }
+                __syncwarp();
+                if (__all_sync(0xffffffffu, mbar_wait(q_tma, 0) && wait(rot_in, 0))) {
+                    tc_fence_after();
+                    const uint32_t idR = p.q_bf16 ? idesc_bf16(D, 0) : idesc_f16(D, 0);
+                    const uint64_t rd = smem_desc_sw128(smem_u32(vtile(1)), 16u, 1024u);
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < KSTEPS; ++kk)
+                            mma_ss(tmem + Tm::kS0, kd1 + (((kk / 4) * (kPfRows * 128) + (kk % 4) * 32) >> 4),
+                                   rd + (((kk / 4) * (D * 128) + (kk % 4) * 32) >> 4), idR, kk > 0);
+                        mma_commit(rot_done);
+                    }
+                    __syncwarp();
+                }
+            }
+            auto issue_s = [&](int j) {
+                const uint32_t sd = tmem + ((j & 1) ? Tm::kS1 : Tm::kS0);
+                const uint64_t kd = (j & 1) ? kd1 : kd0;
+                if (leader) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                        for (int kk = 0; kk < KSTEPS; ++kk)
+                            mma_ts(sd, tmem + (half ? Tm::kQl : Tm::kQh) + 8u * kk,
+                                   kd + (((kk / 4) * (kPfKeys * 128) + (kk % 4) * 32) >> 4), idS, half > 0 || kk > 0);
+                    }
+                    mma_commit(&s_full[j & 1]);
+                    mma_commit(&k_free[j % kPfPairs]);
+                }
+                __syncwarp();
+            };
+            auto issue_pv = [&](int t) {
+                const uint32_t pcol = tmem + ((t & 1) ? Tm::kS1 : Tm::kS0);
+                const uint64_t vd = (t & 1) ? vd1 : vd0;
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < kPfKeys / 16; ++kk) {   // P of keys 16 kk .. 16 kk + 15 (in contraction order)
+                        mma_ts(tmem + Tm::kO, pcol + 8u * kk, vd + ((kk * 16 * 128) >> 4), idPV, t > 0 || kk > 0);
+                        if constexpr (TWO) mma_ts(tmem + Tm::kO, pcol + 64u + 8u * kk, vd + ((kk * 16 * 128) >> 4), idPV, true);
+                    }
+                    mma_commit(&pv_done[t & 1]);
+                    mma_commit(&v_free[t % kPfPairs]);
+                }
+                __syncwarp();
+            };
+            static_assert(kPfPairs == 2, "one descriptor per pair");
+            bool ok = __all_sync(0xffffffffu, wait(q_ready, 0));
+            for (int t = 0; t <= nkt && ok; ++t) {
+                if (t < nkt) {
+                    ok = soon(&k_full[t % kPfKRing], (uint32_t)(t / kPfKRing) & 1u) &&
+                         (t < 2 || soon(&pv_done[t & 1], (uint32_t)((t - 2) >> 1) & 1u));
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    tc_fence_after();
+                    issue_s(t);
+                }
+                if (t > 0) {
+                    ok = soon(&p_full[(t - 1) & 1], (uint32_t)((t - 1) >> 1) & 1u) && soon(&v_full[(t - 1) % kPfPairs], (uint32_t)((t - 1) / kPfPairs) & 1u);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    tc_fence_after();
+                    issue_pv(t - 1);
+                }
+            }
+            // every MMA issued has completed before the CTA tears tensor memory down
+            if (leader) mma_commit(flush);
+            __syncwarp();
+            (void)mbar_wait(flush, 0);
+        }
+    }
+    if (nkt == 0 && threadIdx.x < kPfRows) {   // rows that see nothing here
+        const int row = threadIdx.x, qt = qt0 + row / G;
+        if (qt < qcount) {
+            const int64_t orow = (int64_t)(q0 + qt) * Hq + h * G + row % G;
+            if (p.splits > 1) {
+                reinterpret_cast<float2*>(p.part_ml)[orow * p.splits + split] = make_float2(kNegBig, 0.0f);
+            } else {
+                const float zero[8] = {};
+                for (int i = 0; i < D; i += 8) store_values<8>(p.out, p.out_dt, orow * D + i, zero);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kPxMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
+}
+
+// Joins the splits of one row per warp: out = sum_s (l_s 2^(m_s - M)) o_s / sum_s l_s 2^(m_s - M), un-rotated.
+constexpr int kSpanCombineWarps = 4;
+
+template <int D, bool ROTATED>
+__global__ void __launch_bounds__(kSpanCombineWarps * 32) span_combine_kernel(const __grid_constant__ SpanParams p) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * kSpanCombineWarps + warp, rows = p.num_q_tokens * p.Hq;
+    const bool live = row < rows;
+    const int tok = live ? (int)(row / p.Hq) : 0;
+    float sgn[D / 32];
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) sgn[k] = ROTATED && p.signs[lane + 32 * k] < 0.0f ? -1.0f : 1.0f;
+    int b = 0, hi = p.num_seqs;   // the last sequence with qsl[b] <= tok
+    while (hi - b > 1) {
+        const int mid = (b + hi) >> 1;
+        if (__ldg(p.qsl + mid) <= tok) b = mid;
+        else hi = mid;
+    }
+    const int q0 = __ldg(p.qsl + b), q1 = __ldg(p.qsl + b + 1);
+    const bool mine = live && tok >= q0 && tok < q0 + min(q1 - q0, p.max_query_len) && q0 >= 0 && q1 <= p.num_q_tokens;
+    griddep_wait();
+    if (!mine) return;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row * p.splits;
+    // lane s holds split s (and s + 32)
+    const float2 v0 = lane < p.splits ? ml[lane] : make_float2(kNegBig, 0.0f);
+    const float2 v1 = lane + 32 < p.splits ? ml[lane + 32] : make_float2(kNegBig, 0.0f);
+    const float M = warp_max(fmaxf(v0.x, v1.x));
+    float w0 = v0.y == 0.0f ? 0.0f : v0.y * fast_exp2(v0.x - M), w1 = v1.y == 0.0f ? 0.0f : v1.y * fast_exp2(v1.x - M);
+    float total = w0 + w1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    float x[D / 32];
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) x[k] = 0.0f;
+    const float* po = p.part_o + row * p.splits * D + lane;
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+        const float w = __shfl_sync(0xffffffffu, s < 32 ? w0 : w1, s & 31) * inv;
+        if (w == 0.0f) continue;   // nothing seen: its output was not written
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) x[k] = fmaf(po[(int64_t)s * D + 32 * k], w, x[k]);
+    }
+    if constexpr (ROTATED) warp_fwht<D>(x);
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {
+        const float y = ROTATED ? x[k] * p.c * sgn[k] : x[k];
+        const int64_t i = row * D + lane + 32 * k;
+        if (p.out_dt == DType::BF16) store_elem<__nv_bfloat16>(p.out, i, y);
+        else if (p.out_dt == DType::F16) store_elem<__half>(p.out, i, y);
+        else store_elem<float>(p.out, i, y);
+    }
+}
+
+// The queries as [token][q head][D], in boxes of [128 / G tokens][G heads][64 dims] with the 128-byte swizzle.
+template <int D>
+cudaError_t span_query_map(const SpanParams& p, CUtensorMap* map) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.num_q_tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.Hq * D * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)p.G, (cuuint32_t)(kPfRows / p.G)};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    const CUresult r = enc(map, p.q_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                           const_cast<void*>(p.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// The cache as bytes [block][plane][token][heads' rows], in boxes of one block's windows of one head (4 or 8 kv
+// heads).  Block ids are int32, so a larger cache has no block past 2^31 that could be named.
+template <int D, int BITS>
+cudaError_t span_cache_map(const SpanParams& p, CUtensorMap* map) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr) return cudaErrorNotSupported;
+    using Ly = SpLayout<D, BITS>;
+    const cuuint64_t row = (cuuint64_t)p.H * Ly::kRowBytes;
+    const cuuint64_t blocks = (cuuint64_t)std::min<int64_t>(std::max<int64_t>(p.num_blocks, 1), (int64_t)1 << 31);
+    const cuuint64_t dims[4] = {row, kBlockSize, 2, blocks};
+    const cuuint64_t strides[3] = {row, row * kBlockSize, row * kBlockSize * 2};
+    const cuuint32_t box[4] = {Ly::kWindow * 4, kBlockSize, 1, 1};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(p.cache), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D, int BITS, bool OPTS, bool TWO>
+cudaError_t launch_span_t(const SpanParams& p, cudaStream_t stream) {
+    const size_t smem = SpLayout<D, BITS>::kBytes;
+    cudaError_t err = opt_in_smem<span_kernel<D, BITS, OPTS, TWO>>(smem);
+    if (err != cudaSuccess) return err;
+    // the register split waits for registers the launch did not give out if this does not hold
+    static std::atomic<int> regs{0};
+    if (regs.load(std::memory_order_acquire) == 0) {
+        cudaFuncAttributes fa;
+        err = cudaFuncGetAttributes(&fa, span_kernel<D, BITS, OPTS, TWO>);
+        if (err != cudaSuccess) return err;
+        regs.store(fa.numRegs, std::memory_order_release);
+    }
+    if (regs.load(std::memory_order_acquire) != kPxLaunchRegs) return cudaErrorInvalidKernelImage;
+    CUtensorMap qmap, cmap;
+    err = span_query_map<D>(p, &qmap);
+    if (err != cudaSuccess) return err;
+    if (p.H % 4 == 0) {
+        err = span_cache_map<D, BITS>(p, &cmap);
+        if (err != cudaSuccess) return err;
+    } else {
+        cmap = qmap;   // not used
+    }
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.tiles * (unsigned)p.H, (unsigned)p.splits, p.tiled ? 1u : (unsigned)p.num_seqs);
+    cfg.blockDim = dim3(kPxThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, span_kernel<D, BITS, OPTS, TWO>, p, qmap, cmap);
+    if (err != cudaSuccess || p.splits == 1) return err;
+    cfg.gridDim = dim3((unsigned)((p.num_q_tokens * p.Hq + kSpanCombineWarps - 1) / kSpanCombineWarps));
+    cfg.blockDim = dim3(kSpanCombineWarps * 32);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, span_combine_kernel<D, BITS != 8>, p);
+}
+
+// Every (head size, options, weights) instantiation of one cache mode.
+template <int D, int BITS>
+cudaError_t launch_span_head(const SpanParams& p, cudaStream_t s) {
+    const bool opts = p.softcap > 0.0f || p.alibi != nullptr;
+    if (p.out_dt == DType::BF16) return opts ? launch_span_t<D, BITS, true, false>(p, s) : launch_span_t<D, BITS, false, false>(p, s);
+    return opts ? launch_span_t<D, BITS, true, true>(p, s) : launch_span_t<D, BITS, false, true>(p, s);
+}
+
+}  // namespace
+}  // namespace kvi4

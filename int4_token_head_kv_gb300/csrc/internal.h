@@ -139,7 +139,16 @@ struct SpanParams {
     float softmax_scale;
     float c;                    // fp32(1 / sqrt(head_size)); 1 for INT8 rows
     float softcap;              // 0: none
+    float cap_l2, cap_in;       // softcap log2 e, 2 / softcap
+    DType out_dt;
+    int q_bf16;
+    int tiles;                  // row tiles per kv head of the grid: of the batch (tiled) or of a sequence
+    int tiled;
+    int splits;                 // of a row tile's keys among CTAs
+    float* part_o;              // [num_q_tokens][Hq][splits][head_size] partial outputs (normalised)
+    float* part_ml;             // [num_q_tokens][Hq][splits][2] their (max in log2 units, sum)
 };
+constexpr int kMaxSpanSplits = 64;
 
 // Launchers (return cudaSuccess or the launch error).
 cudaError_t launch_write(const WriteParams& p, int head_size, DType dt, cudaStream_t stream);
@@ -196,7 +205,9 @@ int prefix_splits(int64_t row_tiles, int num_kv_heads, int prefix_len);
 constexpr int kMaxPrefixSplits = 64;
 
 // Attention over key spans (bits 4, 8 or 2).
-cudaError_t launch_span(const SpanParams& p, int bits, int head_size, DType q_dt, DType out_dt, cudaStream_t stream);
+cudaError_t launch_span(const SpanParams& p, int bits, int head_size, cudaStream_t stream);
+cudaError_t launch_span_int8(const SpanParams& p, int head_size, cudaStream_t stream);
+cudaError_t launch_span_int2(const SpanParams& p, int head_size, cudaStream_t stream);
 
 int num_sms();
 
