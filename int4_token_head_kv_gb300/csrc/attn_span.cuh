@@ -15,6 +15,10 @@
 // some of them see, 128 at a time; tiles outside that range are not touched, so a document mask costs what its
 // documents hold.  With few row tiles the range is split among CTAs and span_combine_kernel joins the partials.
 // Tiles that every row of a warp sees whole take no mask; tiles that none of them sees take no arithmetic.
+// With a distance bias the tiles go from the last key to the first: the largest logits come first, and the reference
+// maxima, whose moves rescale O and stall the pipeline, settle at once (608 queries behind 8192 tokens, 32 q / 8 kv heads:
+// 181 us forwards, 132 backwards).  Without one they go forwards: a causal row's last tile is cut off, and
+// references taken from its few keys move again (107 us forwards, 121 backwards).
 #pragma once
 
 #include "attn_prefix.cuh"
@@ -61,6 +65,7 @@ struct SpLayout {
 // The INT2 centroids as the tiles hold them are 1.0002228 a and 1.0002134 b in fp16; with 1 / 1.0002181 in the scales both are
 // within 5e-6.
 constexpr float kU2Scale = 0.99978195f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 // The dimension a tile column holds.
 template <int BITS>
@@ -106,14 +111,26 @@ __device__ __forceinline__ void store_values(void* out, DType dt, int64_t at, co
     }
 }
 
-// The options on a visible key's logit x (log2 units): the cap, then the distance bias.
-__device__ __forceinline__ float span_opts(float x, float dist, float slope_l2, const SpanParams& p) {
-    if (p.softcap > 0.0f) {   // C tanh(x / C) = C - 2 C / (e^(2 x / C) + 1)
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fast_exp2(x * p.cap_in) + 1.0f));
-        x = fmaf(-2.0f * p.cap_l2, r, p.cap_l2);
-    }
-    return fmaf(-slope_l2, dist, x);
+// C tanh(x / C) + off of two logits: C - 2 C / (2^(x cap_in) + 1), cap_in = 2 / C for x and C in log2 units (C in
+// natural ones in cap_in).  The absolute error is a few 2^-24 of C.
+__device__ __forceinline__ float2 capped(float2 x, float cap_in, float cap, float2 off) {
+    const float2 y = mul_f32x2(x, make_float2(cap_in, cap_in));
+    const float2 u = add_f32x2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), make_float2(1.0f, 1.0f));
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(u.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(u.y));
+    return fma_f32x2(r, make_float2(-2.0f * cap, -2.0f * cap), add_f32x2(off, make_float2(cap, cap)));
+}
+// The same for |x| <= kCapSmall C, without the two special functions: x P((x / C)^2), P a least-squares fit of
+// tanh(y) / y that is off by 1.6e-7 at most for |y| <= 0.6.
+constexpr float kCapSmall = 0.6f;
+__device__ __forceinline__ float2 capped_small(float2 x, float inv_cap, float2 off) {
+    const float2 y = mul_f32x2(x, make_float2(inv_cap, inv_cap)), t = mul_f32x2(y, y);
+    float2 q = fma_f32x2(t, make_float2(0.01513351f, 0.01513351f), make_float2(-0.05184597f, -0.05184597f));
+    q = fma_f32x2(t, q, make_float2(0.13304033f, 0.13304033f));
+    q = fma_f32x2(t, q, make_float2(-0.33331803f, -0.33331803f));
+    q = fma_f32x2(t, q, make_float2(0.99999984f, 0.99999984f));
+    return fma_f32x2(x, q, off);
 }
 
 // Where a query row's keys are: lo <= j < hi (none: an empty span, or no row).
@@ -287,6 +304,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
     const int tiles_all = key_end > where[2] ? (key_end - key_base + kPfKeys - 1) / kPfKeys : 0;
     const int kt0 = (int)((int64_t)tiles_all * split / p.splits), kt1 = (int)((int64_t)tiles_all * (split + 1) / p.splits);
     const int nkt = kt1 - kt0;
+    auto tile_at = [&](int j) -> int { return OPTS && p.alibi != nullptr ? kt1 - 1 - j : kt0 + j; };   // the j-th tile taken
     uint8_t* tiles = smem;   // [K0][V0][K1][V1]
     auto ktile = [&](int b) { return tiles + (uint32_t)b * 2u * Ly::kTile; };
     auto vtile = [&](int b) { return tiles + (uint32_t)b * 2u * Ly::kTile + Ly::kTile; };
@@ -448,7 +466,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             }
             tc_fence_after();
             const uint32_t scol = trow + (b ? Tm::kS1 : Tm::kS0);
-            const int key0 = key_base + (kt0 + j) * kPfKeys;
+            const int key0 = key_base + tile_at(j) * kPfKeys;
             if (key0 >= any_hi || key0 + kPfKeys <= any_lo) {   // none of the warp's rows sees any of it
                 const uint32_t zero[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -487,47 +505,107 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     bmb = max3(bmb, eb.x, eb.y);
                 }
             } else {
-                const float rs_a = rs[ra], rs_b = rs[rb];
-                const float da0 = pos_a - (float)key0 - (float)(2 * t4), db0 = pos_b - (float)key0 - (float)(2 * t4);
+                // bit 2i + e of vis: the row sees the key of column 8i + 2t + e
+                uint32_t vis_a = 0xFFFFFFFFu, vis_b = 0xFFFFFFFFu;
+                if (!clean) {
+                    auto below = [&](int key) -> uint32_t {   // the columns of keys before this one
+                        const int y = max(0, min(kPfKeys, key - key0)), n = 2 * (y >> 3) + max(0, min(2, (y & 7) - 2 * t4));
+                        return n < 32 ? (1u << n) - 1u : 0xFFFFFFFFu;
+                    };
+                    vis_a = below(sa.hi) & ~below(sa.lo);
+                    vis_b = below(sb.hi) & ~below(sb.lo);
+                    if (dead != 0u) {
+                        uint32_t gone = 0u;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float4 k4 = skb[4 * (i / 2)];
-                    const float2 k2 = (i & 1) ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float kk = e ? k2.y : k2.x;
-                        const int key = key0 + 8 * i + 2 * t4 + e;
-                        float ea, eb;
-                        if constexpr (OPTS) {   // on the log2 logit
-                            ea = span_opts(__uint_as_float(s[4 * i + e]) * rs_a * kk, fabsf(da0 - (float)(8 * i + e)), sl_a, p) + off_a;
-                            eb = span_opts(__uint_as_float(s[4 * i + 2 + e]) * rs_b * kk, fabsf(db0 - (float)(8 * i + e)), sl_b, p) + off_b;
-                        } else {
-                            ea = fmaf(__uint_as_float(s[4 * i + e]) * rs_a, kk, off_a);
-                            eb = fmaf(__uint_as_float(s[4 * i + 2 + e]) * rs_b, kk, off_b);
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t d = deadf[kr * 4 + w] >> (2 * t4);
+                            gone |= ((d & 3u) | ((d >> 6) & 0xCu) | ((d >> 12) & 0x30u) | ((d >> 18) & 0xC0u)) << (8 * w);
                         }
-                        if (!clean) {
-                            const bool live = ((deadf[kr * 4 + i / 4] >> (8 * (i % 4) + 2 * t4 + e)) & 1u) == 0u;
-                            ea = live && key >= sa.lo && key < sa.hi ? ea : -INFINITY;
-                            eb = live && key >= sb.lo && key < sb.hi ? eb : -INFINITY;
-                        }
-                        s[4 * i + e] = __float_as_uint(ea);
-                        s[4 * i + 2 + e] = __float_as_uint(eb);
-                        bma = fmaxf(bma, ea);
-                        bmb = fmaxf(bmb, eb);
+                        vis_a &= ~gone;
+                        vis_b &= ~gone;
                     }
                 }
-                if (!clean) {   // the V scales of the visible keys alone
+                const float rs_a = rs[ra], rs_b = rs[rb];
+                const float2 rsa2 = make_float2(rs_a, rs_a), rsb2 = make_float2(rs_b, rs_b);
+                const float2 moa2 = make_float2(off_a, off_a), mob2 = make_float2(off_b, off_b);
+                auto at = [&](int i) -> float2 { return make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])); };
+                auto set = [&](int i, float2 x) {
+                    s[i] = __float_as_uint(x.x);
+                    s[i + 1] = __float_as_uint(x.y);
+                };
+                if (own_any) {   // (rare) rows with a prescale of their own
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        set(4 * i, mul_f32x2(at(4 * i), rsa2));
+                        set(4 * i + 2, mul_f32x2(at(4 * i + 2), rsb2));
+                    }
+                }
+                const bool cap = OPTS && p.softcap > 0.0f;
+                if (cap) {
+                    float mag = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float4 k4 = skb[4 * (i / 2)];
+                        const float2 k2 = (i & 1) ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
+                        const float2 xa = mul_f32x2(at(4 * i), k2), xb = mul_f32x2(at(4 * i + 2), k2);
+                        set(4 * i, xa);
+                        set(4 * i + 2, xb);
+                        mag = max3(mag, fabsf(xa.x), fabsf(xa.y));
+                        mag = max3(mag, fabsf(xb.x), fabsf(xb.y));
+                    }
+                    if (__all_sync(0xffffffffu, mag <= kCapSmall * p.cap_l2)) {
+                        const float inv = 0.5f * p.cap_in * kLn2;   // 1 / C in log2 units
+#pragma unroll
+                        for (int i = 0; i < 64; i += 2) set(i, capped_small(at(i), inv, (i & 2) ? mob2 : moa2));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 64; i += 2) set(i, capped(at(i), p.cap_in, p.cap_l2, (i & 2) ? mob2 : moa2));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float4 k4 = skb[4 * (i / 2)];
+                        const float2 k2 = (i & 1) ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
+                        set(4 * i, fma_f32x2(at(4 * i), k2, moa2));
+                        set(4 * i + 2, fma_f32x2(at(4 * i + 2), k2, mob2));
+                    }
+                }
+                if (OPTS && p.alibi) {
+                    const float da0 = pos_a - (float)(key0 + 2 * t4), db0 = pos_b - (float)(key0 + 2 * t4);
+                    const float2 sla2 = make_float2(-sl_a, -sl_a), slb2 = make_float2(-sl_b, -sl_b);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float c = (float)(8 * i);
+                        set(4 * i, fma_f32x2(make_float2(fabsf(da0 - c), fabsf(da0 - (c + 1.0f))), sla2, at(4 * i)));
+                        set(4 * i + 2, fma_f32x2(make_float2(fabsf(db0 - c), fabsf(db0 - (c + 1.0f))), slb2, at(4 * i + 2)));
+                    }
+                }
+                if (!clean) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if (!(vis_a & (1u << (2 * i)))) s[4 * i] = 0xFF800000u;
+                        if (!(vis_a & (2u << (2 * i)))) s[4 * i + 1] = 0xFF800000u;
+                        if (!(vis_b & (1u << (2 * i)))) s[4 * i + 2] = 0xFF800000u;
+                        if (!(vis_b & (2u << (2 * i)))) s[4 * i + 3] = 0xFF800000u;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    bma = max3(bma, __uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
+                    bmb = max3(bmb, __uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
+                }
+                // the V scales of the visible keys alone, where the tile's largest would move a reference
+                if (!clean && __any_sync(0xffffffffu, eb_a > E_a + (E_a ? kPxLazyExp : 0u) || eb_b > E_b + (E_b ? kPxLazyExp : 0u))) {
                     uint32_t ma = 0u, mb = 0u;
-#pragma unroll 1
+#pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         const float4 v4 = svb[4 * q];
                         const float v[4] = {v4.x, v4.y, v4.z, v4.w};   // keys 16q + (2t, 2t + 1, 8 + 2t, 9 + 2t)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int key = key0 + 16 * q + 8 * (e >> 1) + 2 * t4 + (e & 1);
                             const uint32_t bits = (__float_as_uint(v[e]) & 0x7FFFFFFFu) + 1u;   // the largest finite value stands for infinity
-                            if (key >= sa.lo && key < sa.hi) ma = max(ma, bits);
-                            if (key >= sb.lo && key < sb.hi) mb = max(mb, bits);
+                            ma = max(ma, vis_a & (1u << (4 * q + e)) ? bits : 0u);
+                            mb = max(mb, vis_b & (1u << (4 * q + e)) ? bits : 0u);
                         }
                     }
 #pragma unroll
@@ -589,17 +667,17 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     tc_fence_after();
                     const float2 fa2 = make_float2(f_a, f_a), fb2 = make_float2(f_b, f_b);
 #pragma unroll 1
-                    for (int c0 = 0; c0 < D; c0 += 8) {
-                        uint32_t o[4];
-                        tmem_ld_q1(trow + Tm::kO + c0, o);
+                    for (int c0 = 0; c0 < D; c0 += 32) {
+                        uint32_t o[16];
+                        tmem_ld_q4(trow + Tm::kO + c0, o);
                         tmem_ld_wait();
-                        const float2 oa = mul_f32x2(make_float2(__uint_as_float(o[0]), __uint_as_float(o[1])), fa2);
-                        const float2 ob = mul_f32x2(make_float2(__uint_as_float(o[2]), __uint_as_float(o[3])), fb2);
-                        o[0] = __float_as_uint(oa.x);
-                        o[1] = __float_as_uint(oa.y);
-                        o[2] = __float_as_uint(ob.x);
-                        o[3] = __float_as_uint(ob.y);
-                        tmem_st_q1(trow + Tm::kO + c0, o);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 oa = mul_f32x2(make_float2(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1])), fa2);
+                            const float2 ob = mul_f32x2(make_float2(__uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3])), fb2);
+                            const uint32_t w[4] = {__float_as_uint(oa.x), __float_as_uint(oa.y), __float_as_uint(ob.x), __float_as_uint(ob.y)};
+                            tmem_st_q1(trow + Tm::kO + c0 + 8 * i, w);
+                        }
                     }
                     tmem_st_wait();
                 }
@@ -850,11 +928,12 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             const uint8_t* base = p.cache + (int64_t)pl * kBlockSize * tok_stride;
             const int ck = lane / C, cc = lane - ck * C;   // this lane's key of a pass and its chunk
             const bool mine = ck < kKeys;
-            // Block ids of four tiles at a time, lane l's that of tile (group) + l / 8, block l % 8 of it
-            // (-1: none, or not in the cache), loaded a group ahead.
+            // Block ids of four tiles at a time, lane l's that of the l / 8-th, block l % 8 of it (-1: none, or not in
+            // the cache), loaded a group ahead.
             const int nblocks = (key_end + kBlockSize - 1) / kBlockSize - key_base / kBlockSize;
-            auto inside = [&](int j) -> bool { return j + lane / 8 < nkt && (kt0 + j) * (kPfKeys / kBlockSize) + lane < nblocks; };
-            auto lookup = [&](int j) -> int { return inside(j) ? __ldg(table + (kt0 + j) * (kPfKeys / kBlockSize) + lane) : -1; };
+            auto block_of = [&](int j) -> int { return tile_at(j + lane / 8) * (kPfKeys / kBlockSize) + (lane & 7); };
+            auto inside = [&](int j) -> bool { return j + lane / 8 < nkt && block_of(j) < nblocks; };
+            auto lookup = [&](int j) -> int { return inside(j) ? __ldg(table + block_of(j)) : -1; };
             int blk_next = lookup(0), blkv = -1;
             uint32_t blocks = 0;
             bool ok = true;
