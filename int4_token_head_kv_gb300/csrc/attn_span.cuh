@@ -44,8 +44,7 @@ struct SpLayout {
     static constexpr uint32_t kDeadF = kSk + kPfKRing * kPfKeys * 4;              // [kring][4] u32: positions with no key
     static constexpr uint32_t kSv = kDeadF + kPfKRing * 4 * 4;                    // [pairs][128] f32 s_V
     static constexpr uint32_t kEblk = kSv + kPfPairs * kPfKeys * 4;               // [pairs][4] per-warp largest V exponent
-    static constexpr uint32_t kQexp = kEblk + kPfPairs * 4 * 4;                   // u32: first usable row and its exponent
-    static constexpr uint32_t kWhere = kQexp + 4;                                 // i32: sequence, query tile, first key, end of the keys
+    static constexpr uint32_t kWhere = kEblk + kPfPairs * 4 * 4;                               // i32: sequence, query tile, first key, end of the keys
     static constexpr uint32_t kHeld = kWhere + 16;                                // [stages] u32: blocks of a staged tile that hold keys
     static constexpr uint32_t kScan = kHeld + kStages * 4;                        // [20] u32
     static constexpr uint32_t kRs = kScan + 20 * 4;                               // [128] f32 2^-d of each row's own prescale
@@ -53,8 +52,8 @@ struct SpLayout {
     static constexpr uint32_t kSignBits = kFin + 128 * 4;                         // [4] u32
     static constexpr uint32_t kBars = (kSignBits + 16 + 7u) & ~7u;
     // k_full[kring], k_free[pairs], v_full[pairs], v_free[pairs], pv_done[2], s_full[2], p_full[2], q_ready,
-    // flush, q_tma, rot_in, rot_done, q_max, epi[2], raw_full[plane][stages], raw_free[plane][stages]
-    static constexpr int kNumBars = kPfKRing + 3 * kPfPairs + 6 + 6 + 2 + 4 * kStages;
+    // flush, q_tma, rot_in, rot_done, epi[2], raw_full[plane][stages], raw_free[plane][stages]
+    static constexpr int kNumBars = kPfKRing + 3 * kPfPairs + 6 + 5 + 2 + 4 * kStages;
     static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr uint32_t kFlags = kTmemSlot + 4;
     static constexpr uint32_t kBytes = kFlags + 4 + 1024;                         // + alignment slack
@@ -133,13 +132,19 @@ __device__ __forceinline__ float2 capped_small(float2 x, float inv_cap, float2 o
     return fma_f32x2(x, q, off);
 }
 
+// The rows' power-of-two prescale: rotated queries of size 2^-4 .. 2^13 keep 22 bits in their fp16 halves; others take a
+// further power of two of their own, and the masked path.
+constexpr int kSpanExp = 2;
+
 // Where a query row's keys are: lo <= j < hi (none: an empty span, or no row).
 struct Span {
     int lo, hi;
 };
 
-// OPTS: the call caps its scores or has a distance bias.  TWO: the weights as fp16 high + low halves.
-template <int D, int BITS, bool OPTS, bool TWO>
+// OPTS: the call caps its scores or has a distance bias.  TWO: the weights as fp16 high + low halves.  FEW: no tile has
+// more than eight rows (single tokens); the low halves of rows 0..7, of the queries and of the weights, are then rows
+// 8..15, and half of the products do.
+template <int D, int BITS, bool OPTS, bool TWO, bool FEW>
 __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_constant__ SpanParams p, const __grid_constant__ CUtensorMap qmap,
                                                              const __grid_constant__ CUtensorMap cmap) {
     using Ly = SpLayout<D, BITS>;
@@ -151,6 +156,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
     griddep_wait();   // the previous kernel may produce any of the inputs
     if (p.splits > 1) griddep_launch_dependents();   // the combine, which waits for this grid before it reads anything
 
+    if (threadIdx.x == kPxMmaWarp * 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&qmap)) : "memory");
+    if (threadIdx.x == kPxLoadWarp * 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&cmap)) : "memory");
     const int G = p.G, Hq = p.Hq, H = p.H;
     const int BQ = kPfRows / G;
     const int h = (int)(blockIdx.x % (unsigned)H), split = (int)blockIdx.y;
@@ -229,14 +236,12 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
     uint64_t* q_tma = flush + 1;                // the CTA's query rows in shared memory (bytes)
     uint64_t* rot_in = q_tma + 1;               // the rotation matrix in shared memory (256 arrivals)
     uint64_t* rot_done = rot_in + 1;            // the rotated queries in tensor memory (commit)
-    uint64_t* q_max = rot_done + 1;             // the rows' exponent is known (256 arrivals)
-    uint64_t* epi = q_max + 1;                  // [2] the row threads meet (256 arrivals)
+    uint64_t* epi = rot_done + 1;                // [2] the row threads meet (256 arrivals)
     uint64_t* raw_full = epi + 2;               // [plane][stages] packed rows of a key tile landed (one arrival and bytes, or and 32 lanes)
     uint64_t* raw_free = raw_full + 2 * kStages;   // [plane][stages] that plane converted (128 arrivals)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kFlags);
     uint32_t* deadf = reinterpret_cast<uint32_t*>(smem + Ly::kDeadF);
-    uint32_t* qexp = reinterpret_cast<uint32_t*>(smem + Ly::kQexp);
     uint32_t* held = reinterpret_cast<uint32_t*>(smem + Ly::kHeld);
     float* fin = reinterpret_cast<float*>(smem + Ly::kFin);
 
@@ -274,8 +279,6 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         mbar_init(q_tma, 1);
         mbar_init(rot_in, kPfSoftmaxThreads);
         mbar_init(rot_done, 1);
-        mbar_init(q_max, kPfSoftmaxThreads);
-        *qexp = 0xFFFFFFFFu;
         for (int i = 0; i < 2 * kStages; ++i) {
             mbar_init(&raw_full[i], boxes ? 1 : 33);
             mbar_init(&raw_free[i], 128);
@@ -373,12 +376,12 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         const int all_lo = __reduce_max_sync(0xffffffffu, max(sa.lo, sb.lo)), all_hi = __reduce_min_sync(0xffffffffu, min(sa.hi, sb.hi));
         const int any_lo = __reduce_min_sync(0xffffffffu, min(none_a ? 0x7FFFFFFF : sa.lo, none_b ? 0x7FFFFFFF : sb.lo));
         const int any_hi = __reduce_max_sync(0xffffffffu, max(none_a ? 0 : sa.hi, none_b ? 0 : sb.hi));
-        // ---- a power-of-two prescale of the rows, then fp16 high + low halves into tensor memory, by the shared-prefix
-        // kernel's rule: one exponent serves the CTA, so that 2^-e sits in the keys' scales; a row whose largest value
-        // then lies outside [2^-2, 2^15) takes a further power of two of its own.
+        // ---- a power-of-two prescale of the rows, the same for all, so that 2^-e sits in the keys' scales, then fp16 high +
+        // low halves into tensor memory.  A row whose largest value then lies outside [2^-2, 2^15) takes a further power
+        // of two of its own.
         float* rs = reinterpret_cast<float*>(smem + Ly::kRs);   // what a row's S is multiplied with
         bool own_any = false;
-        bool ok = wait(rot_done, 0);
+        bool ok = soon(rot_done, 0);
         if (__all_sync(0xffffffffu, ok)) {
             tc_fence_after();
             float v[D / 2];   // v[4i], v[4i + 1]: row a, columns 8i + 2t, + 1; v[4i + 2], v[4i + 3]: row b
@@ -396,27 +399,18 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             mxb = max(mxb, __shfl_xor_sync(0xffffffffu, mxb, 1));
             mxa = max(mxa, __shfl_xor_sync(0xffffffffu, mxa, 2));
             mxb = max(mxb, __shfl_xor_sync(0xffffffffu, mxb, 2));
-            const int xa = (int)(mxa >> 23), xb = (int)(mxb >> 23);   // biased exponents
-            if (t4 == 0) {
-                if (!none_a && xa > 0 && xa < 255) atomicMin(qexp, (uint32_t)ra << 8 | (uint32_t)xa);
-                if (!none_b && xb > 0 && xb < 255) atomicMin(qexp, (uint32_t)rb << 8 | (uint32_t)xb);
-            }
-            __syncwarp();
-            mbar_arrive(q_max);
-            ok = __all_sync(0xffffffffu, wait(q_max, 0));
-            const int e = rows_exponent(*reinterpret_cast<volatile uint32_t*>(qexp));
-            auto own = [&](int x) -> int {   // a row's further exponent
-                const int y = x - 127 + e;
-                return x == 0 || (y >= -2 && y <= 14) ? 0 : max(-126 - e, min(127 - e, 7 - y));
+            auto own = [&](uint32_t m, bool none) -> int {   // a row's further exponent
+                const int x = (int)(m >> 23), y = x - 127 + kSpanExp;
+                return none || x == 0 || (y >= -2 && y <= 14) ? 0 : max(-126 - kSpanExp, min(127 - kSpanExp, 7 - y));
             };
-            const int da = own(xa), db = own(xb);
+            const int da = own(mxa, none_a), db = own(mxb, none_b);
             own_any = __any_sync(0xffffffffu, da != 0 || db != 0);
             if (t4 == 0) {
                 rs[ra] = exp2f((float)-da);
                 rs[rb] = exp2f((float)-db);
             }
             __syncwarp();
-            const float sca = exp2i(e + da), scb = exp2i(e + db);
+            const float sca = exp2i(kSpanExp + da), scb = exp2i(kSpanExp + db);
 #pragma unroll
             for (int q = 0; q < D / 16; ++q) {
                 uint32_t hw[4], lw[4];
@@ -425,8 +419,13 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     split_f16x2(v[4 * i] * sca, v[4 * i + 1] * sca, hw[i & 1], lw[i & 1]);
                     split_f16x2(v[4 * i + 2] * scb, v[4 * i + 3] * scb, hw[2 + (i & 1)], lw[2 + (i & 1)]);
                 }
+                if constexpr (FEW) {   // rows 8..15: the low halves of rows 0..7
+                    hw[2] = lw[0];
+                    hw[3] = lw[1];
+                } else {
+                    tmem_st_q1(trow + Tm::kQl + 8 * q, lw);
+                }
                 tmem_st_q1(trow + Tm::kQh + 8 * q, hw);
-                tmem_st_q1(trow + Tm::kQl + 8 * q, lw);
             }
             tmem_st_wait();
         } else {
@@ -470,7 +469,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             if (key0 >= any_hi || key0 + kPfKeys <= any_lo) {   // none of the warp's rows sees any of it
                 const uint32_t zero[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-                for (int q = 0; q < (TWO ? 16 : 8); ++q) tmem_st_q1(scol + 8 * q, zero);
+                for (int q = 0; q < (TWO && !FEW ? 16 : 8); ++q) tmem_st_q1(scol + 8 * q, zero);
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(&p_full[b]);
@@ -480,6 +479,14 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             tmem_ld_q8(scol, s);
             tmem_ld_q8(scol + 64, s + 32);
             tmem_ld_wait();
+            if constexpr (FEW) {   // row b holds the low halves' share of row a
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    s[4 * i] = __float_as_uint(__uint_as_float(s[4 * i]) + __uint_as_float(s[4 * i + 2]));
+                    s[4 * i + 1] = __float_as_uint(__uint_as_float(s[4 * i + 1]) + __uint_as_float(s[4 * i + 3]));
+                    s[4 * i + 2] = s[4 * i + 3] = 0u;
+                }
+            }
             // Exponents e = S s_K k0 2^-e - m + 127 + raise - E (one FMA) against the references as they
             // are, and their row maxima; a reference that moves is added to them afterwards, which is rare.
             const float4* skb = reinterpret_cast<const float4*>(sk + kr * kPfKeys) + t4;   // columns 16q + (2t, 2t + 1, 8 + 2t, 9 + 2t)
@@ -624,9 +631,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             // the four threads of a row take the same decisions; a row without a reference takes the first one
             const float eoff_a = (float)(127 + kPxRaise - (int)(E_a ? E_a : 127u)), eoff_b = (float)(127 + kPxRaise - (int)(E_b ? E_b : 127u));
             const bool newE_a = E_a == 0u ? eb_a > 0u : eb_a > E_a + kPxLazyExp;
-            const bool newE_b = E_b == 0u ? eb_b > 0u : eb_b > E_b + kPxLazyExp;
+            const bool newE_b = !FEW && (E_b == 0u ? eb_b > 0u : eb_b > E_b + kPxLazyExp);
             const bool up_a = any_a ? bma > eoff_a + kPfLazyMax : bma > -INFINITY;
-            const bool up_b = any_b ? bmb > eoff_b + kPfLazyMax : bmb > -INFINITY;
+            const bool up_b = !FEW && (any_b ? bmb > eoff_b + kPfLazyMax : bmb > -INFINITY);
             if (__any_sync(0xffffffffu, up_a || up_b || newE_a || newE_b)) {
                 const float da = up_a ? eoff_a - bma : 0.0f, db = up_b ? eoff_b - bmb : 0.0f;   // old reference - new one
                 const float fm_a = up_a ? (any_a ? fast_exp2(da) : 0.0f) : 1.0f, fm_b = up_b ? (any_b ? fast_exp2(db) : 0.0f) : 1.0f;
@@ -642,7 +649,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 float fe_a = 1.0f, fe_b = 1.0f, de_a = 0.0f, de_b = 0.0f;
                 if (newE_a) rebase(E_a, eb_a, fe_a, de_a);
                 if (newE_b) rebase(E_b, eb_b, fe_b, de_b);
-                const float f_a = fm_a * fe_a, f_b = fm_b * fe_b;
+                const float f_a = fm_a * fe_a, f_b = FEW ? f_a : fm_b * fe_b;
                 l_a *= f_a;
                 l_b *= f_b;
                 off_a += da + de_a;
@@ -685,29 +692,46 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             // p' = 2^e, w = p' s_V as fp16 pairs over the first 64 S columns: the pair of columns 8i + 2t, + 1
             // goes to column 8 (i / 2) + 2t + i % 2 (the V tile holds its rows in the matching order)
             float2 lsa = make_float2(0.0f, 0.0f), lsb = make_float2(0.0f, 0.0f);
+            if constexpr (FEW) {   // the low halves of the weights as row b
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                uint32_t pw[4], pl[4];
-                const float4 v4 = svb[4 * q];
+                for (int q = 0; q < 8; ++q) {
+                    uint32_t pw[4];
+                    const float4 v4 = svb[4 * q];
 #pragma unroll
-                for (int i = 2 * q; i < 2 * q + 2; ++i) {
-                    const float2 v2 = (i & 1) ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y);
-                    const float2 pa = make_float2(fast_exp2(__uint_as_float(s[4 * i])), fast_exp2(__uint_as_float(s[4 * i + 1])));
-                    const float2 pb = make_float2(fast_exp2(__uint_as_float(s[4 * i + 2])), fast_exp2(__uint_as_float(s[4 * i + 3])));
-                    lsa = add_f32x2(lsa, pa);
-                    lsb = add_f32x2(lsb, pb);
-                    const float2 wa = mul_f32x2(pa, v2), wb = mul_f32x2(pb, v2);
-                    const int e = i & 1;
-                    if constexpr (TWO) {
-                        split_f16x2(wa.x, wa.y, pw[e], pl[e]);
-                        split_f16x2(wb.x, wb.y, pw[2 + e], pl[2 + e]);
-                    } else {
-                        pw[e] = pack_f16x2(wa.x, wa.y);
-                        pw[2 + e] = pack_f16x2(wb.x, wb.y);
+                    for (int i = 2 * q; i < 2 * q + 2; ++i) {
+                        const float2 v2 = (i & 1) ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y);
+                        const float2 pa = make_float2(fast_exp2(__uint_as_float(s[4 * i])), fast_exp2(__uint_as_float(s[4 * i + 1])));
+                        lsa = add_f32x2(lsa, pa);
+                        const float2 wa = mul_f32x2(pa, v2);
+                        split_f16x2(wa.x, wa.y, pw[i & 1], pw[2 + (i & 1)]);
                     }
+                    tmem_st_q1(scol + 8 * q, pw);
                 }
-                tmem_st_q1(scol + 8 * q, pw);
-                if constexpr (TWO) tmem_st_q1(scol + 64 + 8 * q, pl);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    uint32_t pw[4], pl[4];
+                    const float4 v4 = svb[4 * q];
+#pragma unroll
+                    for (int i = 2 * q; i < 2 * q + 2; ++i) {
+                        const float2 v2 = (i & 1) ? make_float2(v4.z, v4.w) : make_float2(v4.x, v4.y);
+                        const float2 pa = make_float2(fast_exp2(__uint_as_float(s[4 * i])), fast_exp2(__uint_as_float(s[4 * i + 1])));
+                        const float2 pb = make_float2(fast_exp2(__uint_as_float(s[4 * i + 2])), fast_exp2(__uint_as_float(s[4 * i + 3])));
+                        lsa = add_f32x2(lsa, pa);
+                        lsb = add_f32x2(lsb, pb);
+                        const float2 wa = mul_f32x2(pa, v2), wb = mul_f32x2(pb, v2);
+                        const int e = i & 1;
+                        if constexpr (TWO) {
+                            split_f16x2(wa.x, wa.y, pw[e], pl[e]);
+                            split_f16x2(wb.x, wb.y, pw[2 + e], pl[2 + e]);
+                        } else {
+                            pw[e] = pack_f16x2(wa.x, wa.y);
+                            pw[2 + e] = pack_f16x2(wb.x, wb.y);
+                        }
+                    }
+                    tmem_st_q1(scol + 8 * q, pw);
+                    if constexpr (TWO) tmem_st_q1(scol + 64 + 8 * q, pl);
+                }
             }
             l_a += lsa.x + lsa.y;
             l_b += lsb.x + lsb.y;
@@ -762,7 +786,11 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             tmem_ld_wait();
             const float f = fin[row];
 #pragma unroll
-            for (int c = 0; c < HD; ++c) x[span_dim<BITS>(c)] = f == 0.0f ? 0.0f : __uint_as_float(o[c]) * f;
+            for (int c = 0; c < HD; ++c) {
+                float y = __uint_as_float(o[c]);
+                if (FEW) y += __shfl_down_sync(0xffffffffu, y, 8);
+                x[span_dim<BITS>(c)] = f == 0.0f ? 0.0f : y * f;
+            }
         } else {
 #pragma unroll
             for (int c = 0; c < HD; ++c) x[c] = 0.0f;
@@ -807,7 +835,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         const int k = pl ? v_key(i128) : i128;
         const uint32_t trow = (uint32_t)(pl ? slot_of_column(k) : k);
         constexpr int NW = (int)Ly::kRowWords;            // words of a row: codes, then the scale word
-        float k0 = p.c * p.softmax_scale * kLog2e;        // raw score -> log2 logit, with 2^-e once it is known
+        const float k0 = p.c * p.softmax_scale * kLog2e * exp2i(-kSpanExp);   // raw score -> log2 logit
         const int row_off = ((k % kBlockSize) * H + h) & 3;   // the row's first word in its window (row bytes are 4 mod 16)
         for (int j = 0; j < nkt; ++j) {
             const int kb = j % kPfPairs, st = j % kStages;
@@ -895,11 +923,6 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             }
             const float sc = BITS == 2 ? __uint_as_float(scale) * kU2Scale : __uint_as_float(scale);
             if (pl == 0) {
-                if (j == 0) {   // the rows' prescale
-                    ok = wait(q_max, 0);
-                    if (!__all_sync(0xffffffffu, ok)) break;
-                    k0 *= exp2i(-rows_exponent(*reinterpret_cast<volatile uint32_t*>(qexp)));
-                }
                 sk[(j % kPfKRing) * kPfKeys + slot_of_column(k)] = sc * k0;
                 const uint32_t nokey = __ballot_sync(0xffffffffu, ((blocks >> (k / kBlockSize)) & 1u) == 0u);   // a row of zeros is a key, of logit 0
                 if (lane == 0) deadf[(j % kPfKRing) * 4 + (warp & 3)] = nokey;
@@ -1018,7 +1041,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 const uint64_t kd = (j & 1) ? kd1 : kd0;
                 if (leader) {
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
+                    for (int half = 0; half < (FEW ? 1 : 2); ++half) {
 #pragma unroll
                         for (int kk = 0; kk < KSTEPS; ++kk)
                             mma_ts(sd, tmem + (half ? Tm::kQl : Tm::kQh) + 8u * kk,
@@ -1036,7 +1059,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
 #pragma unroll
                     for (int kk = 0; kk < kPfKeys / 16; ++kk) {   // P of keys 16 kk .. 16 kk + 15 (in contraction order)
                         mma_ts(tmem + Tm::kO, pcol + 8u * kk, vd + ((kk * 16 * 128) >> 4), idPV, t > 0 || kk > 0);
-                        if constexpr (TWO) mma_ts(tmem + Tm::kO, pcol + 64u + 8u * kk, vd + ((kk * 16 * 128) >> 4), idPV, true);
+                        if constexpr (TWO && !FEW) mma_ts(tmem + Tm::kO, pcol + 64u + 8u * kk, vd + ((kk * 16 * 128) >> 4), idPV, true);
                     }
                     mma_commit(&pv_done[t & 1]);
                     mma_commit(&v_free[t % kPfPairs]);
@@ -1044,7 +1067,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 __syncwarp();
             };
             static_assert(kPfPairs == 2, "one descriptor per pair");
-            bool ok = __all_sync(0xffffffffu, wait(q_ready, 0));
+            bool ok = __all_sync(0xffffffffu, soon(q_ready, 0));
             for (int t = 0; t <= nkt && ok; ++t) {
                 if (t < nkt) {
                     ok = soon(&k_full[t % kPfKRing], (uint32_t)(t / kPfKRing) & 1u) &&
@@ -1174,16 +1197,16 @@ cudaError_t span_cache_map(const SpanParams& p, CUtensorMap* map) {
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, int BITS, bool OPTS, bool TWO>
+template <int D, int BITS, bool OPTS, bool TWO, bool FEW>
 cudaError_t launch_span_t(const SpanParams& p, cudaStream_t stream) {
     const size_t smem = SpLayout<D, BITS>::kBytes;
-    cudaError_t err = opt_in_smem<span_kernel<D, BITS, OPTS, TWO>>(smem);
+    cudaError_t err = opt_in_smem<span_kernel<D, BITS, OPTS, TWO, FEW>>(smem);
     if (err != cudaSuccess) return err;
     // the register split waits for registers the launch did not give out if this does not hold
     static std::atomic<int> regs{0};
     if (regs.load(std::memory_order_acquire) == 0) {
         cudaFuncAttributes fa;
-        err = cudaFuncGetAttributes(&fa, span_kernel<D, BITS, OPTS, TWO>);
+        err = cudaFuncGetAttributes(&fa, span_kernel<D, BITS, OPTS, TWO, FEW>);
         if (err != cudaSuccess) return err;
         regs.store(fa.numRegs, std::memory_order_release);
     }
@@ -1207,7 +1230,7 @@ cudaError_t launch_span_t(const SpanParams& p, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    err = cudaLaunchKernelEx(&cfg, span_kernel<D, BITS, OPTS, TWO>, p, qmap, cmap);
+    err = cudaLaunchKernelEx(&cfg, span_kernel<D, BITS, OPTS, TWO, FEW>, p, qmap, cmap);
     if (err != cudaSuccess || p.splits == 1) return err;
     cfg.gridDim = dim3((unsigned)((p.num_q_tokens * p.Hq + kSpanCombineWarps - 1) / kSpanCombineWarps));
     cfg.blockDim = dim3(kSpanCombineWarps * 32);
@@ -1219,8 +1242,9 @@ cudaError_t launch_span_t(const SpanParams& p, cudaStream_t stream) {
 template <int D, int BITS>
 cudaError_t launch_span_head(const SpanParams& p, cudaStream_t s) {
     const bool opts = p.softcap > 0.0f || p.alibi != nullptr;
-    if (p.out_dt == DType::BF16) return opts ? launch_span_t<D, BITS, true, false>(p, s) : launch_span_t<D, BITS, false, false>(p, s);
-    return opts ? launch_span_t<D, BITS, true, true>(p, s) : launch_span_t<D, BITS, false, true>(p, s);
+    if (p.max_query_len * p.G <= 8) return opts ? launch_span_t<D, BITS, true, true, true>(p, s) : launch_span_t<D, BITS, false, true, true>(p, s);
+    if (p.out_dt == DType::BF16) return opts ? launch_span_t<D, BITS, true, false, false>(p, s) : launch_span_t<D, BITS, false, false, false>(p, s);
+    return opts ? launch_span_t<D, BITS, true, true, false>(p, s) : launch_span_t<D, BITS, false, true, false>(p, s);
 }
 
 }  // namespace
