@@ -38,7 +38,14 @@ struct SpLayout {
     static constexpr uint32_t kWindow = 4 * kChunks;
     static constexpr int kStages = kRowWords > 20 ? 2 : 4;                        // packed tiles staged ahead
     static constexpr uint32_t kTile = (D / 64) * kPfKeys * 128;
-    static constexpr uint32_t kPlane = kPfKeys * kWindow * 4;                     // one plane of a staged tile
+    // A block's rows of one head lie in boxes of 16 / m tokens, m the tokens whose rows make a multiple of 16 bytes: 1
+    // with 4 or 8 kv heads, else 4 / H.  Boxes start on 128 bytes.  m > 1 is for INT8 rows alone, whose 16-byte copies
+    // take longer than the rest of a tile (4864 queries on 4096 tokens, 2 kv heads, d 128: 222 us with them).
+    static constexpr bool kGroups = BITS == 8;
+    static constexpr uint32_t box_bytes(uint32_t m) { return (kBlockSize / m * kWindow * 4 + 127u) & ~127u; }
+    static constexpr uint32_t kLoaded = kPfKeys * kWindow * 4;                    // bytes of one plane of a tile
+    static constexpr uint32_t kPlane = kGroups ? kPfKeys / kBlockSize * 4 * box_bytes(4) : kLoaded;   // and their room
+    static_assert(!kGroups || (2 * box_bytes(2) <= 4 * box_bytes(4) && box_bytes(1) <= 4 * box_bytes(4)), "room for every grouping");
     static constexpr uint32_t kRaw = 2 * kPfPairs * kTile;
     static constexpr uint32_t kSk = kRaw + kStages * 2 * kPlane;                  // [kring][128] f32 s_K k0 2^-e
     static constexpr uint32_t kDeadF = kSk + kPfKRing * kPfKeys * 4;              // [kring][4] u32: positions with no key
@@ -161,7 +168,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
     const int G = p.G, Hq = p.Hq, H = p.H;
     const int BQ = kPfRows / G;
     const int h = (int)(blockIdx.x % (unsigned)H), split = (int)blockIdx.y;
-    const bool boxes = H % 4 == 0;   // rows of a multiple of 16 bytes: TMA loads packed rows (see the loaders)
+    const int group = H >= 4 ? 1 : 4 / H;              // tokens whose rows are a multiple of 16 bytes
+    const bool boxes = Ly::kGroups || group == 1;      // TMA loads packed rows (see the loaders)
     volatile int* where = reinterpret_cast<volatile int*>(smem + Ly::kWhere);
 
     // ---- the CTA's sequence and query tile, the last tiles (the longest causal rows) first
@@ -837,11 +845,14 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         constexpr int NW = (int)Ly::kRowWords;            // words of a row: codes, then the scale word
         const float k0 = p.c * p.softmax_scale * kLog2e * exp2i(-kSpanExp);   // raw score -> log2 logit
         const int row_off = ((k % kBlockSize) * H + h) & 3;   // the row's first word in its window (row bytes are 4 mod 16)
+        const uint32_t row_at = boxes ? (uint32_t)(k / kBlockSize * group + k % group) * Ly::box_bytes((uint32_t)group) +
+                                            (uint32_t)(k % kBlockSize / group) * Ly::kWindow * 4
+                                      : (uint32_t)k * Ly::kWindow * 4;
         for (int j = 0; j < nkt; ++j) {
             const int kb = j % kPfPairs, st = j % kStages;
             bool ok = wait(&raw_full[pl * kStages + st], (uint32_t)(j / kStages) & 1u);
             if (!__all_sync(0xffffffffu, ok)) break;
-            const uint4* win4 = reinterpret_cast<const uint4*>(smem + Ly::kRaw + (uint32_t)(st * 2 + pl) * Ly::kPlane) + k * Ly::kChunks;
+            const uint4* win4 = reinterpret_cast<const uint4*>(smem + Ly::kRaw + (uint32_t)(st * 2 + pl) * Ly::kPlane + row_at);
             const uint32_t blocks = pl == 0 ? held[st] : 0u;
             uint8_t* t = pl ? vtile(kb) : ktile(kb);
             auto tile_free = [&]() -> bool {
@@ -941,8 +952,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             // ============================================================ loads of packed rows
             // Each row's 16-byte-aligned window, keys in a block outside the cache or past the last key's block
             // zero-filled; which blocks hold keys goes along with the K rows.  With 4 or 8 kv heads a token's rows
-            // are a multiple of 16 bytes and TMA takes a block's windows at once; with 1 or 2 they are not, and
-            // the windows are 16-byte copies, kKeys whole windows (C lanes each) a pass.
+            // are a multiple of 16 bytes and TMA takes a block's windows at once; with 1 or 2 the rows of 4 or 2 tokens
+            // are, and INT8 rows take as many boxes.  INT4 and INT2 windows are then 16-byte copies, kKeys whole
+            // windows (C lanes each) a pass.
             constexpr int C = Ly::kChunks, kKeys = 32 / C, kPasses = (kPfKeys + kKeys - 1) / kKeys;
             const int pl = warp - kPxLoadWarp;
             const int32_t* table = p.block_tables + (int64_t)seq * p.max_blocks_per_seq + key_base / kBlockSize;
@@ -977,28 +989,31 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 const uint32_t dst = smem_u32(smem + Ly::kRaw + (uint32_t)(st * 2 + pl) * Ly::kPlane);
                 if (pl == 0 && lane == 0) held[st] = blocks >> (8 * (j & 3));   // this tile's: the low 8 bits; before the arrival below
                 if (boxes) {
-                    // one box [16 tokens][window bytes] per block; block -1 lies outside the tensor and reads as
-                    // zeros, as do a last head's bytes past its token's rows
+                    // boxes [16 / group tokens][window bytes]; block -1 lies outside the tensor and reads as zeros, as do
+                    // a last head's bytes past its tokens' rows
                     uint64_t* full = &raw_full[pl * kStages + st];
-                    const int blk = __shfl_sync(0xffffffffu, blkv, (j & 3) * 8 + (lane & 7));
-                    if (lane == 0) mbar_arrive_expect_tx(full, Ly::kPlane);
+                    const int blk = __shfl_sync(0xffffffffu, blkv, (j & 3) * 8 + (lane / group & 7));
+                    if (lane == 0) mbar_arrive_expect_tx(full, Ly::kLoaded);
                     __syncwarp();
-                    if (lane < kPfKeys / kBlockSize)
-                        tma_load_4d(dst + (uint32_t)lane * (kBlockSize * Ly::kWindow * 4), &cmap, (h * RB) & ~15, 0, pl, blk, full);
+                    if (lane < kPfKeys / kBlockSize * group)
+                        tma_load_4d(dst + (uint32_t)lane * Ly::box_bytes((uint32_t)group), &cmap, (lane % group * tok_stride + h * RB) & ~15, 0, pl,
+                                    blk, full);
                     issued = j + 1;
                     continue;
                 }
+                if constexpr (!Ly::kGroups) {
 #pragma unroll
-                for (int t = 0; t < kPasses; ++t) {
-                    const int key = t * kKeys + ck;
-                    const int blk = __shfl_sync(0xffffffffu, blkv, (j & 3) * 8 + ((key / kBlockSize) & 7));
-                    const bool live = blk >= 0;
-                    const uint32_t row = (uint32_t)(h * RB + (key % kBlockSize) * tok_stride);
-                    const uint8_t* src = base + (int64_t)(live ? blk : 0) * blk_stride + ((row & ~15u) + 16u * (uint32_t)cc);
-                    if (mine && key < kPfKeys) cp_async16_zfill(dst + 16u * (uint32_t)(key * C + cc), src, live);
+                    for (int t = 0; t < kPasses; ++t) {
+                        const int key = t * kKeys + ck;
+                        const int blk = __shfl_sync(0xffffffffu, blkv, (j & 3) * 8 + ((key / kBlockSize) & 7));
+                        const bool live = blk >= 0;
+                        const uint32_t row = (uint32_t)(h * RB + (key % kBlockSize) * tok_stride);
+                        const uint8_t* src = base + (int64_t)(live ? blk : 0) * blk_stride + ((row & ~15u) + 16u * (uint32_t)cc);
+                        if (mine && key < kPfKeys) cp_async16_zfill(dst + 16u * (uint32_t)(key * C + cc), src, live);
+                    }
+                    cp_async_arrive_noinc(&raw_full[pl * kStages + st]);
+                    if (lane == 0) mbar_arrive(&raw_full[pl * kStages + st]);
                 }
-                cp_async_arrive_noinc(&raw_full[pl * kStages + st]);
-                if (lane == 0) mbar_arrive(&raw_full[pl * kStages + st]);
             }
             // no copy outlives the CTA
             cp_async_wait_all();
@@ -1178,18 +1193,18 @@ cudaError_t span_query_map(const SpanParams& p, CUtensorMap* map) {
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// The cache as bytes [block][plane][token][heads' rows], in boxes of one block's windows of one head (4 or 8 kv
-// heads).  Block ids are int32, so a larger cache has no block past 2^31 that could be named.
+// The cache as bytes [block][plane][16 / group tokens][rows of group tokens], in boxes of a block's windows of one head
+// (of every group-th token).  Block ids are int32, so a larger cache has no block past 2^31 that could be named.
 template <int D, int BITS>
 cudaError_t span_cache_map(const SpanParams& p, CUtensorMap* map) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (enc == nullptr) return cudaErrorNotSupported;
     using Ly = SpLayout<D, BITS>;
-    const cuuint64_t row = (cuuint64_t)p.H * Ly::kRowBytes;
+    const cuuint64_t group = p.H >= 4 ? 1 : 4 / p.H, row = group * (cuuint64_t)p.H * Ly::kRowBytes, rows = kBlockSize / group;
     const cuuint64_t blocks = (cuuint64_t)std::min<int64_t>(std::max<int64_t>(p.num_blocks, 1), (int64_t)1 << 31);
-    const cuuint64_t dims[4] = {row, kBlockSize, 2, blocks};
-    const cuuint64_t strides[3] = {row, row * kBlockSize, row * kBlockSize * 2};
-    const cuuint32_t box[4] = {Ly::kWindow * 4, kBlockSize, 1, 1};
+    const cuuint64_t dims[4] = {row, rows, 2, blocks};
+    const cuuint64_t strides[3] = {row, row * rows, row * rows * 2};
+    const cuuint32_t box[4] = {Ly::kWindow * 4, (cuuint32_t)rows, 1, 1};
     const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
     const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(p.cache), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
@@ -1214,7 +1229,7 @@ cudaError_t launch_span_t(const SpanParams& p, cudaStream_t stream) {
     CUtensorMap qmap, cmap;
     err = span_query_map<D>(p, &qmap);
     if (err != cudaSuccess) return err;
-    if (p.H % 4 == 0) {
+    if (p.H >= 4 || SpLayout<D, BITS>::kGroups) {
         err = span_cache_map<D, BITS>(p, &cmap);
         if (err != cudaSuccess) return err;
     } else {
