@@ -200,6 +200,7 @@ kv_int4_status rope_write_impl(int bits, const void* q, int64_t q_token_stride, 
     uint32_t axis_bits[4] = {};
     if (num_axes > 0) {
         if (!pair_axis) return KV_INT4_EINVAL;
+        if (max_position > (int64_t)1 << 32) return KV_INT4_EUNSUPPORTED;   // 32-bit table rows
         for (int i = 0; i < rot_dim / 2; ++i) {
             if (pair_axis[i] >= num_axes) return KV_INT4_EINVAL;
             axis_bits[i / 16] |= (uint32_t)pair_axis[i] << (2 * (i % 16));

@@ -78,10 +78,16 @@ struct RopeTable {
 // The axis of pair i.
 __device__ __forceinline__ int axis_of(const RopeWriteParams& p, int i) { return (int)((p.pair_axis[i >> 4] >> (2 * (i & 15))) & 3u); }
 
-// The table row of token tok on one axis (row 0 for a position outside the table: its rows are not stored).
-__device__ __forceinline__ const float* axis_row(const RopeWriteParams& p, uint32_t tok, int axis) {
-    const int64_t pos = __ldg(p.positions + (int64_t)axis * p.w.num_tokens + tok);
-    return p.cos_sin + (pos >= 0 && pos < p.max_position ? pos : 0) * p.rot;
+// Positions of eight tokens at once: lane 4t + a holds that of token tok0 + t on axis a (0 past the last token or axis).
+__device__ __forceinline__ int64_t axis_positions(const RopeWriteParams& p, uint32_t tok0) {
+    const uint32_t tok = tok0 + ((threadIdx.x & 31) >> 2), a = threadIdx.x & 3;
+    return (int)a < p.axes && tok < (uint32_t)p.w.num_tokens ? __ldg(p.positions + (int64_t)a * p.w.num_tokens + tok) : 0;
+}
+
+// A position's table row (row 0 for one outside the table: its token is not stored).  The host refuses tables of more
+// than 2^32 rows.
+__device__ __forceinline__ uint32_t table_row(const RopeWriteParams& p, int64_t pos) {
+    return pos >= 0 && pos < p.max_position ? (uint32_t)pos : 0u;
 }
 
 // One position that stands for a token's positions on all axes: in the table when all of them are, negative when
@@ -96,31 +102,43 @@ __device__ __forceinline__ int64_t joint_position(const RopeWriteParams& p, uint
     return inside ? 0 : negative ? -1 : p.max_position;
 }
 
-// The lane's part of token tok's table rows.
+// The lane's part of a token's table rows: rows holds them as axis_positions does, the token is its t-th.  All lanes
+// call it.
 template <int D, bool INTER>
-__device__ __forceinline__ RopeTable load_axes(const RopeWriteParams& p, uint32_t tok) {
+__device__ __forceinline__ RopeTable load_axes(const RopeWriteParams& p, uint32_t rows, uint32_t t) {
     constexpr int Q = D / 4;
     const int k = (threadIdx.x & 31) % Q, rot = p.rot, hw = rot >> 2, half = rot >> 1;
-    RopeTable t;
+    auto row = [&](int pair) -> const float* {
+        return p.cos_sin + (int64_t)__shfl_sync(0xffffffffu, rows, 4 * t + axis_of(p, pair)) * rot;
+    };
+    RopeTable r;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int m = k + i * Q;
-        t.c[i] = make_float2(1.0f, 1.0f);
-        t.s[i] = make_float2(0.0f, 0.0f);
-        if (2 * m < rot) {
-            if constexpr (INTER) {
-                const float* cs = axis_row(p, tok, axis_of(p, m));
-                t.c[i].x = __ldg(cs + m);
-                t.s[i].x = __ldg(cs + half + m);
-            } else {
-                const int j = 2 * (m < hw ? m : m - hw);   // pairs j and j + 1
-                const float *ca = axis_row(p, tok, axis_of(p, j)), *cb = axis_row(p, tok, axis_of(p, j + 1));
-                t.c[i] = make_float2(__ldg(ca + j), __ldg(cb + j + 1));
-                t.s[i] = make_float2(__ldg(ca + half + j), __ldg(cb + half + j + 1));
+        const bool turned = 2 * m < rot;
+        r.c[i] = make_float2(1.0f, 1.0f);
+        r.s[i] = make_float2(0.0f, 0.0f);
+        if constexpr (INTER) {
+            const float* cs = row(turned ? m : 0);
+            if (turned) {
+                r.c[i].x = __ldg(cs + m);
+                r.s[i].x = __ldg(cs + half + m);
+            }
+        } else {
+            const int j = turned ? 2 * (m < hw ? m : m - hw) : 0;   // pairs j and j + 1
+            const float *ca = row(j), *cb = row(j + 1);
+            if (turned) {
+                if (ca == cb) {
+                    r.c[i] = __ldg(reinterpret_cast<const float2*>(ca + j));
+                    r.s[i] = __ldg(reinterpret_cast<const float2*>(ca + half + j));
+                } else {
+                    r.c[i] = make_float2(__ldg(ca + j), __ldg(cb + j + 1));
+                    r.s[i] = make_float2(__ldg(ca + half + j), __ldg(cb + half + j + 1));
+                }
             }
         }
     }
-    return t;
+    return r;
 }
 
 // The lane's part of the table row of position pos (row 0 for one outside the table: its rows are not stored).
@@ -151,11 +169,12 @@ __device__ __forceinline__ RopeTable load_table(const RopeWriteParams& p, int64_
 
 // Rotate rows r0 .. r0 + nrows - 1 of the tile (vectors v0 + r of the key plane, staged at in + r * ROWPAD)
 // into stage rows 0 .. nrows - 1, nrows <= kRopeRows.  tab: the table row of the first row's token; pos: lane
-// r * TPV holds the position of row r's token (unused with AXES).  fmask: per word m the signs to apply (bit 15: element 2m, bit
+// r * TPV holds the position of row r's token (with AXES: rows holds the table rows of the tokens from tok0 on, as
+// axis_positions does).  fmask: per word m the signs to apply (bit 15: element 2m, bit
 // 31: 2m + 1), or nullptr for none.  All lanes call it.
 template <int D, typename T, bool INTER, bool AXES, int ROWPAD, int TPV>
 __device__ __forceinline__ void rope_rows(const RopeWriteParams& p, const uint8_t* in, float* stage, uint32_t v0, int r0,
-                                          int nrows, RopeTable tab, int64_t pos, const uint32_t* fmask) {
+                                          int nrows, RopeTable tab, int64_t pos, uint32_t rows, uint32_t tok0, const uint32_t* fmask) {
     constexpr int Q = D / 4, kStep = 32 / Q;   // rows at once: a lane owns words k and k + Q of every kStep-th row
     const int lane = threadIdx.x & 31, k = lane % Q, sub = lane / Q;
     const uint32_t H = (uint32_t)p.w.H;
@@ -172,13 +191,19 @@ __device__ __forceinline__ void rope_rows(const RopeWriteParams& p, const uint8_
     const uint32_t* src = reinterpret_cast<const uint32_t*>(in + r0 * ROWPAD);
     constexpr int kRowWords = ROWPAD / 4;
     int r = 0, r_end = (int)(H - (v0 + r0) % H);   // rows of the first token
+    uint32_t tok = AXES ? (v0 + (uint32_t)r0) / H : 0u;
     while (r < nrows) {
         // a token's rows r .. r_end - 1, the next token's table row on its way
         if (r_end > nrows) r_end = nrows;
         RopeTable next = tab;
         if (r_end < nrows) {
-            if constexpr (AXES) next = load_axes<D, INTER>(p, (v0 + (uint32_t)(r0 + r_end)) / H);
-            else next = load_table<D, INTER>(p, __shfl_sync(0xffffffffu, pos, (r0 + r_end) * TPV));
+            if constexpr (AXES) {
+                if (++tok >= tok0 + 8) {   // (one or two kv heads)
+                    tok0 = tok;
+                    rows = table_row(p, axis_positions(p, tok));
+                }
+                next = load_axes<D, INTER>(p, rows, tok - tok0);
+            } else next = load_table<D, INTER>(p, __shfl_sync(0xffffffffu, pos, (r0 + r_end) * TPV));
         }
         float2 c[2], s[2];
 #pragma unroll
@@ -275,8 +300,10 @@ __device__ __forceinline__ void rotate_queries(const RopeWriteParams& p, uint32_
     using Qi = QueryItem<D>;
     const int lane = threadIdx.x & 31, c = lane % Qi::kSlots, r = lane / Qi::kSlots;
     const uint32_t tok = item / groups, head0 = (item - tok * groups) * Qi::kRows;
-    const int64_t pos = AXES ? joint_position(p, tok) : __ldg(p.positions + tok);
-    if (pos < 0 || pos >= p.max_position) return;   // the cache tiles count it
+    // (with AXES the lanes hold the token's positions, 0 past the last axis)
+    const int64_t pos = AXES ? (lane < p.axes ? __ldg(p.positions + (int64_t)lane * p.w.num_tokens + tok) : 0) : __ldg(p.positions + tok);
+    const bool out = pos < 0 || pos >= p.max_position;
+    if (AXES ? __any_sync(0xffffffffu, out) : out) return;   // the cache tiles count it
     const int rot = p.rot;
     const bool turned = 16 * c < rot;
     // this lane's chunks of eight elements: a rotated lane holds the pairs 8c .. 8c + 7
@@ -303,13 +330,30 @@ __device__ __forceinline__ void rotate_queries(const RopeWriteParams& p, uint32_
         }
     }
     float2 cv[4], sv[4];
-    if (AXES && turned) {
+    if constexpr (AXES) {
+        // the axes of this lane's eight pairs: mostly the same, or at least those of the warp's lanes one each
+        const uint32_t ax = (p.pair_axis[(c >> 1) & 3] >> (16 * (c & 1))) & (turned ? 0xFFFFu : 0u);
+        if (__all_sync(0xffffffffu, ax == (ax & 3u) * 0x5555u)) {
+            const float* cs = p.cos_sin + (int64_t)__shfl_sync(0xffffffffu, (uint32_t)pos, ax & 3u) * rot;
+            if (turned) {
+                const float4 c0 = ldg4(cs + 8 * c), c1 = ldg4(cs + 8 * c + 4);
+                const float4 s0 = ldg4(cs + (rot >> 1) + 8 * c), s1 = ldg4(cs + (rot >> 1) + 8 * c + 4);
+                cv[0] = make_float2(c0.x, c0.y), cv[1] = make_float2(c0.z, c0.w);
+                cv[2] = make_float2(c1.x, c1.y), cv[3] = make_float2(c1.z, c1.w);
+                sv[0] = make_float2(s0.x, s0.y), sv[1] = make_float2(s0.z, s0.w);
+                sv[2] = make_float2(s1.x, s1.y), sv[3] = make_float2(s1.z, s1.w);
+            }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int j = 8 * c + 2 * e, half = rot >> 1;   // pairs j and j + 1
-            const float *ra = axis_row(p, tok, axis_of(p, j)), *rb = axis_row(p, tok, axis_of(p, j + 1));
-            cv[e] = make_float2(__ldg(ra + j), __ldg(rb + j + 1));
-            sv[e] = make_float2(__ldg(ra + half + j), __ldg(rb + half + j + 1));
+            for (int e = 0; e < 4; ++e) {
+                const int j = 8 * c + 2 * e, half = rot >> 1;   // pairs j and j + 1
+                const float* ra = p.cos_sin + (int64_t)__shfl_sync(0xffffffffu, (uint32_t)pos, (ax >> (4 * e)) & 3u) * rot;
+                const float* rb = p.cos_sin + (int64_t)__shfl_sync(0xffffffffu, (uint32_t)pos, (ax >> (4 * e + 2)) & 3u) * rot;
+                if (turned) {
+                    cv[e] = make_float2(__ldg(ra + j), __ldg(rb + j + 1));
+                    sv[e] = make_float2(__ldg(ra + half + j), __ldg(rb + half + j + 1));
+                }
+            }
         }
     } else if (turned) {
         const float* cs = p.cos_sin + pos * rot;
@@ -457,14 +501,21 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
         const uint32_t v = tile * TV + vl;
         uint32_t tok, h, pl;
         split(v < nvec ? v : tile * TV, tok, h, pl);
-        if constexpr (AXES) pos = joint_position(p, tok);
-        else pos = __ldg(p.positions + tok);
+        if constexpr (AXES) {
+            uint32_t tok0;
+            split(tile * TV, tok0, h, pl);
+            pos = axis_positions(p, tok0);   // of the tile's first eight tokens (of the plane it begins in)
+        } else pos = __ldg(p.positions + tok);
         slot = __ldg(p.w.slots + tok);
     };
-    // the lane's table entries of vector v of the key plane; pos: lane src holds its token's position
-    auto table_of = [&](uint32_t v, int64_t pos, int src) -> RopeTable {
-        if constexpr (AXES) return load_axes<D, INTER>(p, v / H);
-        else return load_table<D, INTER>(p, __shfl_sync(0xffffffffu, pos, src));
+    // The lane's table entries of vector v of the key plane; pos: lane src holds its token's position (with AXES: rows and
+    // tok0 as rope_rows takes them).
+    auto table_of = [&](uint32_t v, int64_t pos, int src, uint32_t rows, uint32_t tok0) -> RopeTable {
+        if constexpr (AXES) {
+            const uint32_t tok = v / H;
+            if (tok >= tok0 + 8) return load_axes<D, INTER>(p, table_row(p, axis_positions(p, tok)), 0);
+            return load_axes<D, INTER>(p, rows, tok - tok0);
+        } else return load_table<D, INTER>(p, __shfl_sync(0xffffffffu, pos, src));
     };
     int64_t pos_next = 0, slot_next = 0;
     if (my_tiles > 0) {
@@ -472,12 +523,25 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
         indices(tile, pos_next, slot_next);
     }
     for (; it < my_tiles; tile += nwarps, ++it) {
-        const int64_t pos = pos_next, slot = slot_next;
+        int64_t pos = pos_next;
+        const int64_t slot = slot_next;
         const uint32_t v0 = tile * TV, v = v0 + vl;
         const bool live = v < nvec;
+        uint32_t rows = 0, tok0 = 0;
+        if constexpr (AXES) {   // the table rows of the tile's first tokens, and what stands for this vector's positions
+            uint32_t tok, h, pl;
+            split(v0, tok0, h, pl);
+            split(live ? v : v0, tok, h, pl);
+            const bool none = (lane & 3) >= p.axes;
+            const uint32_t in = __ballot_sync(0xffffffffu, none || (pos >= 0 && pos < p.max_position));
+            const uint32_t neg = __ballot_sync(0xffffffffu, none || pos < 0);
+            rows = table_row(p, pos);
+            const uint32_t t = tok - tok0;
+            pos = t < 8u ? (((in >> (4 * t)) & 15u) == 15u ? 0 : ((neg >> (4 * t)) & 15u) == 15u ? -1 : p.max_position) : joint_position(p, tok);
+        }
         const int keys = v0 < nplane ? (int)min((uint32_t)TV, nplane - v0) : 0;   // key rows of the tile, its first ones
         RopeTable tab = {};
-        if (keys > 0) tab = table_of(v0, pos, 0);
+        if (keys > 0) tab = table_of(v0, pos, 0, rows, tok0);
         // this tile's share of the query items
         const uint32_t until = (uint32_t)((uint64_t)my_items * (it + 1) / my_tiles);
         for (; items_done < until; ++items_done, item += nwarps) rotate_queries<D, T, INTER, AXES>(p, item, groups);
@@ -500,8 +564,8 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
         if constexpr (INT8) {
             float u[D];
             for (int r0 = 0; r0 < keys; r0 += kRopeRows) {
-                if (r0 > 0) tab = table_of(v0 + (uint32_t)r0, pos, r0 * TPV);
-                rope_rows<D, T, INTER, AXES, Sm::kRowPad, TPV>(p, in, stage, v0, r0, min(kRopeRows, keys - r0), tab, pos, nullptr);
+                if (r0 > 0) tab = table_of(v0 + (uint32_t)r0, pos, r0 * TPV, rows, tok0);
+                rope_rows<D, T, INTER, AXES, Sm::kRowPad, TPV>(p, in, stage, v0, r0, min(kRopeRows, keys - r0), tab, pos, rows, tok0, nullptr);
                 __syncwarp();
                 if (row >= r0 && row < min(r0 + kRopeRows, keys)) {
 #pragma unroll
@@ -526,7 +590,7 @@ __global__ void __launch_bounds__(kWriteThreads, kRopeBlocks<BITS>)
             // every lane runs the encoder (it exchanges values within the lane pair)
             float2 P[D / 4];
             if (keys > 0) {
-                rope_rows<D, T, INTER, AXES, Sm::kRowPad, TPV>(p, in, stage, v0, 0, keys, tab, pos, sgn.xmask[0]);
+                rope_rows<D, T, INTER, AXES, Sm::kRowPad, TPV>(p, in, stage, v0, 0, keys, tab, pos, rows, tok0, sgn.xmask[0]);
                 __syncwarp();
             }
             if (row < keys) form_staged_half<D>(stage + row * kRopeRow<D>, part, P);
