@@ -270,6 +270,13 @@ def _current(stream, tensor: torch.Tensor):
     return torch.cuda.stream(stream)
 
 
+def _checked(t, name: str, dtypes):
+    """_cuda for the serving calls: the tests alone while nothing is wrong."""
+    if type(t) is torch.Tensor and t.dtype in dtypes and t.is_cuda and t.is_contiguous():
+        return t
+    return _cuda(t, name, dtypes)
+
+
 def _call(fn: str, tensors, tail, *args) -> None:
     """Call the library's ``fn`` with ``args``, the current stream and ``tail`` (a tuple) on the device that
     all ``tensors`` (None entries skipped) are on."""
@@ -330,16 +337,16 @@ def _rope_write(fn, bits, query, key, value, positions, cos_sin, slot_mapping, r
     kshape, kst = _token_rows(key, "key", _HALF_TYPES)
     dtype = key.dtype
     vshape, vst = _token_rows(value, "value", (dtype,))
-    _cuda(positions, "positions", _I64)
-    _cuda(cos_sin, "cos_sin", _F32)
-    _cuda(slot_mapping, "slot_mapping", _I64)
-    _cuda(kv_cache, "kv_cache", _U8)
+    _checked(positions, "positions", _I64)
+    _checked(cos_sin, "cos_sin", _F32)
+    _checked(slot_mapping, "slot_mapping", _I64)
+    _checked(kv_cache, "kv_cache", _U8)
     if vshape != kshape:
         raise ValueError("key and value must both be [num_tokens, num_kv_heads, head_size]")
     T, H, d = kshape
     signs = ()
     if bits != 8:
-        _cuda(rht_signs, "rht_signs", _F32)
+        _checked(rht_signs, "rht_signs", _F32)
         if rht_signs.shape != (d,):
             raise ValueError("rht_signs must be [head_size]")
         signs = (rht_signs.data_ptr(),)
@@ -445,8 +452,8 @@ def _read(fn, bits, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out
     if stream is not None:
         with _current(stream, kv_cache):
             return _read(fn, bits, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out, None)
-    _cuda(kv_cache, "kv_cache", _U8)
-    _cuda(slot_mapping, "slot_mapping", _I64)
+    _checked(kv_cache, "kv_cache", _U8)
+    _checked(slot_mapping, "slot_mapping", _I64)
     sshape, cshape = slot_mapping.shape, kv_cache.shape
     if len(sshape) != 1:
         raise ValueError("slot_mapping must be [num_tokens]")
@@ -456,7 +463,7 @@ def _read(fn, bits, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out
     T, H = sshape[0], cshape[3]
     signs = ()
     if bits != 8:
-        _cuda(rht_signs, "rht_signs", _F32)
+        _checked(rht_signs, "rht_signs", _F32)
         if rht_signs.shape != (d,):
             raise ValueError("rht_signs must be [head_size]")
         signs = (rht_signs.data_ptr(),)
@@ -466,11 +473,11 @@ def _read(fn, bits, kv_cache, slot_mapping, rht_signs, dtype, key_out, value_out
             raise ValueError(f"dtype {dtype}, expected one of {tuple(_DTYPES)}")
         key_out = torch.empty(shape, dtype=dtype, device=kv_cache.device)
     else:
-        _cuda(key_out, "key_out", tuple(_DTYPES))
+        _checked(key_out, "key_out", tuple(_DTYPES))
     if value_out is None:
         value_out = torch.empty(shape, dtype=key_out.dtype, device=kv_cache.device)
     else:
-        _cuda(value_out, "value_out", (key_out.dtype,))
+        _checked(value_out, "value_out", (key_out.dtype,))
     if key_out.shape != shape or value_out.shape != shape:
         raise ValueError(f"key_out and value_out must be [num_tokens, {H}, {d}]")
     _call(fn, (kv_cache, slot_mapping, rht_signs, key_out, value_out), (), kv_cache.data_ptr(), cshape[0],
@@ -765,6 +772,13 @@ def kv_int4_span_workspace_bytes(num_q_tokens: int, num_q_heads: int, num_kv_hea
                                                    max_query_len, max_seq_len))
 
 
+@functools.lru_cache(maxsize=4096)
+def _span_workspace(device: int, *sizes) -> int:
+    """The workspace size, which depends on the device's SMs; one step's layers ask for the same sizes."""
+    with torch.cuda.device(device):
+        return int(load().kv_int4_span_workspace_bytes(*sizes))
+
+
 def _span_attention(fn, bits, query, kv_cache, block_tables, seq_lens, query_start_loc, softmax_scale, rht_signs,
                     max_query_len, max_seq_len, key_begin, key_end, softcap, alibi_slopes, out, out_dtype, workspace, stream):
     if stream is not None:
@@ -772,11 +786,11 @@ def _span_attention(fn, bits, query, kv_cache, block_tables, seq_lens, query_sta
             return _span_attention(fn, bits, query, kv_cache, block_tables, seq_lens, query_start_loc, softmax_scale,
                                    rht_signs, max_query_len, max_seq_len, key_begin, key_end, softcap, alibi_slopes, out,
                                    out_dtype, workspace, None)
-    _cuda(query, "query", _HALF_TYPES)
-    _cuda(kv_cache, "kv_cache", _U8)
-    _cuda(block_tables, "block_tables", _I32)
-    _cuda(seq_lens, "seq_lens", _I32)
-    _cuda(query_start_loc, "query_start_loc", _I32)
+    _checked(query, "query", _HALF_TYPES)
+    _checked(kv_cache, "kv_cache", _U8)
+    _checked(block_tables, "block_tables", _I32)
+    _checked(seq_lens, "seq_lens", _I32)
+    _checked(query_start_loc, "query_start_loc", _I32)
     qshape, cshape, tshape = query.shape, kv_cache.shape, block_tables.shape
     if len(qshape) != 3 or len(cshape) != 5 or seq_lens.dim() != 1:
         raise ValueError("query must be [num_q_tokens, num_q_heads, head_size], kv_cache 5-D and seq_lens [num_seqs]")
@@ -785,7 +799,7 @@ def _span_attention(fn, bits, query, kv_cache, block_tables, seq_lens, query_sta
     S = seq_lens.shape[0]
     signs = ()
     if bits != 8:
-        _cuda(rht_signs, "rht_signs", _F32)
+        _checked(rht_signs, "rht_signs", _F32)
         if rht_signs.shape != (d,):
             raise ValueError("rht_signs must be [head_size]")
         signs = (rht_signs.data_ptr(),)
@@ -795,24 +809,24 @@ def _span_attention(fn, bits, query, kv_cache, block_tables, seq_lens, query_sta
         raise ValueError("block_tables must be [num_seqs, max_blocks] and query_start_loc [num_seqs + 1]")
     begin = end = slopes = None
     if key_begin is not None:
-        if _cuda(key_begin, "key_begin", _I32).shape != (Nq,):
+        if _checked(key_begin, "key_begin", _I32).shape != (Nq,):
             raise ValueError("key_begin must be [num_q_tokens]")
         begin = key_begin.data_ptr()
     if key_end is not None:
-        if _cuda(key_end, "key_end", _I32).shape != (Nq,):
+        if _checked(key_end, "key_end", _I32).shape != (Nq,):
             raise ValueError("key_end must be [num_q_tokens]")
         end = key_end.data_ptr()
     if alibi_slopes is not None:
-        if _cuda(alibi_slopes, "alibi_slopes", _F32).shape != (Hq,):
+        if _checked(alibi_slopes, "alibi_slopes", _F32).shape != (Hq,):
             raise ValueError("alibi_slopes must be [num_q_heads]")
         slopes = alibi_slopes.data_ptr()
     if out is None:
         out = torch.empty(qshape, dtype=out_dtype or query.dtype, device=query.device)
-    _cuda(out, "out", tuple(_DTYPES))
+    _checked(out, "out", tuple(_DTYPES))
     if out.shape != qshape:
         raise ValueError("out must have the query's shape")
     if workspace is None:
-        need = (_lib or load()).kv_int4_span_workspace_bytes(Nq, Hq, H, d, S, max_query_len, max_seq_len)
+        need = _span_workspace(query.get_device(), Nq, Hq, H, d, S, max_query_len, max_seq_len)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=query.device)
     ws_ptr = workspace.data_ptr() if workspace is not None else None

@@ -836,6 +836,8 @@ kv_int4_status span_attention_impl(int bits, const void* q, kv_int4_dtype q_dtyp
     p.softcap = softcap;
     p.cap_l2 = (float)((double)softcap * 1.4426950408889634);
     p.cap_in = softcap > 0.0f ? 2.0f / softcap : 0.0f;
+    const double fit[3] = {-0.33323427, 0.13162696, -0.04370021}, c2 = (double)p.cap_l2 * (double)p.cap_l2;
+    for (int i = 0; i < 3; ++i) p.cap_q[i] = softcap > 0.0f ? (float)(fit[i] / std::pow(c2, i + 1)) : 0.0f;
     p.out_dt = out_dtype == KV_INT4_BF16 ? DType::BF16 : (out_dtype == KV_INT4_F16 ? DType::F16 : DType::F32);
     p.q_bf16 = q_dtype == KV_INT4_BF16;
     p.tiles = lay.tiles;

@@ -57,64 +57,69 @@ struct SpLayout {
     static constexpr uint32_t kRs = kScan + 20 * 4;                               // [128] f32 2^-d of each row's own prescale
     static constexpr uint32_t kFin = kRs + 128 * 4;                               // [128] f32 what a row's O is multiplied with
     static constexpr uint32_t kSignBits = kFin + 128 * 4;                         // [4] u32
-    static constexpr uint32_t kBars = (kSignBits + 16 + 7u) & ~7u;
+    static constexpr uint32_t kCsign = kSignBits + 16;                            // [D] f32 +-c of each dimension
+    static constexpr uint32_t kBars = (kCsign + D * 4 + 7u) & ~7u;
     // k_full[kring], k_free[pairs], v_full[pairs], v_free[pairs], pv_done[2], s_full[2], p_full[2], q_ready,
-    // flush, q_tma, rot_in, rot_done, epi[2], raw_full[plane][stages], raw_free[plane][stages]
-    static constexpr int kNumBars = kPfKRing + 3 * kPfPairs + 6 + 5 + 2 + 4 * kStages;
+    // flush, q_tma, rot_in, rot_done, epi, raw_full[plane][stages], raw_free[plane][stages]
+    static constexpr int kNumBars = kPfKRing + 3 * kPfPairs + 6 + 6 + 4 * kStages;
     static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr uint32_t kFlags = kTmemSlot + 4;
     static constexpr uint32_t kBytes = kFlags + 4 + 1024;                         // + alignment slack
     static_assert(kBytes <= 232448, "shared memory");
-    static_assert(kPfRows * D * 4 <= 4 * kTile, "output exchange");
 };
 
 // The INT2 centroids as the tiles hold them are 1.0002228 a and 1.0002134 b in fp16; with 1 / 1.0002181 in the scales both are
 // within 5e-6.
 constexpr float kU2Scale = 0.99978195f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 // The dimension a tile column holds.
 template <int BITS>
 __host__ __device__ constexpr int span_dim(int c) { return BITS == 8 ? c : dim_of_column(c); }
 
-// 32 lanes x 32 columns: thread i gets row (lane) i of the address's lanes, 32 consecutive columns.
-__device__ __forceinline__ void tmem_ld_row32(uint32_t taddr, uint32_t* r) {
+// 32 lanes x 16 columns: thread i gets row (lane) i of the address's lanes, 16 consecutive columns.
+__device__ __forceinline__ void tmem_ld_row16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr));
 }
 
-// Store n (a multiple of 8) consecutive values of a row, 16 bytes at a time; at is a multiple of 8.
+// The Walsh-Hadamard butterflies of a thread's own N values.
 template <int N>
-__device__ __forceinline__ void store_values(void* out, DType dt, int64_t at, const float* x) {
-    if (dt == DType::F32) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+__device__ __forceinline__ void thread_fwht(float (&x)[N]) {
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) o[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-        return;
+    for (int i = 0; i < N; i += 2) {
+        const float a = x[i], b = x[i + 1];
+        x[i] = a + b;
+        x[i + 1] = a - b;
     }
-    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + at);
-    const bool bf = dt == DType::BF16;
 #pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-        uint32_t w[4];
+    for (int w = 2; w < N; w <<= 1) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float a = x[8 * i + 2 * e], b = x[8 * i + 2 * e + 1];
-            if (bf) {
-                const __nv_bfloat162 y = __floats2bfloat162_rn(a, b);
-                w[e] = *reinterpret_cast<const uint32_t*>(&y);
-            } else {
-                w[e] = pack_f16x2(a, b);
-            }
+        for (int i = 0; i < N; i += 2) {
+            if (i & w) continue;
+            const float2 a = make_float2(x[i], x[i + 1]), b = make_float2(x[i + w], x[i + w + 1]);
+            const float2 u = add_f32x2(a, b), v = sub_f32x2(a, b);
+            x[i] = u.x, x[i + 1] = u.y;
+            x[i + w] = v.x, x[i + w + 1] = v.y;
         }
-        o[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+}
+
+// Eight values as a 16-byte word of a 16-bit type.
+__device__ __forceinline__ uint4 pack8(DType dt, const float* x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (dt == DType::BF16) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&y);
+        } else {
+            w[e] = pack_f16x2(x[2 * e], x[2 * e + 1]);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // C tanh(x / C) + off of two logits: C - 2 C / (2^(x cap_in) + 1), cap_in = 2 / C for x and C in log2 units (C in
@@ -127,15 +132,14 @@ __device__ __forceinline__ float2 capped(float2 x, float cap_in, float cap, floa
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(u.y));
     return fma_f32x2(r, make_float2(-2.0f * cap, -2.0f * cap), add_f32x2(off, make_float2(cap, cap)));
 }
-// The same for |x| <= kCapSmall C, without the two special functions: x P((x / C)^2), P a least-squares fit of
-// tanh(y) / y that is off by 1.6e-7 at most for |y| <= 0.6.
-constexpr float kCapSmall = 0.6f;
-__device__ __forceinline__ float2 capped_small(float2 x, float inv_cap, float2 off) {
-    const float2 y = mul_f32x2(x, make_float2(inv_cap, inv_cap)), t = mul_f32x2(y, y);
-    float2 q = fma_f32x2(t, make_float2(0.01513351f, 0.01513351f), make_float2(-0.05184597f, -0.05184597f));
-    q = fma_f32x2(t, q, make_float2(0.13304033f, 0.13304033f));
-    q = fma_f32x2(t, q, make_float2(-0.33331803f, -0.33331803f));
-    q = fma_f32x2(t, q, make_float2(0.99999984f, 0.99999984f));
+// The same for |x| <= kCapSmall C, without the two special functions: x P(x^2), P a least-squares fit of tanh(y) / y,
+// y = x / C, that is off by 1.2e-6 at most for |y| <= 1 / 2.  cap_q: its coefficients over powers of C^2.
+constexpr float kCapSmall = 0.5f;
+__device__ __forceinline__ float2 capped_small(float2 x, const SpanParams& p, float2 off) {
+    const float2 t = mul_f32x2(x, x);
+    float2 q = fma_f32x2(t, make_float2(p.cap_q[2], p.cap_q[2]), make_float2(p.cap_q[1], p.cap_q[1]));
+    q = fma_f32x2(t, q, make_float2(p.cap_q[0], p.cap_q[0]));
+    q = fma_f32x2(t, q, make_float2(0.99999885f, 0.99999885f));
     return fma_f32x2(x, q, off);
 }
 
@@ -148,9 +152,9 @@ struct Span {
     int lo, hi;
 };
 
-// OPTS: the call caps its scores or has a distance bias.  TWO: the weights as fp16 high + low halves.  FEW: no tile has
-// more than eight rows (single tokens); the low halves of rows 0..7, of the queries and of the weights, are then rows
-// 8..15, and half of the products do.
+// OPTS: the call caps its scores or has a distance bias.  TWO: the weights as fp16 high + low halves.  FEW: no
+// sequence has more than 64 rows (single tokens, drafts); a tile's rows are then the first eight of every sixteen, and the
+// second eight hold the low halves of the first, of the queries and of the weights, so that half of the products do.
 template <int D, int BITS, bool OPTS, bool TWO, bool FEW>
 __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_constant__ SpanParams p, const __grid_constant__ CUtensorMap qmap,
                                                              const __grid_constant__ CUtensorMap cmap) {
@@ -166,7 +170,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
     if (threadIdx.x == kPxMmaWarp * 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&qmap)) : "memory");
     if (threadIdx.x == kPxLoadWarp * 32) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&cmap)) : "memory");
     const int G = p.G, Hq = p.Hq, H = p.H;
-    const int BQ = kPfRows / G;
+    const int BQ = (FEW ? kPfRows / 2 : kPfRows) / G;
+    // the row (query token x head) of a tensor-memory lane; with FEW of the first eight of sixteen
+    auto row_of = [](int r) -> int { return FEW ? (r >> 4) * 8 + (r & 7) : r; };
     const int h = (int)(blockIdx.x % (unsigned)H), split = (int)blockIdx.y;
     const int group = H >= 4 ? 1 : 4 / H;              // tokens whose rows are a multiple of 16 bytes
     const bool boxes = Ly::kGroups || group == 1;      // TMA loads packed rows (see the loaders)
@@ -244,8 +250,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
     uint64_t* q_tma = flush + 1;                // the CTA's query rows in shared memory (bytes)
     uint64_t* rot_in = q_tma + 1;               // the rotation matrix in shared memory (256 arrivals)
     uint64_t* rot_done = rot_in + 1;            // the rotated queries in tensor memory (commit)
-    uint64_t* epi = rot_done + 1;                // [2] the row threads meet (256 arrivals)
-    uint64_t* raw_full = epi + 2;               // [plane][stages] packed rows of a key tile landed (one arrival and bytes, or and 32 lanes)
+    uint64_t* epi = rot_done + 1;                // the row threads meet (256 arrivals)
+    uint64_t* raw_full = epi + 1;               // [plane][stages] packed rows of a key tile landed (one arrival and bytes, or and 32 lanes)
     uint64_t* raw_free = raw_full + 2 * kStages;   // [plane][stages] that plane converted (128 arrivals)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kFlags);
@@ -280,10 +286,10 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             mbar_init(&pv_done[b], 1);
             mbar_init(&s_full[b], 1);
             mbar_init(&p_full[b], kPfSoftmaxThreads);
-            mbar_init(&epi[b], kPfSoftmaxThreads);
         }
         mbar_init(q_ready, kPfSoftmaxThreads);
         mbar_init(flush, 1);
+        mbar_init(epi, kPfSoftmaxThreads);
         mbar_init(q_tma, 1);
         mbar_init(rot_in, kPfSoftmaxThreads);
         mbar_init(rot_done, 1);
@@ -297,6 +303,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
     uint32_t* signbits = reinterpret_cast<uint32_t*>(smem + Ly::kSignBits);
     if (BITS != 8 && warp >= 4 && warp < 4 + D / 32) {
         const float s = p.signs[(warp - 4) * 32 + lane];
+        reinterpret_cast<float*>(smem + Ly::kCsign)[(warp - 4) * 32 + lane] = s < 0.0f ? -p.c : p.c;
         const uint32_t m = __ballot_sync(0xffffffffu, s < 0.0f);
         if (lane == 0) signbits[warp - 4] = m;
     }
@@ -375,7 +382,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         }
         // ---- each row's keys.  A row that sees none goes along as if it saw all, so that it does not put its warp on
         // the masked path, and is zero at the end; a warp of such rows leaves its weights unwritten.
-        Span sa = span_of(qt0 + ra / G), sb = span_of(qt0 + rb / G);
+        const int wa = row_of(ra), wb = row_of(rb);
+        Span sa = span_of(qt0 + wa / G), sb = FEW ? Span{0, 0} : span_of(qt0 + wb / G);
         const bool none_a = sa.hi <= sa.lo, none_b = sb.hi <= sb.lo;
         if (none_a) sa = Span{0, 0x7FFFFFFF};
         if (none_b) sb = Span{0, 0x7FFFFFFF};
@@ -390,7 +398,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         float* rs = reinterpret_cast<float*>(smem + Ly::kRs);   // what a row's S is multiplied with
         bool own_any = false;
         bool ok = soon(rot_done, 0);
-        if (__all_sync(0xffffffffu, ok)) {
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok && !idle) {
             tc_fence_after();
             float v[D / 2];   // v[4i], v[4i + 1]: row a, columns 8i + 2t, + 1; v[4i + 2], v[4i + 3]: row b
 #pragma unroll
@@ -427,7 +436,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     split_f16x2(v[4 * i] * sca, v[4 * i + 1] * sca, hw[i & 1], lw[i & 1]);
                     split_f16x2(v[4 * i + 2] * scb, v[4 * i + 3] * scb, hw[2 + (i & 1)], lw[2 + (i & 1)]);
                 }
-                if constexpr (FEW) {   // rows 8..15: the low halves of rows 0..7
+                if constexpr (FEW) {   // row b: the low halves of row a
                     hw[2] = lw[0];
                     hw[3] = lw[1];
                 } else {
@@ -436,8 +445,6 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 tmem_st_q1(trow + Tm::kQh + 8 * q, hw);
             }
             tmem_st_wait();
-        } else {
-            ok = false;
         }
         tc_fence_before();
         mbar_arrive(q_ready);
@@ -448,11 +455,11 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         bool any_a = false, any_b = false;
         float l_a = 0.0f, l_b = 0.0f;           // this thread's part of the sums of 2^(127+raise-E) p
         uint32_t E_a = 0, E_b = 0;              // reference biased exponents of the V scales that the rows see (0: none yet)
-        const float pos_a = (float)(pos0 + qt0 + ra / G), pos_b = (float)(pos0 + qt0 + rb / G);
+        const float pos_a = (float)(pos0 + qt0 + wa / G), pos_b = (float)(pos0 + qt0 + wb / G);
         float sl_a = 0.0f, sl_b = 0.0f;
         if (OPTS && p.alibi) {
-            sl_a = __ldg(p.alibi + h * G + ra % G) * kLog2e;
-            sl_b = __ldg(p.alibi + h * G + rb % G) * kLog2e;
+            sl_a = __ldg(p.alibi + h * G + wa % G) * kLog2e;
+            sl_b = __ldg(p.alibi + h * G + wb % G) * kLog2e;
         }
         if (idle) {
             for (int j = 0; j < nkt && ok; ++j) {
@@ -569,9 +576,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                         mag = max3(mag, fabsf(xb.x), fabsf(xb.y));
                     }
                     if (__all_sync(0xffffffffu, mag <= kCapSmall * p.cap_l2)) {
-                        const float inv = 0.5f * p.cap_in * kLn2;   // 1 / C in log2 units
 #pragma unroll
-                        for (int i = 0; i < 64; i += 2) set(i, capped_small(at(i), inv, (i & 2) ? mob2 : moa2));
+                        for (int i = 0; i < 64; i += 2) set(i, capped_small(at(i), p, (i & 2) ? mob2 : moa2));
                     } else {
 #pragma unroll
                         for (int i = 0; i < 64; i += 2) set(i, capped(at(i), p.cap_in, p.cap_l2, (i & 2) ? mob2 : moa2));
@@ -768,69 +774,87 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     reinterpret_cast<float2*>(p.part_ml)[((int64_t)(q0 + qt) * Hq + h * G + r % G) * p.splits + split] =
                         any && ok ? make_float2(m, l * es) : make_float2(kNegBig, 0.0f);
                 };
-                partial(ra, any_a, l_a, off_a, E_a);
-                partial(rb, any_b, l_b, off_b, E_b);
+                partial(wa, any_a, l_a, off_a, E_a);
+                if constexpr (!FEW) partial(wb, any_b, l_b, off_b, E_b);
             }
         }
         __syncwarp();
         // Two threads per row from here on, the other layout: warp w takes the 32 rows 32 (w % 4) .. and column half w / 4.
-        auto rows_meet = [&](uint64_t* bar) -> bool {
-            mbar_arrive(bar);
-            return __all_sync(0xffffffffu, wait(bar, 0));
-        };
-        const bool met = rows_meet(&epi[0]);
-        ok = __all_sync(0xffffffffu, ok) && met;
+        mbar_arrive(epi);
+        ok = __all_sync(0xffffffffu, soon(epi, 0) && ok);
         tc_fence_after();
         constexpr int HD = D / 2;   // this thread's dimensions: half * HD ..
-        const int row = 32 * (warp & 3) + lane, half = warp >> 2;
-        const int qt = qt0 + row / G;
-        const bool stored = qt < qcount;
-        const int64_t orow = (int64_t)(q0 + (stored ? qt : 0)) * Hq + h * G + row % G;
-        float x[HD];
-        if (ok) {
-            uint32_t o[HD];
-#pragma unroll
-            for (int c = 0; c < HD; c += 32) tmem_ld_row32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + Tm::kO + half * HD + c, o + c);
-            tmem_ld_wait();
+        const int row = 32 * (warp & 3) + lane, half = warp >> 2, nrows = min(BQ, qcount - qt0) * G;
+        const bool whole = p.splits == 1;
+        if (ok && nrows > row_of(32 * (warp & 3))) {
+            const uint32_t trow32 = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + Tm::kO;
             const float f = fin[row];
+            float x[HD];
 #pragma unroll
-            for (int c = 0; c < HD; ++c) {
-                float y = __uint_as_float(o[c]);
-                if (FEW) y += __shfl_down_sync(0xffffffffu, y, 8);
-                x[span_dim<BITS>(c)] = f == 0.0f ? 0.0f : y * f;
+            for (int c0 = 0; c0 < HD; c0 += 16) {
+                // out = c D H x: the butterflies between the halves as they are read, the others in registers
+                uint32_t a[16], b[16];
+                tmem_ld_row16(trow32 + (BITS != 8 && whole ? 0 : half * HD) + c0, a);
+                if (BITS != 8 && whole) tmem_ld_row16(trow32 + HD + c0, b);
+                tmem_ld_wait();
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    float y = __uint_as_float(a[c]);
+                    if (BITS != 8 && whole) y = half ? y - __uint_as_float(b[c]) : y + __uint_as_float(b[c]);
+                    if (FEW) y += __shfl_down_sync(0xffffffffu, y, 8);   // the low halves' share
+                    x[c0 + span_dim<BITS>(c)] = f == 0.0f ? 0.0f : y * f;
+                }
             }
-        } else {
+            if (BITS != 8 && whole) {
+                thread_fwht<HD>(x);
+                const float4* cs = reinterpret_cast<const float4*>(smem + Ly::kCsign) + half * (HD / 4);
 #pragma unroll
-            for (int c = 0; c < HD; ++c) x[c] = 0.0f;
-        }
-        if (p.splits > 1) {
-            if (stored) store_values<HD>(p.part_o, DType::F32, (orow * p.splits + split) * D + half * HD, x);
-        } else {
-            if constexpr (BITS != 8) {
-                // out = c D H x: the butterflies of this half in registers, those between the halves through shared
-                // memory (the last P.V is done, so nothing reads the tiles)
+                for (int i = 0; i < HD / 4; ++i) {
+                    const float4 c = cs[i];
+                    x[4 * i] *= c.x;
+                    x[4 * i + 1] *= c.y;
+                    x[4 * i + 2] *= c.z;
+                    x[4 * i + 3] *= c.w;
+                }
+            }
+            // Through shared memory (the last P.V is done, so nothing reads the tiles), 64 bytes of each of the warp's rows
+            // at a time, so that neighbouring lanes store neighbouring words.
+            uint8_t* stage = tiles + warp * 2048;
+            auto store_rows = [&](uint8_t* base, int64_t pitch, int bytes, int c, const uint4 (&w)[4]) {
 #pragma unroll
-                for (int w = 1; w < HD; w <<= 1) {
+                for (int e = 0; e < 4; ++e) *reinterpret_cast<uint4*>(stage + lane * 64 + 16 * (e ^ ((lane >> 1) & 3))) = w[e];
+                __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < HD; ++i) {
-                        if (i & w) continue;
-                        const float a = x[i], c = x[i + w];
-                        x[i] = a + c;
-                        x[i + w] = a - c;
+                for (int e = 0; e < 4; ++e) {
+                    const int l = 8 * e + lane / 4, r = row_of(32 * (warp & 3) + l);
+                    if (r < nrows && (!FEW || (l & 8) == 0)) {
+                        const int64_t at = (int64_t)(q0 + qt0 + r / G) * Hq + h * G + r % G;
+                        *reinterpret_cast<uint4*>(base + at * pitch + half * bytes + 64 * c + 16 * (lane & 3)) =
+                            *reinterpret_cast<const uint4*>(stage + l * 64 + 16 * ((lane & 3) ^ ((l >> 1) & 3)));
                     }
                 }
-                float* xch = reinterpret_cast<float*>(tiles) + row;
+                __syncwarp();
+            };
+            if (!whole || p.out_dt == DType::F32) {
+                uint8_t* base = whole ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.part_o) + (int64_t)split * (D * 4);
 #pragma unroll
-                for (int i = 0; i < HD; ++i) xch[(half * HD + i) * kPfRows] = x[i];
-                ok = rows_meet(&epi[1]);
-                const float sg = half ? -1.0f : 1.0f;
+                for (int c = 0; c < HD / 16; ++c) {
+                    uint4 w[4];
 #pragma unroll
-                for (int i = 0; i < HD; ++i) {
-                    const float y = fmaf(sg, x[i], xch[((half ^ 1) * HD + i) * kPfRows]);   // half 0: x + other, half 1: other - x
-                    x[i] = ((signbits[(half * HD + i) / 32] >> ((half * HD + i) % 32)) & 1u) ? -p.c * y : p.c * y;
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = make_uint4(__float_as_uint(x[16 * c + 4 * e]), __float_as_uint(x[16 * c + 4 * e + 1]),
+                                          __float_as_uint(x[16 * c + 4 * e + 2]), __float_as_uint(x[16 * c + 4 * e + 3]));
+                    store_rows(base, (int64_t)p.splits * (D * 4), HD * 4, c, w);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < HD / 32; ++c) {
+                    uint4 w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = pack8(p.out_dt, x + 32 * c + 8 * e);
+                    store_rows(static_cast<uint8_t*>(p.out), D * 2, HD * 2, c, w);
                 }
             }
-            if (stored && ok) store_values<HD>(p.out, p.out_dt, orow * D + half * HD, x);
         }
     } else if (warp < kPxMmaWarp) {
         fewer_registers<kPxDequantRegs>();
@@ -1031,10 +1055,17 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             const uint64_t vd1 = smem_desc_sw128(smem_u32(vtile(1)), kPfKeys * 128u, 1024u);
             {
                 if (leader) {
-                    mbar_arrive_expect_tx(q_tma, Ly::kTile);
+                    const int eights = (min(BQ, qcount - qt0) * G + 7) / 8;   // FEW: boxes of eight rows
+                    mbar_arrive_expect_tx(q_tma, FEW ? (uint32_t)eights * (D / 64) * 1024u : Ly::kTile);
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load_3d(ktile(1) + c * (kPfRows * 128), &qmap, 64 * c, h * G, q0 + qt0, q_tma);
+                    for (int c = 0; c < D / 64; ++c) {
+                        if constexpr (FEW) {   // eight rows a box, in every second eight rows of the tile
+                            for (int i = 0; i < eights; ++i)
+                                tma_load_3d(ktile(1) + c * (kPfRows * 128) + i * 2048, &qmap, 64 * c, h * G, q0 + qt0 + i * (8 / G), q_tma);
+                        } else {
+                            tma_load_3d(ktile(1) + c * (kPfRows * 128), &qmap, 64 * c, h * G, q0 + qt0, q_tma);
+                        }
+                    }
                 }
                 __syncwarp();
                 if (__all_sync(0xffffffffu, mbar_wait(q_tma, 0) && wait(rot_in, 0))) {
@@ -1111,8 +1142,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             if (p.splits > 1) {
                 reinterpret_cast<float2*>(p.part_ml)[orow * p.splits + split] = make_float2(kNegBig, 0.0f);
             } else {
-                const float zero[8] = {};
-                for (int i = 0; i < D; i += 8) store_values<8>(p.out, p.out_dt, orow * D + i, zero);
+                const int n = p.out_dt == DType::F32 ? D / 4 : D / 8;
+                for (int i = 0; i < n; ++i) reinterpret_cast<uint4*>(p.out)[orow * n + i] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
     }
@@ -1178,14 +1209,14 @@ __global__ void __launch_bounds__(kSpanCombineWarps * 32) span_combine_kernel(co
     }
 }
 
-// The queries as [token][q head][D], in boxes of [128 / G tokens][G heads][64 dims] with the 128-byte swizzle.
+// The queries as [token][q head][D], in boxes of [rows / G tokens][G heads][64 dims] with the 128-byte swizzle.
 template <int D>
-cudaError_t span_query_map(const SpanParams& p, CUtensorMap* map) {
+cudaError_t span_query_map(const SpanParams& p, int rows, CUtensorMap* map) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (enc == nullptr) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)p.Hq, (cuuint64_t)p.num_q_tokens};
     const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)p.Hq * D * 2};
-    const cuuint32_t box[3] = {64u, (cuuint32_t)p.G, (cuuint32_t)(kPfRows / p.G)};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)p.G, (cuuint32_t)(rows / p.G)};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
     const CUresult r = enc(map, p.q_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                            const_cast<void*>(p.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1227,7 +1258,7 @@ cudaError_t launch_span_t(const SpanParams& p, cudaStream_t stream) {
     }
     if (regs.load(std::memory_order_acquire) != kPxLaunchRegs) return cudaErrorInvalidKernelImage;
     CUtensorMap qmap, cmap;
-    err = span_query_map<D>(p, &qmap);
+    err = span_query_map<D>(p, FEW ? 8 : kPfRows, &qmap);
     if (err != cudaSuccess) return err;
     if (p.H >= 4 || SpLayout<D, BITS>::kGroups) {
         err = span_cache_map<D, BITS>(p, &cmap);
@@ -1257,7 +1288,7 @@ cudaError_t launch_span_t(const SpanParams& p, cudaStream_t stream) {
 template <int D, int BITS>
 cudaError_t launch_span_head(const SpanParams& p, cudaStream_t s) {
     const bool opts = p.softcap > 0.0f || p.alibi != nullptr;
-    if (p.max_query_len * p.G <= 8) return opts ? launch_span_t<D, BITS, true, true, true>(p, s) : launch_span_t<D, BITS, false, true, true>(p, s);
+    if (p.max_query_len <= kPfRows / 2 / p.G) return opts ? launch_span_t<D, BITS, true, true, true>(p, s) : launch_span_t<D, BITS, false, true, true>(p, s);
     if (p.out_dt == DType::BF16) return opts ? launch_span_t<D, BITS, true, false, false>(p, s) : launch_span_t<D, BITS, false, false, false>(p, s);
     return opts ? launch_span_t<D, BITS, true, true, false>(p, s) : launch_span_t<D, BITS, false, true, false>(p, s);
 }

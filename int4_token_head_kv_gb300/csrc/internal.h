@@ -139,7 +139,8 @@ struct SpanParams {
     float softmax_scale;
     float c;                    // fp32(1 / sqrt(head_size)); 1 for INT8 rows
     float softcap;              // 0: none
-    float cap_l2, cap_in;       // softcap log2 e, 2 / softcap
+    float cap_l2, cap_in;       // C = softcap log2 e, 2 / softcap
+    float cap_q[3];             // coefficients of the small logits' cap over C^2, C^4, C^6
     DType out_dt;
     int q_bf16;
     int tiles;                  // row tiles per kv head of the grid: of the batch (tiled) or of a sequence
