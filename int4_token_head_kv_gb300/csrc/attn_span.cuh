@@ -59,9 +59,9 @@ struct SpLayout {
     static constexpr uint32_t kSignBits = kFin + 128 * 4;                         // [4] u32
     static constexpr uint32_t kCsign = kSignBits + 16;                            // [D] f32 +-c of each dimension
     static constexpr uint32_t kBars = (kCsign + D * 4 + 7u) & ~7u;
-    // k_full[kring], k_free[pairs], v_full[pairs], v_free[pairs], pv_done[2], s_full[2], p_full[2], q_ready,
+    // k_full[kring], k_free[pairs], v_full[pairs], pv_done[pairs], s_full[2], p_full[2], q_ready,
     // flush, q_tma, rot_in, rot_done, epi, raw_full[plane][stages], raw_free[plane][stages]
-    static constexpr int kNumBars = kPfKRing + 3 * kPfPairs + 6 + 6 + 4 * kStages;
+    static constexpr int kNumBars = kPfKRing + 3 * kPfPairs + 4 + 6 + 4 * kStages;
     static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr uint32_t kFlags = kTmemSlot + 4;
     static constexpr uint32_t kBytes = kFlags + 4 + 1024;                         // + alignment slack
@@ -238,21 +238,20 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
     float* sv = reinterpret_cast<float*>(smem + Ly::kSv);
     uint32_t* eblkw = reinterpret_cast<uint32_t*>(smem + Ly::kEblk);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::kBars);
-    uint64_t* k_full = bars;                    // [kring] K tile and scales of tile j (128 arrivals)
+    uint64_t* k_full = bars;                    // [kring] K tile and scales of tile j (4 warps)
     uint64_t* k_free = k_full + kPfKRing;       // [pairs] K tile j % 2 read by S of tile j (commit)
-    uint64_t* v_full = k_free + kPfPairs;       // [pairs] V tile and scales of tile j (128 arrivals)
-    uint64_t* v_free = v_full + kPfPairs;       // [pairs] V tile j % 2 read by P.V of tile j (commit)
-    uint64_t* pv_done = v_free + kPfPairs;      // [2] P.V of tile j done (commit): S buffer j % 2 and O free
-    uint64_t* s_full = pv_done + 2;             // [2] S of the tile in tensor memory (commit)
-    uint64_t* p_full = s_full + 2;              // [2] P of the tile in tensor memory (256 arrivals)
-    uint64_t* q_ready = p_full + 2;             // queries in tensor memory, staging free (256 arrivals)
+    uint64_t* v_full = k_free + kPfPairs;       // [pairs] V tile and scales of tile j (4 warps)
+    uint64_t* pv_done = v_full + kPfPairs;      // [pairs] P.V of tile j done (commit): V tile j % 2 and O free
+    uint64_t* s_full = pv_done + kPfPairs;      // [2] S of the tile in tensor memory (commit)
+    uint64_t* p_full = s_full + 2;              // [2] P of the tile in tensor memory (8 warps)
+    uint64_t* q_ready = p_full + 2;             // queries in tensor memory, staging free (8 warps)
     uint64_t* flush = q_ready + 1;              // the MMA thread's last commit (teardown)
     uint64_t* q_tma = flush + 1;                // the CTA's query rows in shared memory (bytes)
-    uint64_t* rot_in = q_tma + 1;               // the rotation matrix in shared memory (256 arrivals)
+    uint64_t* rot_in = q_tma + 1;               // the rotation matrix in shared memory (8 warps)
     uint64_t* rot_done = rot_in + 1;            // the rotated queries in tensor memory (commit)
-    uint64_t* epi = rot_done + 1;                // the row threads meet (256 arrivals)
+    uint64_t* epi = rot_done + 1;                // the row warps meet (8 of them)
     uint64_t* raw_full = epi + 1;               // [plane][stages] packed rows of a key tile landed (one arrival and bytes, or and 32 lanes)
-    uint64_t* raw_free = raw_full + 2 * kStages;   // [plane][stages] that plane converted (128 arrivals)
+    uint64_t* raw_free = raw_full + 2 * kStages;   // [plane][stages] that plane converted (4 warps)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Ly::kTmemSlot);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Ly::kFlags);
     uint32_t* deadf = reinterpret_cast<uint32_t*>(smem + Ly::kDeadF);
@@ -276,26 +275,25 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         }
     }
     if (threadIdx.x == 32) {
-        for (int b = 0; b < kPfKRing; ++b) mbar_init(&k_full[b], 128);
+        for (int b = 0; b < kPfKRing; ++b) mbar_init(&k_full[b], 4);
         for (int b = 0; b < kPfPairs; ++b) {
             mbar_init(&k_free[b], 1);
-            mbar_init(&v_full[b], 128);
-            mbar_init(&v_free[b], 1);
+            mbar_init(&v_full[b], 4);
+            mbar_init(&pv_done[b], 1);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(&pv_done[b], 1);
             mbar_init(&s_full[b], 1);
-            mbar_init(&p_full[b], kPfSoftmaxThreads);
+            mbar_init(&p_full[b], kPfSoftmaxWarps);
         }
-        mbar_init(q_ready, kPfSoftmaxThreads);
+        mbar_init(q_ready, kPfSoftmaxWarps);
         mbar_init(flush, 1);
-        mbar_init(epi, kPfSoftmaxThreads);
+        mbar_init(epi, kPfSoftmaxWarps);
         mbar_init(q_tma, 1);
-        mbar_init(rot_in, kPfSoftmaxThreads);
+        mbar_init(rot_in, kPfSoftmaxWarps);
         mbar_init(rot_done, 1);
         for (int i = 0; i < 2 * kStages; ++i) {
             mbar_init(&raw_full[i], boxes ? 1 : 33);
-            mbar_init(&raw_free[i], 128);
+            mbar_init(&raw_free[i], 4);
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -333,12 +331,33 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         if (atomicExch(const_cast<int*>(abort_flag), 1) == 0) count_status(p.status, 3);
         return false;
     };
+    // A warp's arrival, once all its lanes are there: 32 arrivals on one barrier keep the shared-memory pipe busy, which the
+    // products' operands, the conversion and every wait of the chain below go through.
+    auto arrive = [&](uint64_t* bar) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    };
     // the same in the chain S -> weights -> P.V -> next S, where waking a suspended warp would add to every tile:
     // polled first
     auto soon = [&](uint64_t* bar, uint32_t parity) -> bool {
         for (int i = 0; i < kPxPolls; ++i)
             if (mbar_test_wait(bar, parity)) return true;
         return wait(bar, parity);
+    };
+    // several at once: a poll takes 250 cycles or so behind the other users of shared memory
+    auto soon2 = [&](uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb) -> bool {
+        for (int i = 0; i < kPxPolls; ++i) {
+            const bool x = mbar_test_wait(a, pa), y = mbar_test_wait(b, pb);
+            if (x && y) return true;
+        }
+        return wait(a, pa) && wait(b, pb);
+    };
+    auto soon3 = [&](uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc) -> bool {
+        for (int i = 0; i < kPxPolls; ++i) {
+            const bool x = mbar_test_wait(a, pa), y = mbar_test_wait(b, pb), z = mbar_test_wait(c, pc);
+            if (x && y && z) return true;
+        }
+        return wait(a, pa) && wait(b, pb) && wait(c, pc);
     };
 
     if (nkt == 0) {
@@ -378,7 +397,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     make_uint4(w[0], w[1], w[2], w[3]);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // generic writes -> tensor core reads
-            mbar_arrive(rot_in);
+            arrive(rot_in);
         }
         // ---- each row's keys.  A row that sees none goes along as if it saw all, so that it does not put its warp on
         // the masked path, and is zero at the end; a warp of such rows leaves its weights unwritten.
@@ -447,7 +466,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             tmem_st_wait();
         }
         tc_fence_before();
-        mbar_arrive(q_ready);
+        arrive(q_ready);
         // ---- the key tiles
         // Reference maxima m (log2 units) as the exponents' offsets off = 127 + raise - E - m; E = 127 and off = 0
         // until a row has a key (any).
@@ -465,15 +484,14 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             for (int j = 0; j < nkt && ok; ++j) {
                 ok = wait(&s_full[j & 1], (uint32_t)(j >> 1) & 1u);
                 ok = __all_sync(0xffffffffu, ok);
-                if (ok) mbar_arrive(&p_full[j & 1]);
+                if (ok) arrive(&p_full[j & 1]);
             }
         }
         for (int j = idle ? nkt : 0; j < nkt && ok; ++j) {
             const int b = j & 1;
             const uint32_t ph = (uint32_t)(j >> 1) & 1u;
             const int kb = j % kPfPairs, kr = j % kPfKRing;
-            ok = soon(&s_full[b], ph) && wait(&k_full[kr], (uint32_t)(j / kPfKRing) & 1u) &&
-                 wait(&v_full[kb], (uint32_t)(j / kPfPairs) & 1u);
+            ok = soon3(&s_full[b], ph, &k_full[kr], (uint32_t)(j / kPfKRing) & 1u, &v_full[kb], (uint32_t)(j / kPfPairs) & 1u);
             if (__any_sync(0xffffffffu, !ok)) {
                 ok = false;
                 break;
@@ -487,7 +505,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 for (int q = 0; q < (TWO && !FEW ? 16 : 8); ++q) tmem_st_q1(scol + 8 * q, zero);
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(&p_full[b]);
+                arrive(&p_full[b]);
                 continue;
             }
             uint32_t s[64];   // s[4i], s[4i + 1]: row a, columns 8i + 2t, + 1; s[4i + 2], s[4i + 3]: row b
@@ -751,7 +769,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             l_b += lsb.x + lsb.y;
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&p_full[b]);
+            arrive(&p_full[b]);
         }
         // ---- the output, or the split's partial: (m, l 2^(E - 127 - raise)) and O / l
         if (ok) ok = wait(&pv_done[(nkt - 1) & 1], (uint32_t)((nkt - 1) >> 1) & 1u);
@@ -780,7 +798,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         }
         __syncwarp();
         // Two threads per row from here on, the other layout: warp w takes the 32 rows 32 (w % 4) .. and column half w / 4.
-        mbar_arrive(epi);
+        arrive(epi);
         ok = __all_sync(0xffffffffu, soon(epi, 0) && ok);
         tc_fence_after();
         constexpr int HD = D / 2;   // this thread's dimensions: half * HD ..
@@ -881,7 +899,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             uint8_t* t = pl ? vtile(kb) : ktile(kb);
             auto tile_free = [&]() -> bool {
                 bool f = j != 1 || wait(q_ready, 0);        // the query rows and the rotation matrix sat on pair 1
-                if (f && j >= kPfPairs) f = wait(pl ? &v_free[kb] : &k_free[kb], (uint32_t)(j / kPfPairs - 1) & 1u);
+                if (f && j >= kPfPairs) f = wait(pl ? &pv_done[kb] : &k_free[kb], (uint32_t)(j / kPfPairs - 1) & 1u);
                 return __all_sync(0xffffffffu, f);
             };
             auto put = [&](int w, const uint32_t (&o)[4]) {   // dimensions 8w .. 8w + 7 in the tile's order
@@ -908,7 +926,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     c0 = c1;
                 }
                 scale = row_off == 0 ? c0.x : row_off == 1 ? c0.y : row_off == 2 ? c0.z : c0.w;
-                mbar_arrive(&raw_free[pl * kStages + st]);
+                arrive(&raw_free[pl * kStages + st]);
             } else {
                 uint32_t kw[NW];
                 {
@@ -926,7 +944,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
 #pragma unroll
                     for (int w = 0; w < NW; ++w) kw[w] = (row_off & 1) ? wv[w + 1] : wv[w];
                 }
-                mbar_arrive(&raw_free[pl * kStages + st]);
+                arrive(&raw_free[pl * kStages + st]);
                 ok = tile_free();
                 if (!ok) break;
                 scale = kw[NW - 1];
@@ -968,7 +986,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 if (lane == 0) eblkw[kb * 4 + (warp & 3)] = (wmax >> 23) & 0xFFu;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // generic writes -> tensor core reads
-            mbar_arrive(pl ? &v_full[kb] : &k_full[j % kPfKRing]);
+            arrive(pl ? &v_full[kb] : &k_full[j % kPfKRing]);
         }
     } else {
         fewer_registers<kPxOtherRegs>();
@@ -1107,8 +1125,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                         mma_ts(tmem + Tm::kO, pcol + 8u * kk, vd + ((kk * 16 * 128) >> 4), idPV, t > 0 || kk > 0);
                         if constexpr (TWO && !FEW) mma_ts(tmem + Tm::kO, pcol + 64u + 8u * kk, vd + ((kk * 16 * 128) >> 4), idPV, true);
                     }
-                    mma_commit(&pv_done[t & 1]);
-                    mma_commit(&v_free[t % kPfPairs]);
+                    mma_commit(&pv_done[t % kPfPairs]);
                 }
                 __syncwarp();
             };
@@ -1116,14 +1133,15 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             bool ok = __all_sync(0xffffffffu, soon(q_ready, 0));
             for (int t = 0; t <= nkt && ok; ++t) {
                 if (t < nkt) {
-                    ok = soon(&k_full[t % kPfKRing], (uint32_t)(t / kPfKRing) & 1u) &&
-                         (t < 2 || soon(&pv_done[t & 1], (uint32_t)((t - 2) >> 1) & 1u));
+                    uint64_t* full = &k_full[t % kPfKRing];
+                    const uint32_t ph = (uint32_t)(t / kPfKRing) & 1u;
+                    ok = t < 2 ? soon(full, ph) : soon2(full, ph, &pv_done[t & 1], (uint32_t)((t - 2) >> 1) & 1u);
                     if (!__all_sync(0xffffffffu, ok)) break;
                     tc_fence_after();
                     issue_s(t);
                 }
                 if (t > 0) {
-                    ok = soon(&p_full[(t - 1) & 1], (uint32_t)((t - 1) >> 1) & 1u) && soon(&v_full[(t - 1) % kPfPairs], (uint32_t)((t - 1) / kPfPairs) & 1u);
+                    ok = soon(&p_full[(t - 1) & 1], (uint32_t)((t - 1) >> 1) & 1u);   // (which waited for the V tile)
                     if (!__all_sync(0xffffffffu, ok)) break;
                     tc_fence_after();
                     issue_pv(t - 1);
