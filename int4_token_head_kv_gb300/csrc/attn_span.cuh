@@ -57,7 +57,7 @@ struct SpLayout {
     static constexpr uint32_t kRs = kScan + 20 * 4;                               // [128] f32 2^-d of each row's own prescale
     static constexpr uint32_t kFin = kRs + 128 * 4;                               // [128] f32 what a row's O is multiplied with
     static constexpr uint32_t kSignBits = kFin + 128 * 4;                         // [4] u32
-    static constexpr uint32_t kCsign = kSignBits + 16;                            // [D] f32 +-c of each dimension
+    static constexpr uint32_t kCsign = (kSignBits + 16 + 15u) & ~15u;             // [D] f32 +-c of each dimension
     static constexpr uint32_t kBars = (kCsign + D * 4 + 7u) & ~7u;
     // k_full[kring], k_free[pairs], v_full[pairs], pv_done[pairs], s_full[2], p_full[2], q_ready,
     // flush, q_tma, rot_in, rot_done, epi, raw_full[plane][stages], raw_free[plane][stages]
@@ -66,6 +66,8 @@ struct SpLayout {
     static constexpr uint32_t kFlags = kTmemSlot + 4;
     static constexpr uint32_t kBytes = kFlags + 4 + 1024;                         // + alignment slack
     static_assert(kBytes <= 232448, "shared memory");
+    static_assert(kSk % 16 == 0 && kSv % 16 == 0 && kCsign % 16 == 0, "16-byte accesses");
+    static_assert(kRaw % 1024 == 0 && kPlane % 128 == 0 && kTile % 1024 == 0 && kBars % 8 == 0, "boxes on 128 bytes, swizzled tiles on 1024");
 };
 
 // The INT2 centroids as the tiles hold them are 1.0002228 a and 1.0002134 b in fp16; with 1 / 1.0002181 in the scales both are
