@@ -124,8 +124,8 @@ __device__ __forceinline__ uint4 pack8(DType dt, const float* x) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// C tanh(x / C) + off of two logits: C - 2 C / (2^(x cap_in) + 1), cap_in = 2 / C for x and C in log2 units (C in
-// natural ones in cap_in).  The absolute error is a few 2^-24 of C.
+// C tanh(x / C) + off of two logits x, all in log2 units: C - 2 C / (2^(x cap_in) + 1), cap_in two over the cap in natural
+// units.  The absolute error is a few 2^-24 of C.
 __device__ __forceinline__ float2 capped(float2 x, float cap_in, float cap, float2 off) {
     const float2 y = mul_f32x2(x, make_float2(cap_in, cap_in));
     const float2 u = add_f32x2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), make_float2(1.0f, 1.0f));
@@ -134,9 +134,8 @@ __device__ __forceinline__ float2 capped(float2 x, float cap_in, float cap, floa
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(u.y));
     return fma_f32x2(r, make_float2(-2.0f * cap, -2.0f * cap), add_f32x2(off, make_float2(cap, cap)));
 }
-// The same for |x| <= kCapSmall C, without the two special functions: x P(x^2), P a least-squares fit of tanh(y) / y,
-// y = x / C, that is off by 1.2e-6 at most for |y| <= 1 / 2.  cap_q: its coefficients over powers of C^2.
-constexpr float kCapSmall = 0.5f;
+// The same for |x| <= C / 2, without the two special functions: x P(x^2), P a least-squares fit of tanh(y) / y, y = x / C,
+// that is off by 1.2e-6 at most.
 __device__ __forceinline__ float2 capped_small(float2 x, const SpanParams& p, float2 off) {
     const float2 t = mul_f32x2(x, x);
     float2 q = fma_f32x2(t, make_float2(p.cap_q[2], p.cap_q[2]), make_float2(p.cap_q[1], p.cap_q[1]));
@@ -595,7 +594,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                         mag = max3(mag, fabsf(xa.x), fabsf(xa.y));
                         mag = max3(mag, fabsf(xb.x), fabsf(xb.y));
                     }
-                    if (__all_sync(0xffffffffu, mag <= kCapSmall * p.cap_l2)) {
+                    if (__all_sync(0xffffffffu, mag <= p.cap_small)) {
 #pragma unroll
                         for (int i = 0; i < 64; i += 2) set(i, capped_small(at(i), p, (i & 2) ? mob2 : moa2));
                     } else {

@@ -236,6 +236,29 @@ def test_queries_that_are_not_finite_show_in_their_own_rows(bits):
 
 
 @pytest.mark.parametrize("bits", [4, 8, 2])
+@pytest.mark.parametrize("size", [1e-20, 1e-3, 300.0, 3e4])
+def test_queries_of_any_size(bits, size):
+    """All of them, and some rows among others; the softmax scale keeps the logits where they are."""
+    for qlen in (1, 9, 70):
+        b = Batch(bits, (300, 140), (qlen, qlen), 8, 2, 128, seed=21)
+        q = b.q.clone()
+        b.q, b.scale = (q.float() * size).to(q.dtype), 128 ** -0.5 / size
+        _check(b)
+        b.q, b.scale = q.clone(), 128 ** -0.5
+        b.q[::3, 1::2] = (q[::3, 1::2].float() * min(size, 0.01)).to(q.dtype)
+        _check(b, **_spans("prefix", b))
+
+
+@pytest.mark.parametrize("softcap", [1e-44, 1e-30, 1e-3, 0.5, 1e4, 3e38])
+def test_caps_of_any_size(softcap):
+    """Logits far beyond the cap, and far below it; a cap of next to nothing gives every visible key one weight."""
+    for qlen in (1, 70):
+        b = Batch(4, (200, 90), (qlen, qlen), 8, 2, 128, seed=22)
+        b.cache[int(b.tables[0, 2])] = 0                     # rows of zeros: logits of 0
+        _check(b, softcap=float(np.float32(softcap)))
+
+
+@pytest.mark.parametrize("bits", [4, 8, 2])
 def test_rows_of_zeros_are_keys(bits):
     b = Batch(bits, (90,), (30,), 8, 2, 128, seed=13)
     for j in (0, 5, 63, 64, 89):
