@@ -582,6 +582,12 @@ kv_int4_status kv_int4_paged_attention_noalloc_ex(const void* q, kv_int4_dtype q
  * What a row does not see does not reach it: its keys and values may be infinite or NaN.  A visible row of zeros
  * (never written) is a key of logit 0 and a value of 0.
  *
+ * Computation: one kernel for chunks and single tokens (tcgen05), 128 rows (query tokens x the heads of one kv head)
+ * against the keys that some of them see; with few row tiles the keys are split among the SMs and a second kernel
+ * joins the partials.  Queries and sums keep 22 bits and more, the softmax weights 22 (11 for a bf16 output of
+ * sequences with more than 64 rows).  The split depends on the sizes alone: the same call gives the same bits, a
+ * sequence in another batch may differ in the last ones.
+ *
  * key_begin, key_end  [num_q_tokens] int32 or NULL.
  * softcap             0: none; negative or not finite: KV_INT4_EINVAL.
  * alibi_slopes        [num_q_heads] fp32 or NULL.
