@@ -836,14 +836,11 @@ kv_int4_status span_attention_impl(int bits, const void* q, kv_int4_dtype q_dtyp
     p.softcap = softcap;
     p.cap_l2 = (float)((double)softcap * 1.4426950408889634);
     p.cap_in = softcap > 0.0f ? std::min(2.0f / softcap, 3.0e38f) : 0.0f;   // finite: a logit of 0 stays one
-    // tanh(y) / y = 0.99999885 + fit . (y^2, y^4, y^6) for |y| <= 1 / 2, over powers of C^2; no logit is small for a cap
-    // whose powers leave fp32
+    // tanh(y) / y = 0.99999885 + fit . (y^2, y^4, y^6) for |y| <= 1 / 2, over powers of C^2.  Powers that leave fp32 belong
+    // to caps below 2.3e-7, to which a linear term does: within 1e-8 of the capped logit.
     const double fit[3] = {-0.33323427, 0.13162696, -0.04370021}, c2 = (double)p.cap_l2 * (double)p.cap_l2;
-    p.cap_small = 0.5f * p.cap_l2;
-    for (int i = 0; i < 3; ++i) {
-        p.cap_q[i] = softcap > 0.0f ? (float)(fit[i] / std::pow(c2, i + 1)) : 0.0f;
-        if (!std::isfinite(p.cap_q[i])) p.cap_small = -1.0f;
-    }
+    const bool fits = softcap > 0.0f && std::pow(c2, 3) > 1.5e-40;
+    for (int i = 0; i < 3; ++i) p.cap_q[i] = fits ? (float)(fit[i] / std::pow(c2, i + 1)) : 0.0f;
     p.out_dt = out_dtype == KV_INT4_BF16 ? DType::BF16 : (out_dtype == KV_INT4_F16 ? DType::F16 : DType::F32);
     p.q_bf16 = q_dtype == KV_INT4_BF16;
     p.tiles = lay.tiles;

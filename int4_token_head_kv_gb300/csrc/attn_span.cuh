@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                         mag = max3(mag, fabsf(xa.x), fabsf(xa.y));
                         mag = max3(mag, fabsf(xb.x), fabsf(xb.y));
                     }
-                    if (__all_sync(0xffffffffu, mag <= p.cap_small)) {
+                    if (__all_sync(0xffffffffu, mag <= 0.5f * p.cap_l2)) {
 #pragma unroll
                         for (int i = 0; i < 64; i += 2) set(i, capped_small(at(i), p, (i & 2) ? mob2 : moa2));
                     } else {

@@ -140,8 +140,7 @@ struct SpanParams {
     float c;                    // fp32(1 / sqrt(head_size)); 1 for INT8 rows
     float softcap;              // 0: none
     float cap_l2, cap_in;       // C = softcap log2 e, 2 / softcap
-    float cap_small;            // logits of at most this size take the polynomial
-    float cap_q[3];             // its coefficients
+    float cap_q[3];             // coefficients of the polynomial that logits within C / 2 take
     DType out_dt;
     int q_bf16;
     int tiles;                  // row tiles per kv head of the grid: of the batch (tiled) or of a sequence
