@@ -1,4 +1,5 @@
-"""Host-side refusals of the rotary writes with several axes: every call below fails its validation (or has nothing
+"""Host-side refusals of the rotary writes with several axes and of the span attentions: every call below fails its
+validation (or has nothing
 to do) before any CUDA work."""
 import ctypes
 
@@ -68,6 +69,24 @@ def test_span_attention(lib, name):
     for x in ("q", "cache", "out"):
         assert call(**{x: FAKE + 8}) == 3, x
     assert call(n=0, q=None) == 0 and call(ns=0) == 0
+
+
+def test_span_workspace_refusals(lib):
+    # 12 single tokens on up to 64000 keys: split, so the partials need their room
+    need = lib.kv_int4_span_workspace_bytes
+    need.restype, need.argtypes = szt, [i64, i32, i32, i32, i32, i32, i32]
+    n = need(12, 8, 2, 128, 12, 1, 64000)
+    assert n > 0
+    f = lib.kv_int4_span_attention
+    f.restype = ctypes.c_int
+    f.argtypes = [vp, ctypes.c_int, i64, i32, vp, i64, i32, i32, i32, vp, i32, vp, vp, i32, i32, i32, f32, vp, vp, vp, f32,
+                  vp, vp, ctypes.c_int, vp, szt, vp]
+
+    def call(ws, size):
+        return f(FAKE, 1, 12, 8, FAKE, 8, 2, 128, 16, FAKE, 4000, FAKE, FAKE, 12, 1, 64000, 0.1, FAKE, None, None, 0.0,
+                 None, FAKE, 2, ws, size, None)
+
+    assert call(None, n) == 4 and call(FAKE, n - 1) == 4 and call(FAKE, 0) == 4 and call(FAKE + 8, n) == 3
 
 
 def test_span_workspace(lib):
