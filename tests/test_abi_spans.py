@@ -1,6 +1,5 @@
 """Host-side refusals of the rotary writes with several axes and of the span attentions: every call below fails its
-validation (or has nothing
-to do) before any CUDA work."""
+validation (or has nothing to do) before any CUDA work."""
 import ctypes
 
 import pytest
