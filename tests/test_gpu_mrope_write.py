@@ -119,6 +119,20 @@ def test_equal_positions_give_the_one_axis_write():
     assert torch.equal(a, b) and torch.equal(qa, qb)
 
 
+@pytest.mark.parametrize("bits", [4, 8, 2])
+def test_slots_past_32_bit_offsets(bits):
+    """Slots whose rows lie more than 2^32 bytes into a cache: the bytes of the same slots of a small one."""
+    c = _case(50, 8, 2, 64, (12, 10, 10), torch.bfloat16, 3)
+    ref, _, _ = _reference(bits, c, 8, 2, False, False, 0)
+    far = (1 << 32) // ref[0].size + 3
+    cache = torch.zeros((far + c["nb"], *ref.shape[1:]), dtype=torch.uint8, device="cuda")
+    x = c["x"].cuda()
+    _call(bits, x[:, :8], x[:, 8:10], x[:, 10:], torch.from_numpy(c["pos"]).cuda(), torch.from_numpy(c["tab"]).cuda(), c["sections"],
+          torch.from_numpy(c["slots"] + 16 * far).cuda(), torch.from_numpy(c["signs"]).cuda(), cache)
+    assert np.array_equal(cache[far:].cpu().numpy(), ref)
+    assert not bool(cache[:far].any())
+
+
 def test_in_place_on_a_stream_and_replayed():
     c = _case(600, 32, 8, 128, (24, 20, 20), torch.float16, seed=8, max_pos=2048)
     ref, qr, _ = _reference(4, c, 32, 8, True, False, 0)

@@ -334,6 +334,38 @@ def test_captured_calls_on_a_stream_of_their_own():
     assert torch.equal(args[0][2]["out"], wa) and torch.equal(args[1][2]["out"], wb)
 
 
+@pytest.mark.parametrize("bits, hq, h, d", [(4, 8, 2, 128), (4, 16, 8, 64), (8, 4, 1, 128), (8, 8, 8, 64), (2, 4, 4, 128), (2, 8, 2, 64)])
+def test_blocks_past_32_bit_offsets(bits, hq, h, d):
+    """The same rows in blocks more than 2^32 bytes into a cache: the same bits."""
+    b = Batch(bits, [700, 33, 1], [150, 33, 1], hq, h, d)
+    want = b.call()
+    one = b.cache[0].numel()
+    far = (1 << 32) // one + 5
+    cache = torch.empty((far + b.cache.shape[0], *b.cache.shape[1:]), dtype=torch.uint8, device="cuda")
+    cache[far:] = b.cache
+    b.cache, b.tables = cache, np.where(b.tables >= 0, b.tables + far, b.tables).astype(np.int32)
+    assert torch.equal(b.call(), want)
+    single = Batch(bits, [700, 33, 1], [1, 1, 1], hq, h, d)
+    want = single.call()
+    cache[far:] = single.cache
+    single.cache, single.tables = cache, np.where(single.tables >= 0, single.tables + far, single.tables).astype(np.int32)
+    assert torch.equal(single.call(), want)
+
+
+@pytest.mark.parametrize("bits", [4, 8, 2])
+def test_many_sequences(bits):
+    """Thousands of sequences, most of them single tokens, some without any, and a few chunks."""
+    r = np.random.default_rng(5)
+    n = 2500
+    qlens, lens = np.where(r.random(n) < 0.1, 0, 1), r.integers(1, 40, n)
+    some = r.choice(n, 3, replace=False)
+    qlens[some], lens[some] = (70, 200, 33), (70, 300, 400)
+    b = Batch(bits, lens, qlens, 4, 2, 64, seed=5)
+    _check(b, key_begin=b.pos() - 20)
+    singles = Batch(bits, r.integers(0, 40, n), np.ones(n, int), 4, 2, 64, seed=6)
+    _check(singles)
+
+
 def test_the_same_call_gives_the_same_bits():
     b = Batch(4, (4000, 700), (200, 3), 32, 8, 128, seed=19)
     first = b.call(**_spans("any", b))
