@@ -161,6 +161,11 @@ __device__ __forceinline__ float2 capped_small(float2 x, const SpanParams& p, fl
 // further power of two of their own, and the masked path.
 constexpr int kSpanExp = 2;
 
+// INT8 queries are not rotated: their 8 or 11 bits are fp16 numbers, or lie on fp16's smallest step, as they are.  The low
+// halves are 0, and the products with them are left out.
+template <int BITS>
+constexpr bool kSpanLow = BITS != 8;
+
 // Where a query row's keys are: lo <= j < hi (none: an empty span, or no row).
 struct Span {
     int lo, hi;
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 if constexpr (FEW) {   // row b: the low halves of row a
                     hw[2] = lw[0];
                     hw[3] = lw[1];
-                } else {
+                } else if constexpr (kSpanLow<BITS>) {
                     tmem_st_q1(trow + Tm::kQl + 8 * q, lw);
                 }
                 tmem_st_q1(trow + Tm::kQh + 8 * q, hw);
@@ -1119,7 +1124,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 const uint64_t kd = (j & 1) ? kd1 : kd0;
                 if (leader) {
 #pragma unroll
-                    for (int half = 0; half < (FEW ? 1 : 2); ++half) {
+                    for (int half = 0; half < (FEW || !kSpanLow<BITS> ? 1 : 2); ++half) {
 #pragma unroll
                         for (int kk = 0; kk < KSTEPS; ++kk)
                             mma_ts(sd, tmem + (half ? Tm::kQl : Tm::kQh) + 8u * kk,
