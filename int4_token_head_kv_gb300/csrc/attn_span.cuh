@@ -62,9 +62,9 @@ struct SpLayout {
     static constexpr uint32_t kRaw = 2 * kPfPairs * kTile;
     static constexpr uint32_t kSk = kRaw + kStages * 2 * kPlane;                  // [kring][128] f32 s_K k0 2^-e
     static constexpr uint32_t kDeadF = kSk + kPfKRing * kPfKeys * 4;              // [kring][4] u32: positions with no key
-    static constexpr uint32_t kSv = kDeadF + kPfKRing * 4 * 4;                    // [pairs][128] f32 s_V
-    static constexpr uint32_t kEblk = kSv + kPfPairs * kPfKeys * 4;               // [pairs][4] per-warp largest V exponent
-    static constexpr uint32_t kWhere = kEblk + kPfPairs * 4 * 4;                               // i32: sequence, query tile, first key, end of the keys
+    static constexpr uint32_t kSv = kDeadF + kPfKRing * 4 * 4;                    // [kring][128] f32 s_V
+    static constexpr uint32_t kEblk = kSv + kPfKRing * kPfKeys * 4;               // [kring][4] per-warp largest V exponent
+    static constexpr uint32_t kWhere = kEblk + kPfKRing * 4 * 4;                               // i32: sequence, query tile, first key, end of the keys
     static constexpr uint32_t kHeld = kWhere + 16;                                // [stages] u32: blocks of a staged tile that hold keys
     static constexpr uint32_t kScan = kHeld + kStages * 4;                        // [20] u32
     static constexpr uint32_t kRs = kScan + 20 * 4;                               // [128] f32 2^-d of each row's own prescale
@@ -72,9 +72,9 @@ struct SpLayout {
     static constexpr uint32_t kSignBits = kFin + 128 * 4;                         // [4] u32
     static constexpr uint32_t kCsign = (kSignBits + 16 + 15u) & ~15u;             // [D] f32 +-c of each dimension
     static constexpr uint32_t kBars = (kCsign + D * 4 + 7u) & ~7u;
-    // k_full[kring], k_free[pairs], v_full[pairs], pv_done[pairs], s_full[2], p_full[2], q_ready,
+    // k_full[kring], sv_full[kring], k_free[pairs], v_full[pairs], pv_done[pairs], s_full[2], p_full[2], q_ready,
     // flush, q_tma, rot_in, rot_done, epi, raw_full[plane][stages], raw_free[plane][stages]
-    static constexpr int kNumBars = kPfKRing + 3 * kPfPairs + 4 + 6 + 4 * kStages;
+    static constexpr int kNumBars = 2 * kPfKRing + 3 * kPfPairs + 4 + 6 + 4 * kStages;
     static constexpr uint32_t kTmemSlot = kBars + kNumBars * 8;
     static constexpr uint32_t kFlags = kTmemSlot + 4;
     static constexpr uint32_t kBytes = kFlags + 4 + 1024;                         // + alignment slack
@@ -180,6 +180,10 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
     using Ly = SpLayout<D, BITS>;
     using Tm = PfTmem<D>;
     constexpr int KSTEPS = D / 16, RB = (int)Ly::kRowBytes, kStages = Ly::kStages;
+    // Whether the softmax waits for the V scales alone and the MMA warp for the V tile.  608 queries on 8800 keys: INT8, whose
+    // longer rows are converted in one go once their tile is free, 102 us with it and 109 without; with options 141
+    // and 144 (cap), 115 and 118 (bias); INT4 without options 100 and 96, INT2 103 and 101, as P.V waits for two barriers.
+    constexpr bool EARLY = BITS == 8 || OPTS;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -258,8 +262,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
     uint32_t* eblkw = reinterpret_cast<uint32_t*>(smem + Ly::kEblk);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::kBars);
     uint64_t* k_full = bars;                    // [kring] K tile and scales of tile j (4 warps)
-    uint64_t* k_free = k_full + kPfKRing;       // [pairs] K tile j % 2 read by S of tile j (commit)
-    uint64_t* v_full = k_free + kPfPairs;       // [pairs] V tile and scales of tile j (4 warps)
+    uint64_t* sv_full = k_full + kPfKRing;      // [kring] V scales of tile j (4 warps; EARLY)
+    uint64_t* k_free = sv_full + kPfKRing;      // [pairs] K tile j % 2 read by S of tile j (commit)
+    uint64_t* v_full = k_free + kPfPairs;       // [pairs] V tile j converted (4 warps)
     uint64_t* pv_done = v_full + kPfPairs;      // [pairs] P.V of tile j done (commit): V tile j % 2 and O free
     uint64_t* s_full = pv_done + kPfPairs;      // [2] S of the tile in tensor memory (commit)
     uint64_t* p_full = s_full + 2;              // [2] P of the tile in tensor memory (8 warps)
@@ -294,7 +299,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         }
     }
     if (threadIdx.x == 32) {
-        for (int b = 0; b < kPfKRing; ++b) mbar_init(&k_full[b], 4);
+        for (int b = 0; b < 2 * kPfKRing; ++b) mbar_init(&k_full[b], 4);   // and sv_full
         for (int b = 0; b < kPfPairs; ++b) {
             mbar_init(&k_free[b], 1);
             mbar_init(&v_full[b], 4);
@@ -509,8 +514,10 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         for (int j = idle ? nkt : 0; j < nkt && ok; ++j) {
             const int b = j & 1;
             const uint32_t ph = (uint32_t)(j >> 1) & 1u;
-            const int kb = j % kPfPairs, kr = j % kPfKRing;
-            ok = soon3(&s_full[b], ph, &k_full[kr], (uint32_t)(j / kPfKRing) & 1u, &v_full[kb], (uint32_t)(j / kPfPairs) & 1u);
+            const int kr = j % kPfKRing;
+            const uint32_t rph = (uint32_t)(j / kPfKRing) & 1u;
+            ok = EARLY ? soon3(&s_full[b], ph, &k_full[kr], rph, &sv_full[kr], rph)
+                       : soon3(&s_full[b], ph, &k_full[kr], rph, &v_full[j % kPfPairs], (uint32_t)(j / kPfPairs) & 1u);
             if (__any_sync(0xffffffffu, !ok)) {
                 ok = false;
                 break;
@@ -545,8 +552,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             const uint32_t dead = deadf[kr * 4] | deadf[kr * 4 + 1] | deadf[kr * 4 + 2] | deadf[kr * 4 + 3];
             const bool clean = dead == 0u && !own_any && key0 >= all_lo && key0 + kPfKeys <= all_hi;   // warp-uniform
             float bma = -INFINITY, bmb = -INFINITY;
-            const uint32_t* eb4 = eblkw + kb * 4;
-            const float4* svb = reinterpret_cast<const float4*>(sv + kb * kPfKeys) + t4;
+            const uint32_t* eb4 = eblkw + kr * 4;
+            const float4* svb = reinterpret_cast<const float4*>(sv + kr * kPfKeys) + t4;
             uint32_t eb_a = max(max(eb4[0], eb4[1]), max(eb4[2], eb4[3])), eb_b = eb_a;
             if (!OPTS && clean) {   // every key live and visible to both rows, rs 1
                 const float2 moa2 = make_float2(off_a, off_a), mob2 = make_float2(off_b, off_b);
@@ -925,8 +932,27 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 *reinterpret_cast<uint4*>(t + (uint32_t)(w / 8) * (kPfKeys * 128u) + swz128(trow, (uint32_t)(w % 8))) =
                     make_uint4(o[0], o[1], o[2], o[3]);
             };
-            uint32_t scale;   // the scale word
+            // EARLY: the V scales go ahead of the tile, which waits for P.V of tile j - 2; the weights wait for the scales alone.
+            // Their place was last read for the weights of tile j - 4, and P.V of tile j - 3 is done.  The K scales' place
+            // is free once S of tile j - 2 is done, as P.V of tile j - 4 came before it.
+            auto publish = [&](uint32_t scale) {
+                const float sc = BITS == 2 ? __uint_as_float(scale) * kU2Scale : __uint_as_float(scale);
+                if (pl == 0) {
+                    sk[(j % kPfKRing) * kPfKeys + slot_of_column(k)] = sc * k0;
+                    const uint32_t nokey = __ballot_sync(0xffffffffu, ((blocks >> (k / kBlockSize)) & 1u) == 0u);   // a row of zeros is a key, of logit 0
+                    if (lane == 0) deadf[(j % kPfKRing) * 4 + (warp & 3)] = nokey;
+                } else {
+                    // finite, so that a weight of 0 stays one; an infinite scale shows in the exponent
+                    sv[(j % kPfKRing) * kPfKeys + (int)trow] = fmaxf(fminf(sc, 3.4028234664e38f), -3.4028234664e38f);
+                    const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(sc) & 0x7FFFFFFFu);   // magnitudes order like their bits
+                    if (lane == 0) eblkw[(j % kPfKRing) * 4 + (warp & 3)] = (wmax >> 23) & 0xFFu;
+                    if (EARLY) arrive(&sv_full[j % kPfKRing]);
+                }
+            };
+            uint32_t scale;   // the scale word, without a zero point
             if constexpr (NW > 20) {   // long rows: a chunk of 16 numbers at a time
+                scale = reinterpret_cast<const uint32_t*>(win4)[NW - 1 + row_off];
+                if (EARLY && pl == 1) publish(scale);
                 ok = tile_free();
                 if (!ok) break;
                 uint4 c0 = win4[0];
@@ -944,7 +970,6 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     put(2 * c + 1, o);
                     c0 = c1;
                 }
-                scale = row_off == 0 ? c0.x : row_off == 1 ? c0.y : row_off == 2 ? c0.z : c0.w;
                 arrive(&raw_free[pl * kStages + st]);
             } else {
                 uint32_t kw[NW];
@@ -964,12 +989,12 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     for (int w = 0; w < NW; ++w) kw[w] = (row_off & 1) ? wv[w + 1] : wv[w];
                 }
                 arrive(&raw_free[pl * kStages + st]);
+                scale = BITS == 4 ? kw[NW - 1] & 0xFFFFFFF0u : kw[NW - 1];
+                if (EARLY && pl == 1) publish(scale);
                 ok = tile_free();
                 if (!ok) break;
-                scale = kw[NW - 1];
                 if constexpr (BITS == 4) {
-                    const uint32_t zp = scale & 15u, zl = zp_lo_half(zp) * 0x10001u, zh = zp_hi_half(zp) * 0x10001u;
-                    scale &= 0xFFFFFFF0u;
+                    const uint32_t zp = kw[NW - 1] & 15u, zl = zp_lo_half(zp) * 0x10001u, zh = zp_hi_half(zp) * 0x10001u;
 #pragma unroll
                     for (int w = 0; w < NW - 1; ++w) {
                         uint32_t o[4];
@@ -993,17 +1018,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     }
                 }
             }
-            const float sc = BITS == 2 ? __uint_as_float(scale) * kU2Scale : __uint_as_float(scale);
-            if (pl == 0) {
-                sk[(j % kPfKRing) * kPfKeys + slot_of_column(k)] = sc * k0;
-                const uint32_t nokey = __ballot_sync(0xffffffffu, ((blocks >> (k / kBlockSize)) & 1u) == 0u);   // a row of zeros is a key, of logit 0
-                if (lane == 0) deadf[(j % kPfKRing) * 4 + (warp & 3)] = nokey;
-            } else {
-                // finite, so that a weight of 0 stays one; an infinite scale shows in the exponent
-                sv[kb * kPfKeys + (int)trow] = fmaxf(fminf(sc, 3.4028234664e38f), -3.4028234664e38f);
-                const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(sc) & 0x7FFFFFFFu);   // magnitudes order like their bits
-                if (lane == 0) eblkw[kb * 4 + (warp & 3)] = (wmax >> 23) & 0xFFu;
-            }
+            if (!EARLY || pl == 0) publish(scale);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // generic writes -> tensor core reads
             arrive(pl ? &v_full[kb] : &k_full[j % kPfKRing]);
         }
@@ -1160,7 +1175,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     issue_s(t);
                 }
                 if (t > 0) {
-                    ok = soon(&p_full[(t - 1) & 1], (uint32_t)((t - 1) >> 1) & 1u);   // (which waited for the V tile)
+                    const uint32_t ph = (uint32_t)((t - 1) >> 1) & 1u;
+                    if constexpr (EARLY) ok = soon2(&p_full[(t - 1) & 1], ph, &v_full[(t - 1) & 1], ph);
+                    else ok = soon(&p_full[(t - 1) & 1], ph);   // (which waited for the V tile)
                     if (!__all_sync(0xffffffffu, ok)) break;
                     tc_fence_after();
                     issue_pv(t - 1);
