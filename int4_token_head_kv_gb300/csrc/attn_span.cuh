@@ -21,13 +21,13 @@
 // references taken from its few keys move again (107 us forwards, 121 backwards).
 //
 // What bounds it.  2048 queries behind 32768 INT4 tokens, 32 q / 8 kv heads, d 128, bf16: 1222 us, 931 TFLOP/s of the two
-// products that a softmax needs (the kernel does three: the queries' halves).  608 queries behind 8192: 96 us, the tensor
+// products that a softmax needs (the kernel does three, for the queries' halves).  608 queries behind 8192: 96 us, the tensor
 // pipe active for 50%, issue slots 56%, the shared-memory data pipe 47% besides the operands: no pipe is full.  A tile goes
 // through S, the softmax's registers, P.V and the S after next, with tensor memory full (two S, O and the queries), and each
 // hand-over is a commit or an arrival, a poll and a fence through a busy shared memory.  A tile takes about 2400 cycles, its
 // 24 products 2130 if alone.  A CTA's start (where it works, barriers, queries turned and split, first S) takes 7 us and its
 // end 3, which is half of the time of rows that see 1000 keys (one packed prompt of 16384 tokens: 608 us).  Single tokens,
-// 8 x 131072 INT2 keys, 64 q / 8 kv heads: 478 us, the same chain for 8 rows.
+// 8 x 131072 INT2 keys, 64 q / 8 kv heads: 472 us, the same chain for 8 rows.
 // Dropped after measuring: CTAs that stay for several row tiles, statically or by cluster launch control (that prompt: 821
 // and 804 us against 667 then; the hardware balances as well, and queries turned in registers take longer than a
 // product); a third V buffer (single tokens 513 against 505); two warps to a single token's softmax (560 against 504);
