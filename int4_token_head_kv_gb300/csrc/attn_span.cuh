@@ -137,15 +137,16 @@ __device__ __forceinline__ uint4 pack8(DType dt, const float* x) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// C tanh(x / C) + off of two logits x, all in log2 units: C - 2 C / (2^(x cap_in) + 1), cap_in two over the cap in natural
-// units.  The absolute error is a few 2^-24 of C.
+// C tanh(x / C) + off of two logits x, all in log2 units, for |x| > C / 2: C - 2 C / (2^(x cap_in) + 1), cap_in two over the
+// cap in natural units.  The error is a few 2^-24 of C, and of the result.
 __device__ __forceinline__ float2 capped(float2 x, float cap_in, float cap, float2 off) {
     const float2 y = mul_f32x2(x, make_float2(cap_in, cap_in));
     const float2 u = add_f32x2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), make_float2(1.0f, 1.0f));
     float2 r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(u.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(u.y));
-    return fma_f32x2(r, make_float2(-2.0f * cap, -2.0f * cap), add_f32x2(off, make_float2(cap, cap)));
+    const float2 c2 = make_float2(cap, cap);
+    return add_f32x2(fma_f32x2(mul_f32x2(r, make_float2(-2.0f, -2.0f)), c2, c2), off);
 }
 // The same for |x| <= C / 2, without the two special functions: x P(x^2), P a least-squares fit of tanh(y) / y, y = x / C,
 // that is off by 1.2e-6 at most.
@@ -622,9 +623,15 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     if (__all_sync(0xffffffffu, mag <= 0.5f * p.cap_l2)) {
 #pragma unroll
                         for (int i = 0; i < 64; i += 2) set(i, capped_small(at(i), p, (i & 2) ? mob2 : moa2));
-                    } else {
+                    } else {   // every logit takes the form of its own size, so that no hidden key and no other row reaches it
+                        // (608 queries behind 8192 tokens, a cap of 4: 200 us; 167 with one form for the warp)
+                        const float half = 0.5f * p.cap_l2;
 #pragma unroll
-                        for (int i = 0; i < 64; i += 2) set(i, capped(at(i), p.cap_in, p.cap_l2, (i & 2) ? mob2 : moa2));
+                        for (int i = 0; i < 64; i += 2) {
+                            const float2 x = at(i), off = (i & 2) ? mob2 : moa2;
+                            const float2 lo = capped_small(x, p, off), hi = capped(x, p.cap_in, p.cap_l2, off);
+                            set(i, make_float2(fabsf(x.x) <= half ? lo.x : hi.x, fabsf(x.y) <= half ? lo.y : hi.y));
+                        }
                     }
                 } else {
 #pragma unroll
