@@ -810,7 +810,7 @@ kv_int4_status span_attention_impl(int bits, const void* q, kv_int4_dtype q_dtyp
         return KV_INT4_EUNSUPPORTED;
     if (lay.total > 0 && (workspace == nullptr || workspace_bytes < lay.total)) return KV_INT4_EWORKSPACE;
     if (lay.total > 0 && !aligned16(workspace)) return KV_INT4_EALIGN;
-    SpanParams p;
+    SpanParams p = {};
     p.q = q;
     p.cache = cache;
     p.block_tables = block_tables;
@@ -834,13 +834,18 @@ kv_int4_status span_attention_impl(int bits, const void* q, kv_int4_dtype q_dtyp
     p.softmax_scale = softmax_scale;
     p.c = bits != 8 ? (float)(1.0 / std::sqrt((double)head_size)) : 1.0f;
     p.softcap = softcap;
-    p.cap_l2 = (float)((double)softcap * 1.4426950408889634);
-    p.cap_in = softcap > 0.0f ? std::min(2.0f / softcap, 3.0e38f) : 0.0f;   // finite: a logit of 0 stays one
-    // tanh(y) / y = 0.99999885 + fit . (y^2, y^4, y^6) for |y| <= 1 / 2, over powers of C^2.  Powers that leave fp32 belong
-    // to caps below 2.3e-7, to which a linear term does: within 1e-8 of the capped logit.
-    const double fit[3] = {-0.33323427, 0.13162696, -0.04370021}, c2 = (double)p.cap_l2 * (double)p.cap_l2;
-    const bool fits = softcap > 0.0f && std::pow(c2, 3) > 1.5e-40;
-    for (int i = 0; i < 3; ++i) p.cap_q[i] = fits ? (float)(fit[i] / std::pow(c2, i + 1)) : 0.0f;
+    p.cap_unit = 1.44269504f;
+    if (softcap > 0.0f) {
+        // tanh(y) / y = 1 - 0.33331882 y^2 + 0.13277628 y^4 - 0.04779421 y^6 for |y| <= 2 / 5, over powers of U / softcap
+        const double fit[4] = {1.0, -0.33331882, 0.13277628, -0.04779421};
+        const double unit = std::min(std::max((double)softcap, std::pow(2.0, -40)), std::pow(2.0, 60)), r = unit / softcap;
+        p.cap_unit = (float)(1.0 / unit);
+        p.cap_l2 = (float)std::min((double)softcap * 1.4426950408889634, 3.4e38);
+        p.cap_exp = (float)(2.0 * 1.4426950408889634 * r);
+        p.cap_small = (float)std::min(0.4 / r, 1.0e18);   // y^2 stays finite
+        // (below 2^-40: the linear term alone, which is within 1e-13)
+        for (int i = 0; i < 4; ++i) p.cap_q[i] = (float)(i > 0 && r > 1.0 ? 0.0 : fit[i] * std::pow(r, 2 * i) * unit * 1.4426950408889634);
+    }
     p.out_dt = out_dtype == KV_INT4_BF16 ? DType::BF16 : (out_dtype == KV_INT4_F16 ? DType::F16 : DType::F32);
     p.q_bf16 = q_dtype == KV_INT4_BF16;
     p.tiles = lay.tiles;

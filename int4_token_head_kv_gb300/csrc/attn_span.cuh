@@ -137,25 +137,27 @@ __device__ __forceinline__ uint4 pack8(DType dt, const float* x) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// C tanh(x / C) + off of two logits x, all in log2 units, for |x| > C / 2: C - 2 C / (2^(x cap_in) + 1), cap_in two over the
-// cap in natural units.  The error is a few 2^-24 of C, and of the result.
-__device__ __forceinline__ float2 capped(float2 x, float cap_in, float cap, float2 off) {
-    const float2 y = mul_f32x2(x, make_float2(cap_in, cap_in));
-    const float2 u = add_f32x2(make_float2(fast_exp2(y.x), fast_exp2(y.y)), make_float2(1.0f, 1.0f));
+// Capped scores come as y, the logit over the cap (or over the nearest bound of SpanParams::cap_unit's range): C tanh(y) + off of
+// two of them, C in log2 units, beyond the polynomial's range: C - 2 C / (e^(2y) + 1).  The error is a few 2^-24 of C,
+// and of the result.
+__device__ __forceinline__ float2 capped(float2 y, const SpanParams& p, float2 off) {
+    const float2 z = mul_f32x2(y, make_float2(p.cap_exp, p.cap_exp));
+    const float2 u = add_f32x2(make_float2(fast_exp2(z.x), fast_exp2(z.y)), make_float2(1.0f, 1.0f));
     float2 r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(u.x));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(u.y));
-    const float2 c2 = make_float2(cap, cap);
+    const float2 c2 = make_float2(p.cap_l2, p.cap_l2);
     return add_f32x2(fma_f32x2(mul_f32x2(r, make_float2(-2.0f, -2.0f)), c2, c2), off);
 }
-// The same for |x| <= C / 2, without the two special functions: x P(x^2), P a least-squares fit of tanh(y) / y, y = x / C,
-// that is off by 1.2e-6 at most.
-__device__ __forceinline__ float2 capped_small(float2 x, const SpanParams& p, float2 off) {
-    const float2 t = mul_f32x2(x, x);
-    float2 q = fma_f32x2(t, make_float2(p.cap_q[2], p.cap_q[2]), make_float2(p.cap_q[1], p.cap_q[1]));
+// The same for |y| <= 2 / 5, without the two special functions: y (C + C a1 y^2 + C a2 y^4 + C a3 y^6), a minimax fit of
+// tanh(y) / y with the value 1 at 0 that is off by 1.2e-7 at most, two roundings.  A fourth term would take logits within
+// half of the cap, and 785 us instead of 775 for 4 x 2048 queries behind 2048 keys, prefix masks, a cap of 50.
+__device__ __forceinline__ float2 capped_small(float2 y, const SpanParams& p, float2 off) {
+    const float2 t = mul_f32x2(y, y);
+    float2 q = fma_f32x2(t, make_float2(p.cap_q[3], p.cap_q[3]), make_float2(p.cap_q[2], p.cap_q[2]));
+    q = fma_f32x2(t, q, make_float2(p.cap_q[1], p.cap_q[1]));
     q = fma_f32x2(t, q, make_float2(p.cap_q[0], p.cap_q[0]));
-    q = fma_f32x2(t, q, make_float2(0.99999885f, 0.99999885f));
-    return fma_f32x2(x, q, off);
+    return fma_f32x2(y, q, off);
 }
 
 // The rows' power-of-two prescale: rotated queries of size 2^-4 .. 2^13 keep 22 bits in their fp16 halves; others take a
@@ -608,29 +610,32 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     }
                 }
                 const bool cap = OPTS && p.softcap > 0.0f;
+                constexpr int kPairStep = FEW ? 4 : 2;   // (FEW: row b's are none)
                 if (cap) {
                     float mag = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float4 k4 = skb[4 * (i / 2)];
                         const float2 k2 = (i & 1) ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
-                        const float2 xa = mul_f32x2(at(4 * i), k2), xb = mul_f32x2(at(4 * i + 2), k2);
+                        const float2 xa = mul_f32x2(at(4 * i), k2);
                         set(4 * i, xa);
-                        set(4 * i + 2, xb);
                         mag = max3(mag, fabsf(xa.x), fabsf(xa.y));
-                        mag = max3(mag, fabsf(xb.x), fabsf(xb.y));
+                        if constexpr (!FEW) {
+                            const float2 xb = mul_f32x2(at(4 * i + 2), k2);
+                            set(4 * i + 2, xb);
+                            mag = max3(mag, fabsf(xb.x), fabsf(xb.y));
+                        }
                     }
-                    if (__all_sync(0xffffffffu, mag <= 0.5f * p.cap_l2)) {
+                    if (__all_sync(0xffffffffu, mag <= p.cap_small)) {
 #pragma unroll
-                        for (int i = 0; i < 64; i += 2) set(i, capped_small(at(i), p, (i & 2) ? mob2 : moa2));
+                        for (int i = 0; i < 64; i += kPairStep) set(i, capped_small(at(i), p, (i & 2) ? mob2 : moa2));
                     } else {   // every logit takes the form of its own size, so that no hidden key and no other row reaches it
-                        // (608 queries behind 8192 tokens, a cap of 4: 200 us; 167 with one form for the warp)
-                        const float half = 0.5f * p.cap_l2;
+                        // (608 queries behind 8192 tokens, a cap of 4: 195 us; 167 with one form for the warp)
 #pragma unroll
-                        for (int i = 0; i < 64; i += 2) {
-                            const float2 x = at(i), off = (i & 2) ? mob2 : moa2;
-                            const float2 lo = capped_small(x, p, off), hi = capped(x, p.cap_in, p.cap_l2, off);
-                            set(i, make_float2(fabsf(x.x) <= half ? lo.x : hi.x, fabsf(x.y) <= half ? lo.y : hi.y));
+                        for (int i = 0; i < 64; i += kPairStep) {
+                            const float2 y = at(i), off = (i & 2) ? mob2 : moa2;
+                            const float2 lo = capped_small(y, p, off), hi = capped(y, p, off);
+                            set(i, make_float2(fabsf(y.x) <= p.cap_small ? lo.x : hi.x, fabsf(y.y) <= p.cap_small ? lo.y : hi.y));
                         }
                     }
                 } else {
@@ -918,7 +923,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         const int k = pl ? v_key(i128) : i128;
         const uint32_t trow = (uint32_t)(pl ? slot_of_column(k) : k);
         constexpr int NW = (int)Ly::kRowWords;            // words of a row: codes, then the scale word
-        const float k0 = p.c * p.softmax_scale * kLog2e * exp2i(-kSpanExp);   // raw score -> log2 logit
+        // raw score -> log2 logit, or logit over the cap (finite, so that a row of zeros has a logit of 0)
+        float k0 = p.c * p.softmax_scale * (OPTS ? p.cap_unit : kLog2e) * exp2i(-kSpanExp);
+        if (OPTS) k0 = fmaxf(fminf(k0, 3.0e38f), -3.0e38f);
         const int row_off = ((k % kBlockSize) * H + h) & 3;   // the row's first word in its window (row bytes are 4 mod 16)
         const uint32_t row_at = boxes ? (uint32_t)(k / kBlockSize * group + k % group) * Ly::box_bytes((uint32_t)group) +
                                             (uint32_t)(k % kBlockSize / group) * Ly::kWindow * 4

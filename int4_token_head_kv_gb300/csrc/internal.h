@@ -139,8 +139,12 @@ struct SpanParams {
     float softmax_scale;
     float c;                    // fp32(1 / sqrt(head_size)); 1 for INT8 rows
     float softcap;              // 0: none
-    float cap_l2, cap_in;       // C = softcap log2 e, 2 / softcap
-    float cap_q[3];             // coefficients of the polynomial that logits within C / 2 take
+    // With a cap the kernel forms y = logit cap_unit, cap_unit = 1 / U, U = softcap within 2^-40 .. 2^60 (without: log2 e)
+    float cap_unit;
+    float cap_l2;               // softcap log2 e
+    float cap_exp;              // e^(2 logit / softcap) = 2^(y cap_exp)
+    float cap_small;            // up to this |y| softcap tanh(logit / softcap) log2 e = y (cap_q . (1, y^2, y^4, y^6))
+    float cap_q[4];
     DType out_dt;
     int q_bf16;
     int tiles;                  // row tiles per kv head of the grid: of the batch (tiled) or of a sequence

@@ -1,5 +1,5 @@
-"""The attention over key spans at the edges of what its arithmetic holds: capped scores and what a row does not see,
-the accuracy of the cap, values that are not finite, scales far apart, and positions past 2^24."""
+"""The attention over key spans at the edges of what its arithmetic holds: capped scores and what a row does not see, and the
+accuracy of the cap."""
 import numpy as np
 import pytest
 import torch
@@ -68,3 +68,42 @@ def test_other_rows_queries_reach_no_bit(bits, softcap):
         rest = torch.ones(2 * qlen, 8, dtype=torch.bool, device="cuda")
         rest[::2, 1::2] = False
         assert torch.equal(got[rest], clean[rest])
+
+
+# ------------------------------------------------------------------ the accuracy of the cap
+
+@pytest.mark.parametrize("qlen", [1, 70])
+@pytest.mark.parametrize("softcap", [8.0, 50.0, 1e3, 1e5, 1e12, 3e38])
+def test_capped_scores_keep_their_bits(softcap, qlen):
+    """Logits of -3 .. 3 through caps from 8 on, the weights read off one by one: INT8 keys a_j e_0, values
+    127 e_j and queries e_0 are exact, so the weight of key j is the output's element j over 127.
+
+    Relative tolerance.  A logit s of at most 3: three roundings up to the product S s_K, the fit (1.2e-7, two
+    roundings) and its last two roundings, 7 2^-24 of s: 1.26e-6.  Its exponent, below 16 in log2 units, is rounded when
+    the offset is added and again when the reference moves: 2^-21 + 2^-22 log2 units at most, 0.5e-6.  A weight takes its
+    own logit's error and, through the sum, those of the others: twice 1.76e-6.  Its exponential 2^-22, its two fp16 halves
+    2^-22 (the weights lie above 2^-9 of the largest, which is raised to 2^6), scale, sum and quotient 3 2^-24: 0.7e-6.
+    Together 4.2e-6."""
+    kv = _kv()
+    n, d = 96, 128
+    k, v = torch.zeros(n, 1, d, device="cuda"), torch.zeros(n, 1, d, device="cuda")
+    k[:, 0, 0] = torch.linspace(-3, 3, n, device="cuda")
+    v[torch.arange(n), 0, torch.arange(n)] = 127.0
+    cache = torch.zeros(kv.kv_int8_cache_shape(n // 16, 16, 1, d), dtype=torch.uint8, device="cuda")
+    kv.kv_int8_write(k.half(), v.half(), torch.arange(n, device="cuda"), cache)
+    q = torch.zeros(qlen, 1, d, device="cuda", dtype=torch.float16)
+    q[:, 0, 0] = 1.0
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    out = kv.kv_int8_span_attention(q, cache, torch.arange(n // 16, dtype=torch.int32, device="cuda")[None], ints(n),
+                                    ints(0, qlen), 1.0, max_query_len=qlen, max_seq_len=n, softcap=softcap,
+                                    key_end=torch.full((qlen,), n, dtype=torch.int32, device="cuda"), out_dtype=torch.float32)
+    from oracle import int8 as o8
+    rows = cache.cpu().numpy()[:, 0].reshape(n, -1)
+    s = o8.decode_rows(np.ascontiguousarray(rows)).astype(np.float64)[:, 0]
+    assert abs(s).max() > 2.99
+    cap = float(np.float32(softcap))
+    s = cap * np.tanh(s / cap)
+    w = np.exp(s - s.max())
+    w /= w.sum()
+    got = out.double().cpu().numpy()[:, 0, :n] / 127.0
+    assert np.abs(got / w - 1).max() <= 4.3e-6
