@@ -579,8 +579,9 @@ kv_int4_status kv_int4_paged_attention_noalloc_ex(const void* q, kv_int4_dtype q
  *   out = sum_j softmax(s)_j x_V,j;  zeros for an empty span.
  * Document mask: key_begin = the first position of the query's document.  Prefix mask: key_end = max(pos + 1, prefix
  * length).  An image's tokens: key_end = the image's end.  Sliding window: key_begin = pos - window.
- * What a row does not see does not reach it: its keys and values may be infinite or NaN.  A visible row of zeros
- * (never written) is a key of logit 0 and a value of 0.
+ * What a row does not see does not reach it: its keys and values may be infinite or NaN.  A visible key or value that
+ * is not finite leaves nothing finite in the row's output.  A visible row of zeros (never written) is a key of logit
+ * 0 and a value of 0.
  *
  * Computation: one kernel for chunks and single tokens (tcgen05), 128 rows (query tokens x the heads of one kv head)
  * against the keys that some of them see; with few row tiles the keys are split among the SMs and a second kernel

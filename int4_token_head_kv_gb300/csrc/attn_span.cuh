@@ -709,6 +709,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 const float fm_a = up_a ? (any_a ? fast_exp2(da) : 0.0f) : 1.0f, fm_b = up_b ? (any_b ? fast_exp2(db) : 0.0f) : 1.0f;
                 any_a = any_a || up_a;
                 any_b = any_b || up_b;
+                // a visible value that is not finite shows in the sum, whatever its weight
+                if (eb_a == 255u) l_a = __uint_as_float(0x7FC00000u), eb_a = 254u;
+                if (eb_b == 255u) l_b = __uint_as_float(0x7FC00000u), eb_b = 254u;
                 // rebase from 2^(127 - E) to 2^(127 - eb); 0 when the jump underflows
                 auto rebase = [](uint32_t& E, uint32_t eb, float& fe, float& de) {
                     const uint32_t Eeff = E ? E : 127u;
@@ -952,11 +955,12 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             auto publish = [&](uint32_t scale) {
                 const float sc = BITS == 2 ? __uint_as_float(scale) * kU2Scale : __uint_as_float(scale);
                 if (pl == 0) {
-                    sk[(j % kPfKRing) * kPfKeys + slot_of_column(k)] = sc * k0;
+                    // (a key that is not finite: NaN, also where its products with a query have the same sign)
+                    sk[(j % kPfKRing) * kPfKeys + slot_of_column(k)] = fabsf(sc) <= 3.4028234664e38f ? sc * k0 : __uint_as_float(0x7FC00000u);
                     const uint32_t nokey = __ballot_sync(0xffffffffu, ((blocks >> (k / kBlockSize)) & 1u) == 0u);   // a row of zeros is a key, of logit 0
                     if (lane == 0) deadf[(j % kPfKRing) * 4 + (warp & 3)] = nokey;
                 } else {
-                    // finite, so that a weight of 0 stays one; an infinite scale shows in the exponent
+                    // finite, so that a weight of 0 stays one; a scale that is not finite shows in the exponent
                     sv[(j % kPfKRing) * kPfKeys + (int)trow] = fmaxf(fminf(sc, 3.4028234664e38f), -3.4028234664e38f);
                     const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(sc) & 0x7FFFFFFFu);   // magnitudes order like their bits
                     if (lane == 0) eblkw[(j % kPfKRing) * 4 + (warp & 3)] = (wmax >> 23) & 0xFFu;
