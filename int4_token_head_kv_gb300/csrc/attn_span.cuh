@@ -64,8 +64,8 @@ struct SpLayout {
     static constexpr uint32_t kDeadF = kSk + kPfKRing * kPfKeys * 4;              // [kring][4] u32: positions with no key
     static constexpr uint32_t kSv = kDeadF + kPfKRing * 4 * 4;                    // [kring][128] f32 s_V
     static constexpr uint32_t kEblk = kSv + kPfKRing * kPfKeys * 4;               // [kring][4] per-warp largest V exponent
-    static constexpr uint32_t kWhere = kEblk + kPfKRing * 4 * 4;                               // i32: sequence, query tile, first key, end of the keys
-    static constexpr uint32_t kHeld = kWhere + 16;                                // [stages] u32: blocks of a staged tile that hold keys
+    static constexpr uint32_t kWhere = kEblk + kPfKRing * 4 * 4;                               // i32: sequence, query tile, first key, end of the keys, first query's position
+    static constexpr uint32_t kHeld = kWhere + 32;                                // [stages] u32: blocks of a staged tile that hold keys
     static constexpr uint32_t kScan = kHeld + kStages * 4;                        // [20] u32
     static constexpr uint32_t kRs = kScan + 20 * 4;                               // [128] f32 2^-d of each row's own prescale
     static constexpr uint32_t kFin = kRs + 128 * 4;                               // [128] f32 what a row's O is multiplied with
@@ -299,6 +299,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         if (lane == 0) {
             where[2] = lo;
             where[3] = hi;
+            where[4] = pos0 + qt0;
         }
     }
     if (threadIdx.x == 32) {
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         bool any_a = false, any_b = false;
         float l_a = 0.0f, l_b = 0.0f;           // this thread's part of the sums of 2^(127+raise-E) p
         uint32_t E_a = 0, E_b = 0;              // reference biased exponents of the V scales that the rows see (0: none yet)
-        const float pos_a = (float)(pos0 + qt0 + wa / G), pos_b = (float)(pos0 + qt0 + wb / G);
+        const float pos_a = (float)(wa / G - 2 * t4), pos_b = (float)(wb / G - 2 * t4);   // the row's position - 2t from the tile's first one
         float sl_a = 0.0f, sl_b = 0.0f;
         if (OPTS && p.alibi) {
             sl_a = __ldg(p.alibi + h * G + wa % G) * kLog2e;
@@ -648,7 +649,9 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     }
                 }
                 if (OPTS && p.alibi) {
-                    const float da0 = pos_a - (float)(key0 + 2 * t4), db0 = pos_b - (float)(key0 + 2 * t4);
+                    // distances, not positions, as fp32 numbers: near ones are exact however long the context.  (The first
+                    // query's position from shared memory: registers are short here, 4 x 2048 queries with a cap 781 us against 783.)
+                    const float first = (float)(where[4] - key0), da0 = first + pos_a, db0 = first + pos_b;
                     const float2 sla2 = make_float2(-sl_a, -sl_a), slb2 = make_float2(-sl_b, -sl_b);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {

@@ -1,9 +1,9 @@
-"""The attention over key spans on rows that are not finite."""
+"""The attention over key spans on rows that are not finite, and at positions past 2^24."""
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_span import Batch
+from test_gpu_span import Batch, _close
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +63,18 @@ def test_written_infinities_show(bits):
             if bool(torch.isfinite(_row(b, 0, 35)[0 if bad_key else 1, :, -4:].contiguous().view(torch.float32)).all()):
                 continue   # (the write made a finite row of it)
             assert not bool(torch.isfinite(b.call()).any())
+
+
+@pytest.mark.parametrize("far", [0, 1 << 24, 1 << 27])
+@pytest.mark.parametrize("bits", [4, 8, 2])
+def test_distances_in_long_contexts(bits, far):
+    """The last keys of a context of millions of tokens, whose earlier blocks nothing sees: distances are exact there."""
+    for qlen in (1, 3, 80):
+        b = Batch(bits, (300,), (qlen,), 8, 2, 128, seed=43)
+        slopes = np.linspace(0.1, 0.8, 8)
+        begin, end = np.full(qlen, 140), np.full(qlen, 300)
+        want = b.oracle(key_begin=begin, key_end=end, alibi_slopes=np.float32(slopes))
+        b.tables = np.concatenate([np.zeros((1, far // 16), np.int32), b.tables], axis=1)
+        b.lens = b.lens + np.int32(far)
+        got = b.call(max_seq_len=300 + far, key_begin=begin + far, key_end=end + far, alibi_slopes=slopes)
+        _close(got, *want)
