@@ -7,9 +7,8 @@
 // The products run on the fifth-generation tensor cores with the rows left in the domain they are stored in
 // (rotated, but for INT8): S = Q' N_K^T with the stored numbers N exact in fp16 (INT4 code - zp, INT8 code, INT2
 // centroid) and the rotated queries Q' as fp16 high + low halves, logit = S s_K k0 2^-e, one pass over the keys with
-// a running reference maximum m and a reference exponent E of the V scales per row, weights
-// w = 2^(logit - m + 127 + raise - E) s_V in fp16 (two halves but for a bf16 output), O += w N_V, everything
-// accumulated in fp32, out = O / l un-rotated.
+// one reference off per row, p = 2^(logit + off), weights w = p s_V in fp16 (two halves but for a bf16 output) with the
+// largest of a row between 2^6 and 2^15.9, l += p, O += w N_V, everything accumulated in fp32, out = O / l un-rotated.
 //
 // A CTA takes 128 rows (128 / G query tokens of one sequence x the G query heads of a kv head) against the keys that
 // some of them see, 128 at a time; tiles outside that range are not touched, so a document mask costs what its
@@ -63,7 +62,7 @@ struct SpLayout {
     static constexpr uint32_t kSk = kRaw + kStages * 2 * kPlane;                  // [kring][128] f32 s_K k0 2^-e
     static constexpr uint32_t kDeadF = kSk + kPfKRing * kPfKeys * 4;              // [kring][4] u32: positions with no key
     static constexpr uint32_t kSv = kDeadF + kPfKRing * 4 * 4;                    // [kring][128] f32 s_V
-    static constexpr uint32_t kEblk = kSv + kPfKRing * kPfKeys * 4;               // [kring][4] per-warp largest V exponent
+    static constexpr uint32_t kEblk = kSv + kPfKRing * kPfKeys * 4;               // [kring][4] per-warp largest |s_V| (its bits)
     static constexpr uint32_t kWhere = kEblk + kPfKRing * 4 * 4;                               // i32: sequence, query tile, first key, end of the keys, first query's position
     static constexpr uint32_t kHeld = kWhere + 32;                                // [stages] u32: blocks of a staged tile that hold keys
     static constexpr uint32_t kScan = kHeld + kStages * 4;                        // [20] u32
@@ -79,7 +78,7 @@ struct SpLayout {
     static constexpr uint32_t kFlags = kTmemSlot + 4;
     static constexpr uint32_t kBytes = kFlags + 4 + 1024;                         // + alignment slack
     static_assert(kBytes <= 232448, "shared memory");
-    static_assert(kSk % 16 == 0 && kSv % 16 == 0 && kCsign % 16 == 0, "16-byte accesses");
+    static_assert(kSk % 16 == 0 && kSv % 16 == 0 && kEblk % 16 == 0 && kCsign % 16 == 0, "16-byte accesses");
     static_assert(kRaw % 1024 == 0 && kPlane % 128 == 0 && kTile % 1024 == 0 && kBars % 8 == 0, "boxes on 128 bytes, swizzled tiles on 1024");
 };
 
@@ -164,6 +163,10 @@ __device__ __forceinline__ float2 capped_small(float2 y, const SpanParams& p, fl
 // further power of two of their own, and the masked path.
 constexpr int kSpanExp = 2;
 
+// The largest weights times scale, and weights, that a row may come to before its reference moves (log2), and the largest
+// finite number, which stands for a V scale that is not finite.
+constexpr float kSpanMaxW = 15.9f, kSpanMaxP = 90.0f, kSpanLargest = 3.4028234664e38f;
+
 // INT8 queries are not rotated: their 8 or 11 bits are fp16 numbers, or lie on fp16's smallest step, as they are.  The low
 // halves are 0, and the products with them are left out.
 template <int BITS>
@@ -183,10 +186,11 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
     using Ly = SpLayout<D, BITS>;
     using Tm = PfTmem<D>;
     constexpr int KSTEPS = D / 16, RB = (int)Ly::kRowBytes, kStages = Ly::kStages;
-    // Whether the softmax waits for the V scales alone and the MMA warp for the V tile.  608 queries on 8800 keys: INT8, whose
-    // longer rows are converted in one go once their tile is free, 102 us with it and 109 without; with options 141
-    // and 144 (cap), 115 and 118 (bias); INT4 without options 100 and 96, INT2 103 and 101, as P.V waits for two barriers.
-    constexpr bool EARLY = BITS == 8 || OPTS;
+    // Whether the softmax waits for the V scales alone and the MMA warp for the V tile.  INT8, whose longer rows are converted
+    // in one go once their tile is free, 608 queries on 8800 keys: 102 us with it and 109 without; with options 141 and 144
+    // (cap), 115 and 118 (bias).  Few rows: 8 x 131072 INT4 tokens 442 and 537.  INT4 and INT2 chunks without options: 101
+    // and 95, 108 and 104, as P.V waits for two barriers.
+    constexpr bool EARLY = BITS == 8 || OPTS || FEW;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -496,12 +500,12 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
         tc_fence_before();
         arrive(q_ready);
         // ---- the key tiles
-        // Reference maxima m (log2 units) as the exponents' offsets off = 127 + raise - E - m; E = 127 and off = 0
-        // until a row has a key (any).
+        // A row's reference: what is added to its logits (log2 units), so that its largest weight times scale lies between 2^6
+        // and 2^15.  The bound on its exponents that calls for another is the tile's, plus: 0, -inf for a row that has met
+        // no key yet, inf for one that is none.
         float off_a = 0.0f, off_b = 0.0f;
-        bool any_a = false, any_b = false;
-        float l_a = 0.0f, l_b = 0.0f;           // this thread's part of the sums of 2^(127+raise-E) p
-        uint32_t E_a = 0, E_b = 0;              // reference biased exponents of the V scales that the rows see (0: none yet)
+        float set_a = none_a ? INFINITY : -INFINITY, set_b = none_b ? INFINITY : -INFINITY;
+        float l_a = 0.0f, l_b = 0.0f;           // this thread's part of the sums of 2^(logit + off)
         const float pos_a = (float)(wa / G - 2 * t4), pos_b = (float)(wb / G - 2 * t4);   // the row's position - 2t from the tile's first one
         float sl_a = 0.0f, sl_b = 0.0f;
         if (OPTS && p.alibi) {
@@ -550,15 +554,15 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     s[4 * i + 2] = s[4 * i + 3] = 0u;
                 }
             }
-            // Exponents e = S s_K k0 2^-e - m + 127 + raise - E (one FMA) against the references as they
-            // are, and their row maxima; a reference that moves is added to them afterwards, which is rare.
+            // Exponents S s_K k0 2^-e + off (one FMA) with the references as they are, and the largest of the thread's; a
+            // reference that moves is added to them afterwards, which is rare.
+            float max_a = -INFINITY, max_b = -INFINITY;
             const float4* skb = reinterpret_cast<const float4*>(sk + kr * kPfKeys) + t4;   // columns 16q + (2t, 2t + 1, 8 + 2t, 9 + 2t)
             const uint32_t dead = deadf[kr * 4] | deadf[kr * 4 + 1] | deadf[kr * 4 + 2] | deadf[kr * 4 + 3];
             const bool clean = dead == 0u && !own_any && key0 >= all_lo && key0 + kPfKeys <= all_hi;   // warp-uniform
-            float bma = -INFINITY, bmb = -INFINITY;
-            const uint32_t* eb4 = eblkw + kr * 4;
+            const uint4 eb4 = *reinterpret_cast<const uint4*>(eblkw + kr * 4);
+            const uint32_t largest = max(max(eb4.x, eb4.y), max(eb4.z, eb4.w));   // the tile's largest V scale
             const float4* svb = reinterpret_cast<const float4*>(sv + kr * kPfKeys) + t4;
-            uint32_t eb_a = max(max(eb4[0], eb4[1]), max(eb4[2], eb4[3])), eb_b = eb_a;
             if (!OPTS && clean) {   // every key live and visible to both rows, rs 1
                 const float2 moa2 = make_float2(off_a, off_a), mob2 = make_float2(off_b, off_b);
 #pragma unroll
@@ -566,13 +570,15 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     const float4 k4 = skb[4 * (i / 2)];
                     const float2 k2 = (i & 1) ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
                     const float2 ea = fma_f32x2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), k2, moa2);
-                    const float2 eb = fma_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k2, mob2);
                     s[4 * i] = __float_as_uint(ea.x);
                     s[4 * i + 1] = __float_as_uint(ea.y);
-                    s[4 * i + 2] = __float_as_uint(eb.x);
-                    s[4 * i + 3] = __float_as_uint(eb.y);
-                    bma = max3(bma, ea.x, ea.y);
-                    bmb = max3(bmb, eb.x, eb.y);
+                    max_a = max3(max_a, ea.x, ea.y);
+                    if constexpr (!FEW) {
+                        const float2 eb2 = fma_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), k2, mob2);
+                        s[4 * i + 2] = __float_as_uint(eb2.x);
+                        s[4 * i + 3] = __float_as_uint(eb2.y);
+                        max_b = max3(max_b, eb2.x, eb2.y);
+                    }
                 }
             } else {
                 // bit 2i + e of vis: the row sees the key of column 8i + 2t + e
@@ -645,7 +651,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                         const float4 k4 = skb[4 * (i / 2)];
                         const float2 k2 = (i & 1) ? make_float2(k4.z, k4.w) : make_float2(k4.x, k4.y);
                         set(4 * i, fma_f32x2(at(4 * i), k2, moa2));
-                        set(4 * i + 2, fma_f32x2(at(4 * i + 2), k2, mob2));
+                        if constexpr (!FEW) set(4 * i + 2, fma_f32x2(at(4 * i + 2), k2, mob2));
                     }
                 }
                 if (OPTS && p.alibi) {
@@ -657,7 +663,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     for (int i = 0; i < 16; ++i) {
                         const float c = (float)(8 * i);
                         set(4 * i, fma_f32x2(make_float2(fabsf(da0 - c), fabsf(da0 - (c + 1.0f))), sla2, at(4 * i)));
-                        set(4 * i + 2, fma_f32x2(make_float2(fabsf(db0 - c), fabsf(db0 - (c + 1.0f))), slb2, at(4 * i + 2)));
+                        if constexpr (!FEW) set(4 * i + 2, fma_f32x2(make_float2(fabsf(db0 - c), fabsf(db0 - (c + 1.0f))), slb2, at(4 * i + 2)));
                     }
                 }
                 if (!clean) {
@@ -671,74 +677,83 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    bma = max3(bma, __uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
-                    bmb = max3(bmb, __uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
-                }
-                // the V scales of the visible keys alone, where the tile's largest would move a reference
-                if (!clean && __any_sync(0xffffffffu, eb_a > E_a + (E_a ? kPxLazyExp : 0u) || eb_b > E_b + (E_b ? kPxLazyExp : 0u))) {
-                    uint32_t ma = 0u, mb = 0u;
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float4 v4 = svb[4 * q];
-                        const float v[4] = {v4.x, v4.y, v4.z, v4.w};   // keys 16q + (2t, 2t + 1, 8 + 2t, 9 + 2t)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t bits = (__float_as_uint(v[e]) & 0x7FFFFFFFu) + 1u;   // the largest finite value stands for infinity
-                            ma = max(ma, vis_a & (1u << (4 * q + e)) ? bits : 0u);
-                            mb = max(mb, vis_b & (1u << (4 * q + e)) ? bits : 0u);
-                        }
-                    }
-#pragma unroll
-                    for (int off = 1; off < 4; off <<= 1) {
-                        ma = max(ma, __shfl_xor_sync(0xffffffffu, ma, off));
-                        mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, off));
-                    }
-                    eb_a = ma >> 23;
-                    eb_b = mb >> 23;
+                    max_a = max3(max_a, __uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1]));
+                    if constexpr (!FEW) max_b = max3(max_b, __uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3]));
                 }
             }
-            bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 1));
-            bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 1));
-            bma = fmaxf(bma, __shfl_xor_sync(0xffffffffu, bma, 2));
-            bmb = fmaxf(bmb, __shfl_xor_sync(0xffffffffu, bmb, 2));
-            // the four threads of a row take the same decisions; a row without a reference takes the first one
-            const float eoff_a = (float)(127 + kPxRaise - (int)(E_a ? E_a : 127u)), eoff_b = (float)(127 + kPxRaise - (int)(E_b ? E_b : 127u));
-            const bool newE_a = E_a == 0u ? eb_a > 0u : eb_a > E_a + kPxLazyExp;
-            const bool newE_b = !FEW && (E_b == 0u ? eb_b > 0u : eb_b > E_b + kPxLazyExp);
-            const bool up_a = any_a ? bma > eoff_a + kPfLazyMax : bma > -INFINITY;
-            const bool up_b = !FEW && (any_b ? bmb > eoff_b + kPfLazyMax : bmb > -INFINITY);
-            if (__any_sync(0xffffffffu, up_a || up_b || newE_a || newE_b)) {
-                const float da = up_a ? eoff_a - bma : 0.0f, db = up_b ? eoff_b - bmb : 0.0f;   // old reference - new one
-                const float fm_a = up_a ? (any_a ? fast_exp2(da) : 0.0f) : 1.0f, fm_b = up_b ? (any_b ? fast_exp2(db) : 0.0f) : 1.0f;
-                any_a = any_a || up_a;
-                any_b = any_b || up_b;
-                // a visible value that is not finite shows in the sum, whatever its weight
-                if (eb_a == 255u) l_a = __uint_as_float(0x7FC00000u), eb_a = 254u;
-                if (eb_b == 255u) l_b = __uint_as_float(0x7FC00000u), eb_b = 254u;
-                // rebase from 2^(127 - E) to 2^(127 - eb); 0 when the jump underflows
-                auto rebase = [](uint32_t& E, uint32_t eb, float& fe, float& de) {
-                    const uint32_t Eeff = E ? E : 127u;
-                    fe = eb > Eeff + 126u ? 0.0f : __uint_as_float((127u + Eeff - eb) << 23);
-                    de = (float)((int)Eeff - (int)eb);
-                    E = eb;
+            // Weights p = 2^e and w = p s_V; w stays below 2^15.99, which is within fp16's range, and p below 2^90.  A row
+            // that meets its first key, or may pass a bound by the tile's largest scale, is looked at.  (A number's bits over
+            // 2^23 are its logarithm + 127, at most 0.087 too low.)
+            const float bound = fminf(fmaf((float)largest, -1.1920929e-7f, 127.0f + kSpanMaxW), kSpanMaxP);
+            const bool broken = largest >= 0x7F800000u;
+            if (__any_sync(0xffffffffu, max_a > bound + set_a || (!FEW && max_b > bound + set_b) || broken)) {
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    max_a = fmaxf(max_a, __shfl_xor_sync(0xffffffffu, max_a, o));
+                    max_b = fmaxf(max_b, __shfl_xor_sync(0xffffffffu, max_b, o));
+                }
+                // The largest w itself, over that of the largest p (or of 1): the largest scale may belong to a key of next to no
+                // weight, and a reference taken from it would leave the others' w below fp16's range.
+                float top_a = 0.0f, top_b = 0.0f;
+                const float2 ma2 = make_float2(-max_a, -max_a), mb2 = make_float2(-max_b, -max_b);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 v4 = svb[4 * (i / 2)];
+                    const float vx = fabsf((i & 1) ? v4.z : v4.x), vy = fabsf((i & 1) ? v4.w : v4.y);
+                    const float2 ea = add_f32x2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), ma2);
+                    top_a = max3(top_a, fast_exp2(ea.x) * vx, fast_exp2(ea.y) * vy);
+                    if constexpr (!FEW) {
+                        const float2 eb2 = add_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), mb2);
+                        top_b = max3(top_b, fast_exp2(eb2.x) * vx, fast_exp2(eb2.y) * vy);
+                    }
+                }
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    top_a = fmaxf(top_a, __shfl_xor_sync(0xffffffffu, top_a, o));
+                    top_b = fmaxf(top_b, __shfl_xor_sync(0xffffffffu, top_b, o));
+                }
+                if (broken) {   // a visible value that is not finite shows in the sum, whatever its weight
+#pragma unroll 1
+                    for (int q = 0; q < 8; ++q) {
+                        const float4 v4 = svb[4 * q];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0 + 16 * q + 8 * (e >> 1) + 2 * t4 + (e & 1);
+                            const float v = e == 0 ? v4.x : e == 1 ? v4.y : e == 2 ? v4.z : v4.w;
+                            if (fabsf(v) >= kSpanLargest) {
+                                if (key >= sa.lo && key < sa.hi) l_a = __uint_as_float(0x7FC00000u);
+                                if (key >= sb.lo && key < sb.hi) l_b = __uint_as_float(0x7FC00000u);
+                            }
+                        }
+                    }
+                }
+                // What a row's reference moves by: the largest w goes to 2^6 .. 2^7, if that is p <= 2^80.  A reference that
+                // holds stays, to the bit, whatever called: only what the row sees counts.
+                auto move = [](float& set, float m, float top) -> float {
+                    const float lg = fmaf((float)__float_as_uint(top), 1.1920929e-7f, -127.0f);
+                    if (!(m > -INFINITY) || set > 0.0f || (set == 0.0f && !(m + lg > kSpanMaxW || m > kSpanMaxP))) return 0.0f;
+                    set = 0.0f;
+                    return (float)(top > 0.0f ? min(kPxRaise + 127 - (int)(__float_as_uint(top) >> 23), 80) : 0) - m;
                 };
-                float fe_a = 1.0f, fe_b = 1.0f, de_a = 0.0f, de_b = 0.0f;
-                if (newE_a) rebase(E_a, eb_a, fe_a, de_a);
-                if (newE_b) rebase(E_b, eb_b, fe_b, de_b);
-                const float f_a = fm_a * fe_a, f_b = FEW ? f_a : fm_b * fe_b;
+                const bool had_a = set_a == 0.0f, had_b = set_b == 0.0f;
+                const float da = move(set_a, max_a, top_a), db = FEW ? 0.0f : move(set_b, max_b, top_b);
+                off_a += da;
+                off_b += db;
+                const float f_a = had_a && da != 0.0f ? fast_exp2(da) : 1.0f;
+                const float f_b = FEW ? f_a : had_b && db != 0.0f ? fast_exp2(db) : 1.0f;
                 l_a *= f_a;
                 l_b *= f_b;
-                off_a += da + de_a;
-                off_b += db + de_b;
-                const float2 da2 = make_float2(da + de_a, da + de_a), db2 = make_float2(db + de_b, db + de_b);
+                const float2 da2 = make_float2(da, da), db2 = make_float2(db, db);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float2 ea = add_f32x2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), da2);
-                    const float2 eb2 = add_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), db2);
                     s[4 * i] = __float_as_uint(ea.x);
                     s[4 * i + 1] = __float_as_uint(ea.y);
-                    s[4 * i + 2] = __float_as_uint(eb2.x);
-                    s[4 * i + 3] = __float_as_uint(eb2.y);
+                    if constexpr (!FEW) {
+                        const float2 eb2 = add_f32x2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), db2);
+                        s[4 * i + 2] = __float_as_uint(eb2.x);
+                        s[4 * i + 3] = __float_as_uint(eb2.y);
+                    }
                 }
                 if (j > 0 && __any_sync(0xffffffffu, f_a != 1.0f || f_b != 1.0f)) {
                     // O must hold P.V of the previous tile before it is rescaled
@@ -765,8 +780,8 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                     tmem_st_wait();
                 }
             }
-            // p' = 2^e, w = p' s_V as fp16 pairs over the first 64 S columns: the pair of columns 8i + 2t, + 1
-            // goes to column 8 (i / 2) + 2t + i % 2 (the V tile holds its rows in the matching order)
+            // w as fp16 pairs over the first 64 S columns: the pair of columns 8i + 2t, + 1 goes to column
+            // 8 (i / 2) + 2t + i % 2 (the V tile holds its rows in the matching order)
             float2 lsa = make_float2(0.0f, 0.0f), lsb = make_float2(0.0f, 0.0f);
             if constexpr (FEW) {   // the low halves of the weights as row b
 #pragma unroll
@@ -815,29 +830,29 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
             tc_fence_before();
             arrive(&p_full[b]);
         }
-        // ---- the output, or the split's partial: (m, l 2^(E - 127 - raise)) and O / l
+        // ---- the output, or the split's partial: (-off, l) with l normalised to 1 .. 2, and O / l
         if (ok) ok = wait(&pv_done[(nkt - 1) & 1], (uint32_t)((nkt - 1) >> 1) & 1u);
         l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
         l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
         l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
         l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
-        // a row that met only NaN (its query or the keys are not finite) shows it: no maximum tells
-        any_a = (any_a || l_a != l_a) && !none_a;
-        any_b = (any_b || l_b != l_b) && !none_b;
+        // (a row that met NaN shows it in its sum)
+        const bool any_a = l_a != 0.0f && !none_a, any_b = l_b != 0.0f && !none_b;
         if (t4 == 0) {
-            fin[ra] = any_a && l_a != 0.0f ? 1.0f / l_a : 0.0f;
-            fin[rb] = any_b && l_b != 0.0f ? 1.0f / l_b : 0.0f;
+            fin[ra] = any_a ? 1.0f / l_a : 0.0f;
+            fin[rb] = any_b ? 1.0f / l_b : 0.0f;
             if (p.splits > 1) {
-                auto partial = [&](int r, bool any, float l, float off, uint32_t E) {
+                auto partial = [&](int r, bool any, float l, float off) {
                     const int qt = qt0 + r / G;
                     if (qt >= qcount) return;
-                    E = E ? E : 127u;   // none: only rows of zeros
-                    const float m = (float)(127 + kPxRaise - (int)E) - off, es = __uint_as_float(E << 23) * exp2i(-kPxRaise);
+                    const uint32_t bits = __float_as_uint(l);
+                    float2 ml = make_float2((float)((int)(bits >> 23) - 127) - off, __uint_as_float((bits & 0x7FFFFFu) | 0x3F800000u));
+                    if (!(l < INFINITY)) ml = make_float2(0.0f, l);
                     reinterpret_cast<float2*>(p.part_ml)[((int64_t)(q0 + qt) * Hq + h * G + r % G) * p.splits + split] =
-                        any && ok ? make_float2(m, l * es) : make_float2(kNegBig, 0.0f);
+                        any && ok ? ml : make_float2(kNegBig, 0.0f);
                 };
-                partial(wa, any_a, l_a, off_a, E_a);
-                if constexpr (!FEW) partial(wb, any_b, l_b, off_b, E_b);
+                partial(wa, any_a, l_a, off_a);
+                if constexpr (!FEW) partial(wb, any_b, l_b, off_b);
             }
         }
         __syncwarp();
@@ -959,14 +974,14 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 const float sc = BITS == 2 ? __uint_as_float(scale) * kU2Scale : __uint_as_float(scale);
                 if (pl == 0) {
                     // (a key that is not finite: NaN, also where its products with a query have the same sign)
-                    sk[(j % kPfKRing) * kPfKeys + slot_of_column(k)] = fabsf(sc) <= 3.4028234664e38f ? sc * k0 : __uint_as_float(0x7FC00000u);
+                    sk[(j % kPfKRing) * kPfKeys + slot_of_column(k)] = fabsf(sc) <= kSpanLargest ? sc * k0 : __uint_as_float(0x7FC00000u);
                     const uint32_t nokey = __ballot_sync(0xffffffffu, ((blocks >> (k / kBlockSize)) & 1u) == 0u);   // a row of zeros is a key, of logit 0
                     if (lane == 0) deadf[(j % kPfKRing) * 4 + (warp & 3)] = nokey;
                 } else {
-                    // finite, so that a weight of 0 stays one; a scale that is not finite shows in the exponent
-                    sv[(j % kPfKRing) * kPfKeys + (int)trow] = fmaxf(fminf(sc, 3.4028234664e38f), -3.4028234664e38f);
+                    // finite, so that a weight of 0 stays one; a scale that is not finite shows in the largest one
+                    sv[(j % kPfKRing) * kPfKeys + (int)trow] = fmaxf(fminf(sc, kSpanLargest), -kSpanLargest);
                     const uint32_t wmax = __reduce_max_sync(0xffffffffu, __float_as_uint(sc) & 0x7FFFFFFFu);   // magnitudes order like their bits
-                    if (lane == 0) eblkw[(j % kPfKRing) * 4 + (warp & 3)] = (wmax >> 23) & 0xFFu;
+                    if (lane == 0) eblkw[(j % kPfKRing) * 4 + (warp & 3)] = wmax;
                     if (EARLY) arrive(&sv_full[j % kPfKRing]);
                 }
             };
