@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -317,15 +318,24 @@ _I64, _F32, _U8, _I32 = (torch.int64,), (torch.float32,), (torch.uint8,), (torch
 
 
 @functools.lru_cache(maxsize=256)
-def _pair_axes(sections: tuple, mixed: bool) -> bytes:
-    """The axis of every rotated pair, one byte each: the sections one after another, or dealt out in turn while
-    they last when ``mixed``."""
-    if not sections or len(sections) > 4 or any(not isinstance(n, int) or n < 0 for n in sections):
-        raise ValueError("sections must be one to four counts of pairs, one for each axis")
+def _axes_of(counts: tuple, mixed: bool) -> bytes:
+    """_pair_axes for a tuple of plain integers."""
     if not mixed:
-        return bytes(a for a, n in enumerate(sections) for _ in range(n))
-    turns = range(max(sections))
-    return bytes(a for i in turns for a, n in enumerate(sections) if i < n)
+        return bytes(a for a, n in enumerate(counts) for _ in range(n))
+    turns = range(max(counts))
+    return bytes(a for i in turns for a, n in enumerate(counts) if i < n)
+
+
+def _pair_axes(sections, mixed: bool) -> bytes:
+    """The axis of every rotated pair, one byte each: the sections one after another, or dealt out in turn while
+    they last when ``mixed``.  Integers of any type; what is refused does not depend on what was asked before."""
+    try:
+        counts = tuple(operator.index(n) for n in sections)
+    except TypeError:
+        counts = ()
+    if not 1 <= len(counts) <= 4 or min(counts) < 0 or sum(counts) > 1024:
+        raise ValueError("sections must be one to four counts of pairs, one for each axis")
+    return _axes_of(counts, mixed)
 
 
 def _rope_write(fn, bits, query, key, value, positions, cos_sin, slot_mapping, rht_signs, kv_cache, query_out,
@@ -358,7 +368,7 @@ def _rope_write(fn, bits, query, key, value, positions, cos_sin, slot_mapping, r
         if slot_mapping.shape != (T,) or positions.shape != (T,):
             raise ValueError("positions and slot_mapping must be [num_tokens]")
     else:
-        pairs = _pair_axes(tuple(sections), bool(mixed))
+        pairs = _pair_axes(sections, bool(mixed))
         if 2 * len(pairs) != table[1]:
             raise ValueError("the sections must sum to rot_dim / 2 pairs")
         if slot_mapping.shape != (T,) or positions.shape != (len(sections), T):
