@@ -594,7 +594,8 @@ kv_int4_status kv_int4_paged_attention_noalloc_ex(const void* q, kv_int4_dtype q
  * alibi_slopes        [num_q_heads] fp32 or NULL.
  * max_query_len       host int: max over b of q_len_b.  Queries past it are left as they were (counted as bad metadata).
  * max_seq_len         host int: >= max over b of seq_lens[b].  Longer contexts are clamped to it, and to the block
- *                     table (and counted as bad metadata).
+ *                     table (and counted as bad metadata).  The smaller of both at most 2^31 - 129, else
+ *                     KV_INT4_EUNSUPPORTED.
  * out                 [num_q_tokens, num_q_heads, head_size]; rows of no sequence are left as they were.
  * workspace           >= kv_int4_span_workspace_bytes(...) bytes, 16-B aligned (NULL when that is 0).  Overlapping
  *                     calls must not share a workspace.

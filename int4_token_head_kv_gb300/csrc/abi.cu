@@ -801,6 +801,8 @@ kv_int4_status span_attention_impl(int bits, const void* q, kv_int4_dtype q_dtyp
     if (!valid_dtype_16(q_dtype) || !(valid_dtype_16(out_dtype) || out_dtype == KV_INT4_F32)) return KV_INT4_EUNSUPPORTED;
     if (num_seqs > 65535 || num_q_tokens >= ((int64_t)1 << 31)) return KV_INT4_EUNSUPPORTED;
     if (!(softmax_scale == softmax_scale) || !(softcap >= 0.0f && softcap <= 3.0e38f)) return KV_INT4_EINVAL;
+    // 32-bit positions up to the end of the last tile of keys
+    if (std::min<int64_t>(max_seq_len, (int64_t)max_blocks_per_seq * kBlockSize) > INT32_MAX - 128) return KV_INT4_EUNSUPPORTED;
     if (num_q_tokens == 0 || num_seqs == 0) return KV_INT4_OK;
     if (!q || !cache || !block_tables || !seq_lens || !query_start_loc || (bits != 8 && !rht_signs) || !out) return KV_INT4_EINVAL;
     if (max_query_len < 1 || max_blocks_per_seq < 1) return KV_INT4_EINVAL;
