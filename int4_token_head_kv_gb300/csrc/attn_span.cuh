@@ -82,9 +82,10 @@ struct SpLayout {
     static_assert(kRaw % 1024 == 0 && kPlane % 128 == 0 && kTile % 1024 == 0 && kBars % 8 == 0, "boxes on 128 bytes, swizzled tiles on 1024");
 };
 
-// The INT2 centroids as the tiles hold them are 1.0002228 a and 1.0002134 b in fp16; with 1 / 1.0002181 in the scales both are
-// within 5e-6.
-constexpr float kU2Scale = 0.99978195f;
+// The INT2 centroids as the tiles hold them: of all pairs of fp16 numbers the one whose ratio is nearest b / a, 1.7939453 and
+// 5.984375 (a byte table as kU2Lo, kU2Hi).  With a / 1.7939453 in the scales both are within 2.2e-7.
+constexpr uint32_t kSpanU2Lo = 0xBF2DC5FCu, kSpanU2Hi = 0x45FC3F2Du;
+constexpr float kU2Scale = 0.25239348f;
 
 // The dimension a tile column holds.
 template <int BITS>
@@ -1048,7 +1049,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
 #pragma unroll
                     for (int w = 0; w < NW - 1; ++w) {
                         uint32_t oa[4], ob[4];
-                        unpack_u2_x2(kw[w], oa, ob);
+                        unpack_u2_x2<kSpanU2Lo, kSpanU2Hi>(kw[w], oa, ob);
                         put(2 * w, oa);
                         put(2 * w + 1, ob);
                     }

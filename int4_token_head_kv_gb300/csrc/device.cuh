@@ -364,13 +364,14 @@ __device__ __forceinline__ void unpack_u2(uint32_t h, uint32_t (&o)[4]) {
 
 // Two 16-bit groups packed in x (group a in the low half, b in the high half; dims 0..3 of a group
 // in its byte 0, 4..7 in its byte 1, dim 4j + k at bits 2k of byte j) -> 4 fp16 pairs each, (dim k,
-// dim k + 4), k = 0..3: the order unpack_word gives INT4 nibbles.
+// dim k + 4), k = 0..3: the order unpack_word gives INT4 nibbles.  LO, HI: the byte table.
+template <uint32_t LO = kU2Lo, uint32_t HI = kU2Hi>
 __device__ __forceinline__ void unpack_u2_x2(uint32_t x, uint32_t (&oa)[4], uint32_t (&ob)[4]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const uint32_t s = u2_selectors(x, k);
-        oa[k] = prmt(kU2Lo, kU2Hi, s);
-        ob[k] = prmt(kU2Lo, kU2Hi, s >> 16);
+        oa[k] = prmt(LO, HI, s);
+        ob[k] = prmt(LO, HI, s >> 16);
     }
 }
 

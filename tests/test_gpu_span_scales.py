@@ -1,4 +1,5 @@
-"""The attention over key spans on rows that are not finite, at positions past 2^24, and on values of very different sizes."""
+"""The attention over key spans on rows that are not finite, at positions past 2^24, on values of very different
+sizes, and the values themselves."""
 import numpy as np
 import pytest
 import torch
@@ -170,3 +171,21 @@ def test_rows_of_zeros_before_everything(bits):
                 for j in range(first, first + 50):
                     _row(b, 0, j).zero_()
                 _far_apart(b, torch.float32, key_end=np.full(qlen, 400))
+
+
+# ------------------------------------------------------------------ the values themselves
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bits", [4, 8, 2])
+def test_a_row_that_sees_one_key_gives_its_value(bits, d):
+    """The output is the cached value as the read-back gives it, in the 2-norm within: the INT2 numbers in the tiles 2.5e-7,
+    the weight's two halves 2^-23, the quotient by the sum and the factor of the rotation 3 2^-24, and the seven steps of the
+    rotation 7 2^-24 of the norm: 1e-6."""
+    for qlen in (1, 70):
+        b = Batch(bits, (200, 90), (qlen, qlen), 8, 2, d, seed=47)
+        got = b.call(key_begin=b.pos()).double().cpu().numpy()
+        slots = np.concatenate([np.asarray(b.tables[i])[np.arange(n - qlen, n) // 16].astype(np.int64) * 16 + np.arange(n - qlen, n) % 16
+                                for i, n in enumerate(b.lens)])
+        rows = b.cache.cpu().numpy()[slots // 16, 1, slots % 16]
+        want = b.decode(np.ascontiguousarray(rows.reshape(-1, rows.shape[-1]))).reshape(2 * qlen, 2, d).repeat(4, axis=1)
+        assert (np.linalg.norm(got - want, axis=2) / np.linalg.norm(want, axis=2)).max() <= 1e-6
