@@ -585,12 +585,16 @@ kv_int4_status kv_int4_paged_attention_noalloc_ex(const void* q, kv_int4_dtype q
  *
  * Computation: one kernel for chunks and single tokens (tcgen05), 128 rows (query tokens x the heads of one kv head)
  * against the keys that some of them see; with few row tiles the keys are split among the SMs and a second kernel
- * joins the partials.  Queries and sums keep 22 bits and more, the softmax weights 22 (11 for a bf16 output of
- * sequences with more than 64 rows).  The split depends on the sizes alone: the same call gives the same bits, a
- * sequence in another batch may differ in the last ones.
+ * joins the partials.  Queries, cached values, capped scores and sums keep 22 bits and more.  The softmax weights keep 22
+ * (those times their value's scale in steps of 2^-30 of the row's largest), but 11 in a call with a bf16 output and
+ * max_query_len * (query heads per kv head) > 64; that holds for all of its sequences, single tokens among them.  The split depends on the sizes alone: the same call gives the same bits, a
+ * sequence in another batch may differ by what its weights keep.
+ * Plain causal single tokens are the paged attention's work too, and faster there as a rule (GPU time of this call and
+ * of kv_int{4,8,2}_paged_attention, us: 8 x 131072 tokens, 64 query / 8 kv heads, INT4 433 and 292, INT8 527 and 415, INT2
+ * 459 and 450; 64 x 8192, 32 / 8 heads, 272 and 147, 307 and 209, 275 and 171; 16 x 2048, 24-26 and 25-26).
  *
  * key_begin, key_end  [num_q_tokens] int32 or NULL.
- * softcap             0: none; negative or not finite: KV_INT4_EINVAL.
+ * softcap             0: none; negative, above 3e38 or not a number: KV_INT4_EINVAL.
  * alibi_slopes        [num_q_heads] fp32 or NULL.
  * max_query_len       host int: max over b of q_len_b.  Queries past it are left as they were (counted as bad metadata).
  * max_seq_len         host int: >= max over b of seq_lens[b].  Longer contexts are clamped to it, and to the block
@@ -601,7 +605,9 @@ kv_int4_status kv_int4_paged_attention_noalloc_ex(const void* q, kv_int4_dtype q
  *                     calls must not share a workspace.
  * A block id outside [0, num_blocks) hides its keys and is counted; a chunk longer than its sequence is counted, but
  * for a sequence of no tokens (a padding row), which gives zeros.
- * Other arguments, alignment, supported sizes and error behaviour as kv_int4_paged_attention.
+ * Supported sizes: head_size 64 or 128; 1, 2, 4 or 8 kv heads with 1, 2, 4 or 8 query heads each; at most 65535 sequences.
+ * Others (6 or 7 query heads per kv head, 16 or 32 kv heads among them) give KV_INT4_EUNSUPPORTED.
+ * Other arguments, alignment and error behaviour as kv_int4_paged_attention.
  */
 kv_int4_status kv_int4_span_attention(const void* q, kv_int4_dtype q_dtype, int64_t num_q_tokens, int32_t num_q_heads,
                                       const uint8_t* cache, int64_t num_blocks, int32_t num_kv_heads,

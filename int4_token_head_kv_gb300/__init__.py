@@ -858,7 +858,9 @@ def kv_int4_span_attention(query: torch.Tensor, kv_cache: torch.Tensor, block_ta
     document masks of packed prompts, prefixes and images that see themselves whole, windows, or plain causal
     attention, for chunks of any length and single tokens.  ``softcap`` > 0 caps the scaled scores by a tanh,
     ``alibi_slopes`` (fp32 [Hq]) takes slope * |pos - j| off them.  A row whose span is empty gives zeros.  The other
-    arguments as kv_int4_paged_attention's; the workspace is sized by kv_int4_span_workspace_bytes."""
+    arguments as kv_int4_paged_attention's (1, 2, 4 or 8 kv heads with 1, 2, 4 or 8 query heads each, head size 64 or 128);
+    the workspace is sized by kv_int4_span_workspace_bytes.  kv_int4_paged_attention takes plain causal single tokens
+    in less time."""
     return _span_attention("kv_int4_span_attention", 4, query, kv_cache, block_tables, seq_lens, query_start_loc,
                            softmax_scale, rht_signs, max_query_len, max_seq_len, key_begin, key_end, softcap, alibi_slopes,
                            out, out_dtype, workspace, stream)

@@ -749,7 +749,11 @@ struct SpanLayout {
 // Row tiles hold 128 / G tokens of one sequence.  One grid slice per sequence, unless that is much more than a bound
 // on the batch's tiles (a few chunks among many single tokens).  The keys of a tile are split among CTAs so that
 // the estimated time is least: rounds of one CTA per SM, each the tile's key tiles and about five of them for its
-// start and end, and three for the combine.
+// start and end, and three for the combine.  Over 145 shapes (1 to 64 single tokens and chunks of 8 to 1024 queries on 200
+// to 64000 keys, three head layouts, every number of parts timed) that is 2% behind the best number on average and at it for
+// half of them; the furthest takes 32 parts where 10 do (2 x 4000 tokens, 8 q / 2 kv heads: 23.7 us and 17.0).  The
+// batch's tiles against slices: 64 sequences, one of them a chunk of 512 queries, 13 times as many slices: 93 us and 136; a
+// chunk of 200 among 16, 5 times: 38.7 both; 8 of them, 1.7 times: 78.3 and 78.4.
 bool span_layout(int64_t num_q_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size, int32_t num_seqs,
                  int32_t max_query_len, int32_t max_seq_len, SpanLayout* x) {
     if (num_q_tokens <= 0 || num_seqs <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % num_kv_heads != 0 ||

@@ -14,23 +14,25 @@
 // some of them see, 128 at a time; tiles outside that range are not touched, so a document mask costs what its
 // documents hold.  With few row tiles the range is split among CTAs and span_combine_kernel joins the partials.
 // Tiles that every row of a warp sees whole take no mask; tiles that none of them sees take no arithmetic.
-// With a distance bias the tiles go from the last key to the first: the largest logits come first, and the reference
-// maxima, whose moves rescale O and stall the pipeline, settle at once (608 queries behind 8192 tokens, 32 q / 8 kv heads:
+// With a distance bias the tiles go from the last key to the first: the largest logits come first, and the
+// references, whose moves rescale O and stall the pipeline, settle at once (608 queries behind 8192 tokens, 32 q / 8 kv heads:
 // 181 us forwards, 132 backwards).  Without one they go forwards: a causal row's last tile is cut off, and
 // references taken from its few keys move again (107 us forwards, 121 backwards).
 //
-// What bounds it.  2048 queries behind 32768 INT4 tokens, 32 q / 8 kv heads, d 128, bf16: 1222 us, 931 TFLOP/s of the two
-// products that a softmax needs (the kernel does three, for the queries' halves).  608 queries behind 8192: 96 us, the tensor
-// pipe active for 50%, issue slots 56%, the shared-memory data pipe 47% besides the operands: no pipe is full.  A tile goes
-// through S, the softmax's registers, P.V and the S after next, with tensor memory full (two S, O and the queries), and each
-// hand-over is a commit or an arrival, a poll and a fence through a busy shared memory.  A tile takes about 2400 cycles, its
-// 24 products 2130 if alone.  A CTA's start (where it works, barriers, queries turned and split, first S) takes 7 us and its
-// end 3, which is half of the time of rows that see 1000 keys (one packed prompt of 16384 tokens: 608 us).  Single tokens,
-// 8 x 131072 INT2 keys, 64 q / 8 kv heads: 472 us, the same chain for 8 rows.
+// What bounds it.  2048 queries behind 32768 INT4 tokens, 32 q / 8 kv heads, d 128, bf16: 1180 us, 961 TFLOP/s of the two
+// products that a softmax needs.  The kernel does three, for the queries' halves: a tile takes 2240 cycles (the fullest
+// SM's 1056 tiles, less the CTAs' starts and ends) and its 24 products 2130 if alone, 88.6 cycles each where the tensor
+// pipe is busy for 62: their operands come through shared memory.  608 queries behind 8192, 93 us: tensor pipe 54%, issue
+// slots 57%, shared-memory data pipe 48% besides the operands.  A tile goes through S, the softmax's registers, P.V and the S
+// after next, with tensor memory full (two S, O and the queries), and each hand-over is a commit or an arrival, a poll and a
+// fence through a busy shared memory.  A CTA's start (where it works, barriers, queries turned and split, first S) takes 7
+// us and its end 3, which is half of the time of rows that see 1000 keys (one packed prompt of 16384 tokens: 568 us).
+// Single tokens, 8 x 131072 INT2 keys, 64 q / 8 kv heads: 462 us, the same chain for 8 rows.
 // Dropped after measuring: CTAs that stay for several row tiles, statically or by cluster launch control (that prompt: 821
 // and 804 us against 667 then; the hardware balances as well, and queries turned in registers take longer than a
 // product); a third V buffer (single tokens 513 against 505); two warps to a single token's softmax (560 against 504);
-// K scales read ahead of S (+2%); one barrier polled after the other (1250 against 1222).
+// K scales read ahead of S (+2%); one barrier polled after the other (1250 against 1222); the products formed in
+// every tile, with the largest one looked at after the weights (1283 against 1200), in place of a bound before them.
 #pragma once
 
 #include "attn_prefix.cuh"
@@ -151,7 +153,7 @@ __device__ __forceinline__ float2 capped(float2 y, const SpanParams& p, float2 o
 }
 // The same for |y| <= 2 / 5, without the two special functions: y (C + C a1 y^2 + C a2 y^4 + C a3 y^6), a minimax fit of
 // tanh(y) / y with the value 1 at 0 that is off by 1.2e-7 at most, two roundings.  A fourth term would take logits within
-// half of the cap, and 785 us instead of 775 for 4 x 2048 queries behind 2048 keys, prefix masks, a cap of 50.
+// half of the cap, and 1.3% longer (4 x 2048 queries behind 2048 keys, prefix masks, a cap of 50).
 __device__ __forceinline__ float2 capped_small(float2 y, const SpanParams& p, float2 off) {
     const float2 t = mul_f32x2(y, y);
     float2 q = fma_f32x2(t, make_float2(p.cap_q[3], p.cap_q[3]), make_float2(p.cap_q[2], p.cap_q[2]));
@@ -187,10 +189,10 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
     using Ly = SpLayout<D, BITS>;
     using Tm = PfTmem<D>;
     constexpr int KSTEPS = D / 16, RB = (int)Ly::kRowBytes, kStages = Ly::kStages;
-    // Whether the softmax waits for the V scales alone and the MMA warp for the V tile.  INT8, whose longer rows are converted
-    // in one go once their tile is free, 608 queries on 8800 keys: 102 us with it and 109 without; with options 141 and 144
-    // (cap), 115 and 118 (bias).  Few rows: 8 x 131072 INT4 tokens 442 and 537.  INT4 and INT2 chunks without options: 101
-    // and 95, 108 and 104, as P.V waits for two barriers.
+    // Whether the softmax waits for the V scales alone and the MMA warp for the V tile.  608 queries on 8800 keys: INT8, whose
+    // longer rows are converted in one go once their tile is free, 102 us with it and 107 without; with a cap 138.8 and
+    // 139.7, with a bias 110 and 112.  Few rows: 8 x 131072 INT4 tokens 442 and 537.  INT4 and INT2 chunks without
+    // options: 101 and 95, 108 and 104, as P.V waits for two barriers.
     constexpr bool EARLY = BITS == 8 || OPTS || FEW;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -638,7 +640,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
 #pragma unroll
                         for (int i = 0; i < 64; i += kPairStep) set(i, capped_small(at(i), p, (i & 2) ? mob2 : moa2));
                     } else {   // every logit takes the form of its own size, so that no hidden key and no other row reaches it
-                        // (608 queries behind 8192 tokens, a cap of 4: 195 us; 167 with one form for the warp)
+                        // (608 queries behind 8192 tokens: a cap of 4 185 us, of 50 139)
 #pragma unroll
                         for (int i = 0; i < 64; i += kPairStep) {
                             const float2 y = at(i), off = (i & 2) ? mob2 : moa2;
@@ -657,7 +659,7 @@ __global__ void __launch_bounds__(kPxThreads, 1) span_kernel(const __grid_consta
                 }
                 if (OPTS && p.alibi) {
                     // distances, not positions, as fp32 numbers: near ones are exact however long the context.  (The first
-                    // query's position from shared memory: registers are short here, 4 x 2048 queries with a cap 781 us against 783.)
+                    // query's position from shared memory: registers are short here.)
                     const float first = (float)(where[4] - key0), da0 = first + pos_a, db0 = first + pos_b;
                     const float2 sla2 = make_float2(-sl_a, -sl_a), slb2 = make_float2(-sl_b, -sl_b);
 #pragma unroll
